@@ -9,6 +9,7 @@ handed over by PyTorch belong to the runtime that launches the kernels; two
 HIP runtimes in one process do not share devices or streams.  Without an
 importable torch it links ROCm's runtime instead.
 """
+import concurrent.futures
 import importlib.util
 import os
 import subprocess
@@ -21,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcpchain.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = [os.path.join(CSRC, "cp_kernels.hip"), os.path.join(CSRC, "cp_chain.cpp")]
+SOURCES = [os.path.join(CSRC, n) for n in ("cp_kernels.hip", "cp_chain.cpp", "cp_ops_gemm_bf16.hip",
+                                           "cp_ops_gemm_f32.hip", "cp_ops_rows.hip", "cp_ops.cpp")]
 ARCH = os.environ.get("CP_OFFLOAD_ARCH", "gfx950")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
@@ -42,8 +44,8 @@ def torch_lib_dir():
 def build(verbose: bool = True, extra=None) -> str:
     t0 = time.time()
     os.makedirs(BUILD_DIR, exist_ok=True)
-    objs = []
-    for src in SOURCES:
+
+    def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
         cmd = [hipcc(), "-x", "hip", "-O3", "-std=c++17", f"--offload-arch={ARCH}",
                "-mcode-object-version=5", "-fPIC", "-c",
@@ -53,7 +55,10 @@ def build(verbose: bool = True, extra=None) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tdir = torch_lib_dir()
     if tdir:
         runtime = ["-L" + tdir, "-l:libamdhip64.so", "-Wl,-rpath," + tdir]

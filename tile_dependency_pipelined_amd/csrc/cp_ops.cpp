@@ -1,0 +1,513 @@
+// cp_ops.cpp -- host side of the feed-forward operators (include/cp_ops.h):
+// argument checks, choice of tile and split, launches.  No allocation, no
+// synchronisation, no state.
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "cp_ops_host.h"
+
+using namespace cpo;
+
+namespace {
+
+thread_local char g_error[512];
+
+int fail(int code, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_error, sizeof g_error, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int launched(hipError_t e, const char *what) {
+    if (e == hipSuccess) return CP_OK;
+    return fail(CP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int kComputeUnits = 256;
+
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int elem_size(int dtype) { return dtype == CP_BF16 ? 2 : 4; }
+
+// ------------------------------------------------------------------- checks
+
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+};
+
+int check_dtype(int dtype) {
+    if (dtype != CP_F32 && dtype != CP_BF16) return fail(CP_ERR_UNSUPPORTED, "dtype %d is not supported", dtype);
+    return CP_OK;
+}
+
+int check_sizes(int64_t M, int64_t K, int64_t N) {
+    if (M < 0 || K < 0 || N < 0)
+        return fail(CP_ERR_SHAPE, "negative size (M=%lld K=%lld N=%lld)", (long long)M, (long long)K, (long long)N);
+    if (M > kMaxRows || K > CP_OPS_MAX_WIDTH || N > CP_OPS_MAX_WIDTH)
+        return fail(CP_ERR_SHAPE, "size too large (M=%lld K=%lld N=%lld; at most 2^30 rows, %d columns)", (long long)M,
+                    (long long)K, (long long)N, CP_OPS_MAX_WIDTH);
+    return CP_OK;
+}
+
+int check_act(int act) {
+    if (act < CP_ACT_NONE || act > CP_ACT_SILU) return fail(CP_ERR_UNSUPPORTED, "activation %d is not supported", act);
+    return CP_OK;
+}
+
+// A matrix that is read or written; its ld is set to something usable where
+// there is at most one row.
+int check_mat(Mat &m, int dtype, const char *name) {
+    if (m.rows == 0 || m.cols == 0) {
+        m.ld = up(m.cols, 8);
+        return CP_OK;
+    }
+    if (!m.p) return fail(CP_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(m.p) % elem_size(dtype)) return fail(CP_ERR_INVALID_ARG, "%s is misaligned", name);
+    if (m.rows == 1) {
+        m.ld = up(m.cols, 8);
+        return CP_OK;
+    }
+    if (m.ld < m.cols || m.ld > CP_OPS_MAX_WIDTH)
+        return fail(CP_ERR_SHAPE, "%s: row stride %lld with rows of %lld (at least that, at most %d)", name,
+                    (long long)m.ld, (long long)m.cols, CP_OPS_MAX_WIDTH);
+    return CP_OK;
+}
+
+bool aligned16(const Mat &m, int dtype) {
+    const int es = elem_size(dtype);
+    return !m.p || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld * es % 16 == 0 && m.cols * es % 16 == 0);
+}
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+#define CP_TRY(expr)                  \
+    do {                              \
+        const int rc_ = (expr);       \
+        if (rc_ != CP_OK) return rc_; \
+    } while (0)
+
+// ------------------------------------------------------------ tile and split
+
+struct Choice {
+    Config cfg;
+    int nsplit;
+};
+
+// Products: what is to be computed, apart from where it lies.
+struct Shape {
+    int dtype;
+    Layout layout;
+    int mode;
+    int64_t M, N, K;  // rows and columns of C, contraction; kGroupRows: M over all experts; kGroupSum: K over all
+    int groups;
+};
+
+// Row tiles of `bm` rows the launch can have at most.
+int64_t max_row_tiles(const Shape &s, int bm) {
+    if (s.mode != kGroupRows) return ceil_div(s.M, bm);
+    const int64_t used = s.M < s.groups + 1 ? s.M : s.groups + 1;  // spans that hold a row
+    return (s.M + used * (bm - 1)) / bm;
+}
+
+Choice choose(const Shape &s, bool direct) {
+    const int bk = 128 / elem_size(s.dtype);
+    const int64_t slabs = ceil_div(s.mode == kGroupSum ? ceil_div(s.K, s.groups) : s.K, bk);
+    // rows an expert (or the whole product) has on average
+    const int64_t rows = s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M;
+    if (rows <= 16 && s.layout != kTN) {
+        const int64_t tiles = max_row_tiles(s, 16) * ceil_div(s.N, 128);
+        int64_t n = 2 * kComputeUnits / (tiles ? tiles : 1);
+        if (n > slabs / 4) n = slabs / 4;
+        if (n > 32) n = 32;
+        return {kTile16, n < 1 ? 1 : (int)n};
+    }
+    // Tiles an average launch has, and the time of the rounds they take in
+    // units of a 128 x 128 tile's share of a CU.
+    auto tiles_of = [&](int b) {
+        const int64_t tm = s.mode == kGroupRows ? s.M / b + (s.groups + 1) / 2 : ceil_div(s.M, b);
+        return tm * ceil_div(s.N, b) * (s.mode == kGroupSum ? s.groups : 1);
+    };
+    const int64_t t128 = tiles_of(128), t256 = tiles_of(256);
+    const double c128 = 2.5 * ceil_div(t128, 2 * kComputeUnits), c256 = 4.0 * ceil_div(t256, kComputeUnits);
+    if (s.dtype == CP_BF16 && direct && c256 <= c128) return {kTile256, 1};
+    int64_t n = 1;
+    if (s.mode == kDense && 2 * t128 <= kComputeUnits) {
+        n = kComputeUnits / t128;
+        if (n > slabs / 8) n = slabs / 8;
+        if (n > 16) n = 16;
+    }
+    return {kTile128, n < 1 ? 1 : (int)n};
+}
+
+int64_t split_bytes(const Shape &s) {
+    if (s.M == 0 || s.N == 0) return 0;
+    int64_t most = 0;
+    for (int direct = 0; direct < 2; ++direct) {
+        const Choice c = choose(s, direct);
+        const int64_t b = c.nsplit > 1 ? (int64_t)c.nsplit * s.M * up(s.N, 8) * 4 : 0;
+        if (b > most) most = b;
+    }
+    return most;
+}
+
+// ------------------------------------------------------------------ products
+
+struct Product {
+    Shape s;
+    Mat A, B, C;  // as stored
+    int64_t sb = 0, sc = 0;
+    const int32_t *off = nullptr;
+    const void *bias = nullptr;
+    Mat R{nullptr, 0, 0, 0}, P{nullptr, 0, 0, 0};
+    int act = CP_ACT_NONE;
+};
+
+int run_product(const Product &p, void *ws, hipStream_t stream) {
+    const Shape &s = p.s;
+    if (s.M == 0 || s.N == 0) return CP_OK;
+    const int es = elem_size(s.dtype);
+    bool direct = aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0;
+    const Choice c = choose(s, direct);
+    GemmArgs g{};
+    g.A = (const char *)p.A.p;
+    g.B = (const char *)p.B.p;
+    g.C = (char *)p.C.p;
+    g.bias = (const char *)p.bias;
+    g.res = (const char *)p.R.p;
+    g.pre = (char *)p.P.p;
+    g.ws = (float *)ws;
+    g.lda = p.A.ld;
+    g.ldb = p.B.ld;
+    g.ldc = p.C.ld;
+    g.ldr = p.R.ld;
+    g.ldp = p.P.ld;
+    g.sb = p.sb;
+    g.sc = p.sc;
+    g.off = p.off;
+    g.groups = s.groups;
+    g.mode = s.mode;
+    g.M = (int)s.M;
+    g.N = (int)s.N;
+    g.K = (int)s.K;
+    g.act = p.act;
+    g.nsplit = c.nsplit;
+    g.ldws = (int)up(s.N, 8);
+    g.vec = aligned16(p.C, s.dtype) && aligned16(p.R, s.dtype) && aligned16(p.P, s.dtype) && aligned16(p.bias) &&
+            p.sc * es % 16 == 0;
+    const ConfigShape t = kShapes[c.cfg];
+    g.ntn = (int)ceil_div(s.N, t.bn);
+    const int64_t ntm = max_row_tiles(s, t.bm);
+    g.ntm = (int)ntm;
+    const int64_t grid = ntm * g.ntn * c.nsplit * (s.mode == kGroupSum ? s.groups : 1);
+    if (grid > 0x7FFFFFFF) return fail(CP_ERR_SHAPE, "too many tiles (%lld)", (long long)grid);
+    CP_TRY(launched(s.dtype == CP_BF16 ? launch_product_bf16(s.layout, c.cfg, direct, g, (int)grid, stream)
+                                       : launch_product_f32(s.layout, c.cfg, direct, g, (int)grid, stream),
+                    "product"));
+    if (c.nsplit > 1) CP_TRY(launched(launch_join(s.dtype, g, stream), "join"));
+    return CP_OK;
+}
+
+// ------------------------------------------------- the linear layers, dense and
+// grouped (groups == 0: dense)
+
+Shape forward_shape(int dtype, int64_t M, int64_t K, int64_t N, int groups, bool wt) {
+    return {dtype, wt ? kNT : kNN, groups ? kGroupRows : kDense, M, N, K, groups};
+}
+Shape dx_shape(int dtype, int64_t M, int64_t K, int64_t N, int groups, bool wt) {
+    return {dtype, wt ? kNN : kNT, groups ? kGroupRows : kDense, M, K, N, groups};
+}
+Shape dw_shape(int dtype, int64_t M, int64_t K, int64_t N, int groups, bool wt) {
+    return {dtype, kTN, groups ? kGroupSum : kDense, wt ? N : K, wt ? K : N, M, groups};
+}
+
+int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
+int64_t forward_ws(int dtype, int64_t M, int64_t K, int64_t N, int groups) {
+    return max64(split_bytes(forward_shape(dtype, M, K, N, groups, false)),
+                 split_bytes(forward_shape(dtype, M, K, N, groups, true)));
+}
+
+struct BackwardWs {
+    int64_t dz, sums, split, total;  // offsets of the parts and the end
+};
+BackwardWs backward_ws(int dtype, int64_t M, int64_t K, int64_t N, int groups) {
+    BackwardWs w{};
+    const Shape rows{dtype, kNN, groups ? kGroupRows : kDense, M, N, K, groups};
+    w.dz = 0;
+    w.sums = up(M * up(N, 8) * elem_size(dtype), 256);
+    w.split = w.sums + up(max_row_tiles(rows, kGradRows) * N * 4, 256);
+    int64_t most = 0;
+    for (int wt = 0; wt < 2; ++wt) {
+        most = max64(most, split_bytes(dx_shape(dtype, M, K, N, groups, wt)));
+        most = max64(most, split_bytes(dw_shape(dtype, M, K, N, groups, wt)));
+    }
+    w.total = w.split + most;
+    return w;
+}
+
+int check_ws(const void *ws, int64_t have, int64_t need) {
+    if (need == 0) return CP_OK;
+    if (!ws || have < need)
+        return fail(CP_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", ws ? (long long)have : 0, (long long)need);
+    if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(CP_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    return CP_OK;
+}
+
+int check_groups(int E, const void *off, int64_t stride, const Mat &w, const char *name) {
+    if (E < 1 || E > CP_OPS_MAX_GROUPS)
+        return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
+    if (!off) return fail(CP_ERR_INVALID_ARG, "offsets is NULL");
+    if (reinterpret_cast<uintptr_t>(off) % 4) return fail(CP_ERR_INVALID_ARG, "offsets is misaligned");
+    const int64_t span = w.rows && w.cols ? (w.rows - 1) * w.ld + w.cols : 0;
+    if (w.p && E > 1 && stride < (w.rows == 1 ? w.cols : span))
+        return fail(CP_ERR_SHAPE, "%s: expert stride %lld, one expert spans %lld", name, (long long)stride,
+                    (long long)span);
+    return CP_OK;
+}
+
+int check_vector(const void *p, int dtype, const char *name) {
+    if (reinterpret_cast<uintptr_t>(p) % elem_size(dtype)) return fail(CP_ERR_INVALID_ARG, "%s is misaligned", name);
+    return CP_OK;
+}
+
+int forward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X, int64_t ldx, const void *W, int64_t ldw,
+            int64_t stride_w, bool wt, const int32_t *off, const void *bias, const void *R, int64_t ldr, int act, void *Y,
+            int64_t ldy, void *pre, int64_t ldp, void *ws, int64_t ws_bytes, void *stream) {
+    CP_TRY(check_dtype(dtype));
+    CP_TRY(check_sizes(M, K, N));
+    CP_TRY(check_act(act));
+    Product p{};
+    p.s = forward_shape(dtype, M, K, N, E, wt);
+    p.A = {X, M, K, ldx};
+    p.B = {W, wt ? N : K, wt ? K : N, ldw};
+    p.C = {Y, M, N, ldy};
+    CP_TRY(check_mat(p.A, dtype, "X"));
+    CP_TRY(check_mat(p.B, dtype, "W"));
+    CP_TRY(check_mat(p.C, dtype, "Y"));
+    if (R) {
+        p.R = {R, M, N, ldr};
+        CP_TRY(check_mat(p.R, dtype, "R"));
+    }
+    if (pre) {
+        p.P = {pre, M, N, ldp};
+        CP_TRY(check_mat(p.P, dtype, "pre"));
+    }
+    CP_TRY(check_vector(bias, dtype, "bias"));
+    if (E) CP_TRY(check_groups(E, off, stride_w, p.B, "W"));
+    CP_TRY(check_ws(ws, ws_bytes, forward_ws(dtype, M, K, N, E)));
+    p.sb = E > 1 ? stride_w : 0;
+    p.off = off;
+    p.bias = bias;
+    p.act = act;
+    return run_product(p, ws, (hipStream_t)stream);
+}
+
+int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, int64_t lddy, const void *X, int64_t ldx,
+             const void *W, int64_t ldw, int64_t stride_w, bool wt, const int32_t *off, const void *pre, int64_t ldp,
+             int act, void *dX, int64_t lddx, void *dW, int64_t lddw, int64_t stride_dw, void *db, void *ws,
+             int64_t ws_bytes, void *stream) {
+    CP_TRY(check_dtype(dtype));
+    CP_TRY(check_sizes(M, K, N));
+    CP_TRY(check_act(act));
+    Mat dy{dY, M, N, lddy}, x{X, M, K, ldx}, w{W, wt ? N : K, wt ? K : N, ldw}, z{pre, M, N, ldp};
+    Mat dx{dX, M, K, lddx}, dw{dW, w.rows, w.cols, lddw};
+    if (dX || dW || db) CP_TRY(check_mat(dy, dtype, "dY"));
+    if (act != CP_ACT_NONE) CP_TRY(check_mat(z, dtype, "pre"));
+    if (dX) {
+        CP_TRY(check_mat(w, dtype, "W"));
+        CP_TRY(check_mat(dx, dtype, "dX"));
+    }
+    if (dW) {
+        CP_TRY(check_mat(x, dtype, "X"));
+        CP_TRY(check_mat(dw, dtype, "dW"));
+    }
+    CP_TRY(check_vector(db, dtype, "db"));
+    if (E) {
+        CP_TRY(check_groups(E, off, stride_w, dX ? w : Mat{nullptr, 0, 0, 0}, "W"));
+        CP_TRY(check_groups(E, off, stride_dw, dW ? dw : Mat{nullptr, 0, 0, 0}, "dW"));
+    }
+    const BackwardWs lay = backward_ws(dtype, M, K, N, E);
+    CP_TRY(check_ws(ws, ws_bytes, lay.total));
+    if (!dX && !dW && !db) return CP_OK;
+    hipStream_t s = (hipStream_t)stream;
+    char *base = (char *)ws;
+    Mat dz = dy;
+    const bool need_dz = act != CP_ACT_NONE && (dX || dW);
+    if (need_dz) dz = {base + lay.dz, M, N, up(N, 8)};
+    if (N > 0 && (act != CP_ACT_NONE || db)) {
+        GradArgs a{};
+        a.dy = (const char *)dy.p;
+        a.ldd = dy.ld;
+        if (act != CP_ACT_NONE) {
+            // without dX and dW the values only pass through to the sums
+            a.pre = (const char *)z.p;
+            a.ldp = z.ld;
+            a.dz = base + lay.dz;
+            a.ldz = up(N, 8);
+        }
+        a.db = (char *)db;
+        a.ws = (float *)(base + lay.sums);
+        a.off = off;
+        a.groups = E ? E : 1;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.act = act;
+        const Shape rows{dtype, kNN, E ? kGroupRows : kDense, M, N, K, E};
+        a.tiles = (int)max_row_tiles(rows, kGradRows);
+        a.vec = aligned16(dy, dtype) && (act == CP_ACT_NONE || aligned16(z, dtype));
+        CP_TRY(launched(launch_grad(dtype, a, s), "activation gradient"));
+    }
+    if (dX) {
+        Product p{};
+        p.s = dx_shape(dtype, M, K, N, E, wt);
+        p.A = dz;
+        p.B = w;
+        p.C = dx;
+        p.sb = E > 1 ? stride_w : 0;
+        p.off = off;
+        CP_TRY(run_product(p, base + lay.split, s));
+    }
+    if (dW) {
+        Product p{};
+        p.s = dw_shape(dtype, M, K, N, E, wt);
+        p.A = wt ? dz : x;
+        p.B = wt ? x : dz;
+        p.C = dw;
+        p.sc = E > 1 ? stride_dw : 0;
+        p.off = off;
+        CP_TRY(run_product(p, base + lay.split, s));
+    }
+    return CP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char *cp_ops_last_error(void) { return g_error; }
+
+int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E) {
+    g_error[0] = 0;
+    CP_TRY(check_dtype(dtype));
+    CP_TRY(check_sizes(M, op == CP_OP_LAYER_NORM_BACKWARD ? 0 : K, N));
+    const bool grouped = op == CP_OP_GROUPED_LINEAR || op == CP_OP_GROUPED_LINEAR_BACKWARD;
+    if (grouped && (E < 1 || E > CP_OPS_MAX_GROUPS))
+        return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
+    switch (op) {
+        case CP_OP_LINEAR: return forward_ws(dtype, M, K, N, 0);
+        case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E);
+        case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0).total;
+        case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E).total;
+        case CP_OP_LAYER_NORM_BACKWARD: return (int64_t)norm_backward_blocks(dtype, M, N) * N * 8;
+    }
+    return fail(CP_ERR_INVALID_ARG, "operator code %d", op);
+}
+
+int cp_linear(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *X, int64_t ldx, const void *W, int64_t ldw,
+              int32_t w_trans, const void *bias, const void *R, int64_t ldr, int32_t act, void *Y, int64_t ldy,
+              void *pre, int64_t ldp, void *ws, int64_t ws_bytes, void *stream) {
+    g_error[0] = 0;
+    return forward(dtype, M, K, N, 0, X, ldx, W, ldw, 0, w_trans != 0, nullptr, bias, R, ldr, act, Y, ldy, pre, ldp, ws,
+                   ws_bytes, stream);
+}
+
+int cp_linear_backward(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *dY, int64_t lddy, const void *X,
+                       int64_t ldx, const void *W, int64_t ldw, int32_t w_trans, const void *pre, int64_t ldp,
+                       int32_t act, void *dX, int64_t lddx, void *dW, int64_t lddw, void *db, void *ws,
+                       int64_t ws_bytes, void *stream) {
+    g_error[0] = 0;
+    return backward(dtype, M, K, N, 0, dY, lddy, X, ldx, W, ldw, 0, w_trans != 0, nullptr, pre, ldp, act, dX, lddx, dW,
+                    lddw, 0, db, ws, ws_bytes, stream);
+}
+
+int cp_grouped_linear(int32_t dtype, int64_t T, int64_t K, int64_t N, int32_t E, const void *X, int64_t ldx,
+                      const void *W, int64_t ldw, int64_t stride_w, int32_t w_trans, const int32_t *offsets,
+                      const void *bias, int32_t act, void *Y, int64_t ldy, void *pre, int64_t ldp, void *ws,
+                      int64_t ws_bytes, void *stream) {
+    g_error[0] = 0;
+    if (E < 1) return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
+    return forward(dtype, T, K, N, E, X, ldx, W, ldw, stride_w, w_trans != 0, offsets, bias, nullptr, 0, act, Y, ldy,
+                   pre, ldp, ws, ws_bytes, stream);
+}
+
+int cp_grouped_linear_backward(int32_t dtype, int64_t T, int64_t K, int64_t N, int32_t E, const void *dY, int64_t lddy,
+                               const void *X, int64_t ldx, const void *W, int64_t ldw, int64_t stride_w,
+                               int32_t w_trans, const int32_t *offsets, const void *pre, int64_t ldp, int32_t act,
+                               void *dX, int64_t lddx, void *dW, int64_t lddw, int64_t stride_dw, void *db, void *ws,
+                               int64_t ws_bytes, void *stream) {
+    g_error[0] = 0;
+    if (E < 1) return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
+    return backward(dtype, T, K, N, E, dY, lddy, X, ldx, W, ldw, stride_w, w_trans != 0, offsets, pre, ldp, act, dX,
+                    lddx, dW, lddw, stride_dw, db, ws, ws_bytes, stream);
+}
+
+int cp_layer_norm(int32_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx, const void *w, const void *b,
+                  float eps, void *Y, int64_t ldy, float *mean, float *rstd, void *stream) {
+    g_error[0] = 0;
+    CP_TRY(check_dtype(dtype));
+    CP_TRY(check_sizes(M, 0, N));
+    if (!(eps >= 0.0f)) return fail(CP_ERR_INVALID_ARG, "eps %g", (double)eps);
+    if (M == 0) return CP_OK;
+    if (N == 0) return fail(CP_ERR_SHAPE, "rows without elements have no mean");
+    Mat x{X, M, N, ldx}, y{Y, M, N, ldy};
+    CP_TRY(check_mat(x, dtype, "X"));
+    CP_TRY(check_mat(y, dtype, "Y"));
+    CP_TRY(check_vector(w, dtype, "w"));
+    CP_TRY(check_vector(b, dtype, "b"));
+    NormArgs a{};
+    a.x = (const char *)X;
+    a.w = (const char *)w;
+    a.b = (const char *)b;
+    a.y = (char *)Y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ldx = x.ld;
+    a.ldy = y.ld;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.eps = eps;
+    a.vec = aligned16(x, dtype) && aligned16(y, dtype) && aligned16(w) && aligned16(b);
+    return launched(launch_norm(dtype, a, (hipStream_t)stream), "layer norm");
+}
+
+int cp_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, int64_t lddy, const void *X,
+                           int64_t ldx, const float *mean, const float *rstd, const void *w, void *dX, int64_t lddx,
+                           void *dw, void *db, void *ws, int64_t ws_bytes, void *stream) {
+    g_error[0] = 0;
+    CP_TRY(check_dtype(dtype));
+    CP_TRY(check_sizes(M, 0, N));
+    if (N == 0 || (!dX && !dw && !db)) return CP_OK;
+    Mat dy{dY, M, N, lddy}, x{X, M, N, ldx}, dx{dX, M, N, lddx};
+    CP_TRY(check_mat(dy, dtype, "dY"));
+    CP_TRY(check_mat(x, dtype, "X"));
+    if (dX) CP_TRY(check_mat(dx, dtype, "dX"));
+    if (M > 0 && (!mean || !rstd)) return fail(CP_ERR_INVALID_ARG, "mean or rstd is NULL");
+    CP_TRY(check_vector(w, dtype, "w"));
+    CP_TRY(check_vector(dw, dtype, "dw"));
+    CP_TRY(check_vector(db, dtype, "db"));
+    NormArgs a{};
+    a.blocks = norm_backward_blocks(dtype, M, N);
+    CP_TRY(check_ws(ws, ws_bytes, (int64_t)a.blocks * N * 8));
+    a.x = (const char *)X;
+    a.dy = (const char *)dY;
+    a.w = (const char *)w;
+    a.y = (char *)dX;
+    a.dw = (char *)dw;
+    a.db = (char *)db;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.ws = (float *)ws;
+    a.ldx = x.ld;
+    a.ldd = dy.ld;
+    a.ldy = dx.ld;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.vec = aligned16(dy, dtype) && aligned16(x, dtype) && aligned16(dx, dtype) && aligned16(w);
+    return launched(launch_norm_backward(dtype, a, (hipStream_t)stream), "layer norm backward");
+}
+
+}  // extern "C"

@@ -1,0 +1,261 @@
+// cp_ops_device.h -- what the feed-forward operators' kernels share: launch
+// arguments, element conversion, activations, the row spans of experts.
+// Internal to the library (the C ABI is include/cp_ops.h).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cp_ops.h"
+
+namespace cpo {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef short v4i16_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
+
+// Elements of 16 bytes, the unit of all wide loads and stores.
+template <class T>
+constexpr int kUnit = 16 / (int)sizeof(T);
+
+enum : int32_t { kDense = 0, kGroupRows = 1, kGroupSum = 2 };
+
+// One product launch: C = epilogue(A . B) with A[m][k], B[k][n]; which of the
+// two indices is contiguous in memory is a template argument of the kernel.
+//   kDense      one product
+//   kGroupRows  rows of A and C are sorted by expert; B (and bias) per expert
+//   kGroupSum   the contraction runs over rows sorted by expert: one C per
+//               expert
+struct GemmArgs {
+    const char *A, *B;
+    char *C;
+    const char *bias, *res;  // epilogue inputs or null
+    char *pre;               // pre-activation output or null
+    float *ws;               // nsplit > 1: fp32 partials [nsplit][M][ldws]
+    int64_t lda, ldb, ldc, ldr, ldp;  // elements
+    int64_t sb, sc;          // per-expert strides of B (kGroupRows) and C (kGroupSum)
+    const int32_t *off;      // device: groups + 1 row offsets, or null
+    int32_t groups, mode;
+    int32_t M, N, K;         // rows and columns of C, contraction (kGroupRows: M = all rows; kGroupSum: K = all rows)
+    int32_t act;
+    int32_t nsplit;          // contraction ranges, each to its own partial
+    int32_t ntm, ntn;        // tiles (kGroupRows: ntm is not used, the device counts)
+    int32_t ldws;
+    int32_t vec;             // C, R, pre and bias can be accessed 16 bytes at a time
+};
+
+// ---------------------------------------------------------------- elements
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v) {
+    return (float)v;
+}
+// fp32 -> T: to nearest even, NaN stays NaN
+template <class T>
+__device__ __forceinline__ T from_f32(float v) {
+    return (T)v;
+}
+
+template <class T>
+__device__ __forceinline__ void load_unit(const void *p, float (&v)[kUnit<T>]) {  // 16-byte aligned
+    union {
+        uint4 u;
+        T e[kUnit<T>];
+    } x;
+    x.u = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+    for (int i = 0; i < kUnit<T>; ++i) v[i] = to_f32(x.e[i]);
+}
+template <class T>
+__device__ __forceinline__ void store_unit(void *p, const float (&v)[kUnit<T>]) {
+    union {
+        uint4 u;
+        T e[kUnit<T>];
+    } x;
+#pragma unroll
+    for (int i = 0; i < kUnit<T>; ++i) x.e[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<uint4 *>(p) = x.u;
+}
+
+// 16 bytes of which only the first `n` elements (0 .. kUnit) may be read, the
+// rest zero; any alignment.  A whole unit is one 16-byte load (global loads
+// need no alignment on this target).
+template <class T>
+__device__ __forceinline__ uint4 load_partial(const char *p, int n) {
+    union {
+        uint4 u;
+        T e[kUnit<T>];
+    } x;
+    if (n >= kUnit<T>) {
+        __builtin_memcpy(&x.u, p, 16);
+    } else {
+        x.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kUnit<T> - 1; ++i)
+            if (i < n) x.e[i] = reinterpret_cast<const T *>(p)[i];
+    }
+    return x.u;
+}
+
+// -------------------------------------------------------------- activations
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+constexpr float kGelu0 = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGelu1 = 0.044715f;
+
+// (1 + tanh u) / 2 = sigmoid(2 u), so the tanh form of GeLU is
+// x sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)): one exponential, one reciprocal,
+// and no cancellation for negative x.
+__device__ __forceinline__ float act_apply(float x, int act) {
+    if (act == CP_ACT_GELU_TANH) return x * sigmoid(2.0f * kGelu0 * (x + kGelu1 * x * x * x));
+    if (act == CP_ACT_SILU) return x * sigmoid(x);
+    if (act == CP_ACT_RELU) return x < 0.0f ? 0.0f : x;
+    return x;
+}
+
+__device__ __forceinline__ float clamp_keep_nan(float x, float lim) { return x < -lim ? -lim : (x > lim ? lim : x); }
+
+// Derivative.  Beyond the clamps it is 0 or 1 to fp32 precision; without them
+// x^2 could overflow and 0 * inf give NaN for a finite x.
+__device__ __forceinline__ float act_grad(float x, int act) {
+    if (act == CP_ACT_GELU_TANH) {
+        x = clamp_keep_nan(x, 10.0f);
+        const float p = sigmoid(2.0f * kGelu0 * (x + kGelu1 * x * x * x));
+        return p + 2.0f * x * p * (1.0f - p) * kGelu0 * (1.0f + 3.0f * kGelu1 * x * x);
+    }
+    if (act == CP_ACT_SILU) {
+        x = clamp_keep_nan(x, 80.0f);
+        const float p = sigmoid(x);
+        return p + x * p * (1.0f - p);
+    }
+    if (act == CP_ACT_RELU) return x > 0.0f ? 1.0f : (x == x ? 0.0f : x);
+    return 1.0f;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// Epilogue of one run of CNT consecutive columns of a row (fp32 sums v):
+// bias, pre-activation store, activation, residual, one rounding, store.
+// WIDE: CNT is a unit and every pointer 16-byte aligned.
+template <class T, int CNT>
+__device__ __forceinline__ void finish(const GemmArgs &g, char *C, const char *bias, int row, int col, float (&v)[CNT],
+                                       bool zero) {
+    constexpr bool WIDE = CNT > 1;
+    static_assert(CNT == 1 || CNT == kUnit<T>, "columns per call");
+    auto get = [](const char *p, float(&x)[CNT]) {
+        if constexpr (WIDE) load_unit<T>(p, x);
+        else x[0] = to_f32(*reinterpret_cast<const T *>(p));
+    };
+    auto put = [](char *p, const float(&x)[CNT]) {
+        if constexpr (WIDE) store_unit<T>(p, x);
+        else *reinterpret_cast<T *>(p) = from_f32<T>(x[0]);
+    };
+    float t[CNT];
+    if (bias) {
+        get(bias + (int64_t)col * sizeof(T), t);
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) v[i] = zero ? 0.0f : v[i] + t[i];
+    }
+    if (g.pre) put(g.pre + ((int64_t)row * g.ldp + col) * sizeof(T), v);
+    if (g.act != CP_ACT_NONE)
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) v[i] = act_apply(v[i], g.act);
+    if (g.res) {
+        get(g.res + ((int64_t)row * g.ldr + col) * sizeof(T), t);
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) v[i] += t[i];
+    }
+    put(C + ((int64_t)row * g.ldc + col) * sizeof(T), v);
+}
+
+// ------------------------------------------------------------- expert spans
+
+// Rows of one expert, as 64 lanes look at 64 experts at a time.  Lane l of a
+// wave holds expert base + l; expert `groups` is the rest of the rows, which
+// belong to none.  Offsets are taken as the running maximum of their values
+// clamped to [0, rows], with the first one 0: any content stays in range.
+struct GroupScan {
+    int start, end;  // this lane's rows
+    int tiles_end;   // tiles of `tile` rows up to and including this lane's expert
+};
+
+__device__ __forceinline__ GroupScan scan_groups(const int32_t *off, int groups, int rows, int tile, int base,
+                                                 int carry_end, int carry_tiles) {
+    const int lane = threadIdx.x & 63, e = base + lane;
+    int end = rows;
+    if (e < groups) {
+        end = off[e + 1];
+        end = end < 0 ? 0 : (end > rows ? rows : end);
+    }
+    end = end > carry_end ? end : carry_end;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(end, d);
+        if (lane >= d) end = o > end ? o : end;
+    }
+    int start = __shfl_up(end, 1);
+    if (lane == 0) start = carry_end;
+    int tiles = e <= groups ? (end - start + tile - 1) / tile : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(tiles, d);
+        if (lane >= d) tiles += o;
+    }
+    return {start, end, tiles + carry_tiles};
+}
+
+// All the row tiles of a launch (uniform over the wave).
+__device__ __forceinline__ int count_tiles(const int32_t *off, int groups, int rows, int tile, GroupScan &s) {
+    int carry_end = 0, carry_tiles = 0;
+    for (int base = 0; base <= groups; base += 64) {
+        s = scan_groups(off, groups, rows, tile, base, carry_end, carry_tiles);
+        carry_end = __builtin_amdgcn_readlane(s.end, 63);
+        carry_tiles = __builtin_amdgcn_readlane(s.tiles_end, 63);
+    }
+    return carry_tiles;
+}
+
+struct RowTile {
+    int expert;      // == groups: rows without an expert
+    int row0, end;   // first row, end of the expert's rows
+};
+
+// The expert and rows of row tile t (0 <= t < count_tiles).  `s` is what
+// count_tiles left: with fewer than 64 experts it is the only chunk.
+__device__ __forceinline__ RowTile find_tile(const int32_t *off, int groups, int rows, int tile, int t, GroupScan s) {
+    int carry_end = 0, carry_tiles = 0;
+    for (int base = 0;; base += 64) {
+        if (groups >= 64) s = scan_groups(off, groups, rows, tile, base, carry_end, carry_tiles);
+        const uint64_t hit = __ballot(s.tiles_end > t);
+        if (hit || base + 64 > groups) {
+            const int l = hit ? __builtin_ctzll(hit) : 63;
+            const int before = l ? __builtin_amdgcn_readlane(s.tiles_end, l - 1) : carry_tiles;
+            const int start = __builtin_amdgcn_readlane(s.start, l);
+            return {base + l, start + (t - before) * tile, __builtin_amdgcn_readlane(s.end, l)};
+        }
+        carry_end = __builtin_amdgcn_readlane(s.end, 63);
+        carry_tiles = __builtin_amdgcn_readlane(s.tiles_end, 63);
+    }
+}
+
+// The rows of expert e (uniform), by the same rule.
+__device__ __forceinline__ RowTile expert_rows(const int32_t *off, int groups, int rows, int e) {
+    int carry_end = 0;
+    for (int base = 0;; base += 64) {
+        const GroupScan s = scan_groups(off, groups, rows, 1, base, carry_end, 0);
+        if (e < base + 64)
+            return {e, __builtin_amdgcn_readlane(s.start, e - base), __builtin_amdgcn_readlane(s.end, e - base)};
+        carry_end = __builtin_amdgcn_readlane(s.end, 63);
+    }
+}
+
+// Workgroups go round-robin to the 8 XCDs, each with its own L2.  Of `n`
+// items, give each XCD a contiguous range: item of workgroup b (b < n).
+__device__ __forceinline__ int xcd_remap(int b, int n) {
+    const int x = b & 7, q = n >> 3, r = n & 7;
+    return x * q + (x < r ? x : r) + (b >> 3);
+}
+
+}  // namespace cpo

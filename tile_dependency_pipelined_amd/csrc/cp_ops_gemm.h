@@ -1,0 +1,461 @@
+// cp_ops_gemm.h -- the products of the feed-forward operators for gfx950: one
+// output tile per workgroup, operands through LDS, fp32 accumulation on the
+// matrix cores, epilogue per wave.  Included by the files that instantiate it.
+//
+// C[M][N] = sum over k of A[m][k] B[k][n].  Each operand is either contiguous
+// in k (KC: rows of k) or in its outer index (rows of m or n, one per k):
+//   forward          A = X  KC     B = W   (KC if W is stored [N][K])
+//   input gradient   A = dZ KC     B = W^t (KC if W is stored [K][N])
+//   weight gradient  A = X^t, B = dZ, both contiguous in the outer index
+//
+// LDS tile of an operand with R outer indices (R x 128 bytes: 64 k of bf16,
+// 32 k of fp32), filled by 16-byte loads that go straight to LDS (lane l of a
+// load lands at base + 16 l, so the swizzle is in which chunk a lane fetches):
+//   KC      [R][128 bytes], chunk c of row r at position c ^ swz_kc(r).  A
+//           fragment (16 bytes of one row) is one ds_read_b128; 16 rows of a
+//           block and the two chunks that lanes l and l + 32 read fall on
+//           distinct 16-byte bank groups.
+//   outer   [k][R elements], chunk c of row k at position c ^ swz_out(k).
+//           bf16: a fragment is two ds_read_b64_tr_b16 (each transposes 4 k x
+//           16 columns over 16 lanes); fp32: four 4-byte reads.
+// MFMA v_mfma_f32_16x16x32_bf16 (32 k) or four v_mfma_f32_16x16x4_f32 (16 k:
+// lane group g holds k 4 g + t of the block for product t; the sum does not
+// care which k a lane holds as long as A and B agree).  B is the first operand,
+// so a lane gets output row lane mod 16 and columns 4 (lane / 16) .. + 3.
+#pragma once
+#include <type_traits>
+
+#include "cp_ops_device.h"
+
+namespace cpo {
+
+template <int U>
+using ic = std::integral_constant<int, U>;
+
+// wait until at most N vector-memory operations of this wave are in flight
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+constexpr int kRawBuffer = 0x00020000;       // word 3 of a raw (stride 0) buffer resource
+constexpr uint32_t kOutside = 0xC0000000u;   // an offset past every resource made here (all < 2^31 bytes): reads zeros
+
+// 16-byte direct load to LDS at `lds` + 16 lane (`lds` wave-uniform) in a form
+// the compiler's wait insertion does not see: it would otherwise wait for all
+// direct loads in flight before the next LDS read, whichever array that reads,
+// and a pipeline of more than two stages would never have two slabs in flight.
+// Every read of data loaded this way follows an explicit wait_vm and a barrier.
+__device__ __forceinline__ void lds_load_untracked(__amdgpu_buffer_rsrc_t r, const void *lds, uint32_t voff) {
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t *)lds);
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(m0), "v"(voff), "s"(r)
+        : "memory");
+}
+
+// MFMAs spread evenly between LDS reads, and direct loads between both.
+template <int I, int RD, int MF, int PER>
+__device__ __forceinline__ void interleave() {
+    if constexpr (I < RD) {
+        constexpr int m = (I + 1) * MF / RD - I * MF / RD, p = (I + 1) * PER / RD - I * PER / RD;
+        if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                       // LDS read
+        if constexpr (p > 0) __builtin_amdgcn_sched_group_barrier(0x020, p, 0);  // vector memory read
+        interleave<I + 1, RD, MF, PER>();
+    }
+}
+
+// One operand's tile of R outer indices.
+template <class T, int R, bool KC, int NW>
+struct Operand {
+    static constexpr int ES = sizeof(T), CE = 16 / ES, BK = 128 / ES;
+    static constexpr bool BF = std::is_same<T, __bf16>::value;
+    static constexpr int BYTES = R * 128;
+    static constexpr int LOADS = BYTES / 1024;             // 1 KiB loads of a slab, over the waves
+    static constexpr int PW = LOADS >= NW ? LOADS / NW : 1;  // per wave (fewer loads than waves: some repeat one)
+    static constexpr int RB = R * ES;                      // bytes of an LDS row, outer-contiguous
+    static constexpr int READS = KC ? 1 : (BF ? 2 : 4);    // LDS reads of a fragment
+    static_assert(LOADS >= NW ? LOADS % NW == 0 : NW % LOADS == 0, "loads per wave");
+    static_assert(KC || R >= 64, "bank swizzle");
+
+    // KC: rows r .. r + 15 of a block and chunks c, c + 2
+    __device__ static int swz_kc(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (((r >> 2) & 1) << 2); }
+    // outer: bf16 reads rows k .. k+3 and k+8 .. k+11 x 2 chunks per 32 lanes;
+    // fp32 rows k, k+4, k+8, k+12 x 64 bytes per 64 lanes
+    __device__ static int swz_out(int k) {
+        if constexpr (!BF) return ((k >> 2) & 3) << 2;
+        else if constexpr (R >= 128) return ((0xCA60 >> ((k & 3) * 4)) & 15) ^ (((k >> 3) & 1) << 1);
+        else return ((k & 3) << 1) ^ ((k >> 3) & 1);
+    }
+
+    const char *base;   // KC: first outer row at contraction index kb; outer: row kb, first column
+    int64_t ld;         // bytes
+    int outer;          // valid outer indices (<= R)
+    int klen;           // contraction length of this workgroup
+    uint32_t off[PW];   // bytes from base of this lane's chunk in load q
+    int kc[PW];         // its first contraction index within a slab
+
+    __device__ __forceinline__ static int load_id(int q, int wave) {
+        return LOADS >= NW ? q * NW + wave : wave % LOADS;
+    }
+
+    __device__ __forceinline__ void init(const char *b, int64_t ld_elems, int outer_, int klen_, int wave, int lane) {
+        base = b;
+        ld = ld_elems * ES;
+        outer = outer_ < R ? outer_ : R;
+        klen = klen_;
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+            const int o = load_id(q, wave) * 1024 + lane * 16;
+            if constexpr (KC) {
+                const int r = o >> 7, c = ((o >> 4) & 7) ^ swz_kc(r);
+                off[q] = (uint32_t)r * (uint32_t)ld + (uint32_t)c * 16u;
+                kc[q] = c * CE;
+            } else {
+                const int k = o / RB, c = ((o % RB) >> 4) ^ swz_out(k);
+                off[q] = (uint32_t)k * (uint32_t)ld + (uint32_t)c * 16u;
+                kc[q] = k;
+            }
+        }
+    }
+
+    // Request slab `s` into LDS `lds`.  Chunks past the contraction or the
+    // outer range read zeros; past the last slab all of them do, without
+    // touching memory, so that the number of loads in flight is constant.
+    template <bool TRACKED>
+    __device__ __forceinline__ void issue(char *lds, int s, int wave) const {
+        const int k0 = s * BK, left = klen - k0;  // uniform
+        const char *p;
+        int64_t bytes;
+        if constexpr (KC) {
+            p = base + (int64_t)k0 * ES;
+            bytes = (int64_t)(outer - 1) * ld + (int64_t)left * ES;
+        } else {
+            p = base + (int64_t)k0 * ld;
+            bytes = (int64_t)((left < BK ? left : BK) - 1) * ld + (int64_t)outer * ES;
+        }
+        if (left <= 0) bytes = 0;
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)bytes, kRawBuffer);
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+            const uint32_t v = KC && kc[q] >= left ? kOutside : off[q];
+            char *dst = lds + load_id(q, wave) * 1024;
+            if constexpr (TRACKED) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t *)dst, 16, v, 0, 0, 0);
+            else lds_load_untracked(r, dst, v);
+        }
+    }
+
+    // The same slab through registers, for rows that are not 16-byte aligned
+    // or not a whole number of 16-byte chunks.
+    __device__ __forceinline__ void fetch(uint4 (&v)[PW], int s, int wave, int lane) const {
+        const int k0 = s * BK, left = klen - k0;
+        const char *p = base + (KC ? (int64_t)k0 * ES : (int64_t)k0 * ld);
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+            const int o = load_id(q, wave) * 1024 + lane * 16;
+            int n;
+            if constexpr (KC) n = (o >> 7) < outer ? left - kc[q] : 0;
+            else n = kc[q] < left ? outer - (((o % RB) >> 4) ^ swz_out(o / RB)) * CE : 0;
+            v[q] = load_partial<T>(p + off[q], n);
+        }
+    }
+    __device__ __forceinline__ static void put(char *lds, const uint4 (&v)[PW], int wave, int lane) {
+#pragma unroll
+        for (int q = 0; q < PW; ++q)
+            *reinterpret_cast<uint4 *>(lds + load_id(q, wave) * 1024 + lane * 16) = v[q];
+    }
+
+    // Fragment of step kk (of two per slab), block of 16 outer indices from o0.
+    __device__ __forceinline__ static uint4 frag(const char *lds, int kk, int o0, int lane) {
+        const int g = lane >> 4;
+        if constexpr (KC) {
+            // o0 is a multiple of 16, which the swizzle does not see
+            return *reinterpret_cast<const uint4 *>(lds + (o0 + (lane & 15)) * 128 +
+                                                    (((kk * 4 + g) ^ swz_kc(lane & 15)) << 4));
+        } else if constexpr (BF) {
+            const int k = kk * 32 + 8 * g + ((lane & 15) >> 2), n = o0 + 4 * (lane & 3);
+            // the swizzle sees bits 0, 1 and 3 of k: the same for k + 4, and for any kk
+            const char *p = lds + k * RB + (((n >> 3) ^ swz_out(8 * g + ((lane & 15) >> 2))) << 4) + ((n >> 2) & 1) * 8;
+            const v4i16_t both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)p),
+                                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)(p + 4 * RB))};
+            return *reinterpret_cast<const uint4 *>(both);
+        } else {
+            const int n = o0 + (lane & 15);
+            uint32_t e[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int k = kk * 16 + 4 * g + t;
+                e[t] = *reinterpret_cast<const uint32_t *>(lds + k * RB + (((n >> 2) ^ swz_out(4 * g)) << 4) + (n & 3) * 4);
+            }
+            return make_uint4(e[0], e[1], e[2], e[3]);
+        }
+    }
+};
+
+// Tile BM x BN, wave grid WGM x WGN, S LDS stages.  DIRECT: loads straight to
+// LDS (16-byte aligned operands); otherwise through registers, two stages.
+template <class T_, int BM_, int BN_, int WGM_, int WGN_, int S_, bool AKC_, bool BKC_, bool DIRECT_>
+struct Product {
+    using T = T_;
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, S = S_;
+    static constexpr bool AKC = AKC_, BKC = BKC_, DIRECT = DIRECT_;
+    static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
+    static constexpr bool BF = std::is_same<T, __bf16>::value;
+    using OpA = Operand<T, BM, AKC, NW>;
+    using OpB = Operand<T, BN, BKC, NW>;
+    static constexpr int BK = OpA::BK;
+    static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
+    static constexpr int PER = OpA::PW + OpB::PW;          // direct loads per wave and slab
+    static constexpr int RD = FM * OpA::READS + FN * OpB::READS;
+    static constexpr int MF = FM * FN * (BF ? 1 : 4);
+    static constexpr int EPI_PITCH = WN + 4;               // floats of a staged output row
+    static_assert(NW * 16 * EPI_PITCH * 4 <= STAGE, "epilogue staging");
+    static_assert(S >= 2 && S <= 4 && (DIRECT || S == 2), "stages");
+    static_assert(WN == 32 || WN == 64, "epilogue layout");
+
+    __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4]) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / WGN, wn = wave % WGN;
+
+        // ---- which tile ----
+        int ntm = g.ntm, b = blockIdx.x, expert = 0, row0, row_end = g.M, k_first = 0, klen = g.K;
+        GroupScan scan{};
+        if (g.mode == kGroupRows) ntm = count_tiles(g.off, g.groups, g.M, BM, scan);
+        const int tiles = ntm * g.ntn;
+        int split = 0;
+        if (g.mode == kGroupSum) {
+            expert = b / tiles;   // experts one after the other, each spread over all XCDs
+            b = xcd_remap(b - expert * tiles, tiles);
+        } else {
+            if (b >= tiles * g.nsplit) return;  // the grid is sized for the most tiles there can be
+            b = xcd_remap(b, tiles * g.nsplit);
+            split = b / tiles;
+            b -= split * tiles;
+        }
+        // Bands of 8 row tiles, row tiles fastest: the ~32 tiles an XCD works
+        // on at a time form a near-square block, which reads least into its L2.
+        constexpr int BAND = 8;
+        const int band = b / (BAND * g.ntn), inband = b - band * BAND * g.ntn;
+        const int left_rows = ntm - band * BAND, high = left_rows < BAND ? left_rows : BAND;
+        int nt = inband / high, mt = band * BAND + inband % high;
+        mt = __builtin_amdgcn_readfirstlane(mt);
+        nt = __builtin_amdgcn_readfirstlane(nt);
+        row0 = mt * BM;
+        const int col0 = nt * BN;
+        const char *A = g.A, *B = g.B, *bias = g.bias;
+        char *C = g.C;
+        bool zero = false;
+        if (g.mode == kGroupRows) {
+            const RowTile t = find_tile(g.off, g.groups, g.M, BM, mt, scan);
+            expert = t.expert;
+            row0 = t.row0;
+            row_end = t.end;
+            zero = expert == g.groups;  // rows without an expert
+            if (zero) {
+                klen = 0;
+            } else {
+                B += (int64_t)expert * g.sb * sizeof(T);
+                if (bias) bias += (int64_t)expert * g.N * sizeof(T);
+            }
+        } else if (g.mode == kGroupSum) {
+            const RowTile t = expert_rows(g.off, g.groups, g.K, expert);
+            k_first = t.row0;
+            klen = t.end - t.row0;
+            C += (int64_t)expert * g.sc * sizeof(T);
+        }
+        if (g.nsplit > 1) {  // whole slabs per split
+            const int slabs = (klen + BK - 1) / BK, per = (slabs + g.nsplit - 1) / g.nsplit;
+            const int from = split * per * BK;
+            k_first += from;
+            klen = klen - from < per * BK ? klen - from : per * BK;
+            if (klen < 0) klen = 0;
+        }
+        klen = __builtin_amdgcn_readfirstlane(klen);
+        k_first = __builtin_amdgcn_readfirstlane(k_first);
+        row0 = __builtin_amdgcn_readfirstlane(row0);
+        row_end = __builtin_amdgcn_readfirstlane(row_end);
+
+        f32x4_t acc[FM][FN];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+        const int nk = (klen + BK - 1) / BK;
+        if (nk > 0) {
+            OpA a;
+            OpB w;
+            a.init(A + ((AKC ? (int64_t)row0 * g.lda + k_first : (int64_t)k_first * g.lda + row0)) * (int64_t)sizeof(T),
+                   g.lda, row_end - row0, klen, wave, lane);
+            w.init(B + ((BKC ? (int64_t)col0 * g.ldb + k_first : (int64_t)k_first * g.ldb + col0)) * (int64_t)sizeof(T),
+                   g.ldb, g.N - col0, klen, wave, lane);
+            struct Frags {
+                uint4 a[FM], b[FN];
+            };
+            auto load = [&](const char *s, int kk, Frags &f) {
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn) f.b[fn] = OpB::frag(s + OpA::BYTES, kk, wn * WN + fn * 16, lane);
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm) f.a[fm] = OpA::frag(s, kk, wm * WM + fm * 16, lane);
+            };
+            auto mma = [&](const Frags &f) {
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+                    for (int fn = 0; fn < FN; ++fn) {
+                        if constexpr (BF) {
+                            acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, f.b[fn]), __builtin_bit_cast(bf16x8_t, f.a[fm]),
+                                acc[fm][fn], 0, 0, 0);
+                        } else {
+                            const f32x4_t x = __builtin_bit_cast(f32x4_t, f.b[fn]);
+                            const f32x4_t y = __builtin_bit_cast(f32x4_t, f.a[fm]);
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[t], y[t], acc[fm][fn], 0, 0, 0);
+                        }
+                    }
+            };
+            if constexpr (DIRECT) {
+                // Slabs s+1 .. s+S-1 are in flight while slab s is multiplied.
+                // The fragments of a step are read between the MFMAs of the
+                // step before it, across slab boundaries: the barrier sits
+                // before a slab's last step, when every wave holds all it
+                // needs of that slab, so its stage can be refilled.
+                constexpr bool TRACKED = S == 2;
+                auto issue = [&](char *s, int slab) {
+                    a.template issue<TRACKED>(s, slab, wave);
+                    w.template issue<TRACKED>(s + OpA::BYTES, slab, wave);
+                };
+                Frags f0, f1;
+                auto step = [&](auto U, int slab) {
+                    constexpr int u = decltype(U)::value;
+                    load(st[u], 1, f1);
+                    mma(f0);
+                    interleave<0, RD, MF, 0>();
+                    wait_vm<(S - 2) * PER>();
+                    __syncthreads();
+                    issue(st[u], slab + S);
+                    load(st[(u + 1) % S], 0, f0);
+                    mma(f1);
+                    interleave<0, RD, MF, TRACKED ? PER : 0>();
+                };
+#pragma unroll
+                for (int u = 0; u < S; ++u) issue(st[u], u);
+                wait_vm<(S - 1) * PER>();
+                __syncthreads();
+                load(st[0], 0, f0);
+                int slab = 0;
+                for (; slab + S <= nk; slab += S) {
+                    step(ic<0>{}, slab);
+                    step(ic<1>{}, slab + 1);
+                    if constexpr (S > 2) step(ic<2 % S>{}, slab + 2);
+                    if constexpr (S > 3) step(ic<3 % S>{}, slab + 3);
+                }
+                if (slab < nk) step(ic<0>{}, slab++);
+                if constexpr (S > 2)
+                    if (slab < nk) step(ic<1>{}, slab++);
+                if constexpr (S > 3)
+                    if (slab < nk) step(ic<2>{}, slab++);
+                wait_vm<0>();  // the trailing requests land before the LDS is reused
+            } else {
+                uint4 ra[OpA::PW], rb[OpB::PW];
+                a.fetch(ra, 0, wave, lane);
+                w.fetch(rb, 0, wave, lane);
+                auto step = [&](char *s, int slab) {
+                    OpA::put(s, ra, wave, lane);
+                    OpB::put(s + OpA::BYTES, rb, wave, lane);
+                    __syncthreads();  // also: every wave is done with the other stage's previous slab
+                    if (slab + 1 < nk) {
+                        a.fetch(ra, slab + 1, wave, lane);
+                        w.fetch(rb, slab + 1, wave, lane);
+                    }
+                    Frags f0;
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        load(s, kk, f0);
+                        mma(f0);
+                    }
+                };
+                int slab = 0;
+                for (; slab + 2 <= nk; slab += 2) {
+                    step(st[0], slab);
+                    step(st[1], slab + 1);
+                }
+                if (slab < nk) step(st[0], slab);
+            }
+            __syncthreads();  // every wave is done with the stages
+        }
+
+        // ---- epilogue: 16 rows at a time through this wave's part of LDS, so
+        // that memory is accessed in runs of whole rows of the wave's tile ----
+        float *sh = reinterpret_cast<float *>(st[0]) + wave * 16 * EPI_PITCH;
+        const int wrow = row0 + wm * WM, wcol = col0 + wn * WN;
+        float *part = g.nsplit > 1 ? g.ws + (int64_t)split * g.M * g.ldws : nullptr;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+                *reinterpret_cast<f32x4_t *>(sh + (lane & 15) * EPI_PITCH + fn * 16 + 4 * (lane >> 4)) = acc[fm][fn];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (part) {
+                constexpr int UPR = WN / 4;
+#pragma unroll
+                for (int i = 0; i < 16 * UPR / 64; ++i) {
+                    const int u = i * 64 + lane, r = u / UPR, c = (u % UPR) * 4;
+                    if (wrow + fm * 16 + r < row_end && wcol + c < g.ldws)  // ldws is a multiple of 4
+                        *reinterpret_cast<f32x4_t *>(part + (int64_t)(wrow + fm * 16 + r) * g.ldws + wcol + c) =
+                            *reinterpret_cast<const f32x4_t *>(sh + r * EPI_PITCH + c);
+                }
+            } else if (g.vec) {
+                constexpr int CE = kUnit<T>, UPR = WN / CE;
+#pragma unroll
+                for (int i = 0; i < 16 * UPR / 64; ++i) {
+                    const int u = i * 64 + lane, r = u / UPR, c = (u % UPR) * CE;
+                    alignas(16) float v[CE];
+#pragma unroll
+                    for (int e = 0; e < CE; e += 4)
+                        *reinterpret_cast<f32x4_t *>(v + e) =
+                            *reinterpret_cast<const f32x4_t *>(sh + r * EPI_PITCH + c + e);
+                    if (wrow + fm * 16 + r < row_end && wcol + c < g.N)
+                        finish<T, CE>(g, C, bias, wrow + fm * 16 + r, wcol + c, v, zero);
+                }
+            } else {
+                for (int i = 0; i < 16 * WN / 64; ++i) {
+                    const int u = i * 64 + lane, r = u / WN, c = u % WN;
+                    float v[1] = {sh[r * EPI_PITCH + c]};
+                    if (wrow + fm * 16 + r < row_end && wcol + c < g.N)
+                        finish<T, 1>(g, C, bias, wrow + fm * 16 + r, wcol + c, v, zero);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+    }
+};
+
+template <class P>
+__global__ __launch_bounds__(P::NT, 2) void product_kernel(GemmArgs g) {
+    // one array per stage: reads of one and direct loads into another do not alias
+    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s2[P::S > 2 ? P::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) char s3[P::S > 3 ? P::STAGE : 16];
+    char *const st[4] = {s0, s1, s2, s3};
+    P::run(g, st);
+}
+
+}  // namespace cpo

@@ -1,0 +1,50 @@
+// cp_ops_host.h -- launchers the host side of the operators calls.  Internal.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "cp_ops_device.h"
+
+namespace cpo {
+
+// Which index of the operands is contiguous (see cp_ops_gemm.h).
+enum Layout : int { kNN = 0, kNT = 1, kTN = 2 };  // A and B: KC/outer, KC/KC, outer/outer
+
+// Tile configurations of the products.
+enum Config : int { kTile256 = 0, kTile128 = 1, kTile16 = 2, kConfigs = 3 };
+struct ConfigShape {
+    int bm, bn;
+};
+constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 128}, {16, 128}};
+
+hipError_t launch_product_bf16(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
+hipError_t launch_product_f32(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
+
+// sums the partials of a split product and runs its epilogue
+hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s);
+
+// dZ = dY act'(pre) and column sums of it per expert (dense: groups = 1, off null)
+struct GradArgs {
+    const char *dy, *pre;
+    char *dz, *db;
+    float *ws;             // [row tiles][N] partial column sums
+    int64_t ldd, ldp, ldz;
+    const int32_t *off;
+    int32_t groups, M, N, act, tiles, vec;
+};
+constexpr int kGradRows = 128;  // rows of a partial column sum
+hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s);
+
+struct NormArgs {
+    const char *x, *dy, *w, *b;
+    char *y, *dw, *db;     // y: output, or dX in the backward pass
+    float *mean, *rstd;
+    float *ws;             // backward: [2][blocks][N] partial sums
+    int64_t ldx, ldd, ldy;
+    int32_t M, N, blocks, vec;
+    float eps;
+};
+hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s);
+int norm_backward_blocks(int dtype, int64_t M, int64_t N);
+hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s);
+
+}  // namespace cpo

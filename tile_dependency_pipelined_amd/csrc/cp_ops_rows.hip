@@ -1,0 +1,509 @@
+// cp_ops_rows.hip -- the operators' row and column passes for gfx950: joining
+// split products, activation gradients with bias sums, layer normalisation.
+// All are bound by memory traffic: one pass over the data, 16 bytes per lane
+// where the rows allow it, sums in fp32 in a fixed order.
+#include "cp_ops_host.h"
+
+namespace cpo {
+
+namespace {
+
+// ------------------------------------------------------------------- joining
+
+// Y = epilogue(sum over splits of partial); one block per row and 256 units.
+template <class T, int CNT>
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_row) {
+    const int row = blockIdx.x / blocks_per_row;
+    const int col = ((blockIdx.x % blocks_per_row) * 256 + threadIdx.x) * CNT;
+    const char *bias = g.bias;
+    bool zero = false;
+    if (g.mode == kGroupRows && bias) {  // the row's expert
+        int carry = 0, e = g.groups;
+        for (int base = 0; base <= g.groups; base += 64) {
+            const GroupScan s = scan_groups(g.off, g.groups, g.M, 1, base, carry, 0);
+            const uint64_t hit = __ballot(s.end > row);
+            if (hit) {
+                e = base + __builtin_ctzll(hit);
+                break;
+            }
+            carry = __builtin_amdgcn_readlane(s.end, 63);
+        }
+        zero = e >= g.groups;
+        if (!zero) bias += (int64_t)e * g.N * sizeof(T);
+    }
+    if (col >= g.N) return;
+    float v[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) v[i] = 0.0f;
+    const float *p = g.ws + (int64_t)row * g.ldws + col;
+    const int64_t step = (int64_t)g.M * g.ldws;
+#pragma unroll 4
+    for (int s = 0; s < g.nsplit; ++s) {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) v[i] += p[s * step + i];
+    }
+    finish<T, CNT>(g, g.C, bias, row, col, v, zero);
+}
+
+// --------------------------------------------- activation gradient, bias sums
+
+// 32 column units x 8 rows per pass; each block one row tile (kGradRows rows of
+// one expert) and 32 units of columns.
+template <class T, int CNT>
+__global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
+    __shared__ float part[8][32 * CNT];
+    const int ct = blockIdx.x % col_blocks, rt = blockIdx.x / col_blocks;
+    int row0 = rt * kGradRows, end = a.M;
+    if (a.off) {
+        GroupScan s;
+        if (rt >= count_tiles(a.off, a.groups, a.M, kGradRows, s)) return;
+        const RowTile t = find_tile(a.off, a.groups, a.M, kGradRows, rt, s);
+        if (t.expert == a.groups) return;  // their dZ is never read
+        row0 = t.row0;
+        end = t.end;
+    }
+    if (end > row0 + kGradRows) end = row0 + kGradRows;
+    const int u = threadIdx.x & 31, r = threadIdx.x >> 5, col = (ct * 32 + u) * CNT;
+    float sum[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) sum[i] = 0.0f;
+    if (col < a.N) {
+#pragma unroll 4
+        for (int row = row0 + r; row < end; row += 8) {
+            float d[CNT];
+            const char *p = a.dy + ((int64_t)row * a.ldd + col) * sizeof(T);
+            if constexpr (CNT > 1) load_unit<T>(p, d);
+            else d[0] = to_f32(*reinterpret_cast<const T *>(p));
+            if (a.dz) {
+                float z[CNT];
+                const char *q = a.pre + ((int64_t)row * a.ldp + col) * sizeof(T);
+                if constexpr (CNT > 1) load_unit<T>(q, z);
+                else z[0] = to_f32(*reinterpret_cast<const T *>(q));
+#pragma unroll
+                for (int i = 0; i < CNT; ++i) d[i] *= act_grad(z[i], a.act);
+                char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
+                if constexpr (CNT > 1) store_unit<T>(o, d);
+                else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
+            }
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) sum[i] += d[i];
+        }
+    }
+    if (!a.db) return;
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) part[r][u * CNT + i] = sum[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 32 * CNT; c += 256) {
+        const int gc = ct * 32 * CNT + c;
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += part[i][c];
+        if (gc < a.N) a.ws[(int64_t)rt * a.N + gc] = v;
+    }
+}
+
+// db[e] = sum of its row tiles' partials, in order
+template <class T>
+__global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a, int col_blocks) {
+    const int e = blockIdx.x / col_blocks, col = (blockIdx.x % col_blocks) * 256 + threadIdx.x;
+    int from = 0, to = (a.M + kGradRows - 1) / kGradRows;
+    if (a.off) {
+        int carry_end = 0, carry_tiles = 0;
+        for (int base = 0;; base += 64) {
+            const GroupScan s = scan_groups(a.off, a.groups, a.M, kGradRows, base, carry_end, carry_tiles);
+            if (e < base + 64) {
+                const int l = e - base;
+                from = l ? __builtin_amdgcn_readlane(s.tiles_end, l - 1) : carry_tiles;
+                to = __builtin_amdgcn_readlane(s.tiles_end, l);
+                break;
+            }
+            carry_end = __builtin_amdgcn_readlane(s.end, 63);
+            carry_tiles = __builtin_amdgcn_readlane(s.tiles_end, 63);
+        }
+    }
+    if (col >= a.N) return;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int t = from; t < to; ++t) v += a.ws[(int64_t)t * a.N + col];
+    reinterpret_cast<T *>(a.db)[(int64_t)e * a.N + col] = from_f32<T>(v);
+}
+
+// ------------------------------------------------------- layer normalisation
+
+// Sum over the THREADS threads of a row: a wave, or a block through LDS
+// (`sh`: one float per wave; two barriers, so it can be called again at once).
+template <int THREADS>
+__device__ __forceinline__ float row_sum(float v, float *sh) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    if constexpr (THREADS > 64) {
+        constexpr int W = THREADS / 64;
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v += sh[i];
+        __syncthreads();
+    }
+    return v;
+}
+
+// Column of element i of unit q of thread t: 16-byte units in turn, or single
+// elements in turn where rows are not aligned (both read whole lines).
+template <class T, int THREADS, bool VEC>
+__device__ __forceinline__ int norm_col(int q, int i, int t) {
+    return VEC ? (q * THREADS + t) * kUnit<T> + i : (q * kUnit<T> + i) * THREADS + t;
+}
+
+template <class T, int THREADS, int VPT, bool VEC>
+__device__ __forceinline__ void norm_load(const char *row, int N, int t, float (&v)[VPT][kUnit<T>]) {
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        if constexpr (VEC) {
+            const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+            if (c < N) load_unit<T>(row + (int64_t)c * sizeof(T), v[q]);
+            else
+#pragma unroll
+                for (int i = 0; i < kUnit<T>; ++i) v[q][i] = 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnit<T>; ++i) {
+                const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                v[q][i] = c < N ? to_f32(reinterpret_cast<const T *>(row)[c]) : 0.0f;
+            }
+        }
+    }
+}
+
+template <class T, int THREADS, int VPT, bool VEC>
+__device__ __forceinline__ void norm_store(char *row, int N, int t, const float (&v)[VPT][kUnit<T>]) {
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        if constexpr (VEC) {
+            const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+            if (c < N) store_unit<T>(row + (int64_t)c * sizeof(T), v[q]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnit<T>; ++i) {
+                const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                if (c < N) reinterpret_cast<T *>(row)[c] = from_f32<T>(v[q][i]);
+            }
+        }
+    }
+}
+
+// One row per THREADS threads, held in registers: the deviation is summed from
+// the values themselves (no difference of large squares).
+template <class T, int THREADS, int VPT, bool VEC>
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(NormArgs a) {
+    constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, CE = kUnit<T>;
+    __shared__ float sh[16];
+    const int t = threadIdx.x % THREADS;
+    const int row = blockIdx.x * (BLOCK / THREADS) + threadIdx.x / THREADS;
+    if (row >= a.M) return;  // whole waves; with one row per block never taken
+    float v[VPT][CE];
+    norm_load<T, THREADS, VPT, VEC>(a.x + (int64_t)row * a.ldx * sizeof(T), a.N, t, v);
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+#pragma unroll
+        for (int i = 0; i < CE; ++i) s += v[q][i];
+    const float mean = row_sum<THREADS>(s, sh) / (float)a.N;
+    float ss = 0.0f;
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+#pragma unroll
+        for (int i = 0; i < CE; ++i) {
+            v[q][i] = norm_col<T, THREADS, VEC>(q, i, t) < a.N ? v[q][i] - mean : 0.0f;
+            ss += v[q][i] * v[q][i];
+        }
+    const float rstd = 1.0f / sqrtf(row_sum<THREADS>(ss, sh) / (float)a.N + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+#pragma unroll
+        for (int i = 0; i < CE; ++i) v[q][i] *= rstd;
+    float p[VPT][CE];
+    if (a.w) {
+        norm_load<T, THREADS, VPT, VEC>(a.w, a.N, t, p);
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int i = 0; i < CE; ++i) v[q][i] *= p[q][i];
+    }
+    if (a.b) {
+        norm_load<T, THREADS, VPT, VEC>(a.b, a.N, t, p);
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int i = 0; i < CE; ++i) v[q][i] += p[q][i];
+    }
+    norm_store<T, THREADS, VPT, VEC>(a.y + (int64_t)row * a.ldy * sizeof(T), a.N, t, v);
+}
+
+// Rows too long for registers: three passes over the row (the second and third
+// mostly from the cache), element by element.
+template <class T>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+    __shared__ float sh[16];
+    const int row = blockIdx.x, t = threadIdx.x;
+    const T *x = reinterpret_cast<const T *>(a.x) + (int64_t)row * a.ldx;
+    const T *w = reinterpret_cast<const T *>(a.w), *b = reinterpret_cast<const T *>(a.b);
+    T *y = reinterpret_cast<T *>(a.y) + (int64_t)row * a.ldy;
+    float s = 0.0f;
+    for (int c = t; c < a.N; c += 1024) s += to_f32(x[c]);
+    const float mean = row_sum<1024>(s, sh) / (float)a.N;
+    float ss = 0.0f;
+    for (int c = t; c < a.N; c += 1024) {
+        const float d = to_f32(x[c]) - mean;
+        ss += d * d;
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<1024>(ss, sh) / (float)a.N + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int c = t; c < a.N; c += 1024) {
+        float v = (to_f32(x[c]) - mean) * rstd;
+        if (w) v *= to_f32(w[c]);
+        if (b) v += to_f32(b[c]);
+        y[c] = from_f32<T>(v);
+    }
+}
+
+// Backward: block b takes rows b, b + blocks, ...; a thread keeps its columns'
+// weight and bias sums in registers over all of them and stores one partial
+// per block, which norm_join_kernel adds up in block order.
+template <class T, int THREADS, int VPT, bool VEC>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
+    constexpr int CE = kUnit<T>;
+    __shared__ float sh[16];
+    const int t = threadIdx.x;
+    float dw[VPT][CE], db[VPT][CE];
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+#pragma unroll
+        for (int i = 0; i < CE; ++i) dw[q][i] = db[q][i] = 0.0f;
+    for (int row = blockIdx.x; row < a.M; row += a.blocks) {
+        float x[VPT][CE], dy[VPT][CE];
+        norm_load<T, THREADS, VPT, VEC>(a.x + (int64_t)row * a.ldx * sizeof(T), a.N, t, x);
+        norm_load<T, THREADS, VPT, VEC>(a.dy + (int64_t)row * a.ldd * sizeof(T), a.N, t, dy);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int i = 0; i < CE; ++i) {
+                // past the row's end dy is zero, so x's value there does not count
+                x[q][i] = norm_col<T, THREADS, VEC>(q, i, t) < a.N ? (x[q][i] - mean) * rstd : 0.0f;
+                dw[q][i] += dy[q][i] * x[q][i];
+                db[q][i] += dy[q][i];
+            }
+        if (!a.y) continue;
+        if (a.w) {
+            float w[VPT][CE];
+            norm_load<T, THREADS, VPT, VEC>(a.w, a.N, t, w);
+#pragma unroll
+            for (int q = 0; q < VPT; ++q)
+#pragma unroll
+                for (int i = 0; i < CE; ++i) dy[q][i] *= w[q][i];
+        }
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int i = 0; i < CE; ++i) {
+                s0 += dy[q][i];
+                s1 += dy[q][i] * x[q][i];
+            }
+        s0 = row_sum<THREADS>(s0, sh) / (float)a.N;
+        s1 = row_sum<THREADS>(s1, sh) / (float)a.N;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int i = 0; i < CE; ++i) dy[q][i] = rstd * (dy[q][i] - s0 - x[q][i] * s1);
+        norm_store<T, THREADS, VPT, VEC>(a.y + (int64_t)row * a.ldy * sizeof(T), a.N, t, dy);
+    }
+    float *pw = a.ws + (int64_t)blockIdx.x * a.N, *pb = pw + (int64_t)a.blocks * a.N;
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+#pragma unroll
+        for (int i = 0; i < CE; ++i) {
+            const int c = norm_col<T, THREADS, VEC>(q, i, t);
+            if (c < a.N) {
+                if (a.dw) pw[c] = dw[q][i];
+                if (a.db) pb[c] = db[q][i];
+            }
+        }
+}
+
+// Rows too long for registers: dX by rows ...
+template <class T>
+__global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormArgs a) {
+    __shared__ float sh[16];
+    const int row = blockIdx.x, t = threadIdx.x;
+    const T *x = reinterpret_cast<const T *>(a.x) + (int64_t)row * a.ldx;
+    const T *dy = reinterpret_cast<const T *>(a.dy) + (int64_t)row * a.ldd;
+    const T *w = reinterpret_cast<const T *>(a.w);
+    T *dx = reinterpret_cast<T *>(a.y) + (int64_t)row * a.ldy;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int c = t; c < a.N; c += 1024) {
+        const float g = to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.0f);
+        s0 += g;
+        s1 += g * ((to_f32(x[c]) - mean) * rstd);
+    }
+    s0 = row_sum<1024>(s0, sh) / (float)a.N;
+    s1 = row_sum<1024>(s1, sh) / (float)a.N;
+    for (int c = t; c < a.N; c += 1024) {
+        const float g = to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.0f);
+        dx[c] = from_f32<T>(rstd * (g - s0 - (to_f32(x[c]) - mean) * rstd * s1));
+    }
+}
+
+// ... and the weight and bias sums by columns, before dX may overwrite dY or X.
+template <class T>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs a, int col_blocks) {
+    const int c = (blockIdx.x % col_blocks) * 256 + threadIdx.x, blk = blockIdx.x / col_blocks;
+    if (c >= a.N) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int row = blk; row < a.M; row += a.blocks) {
+        const float d = to_f32(reinterpret_cast<const T *>(a.dy)[(int64_t)row * a.ldd + c]);
+        const float x = to_f32(reinterpret_cast<const T *>(a.x)[(int64_t)row * a.ldx + c]);
+        dw += d * ((x - a.mean[row]) * a.rstd[row]);
+        db += d;
+    }
+    a.ws[(int64_t)blk * a.N + c] = dw;
+    a.ws[(int64_t)(a.blocks + blk) * a.N + c] = db;
+}
+
+// dw and db from the blocks' partials: 64 columns x 4 ranges of blocks
+template <class T>
+__global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a, int col_blocks) {
+    __shared__ float part[4][64];
+    const int which = blockIdx.x / col_blocks;
+    char *dst = which ? a.db : a.dw;
+    if (!dst) return;  // whole blocks
+    const int t = threadIdx.x & 63, s = threadIdx.x >> 6, c = (blockIdx.x % col_blocks) * 64 + t;
+    const int per = (a.blocks + 3) / 4, to = (s + 1) * per < a.blocks ? (s + 1) * per : a.blocks;
+    float v = 0.0f;
+    if (c < a.N)
+#pragma unroll 8
+        for (int b = s * per; b < to; ++b) v += a.ws[((int64_t)which * a.blocks + b) * a.N + c];
+    part[s][t] = v;
+    __syncthreads();
+    if (s == 0 && c < a.N)
+        reinterpret_cast<T *>(dst)[c] = from_f32<T>(((part[0][t] + part[1][t]) + part[2][t]) + part[3][t]);
+}
+
+// ------------------------------------------------------------------ launchers
+
+template <class T>
+hipError_t join(const GemmArgs &g, hipStream_t s) {
+    const int unit = g.vec ? kUnit<T> : 1;
+    const int per_row = (g.N + 256 * unit - 1) / (256 * unit);
+    const dim3 grid((unsigned)(g.M * per_row));
+    if (g.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, kUnit<T>>), grid, dim3(256), 0, s, g, per_row);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, 1>), grid, dim3(256), 0, s, g, per_row);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t grad(const GradArgs &a, hipStream_t s) {
+    const int unit = a.vec ? kUnit<T> : 1;
+    const int cols = (a.N + 32 * unit - 1) / (32 * unit);
+    if (a.tiles > 0) {
+        const dim3 grid((unsigned)(a.tiles * cols));
+        if (a.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, kUnit<T>>), grid, dim3(256), 0, s, a, cols);
+        else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, 1>), grid, dim3(256), 0, s, a, cols);
+    }
+    if (a.db) {
+        const int cb = (a.N + 255) / 256;
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), dim3((unsigned)(a.groups * cb)), dim3(256), 0, s, a, cb);
+    }
+    return hipGetLastError();
+}
+
+template <class T, bool VEC>
+hipError_t norm(const NormArgs &a, hipStream_t s) {
+    constexpr int CE = kUnit<T>;
+#define CPO_NORM(THREADS, VPT)                                                                                        \
+    if (a.N <= THREADS * VPT * CE) {                                                                                  \
+        constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, ROWS = BLOCK / THREADS;                                  \
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, VEC>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)), \
+                           dim3(BLOCK), 0, s, a);                                                                     \
+        return hipGetLastError();                                                                                     \
+    }
+    CPO_NORM(64, 1)
+    CPO_NORM(64, 2)
+    CPO_NORM(256, 1)
+    CPO_NORM(256, 2)
+    CPO_NORM(256, 4)
+    CPO_NORM(1024, 2)
+    CPO_NORM(1024, 4)
+#undef CPO_NORM
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_long_kernel<T>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class T, bool VEC>
+hipError_t norm_backward(const NormArgs &a, hipStream_t s) {
+    constexpr int CE = kUnit<T>;
+#define CPO_NORM(THREADS, VPT)                                                                                        \
+    if (a.N <= THREADS * VPT * CE) {                                                                                  \
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_kernel<T, THREADS, VPT, VEC>), dim3((unsigned)a.blocks),     \
+                           dim3(THREADS), 0, s, a);                                                                   \
+        return hipGetLastError();                                                                                     \
+    }
+    CPO_NORM(64, 1)
+    CPO_NORM(128, 1)
+    CPO_NORM(256, 1)
+    CPO_NORM(256, 2)
+    CPO_NORM(256, 4)
+    CPO_NORM(1024, 2)
+#undef CPO_NORM
+    const int cb = (a.N + 255) / 256;
+    if (a.dw || a.db)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_columns_kernel<T>), dim3((unsigned)(a.blocks * cb)), dim3(256), 0, s, a, cb);
+    if (a.y)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_long_kernel<T>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t norm_backward_all(const NormArgs &a, hipStream_t s) {
+    if (a.M > 0) {
+        const hipError_t e = a.vec ? norm_backward<T, true>(a, s) : norm_backward<T, false>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dw || a.db) {
+        const int cb = (a.N + 63) / 64;
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_join_kernel<T>), dim3((unsigned)(2 * cb)), dim3(256), 0, s, a, cb);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s) {
+    return dtype == CP_BF16 ? join<__bf16>(g, s) : join<float>(g, s);
+}
+
+hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s) {
+    return dtype == CP_BF16 ? grad<__bf16>(a, s) : grad<float>(a, s);
+}
+
+hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s) {
+    if (dtype == CP_BF16) return a.vec ? norm<__bf16, true>(a, s) : norm<__bf16, false>(a, s);
+    return a.vec ? norm<float, true>(a, s) : norm<float, false>(a, s);
+}
+
+int norm_backward_blocks(int, int64_t M, int64_t) { return (int)(M < 512 ? M : 512); }
+
+hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s) {
+    return dtype == CP_BF16 ? norm_backward_all<__bf16>(a, s) : norm_backward_all<float>(a, s);
+}
+
+}  // namespace cpo
