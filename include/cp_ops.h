@@ -15,7 +15,8 @@
  *   - matrices are row-major with unit stride within a row and `ld` elements
  *     from one row to the next (ld >= the row's length; not read where there
  *     is at most one row).  No alignment beyond the element's own is needed;
- *     16-byte aligned rows run the faster kernels;
+ *     16-byte aligned rows are faster (others are copied first, see
+ *     cp_ops_workspace);
  *   - sums run in fp32 (products on the matrix cores), outputs are rounded
  *     once, to nearest even, and results do not depend on timing: the same
  *     call gives the same bits;
@@ -125,11 +126,13 @@ int cp_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, 
 
 /*
  * cp_ops_workspace -- bytes of scratch memory the operator `op` (CP_OP_*)
- * needs at these sizes, whatever its pointers and optional arguments; may be
- * 0.  K is ignored by CP_OP_LAYER_NORM_BACKWARD, E by the dense operators.
+ * needs at these sizes, whatever its optional arguments; may be 0.  K is
+ * ignored by CP_OP_LAYER_NORM_BACKWARD, E by the dense operators.  `aligned`:
+ * X, W and dY have 16-byte aligned pointers, row strides, expert strides and
+ * row lengths; without that (0) there is room for copies of them that do.
  * Negative status code on bad arguments.  Host only, no device needed.
  */
-int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E);
+int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E, int32_t aligned);
 
 /* cp_ops_last_error -- thread-local detail of the calling thread's most recent
  * failure in this header's functions ("" if its last call succeeded). */

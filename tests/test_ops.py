@@ -69,7 +69,7 @@ def test_linear_refusals(change, code):
 
 
 def test_workspace_refusals():
-    need = ops.workspace_bytes(ops.OP_LINEAR_BACKWARD, nat.CP_BF16, 64, 64, 64)
+    need = ops.workspace_bytes(ops.OP_LINEAR_BACKWARD, nat.CP_BF16, 64, 64, 64, aligned=True)
     assert need > 0
 
     def call(ws, n):

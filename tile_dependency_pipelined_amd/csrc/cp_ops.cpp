@@ -92,11 +92,6 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 // ------------------------------------------------------------ tile and split
 
-struct Choice {
-    Config cfg;
-    int nsplit;
-};
-
 // Products: what is to be computed, apart from where it lies.
 struct Shape {
     int dtype;
@@ -106,6 +101,11 @@ struct Shape {
     int groups;
 };
 
+struct Choice {
+    Config cfg;
+    int nsplit;
+};
+
 // Row tiles of `bm` rows the launch can have at most.
 int64_t max_row_tiles(const Shape &s, int bm) {
     if (s.mode != kGroupRows) return ceil_div(s.M, bm);
@@ -113,45 +113,73 @@ int64_t max_row_tiles(const Shape &s, int bm) {
     return (s.M + used * (bm - 1)) / bm;
 }
 
-Choice choose(const Shape &s, bool direct) {
-    const int bk = 128 / elem_size(s.dtype);
-    const int64_t slabs = ceil_div(s.mode == kGroupSum ? ceil_div(s.K, s.groups) : s.K, bk);
-    // rows an expert (or the whole product) has on average
-    const int64_t rows = s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M;
-    if (rows <= 16 && s.layout != kTN) {
+int64_t slabs_of(const Shape &s) {
+    return ceil_div(s.mode == kGroupSum ? ceil_div(s.K, s.groups) : s.K, 128 / elem_size(s.dtype));
+}
+
+// Few rows (per expert): 16-row tiles, whose time is that of reading B.  The
+// split fills the device twice over, keeping four slabs of 64 (fp32: 32) to a
+// split, so that the loads in flight are worth their latency.
+bool few_rows(const Shape &s) {
+    return s.layout != kTN && (s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M) <= 16;
+}
+
+// Time of a product in microseconds for each configuration that fits, from the
+// rounds of tiles the device takes and, per tile, a time per slab and one for
+// prologue and epilogue.  Measured on 2048 x 8192 x 8192, 2048 x 4096 x 4096
+// and 8192 x 4096 x 2048 (rows x columns x contraction), bf16: 256x256 tiles
+// 204, 91, 115 us; 128x256 238, 62, 134; 128x128 (two on a CU) 257, 62, 129.
+// A split writes and reads its partials and takes another launch.
+Choice choose(const Shape &s) {
+    if (few_rows(s)) {
         const int64_t tiles = max_row_tiles(s, 16) * ceil_div(s.N, 128);
         int64_t n = 2 * kComputeUnits / (tiles ? tiles : 1);
-        if (n > slabs / 4) n = slabs / 4;
+        if (n > slabs_of(s) / 4) n = slabs_of(s) / 4;
         if (n > 32) n = 32;
         return {kTile16, n < 1 ? 1 : (int)n};
     }
-    // Tiles an average launch has, and the time of the rounds they take in
-    // units of a 128 x 128 tile's share of a CU.
-    auto tiles_of = [&](int b) {
-        const int64_t tm = s.mode == kGroupRows ? s.M / b + (s.groups + 1) / 2 : ceil_div(s.M, b);
-        return tm * ceil_div(s.N, b) * (s.mode == kGroupSum ? s.groups : 1);
+    struct Rate {
+        Config cfg;
+        double slab, fixed;
     };
-    const int64_t t128 = tiles_of(128), t256 = tiles_of(256);
-    const double c128 = 2.5 * ceil_div(t128, 2 * kComputeUnits), c256 = 4.0 * ceil_div(t256, kComputeUnits);
-    if (s.dtype == CP_BF16 && direct && c256 <= c128) return {kTile256, 1};
-    int64_t n = 1;
-    if (s.mode == kDense && 2 * t128 <= kComputeUnits) {
-        n = kComputeUnits / t128;
-        if (n > slabs / 8) n = slabs / 8;
-        if (n > 16) n = 16;
+    static const Rate bf16[] = {{kTile256, 1.5, 9.0}, {kTile128x256, 0.90, 5.0}, {kTile128, 0.98, 4.0}};
+    static const Rate f32[] = {{kTile128, 3.6, 4.0}};
+    const Rate *rates = s.dtype == CP_BF16 ? bf16 : f32;
+    const int nrates = s.dtype == CP_BF16 ? 3 : 1;
+    const double slabs = (double)slabs_of(s);
+    Choice best{kTile128, 1};
+    double least = 1e300;
+    for (int i = 0; i < nrates; ++i) {
+        const ConfigShape t = kShapes[rates[i].cfg];
+        // row tiles of an average launch: each expert's last one is half empty
+        const double tm = s.mode == kGroupRows ? (double)s.M / t.bm + 0.5 * s.groups : (double)ceil_div(s.M, t.bm);
+        const double tiles = tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
+        for (int n = 1; n <= 16; n *= 2) {
+            if (n > 1 && (s.mode != kDense || slabs < 4 * n)) break;
+            double rounds, slab = rates[i].slab;
+            if (rates[i].cfg == kTile128) {
+                // two on a CU, taken as they come; alone on its CU a tile is faster
+                rounds = tiles * n / (2 * kComputeUnits);
+                if (rounds <= 0.5) {
+                    rounds = 1.0;
+                    slab *= 0.6;
+                } else if (rounds < 1.0) {
+                    rounds = 1.0;
+                } else {
+                    rounds += 0.25;
+                }
+            } else {
+                rounds = (double)(int64_t)(tiles * n / kComputeUnits + 0.999);
+            }
+            double t_us = rounds * (slab * (slabs / n) + rates[i].fixed);
+            if (n > 1) t_us += 4.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 4e6;
+            if (t_us < least) {
+                least = t_us;
+                best = {rates[i].cfg, n};
+            }
+        }
     }
-    return {kTile128, n < 1 ? 1 : (int)n};
-}
-
-int64_t split_bytes(const Shape &s) {
-    if (s.M == 0 || s.N == 0) return 0;
-    int64_t most = 0;
-    for (int direct = 0; direct < 2; ++direct) {
-        const Choice c = choose(s, direct);
-        const int64_t b = c.nsplit > 1 ? (int64_t)c.nsplit * s.M * up(s.N, 8) * 4 : 0;
-        if (b > most) most = b;
-    }
-    return most;
+    return best;
 }
 
 // ------------------------------------------------------------------ products
@@ -166,12 +194,59 @@ struct Product {
     int act = CP_ACT_NONE;
 };
 
-int run_product(const Product &p, void *ws, hipStream_t stream) {
+// Bytes of a packed copy of `count` matrices.
+int64_t packed_bytes(int dtype, int64_t rows, int64_t cols, int64_t count) {
+    return up(rows * up(cols, 8) * count * elem_size(dtype), 256);
+}
+
+// Scratch memory handed out front to back; with no base it only counts.
+struct Arena {
+    char *base;
+    int64_t used = 0;
+    char *take(int64_t bytes) {
+        char *p = base ? base + used : nullptr;
+        used += up(bytes, 256);
+        return p;
+    }
+};
+
+// Rows of whole 16-byte chunks, as the direct loads need them: the matrix
+// itself if it has them, otherwise a copy.  A copy moves the matrix twice; the
+// kernel that reads unaligned rows through registers instead took 208 us for
+// 2048 x 4096 x 4096 with odd rows, where the aligned one takes 62 and the copies 25.
+int packed(Mat &m, int64_t *stride, int count, int dtype, Arena &ws, hipStream_t stream) {
+    const int64_t es = elem_size(dtype);
+    if (m.rows == 0 || m.cols == 0) return CP_OK;
+    if (aligned16(m, dtype) && (!stride || *stride * es % 16 == 0)) return CP_OK;
+    PackArgs a{};
+    a.src = (const char *)m.p;
+    a.dst = ws.take(packed_bytes(dtype, m.rows, m.cols, count));
+    a.ld = m.ld;
+    a.ldd = up(m.cols, 8);
+    a.stride = stride ? *stride : 0;
+    a.stride_d = m.rows * a.ldd;
+    a.rows = (int)m.rows;
+    a.cols = (int)m.cols;
+    a.count = count;
+    m.p = a.dst;
+    m.ld = a.ldd;
+    if (stride) *stride = a.stride_d;
+    return launched(launch_pack(dtype, a, stream), "pack");
+}
+
+int64_t split_bytes(const Shape &s) {
+    if (s.M == 0 || s.N == 0) return 0;
+    const Choice c = choose(s);
+    return c.nsplit > 1 ? (int64_t)c.nsplit * s.M * up(s.N, 8) * 4 : 0;
+}
+
+// `split`: room for split_bytes().  The operands are aligned unless few_rows().
+int run_product(const Product &p, void *split, hipStream_t stream) {
     const Shape &s = p.s;
     if (s.M == 0 || s.N == 0) return CP_OK;
     const int es = elem_size(s.dtype);
-    bool direct = aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0;
-    const Choice c = choose(s, direct);
+    const Choice c = choose(s);
+    const bool direct = c.cfg != kTile16 || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0);
     GemmArgs g{};
     g.A = (const char *)p.A.p;
     g.B = (const char *)p.B.p;
@@ -179,7 +254,7 @@ int run_product(const Product &p, void *ws, hipStream_t stream) {
     g.bias = (const char *)p.bias;
     g.res = (const char *)p.R.p;
     g.pre = (char *)p.P.p;
-    g.ws = (float *)ws;
+    g.ws = (float *)split;
     g.lda = p.A.ld;
     g.ldb = p.B.ld;
     g.ldc = p.C.ld;
@@ -226,27 +301,38 @@ Shape dw_shape(int dtype, int64_t M, int64_t K, int64_t N, int groups, bool wt) 
 
 int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
-int64_t forward_ws(int dtype, int64_t M, int64_t K, int64_t N, int groups) {
-    return max64(split_bytes(forward_shape(dtype, M, K, N, groups, false)),
-                 split_bytes(forward_shape(dtype, M, K, N, groups, true)));
+// Scratch memory of a forward pass: partials of a split, and with unaligned
+// operands their copies.
+int64_t forward_ws(int dtype, int64_t M, int64_t K, int64_t N, int E, bool aligned) {
+    const Shape s = forward_shape(dtype, M, K, N, E, false);
+    int64_t n = up(max64(split_bytes(s), split_bytes(forward_shape(dtype, M, K, N, E, true))), 256);
+    if (!aligned && !few_rows(s))
+        n += packed_bytes(dtype, M, K, 1) +
+             max64(packed_bytes(dtype, K, N, E ? E : 1), packed_bytes(dtype, N, K, E ? E : 1));
+    return n;
 }
 
-struct BackwardWs {
-    int64_t dz, sums, split, total;  // offsets of the parts and the end
-};
-BackwardWs backward_ws(int dtype, int64_t M, int64_t K, int64_t N, int groups) {
-    BackwardWs w{};
-    const Shape rows{dtype, kNN, groups ? kGroupRows : kDense, M, N, K, groups};
-    w.dz = 0;
-    w.sums = up(M * up(N, 8) * elem_size(dtype), 256);
-    w.split = w.sums + up(max_row_tiles(rows, kGradRows) * N * 4, 256);
+// Of a backward pass: partial column sums, dZ (or a copy of dY), partials of a
+// split, copies of X and W.
+int64_t sums_bytes(int dtype, int64_t M, int64_t N, int E) {
+    const Shape rows{dtype, kNN, E ? kGroupRows : kDense, M, N, 0, E};
+    return max_row_tiles(rows, kGradRows) * N * 4;
+}
+int64_t backward_split_bytes(int dtype, int64_t M, int64_t K, int64_t N, int E) {
     int64_t most = 0;
     for (int wt = 0; wt < 2; ++wt) {
-        most = max64(most, split_bytes(dx_shape(dtype, M, K, N, groups, wt)));
-        most = max64(most, split_bytes(dw_shape(dtype, M, K, N, groups, wt)));
+        most = max64(most, split_bytes(dx_shape(dtype, M, K, N, E, wt)));
+        most = max64(most, split_bytes(dw_shape(dtype, M, K, N, E, wt)));
     }
-    w.total = w.split + most;
-    return w;
+    return most;
+}
+int64_t backward_ws(int dtype, int64_t M, int64_t K, int64_t N, int E, bool aligned) {
+    int64_t n = up(sums_bytes(dtype, M, N, E), 256) + packed_bytes(dtype, M, N, 1) +
+                up(backward_split_bytes(dtype, M, K, N, E), 256);
+    if (!aligned)
+        n += packed_bytes(dtype, M, K, 1) +
+             max64(packed_bytes(dtype, K, N, E ? E : 1), packed_bytes(dtype, N, K, E ? E : 1));
+    return n;
 }
 
 int check_ws(const void *ws, int64_t have, int64_t need) {
@@ -298,12 +384,21 @@ int forward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X, in
     }
     CP_TRY(check_vector(bias, dtype, "bias"));
     if (E) CP_TRY(check_groups(E, off, stride_w, p.B, "W"));
-    CP_TRY(check_ws(ws, ws_bytes, forward_ws(dtype, M, K, N, E)));
     p.sb = E > 1 ? stride_w : 0;
     p.off = off;
     p.bias = bias;
     p.act = act;
-    return run_product(p, ws, (hipStream_t)stream);
+    const bool aligned =
+        aligned16(p.A, dtype) && aligned16(p.B, dtype) && p.sb * elem_size(dtype) % 16 == 0;
+    CP_TRY(check_ws(ws, ws_bytes, forward_ws(dtype, M, K, N, E, aligned)));
+    if (M == 0 || N == 0) return CP_OK;
+    Arena mem{(char *)ws};
+    void *split = mem.take(split_bytes(p.s));
+    if (!few_rows(p.s)) {
+        CP_TRY(packed(p.A, nullptr, 1, dtype, mem, (hipStream_t)stream));
+        CP_TRY(packed(p.B, &p.sb, E ? E : 1, dtype, mem, (hipStream_t)stream));
+    }
+    return run_product(p, split, (hipStream_t)stream);
 }
 
 int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, int64_t lddy, const void *X, int64_t ldx,
@@ -330,27 +425,29 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         CP_TRY(check_groups(E, off, stride_w, dX ? w : Mat{nullptr, 0, 0, 0}, "W"));
         CP_TRY(check_groups(E, off, stride_dw, dW ? dw : Mat{nullptr, 0, 0, 0}, "dW"));
     }
-    const BackwardWs lay = backward_ws(dtype, M, K, N, E);
-    CP_TRY(check_ws(ws, ws_bytes, lay.total));
+    const int64_t es = elem_size(dtype);
+    const bool aligned = (dy.p == nullptr || aligned16(dy, dtype)) && (!dW || aligned16(x, dtype)) &&
+                         (!dX || (aligned16(w, dtype) && (E <= 1 || stride_w * es % 16 == 0)));
+    CP_TRY(check_ws(ws, ws_bytes, backward_ws(dtype, M, K, N, E, aligned)));
     if (!dX && !dW && !db) return CP_OK;
     hipStream_t s = (hipStream_t)stream;
-    char *base = (char *)ws;
+    Arena mem{(char *)ws};
+    char *sums = mem.take(sums_bytes(dtype, M, N, E));
+    void *split = mem.take(backward_split_bytes(dtype, M, K, N, E));
     Mat dz = dy;
-    const bool need_dz = act != CP_ACT_NONE && (dX || dW);
-    if (need_dz) dz = {base + lay.dz, M, N, up(N, 8)};
+    if (act != CP_ACT_NONE) dz = {mem.take(packed_bytes(dtype, M, N, 1)), M, N, up(N, 8)};
     if (N > 0 && (act != CP_ACT_NONE || db)) {
         GradArgs a{};
         a.dy = (const char *)dy.p;
         a.ldd = dy.ld;
         if (act != CP_ACT_NONE) {
-            // without dX and dW the values only pass through to the sums
             a.pre = (const char *)z.p;
             a.ldp = z.ld;
-            a.dz = base + lay.dz;
-            a.ldz = up(N, 8);
+            a.dz = (char *)const_cast<void *>(dz.p);
+            a.ldz = dz.ld;
         }
         a.db = (char *)db;
-        a.ws = (float *)(base + lay.sums);
+        a.ws = (float *)sums;
         a.off = off;
         a.groups = E ? E : 1;
         a.M = (int)M;
@@ -361,25 +458,31 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         a.vec = aligned16(dy, dtype) && (act == CP_ACT_NONE || aligned16(z, dtype));
         CP_TRY(launched(launch_grad(dtype, a, s), "activation gradient"));
     }
+    const Shape sx = dx_shape(dtype, M, K, N, E, wt), sw = dw_shape(dtype, M, K, N, E, wt);
+    int64_t sb = E > 1 ? stride_w : 0;
+    // dZ is in aligned rows already, zero past their end
+    if (act == CP_ACT_NONE && (dW || (dX && !few_rows(sx)))) CP_TRY(packed(dz, nullptr, 1, dtype, mem, s));
     if (dX) {
+        if (!few_rows(sx)) CP_TRY(packed(w, &sb, E ? E : 1, dtype, mem, s));
         Product p{};
-        p.s = dx_shape(dtype, M, K, N, E, wt);
+        p.s = sx;
         p.A = dz;
         p.B = w;
         p.C = dx;
-        p.sb = E > 1 ? stride_w : 0;
+        p.sb = sb;
         p.off = off;
-        CP_TRY(run_product(p, base + lay.split, s));
+        CP_TRY(run_product(p, split, s));
     }
     if (dW) {
+        CP_TRY(packed(x, nullptr, 1, dtype, mem, s));
         Product p{};
-        p.s = dw_shape(dtype, M, K, N, E, wt);
+        p.s = sw;
         p.A = wt ? dz : x;
         p.B = wt ? x : dz;
         p.C = dw;
         p.sc = E > 1 ? stride_dw : 0;
         p.off = off;
-        CP_TRY(run_product(p, base + lay.split, s));
+        CP_TRY(run_product(p, split, s));
     }
     return CP_OK;
 }
@@ -390,7 +493,7 @@ extern "C" {
 
 const char *cp_ops_last_error(void) { return g_error; }
 
-int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E) {
+int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E, int32_t aligned) {
     g_error[0] = 0;
     CP_TRY(check_dtype(dtype));
     CP_TRY(check_sizes(M, op == CP_OP_LAYER_NORM_BACKWARD ? 0 : K, N));
@@ -398,10 +501,10 @@ int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_
     if (grouped && (E < 1 || E > CP_OPS_MAX_GROUPS))
         return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
     switch (op) {
-        case CP_OP_LINEAR: return forward_ws(dtype, M, K, N, 0);
-        case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E);
-        case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0).total;
-        case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E).total;
+        case CP_OP_LINEAR: return forward_ws(dtype, M, K, N, 0, aligned != 0);
+        case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E, aligned != 0);
+        case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0, aligned != 0);
+        case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E, aligned != 0);
         case CP_OP_LAYER_NORM_BACKWARD: return (int64_t)norm_backward_blocks(dtype, M, N) * N * 8;
     }
     return fail(CP_ERR_INVALID_ARG, "operator code %d", op);

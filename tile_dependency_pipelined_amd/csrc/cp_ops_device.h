@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cp_ops.h"
 
 namespace cpo {
@@ -100,16 +102,24 @@ __device__ __forceinline__ uint4 load_partial(const char *p, int n) {
 
 // -------------------------------------------------------------- activations
 
-__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
-
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGelu1 = 0.044715f;
 
-// (1 + tanh u) / 2 = sigmoid(2 u), so the tanh form of GeLU is
-// x sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)): one exponential, one reciprocal,
-// and no cancellation for negative x.
+// 1 / (1 + 2^t), two hardware approximations of 1 ulp
+__device__ __forceinline__ float inv_1_exp2(float t) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+}
+__device__ __forceinline__ float sigmoid(float x) { return inv_1_exp2(-kLog2e * x); }
+// sigmoid(2 u) of the tanh form of GeLU, u = sqrt(2/pi) (x + 0.044715 x^3):
+// (1 + tanh u) / 2 without cancellation, and one product less
+__device__ __forceinline__ float gelu_gate(float x) {
+    constexpr float c = -2.0f * kLog2e * kGelu0;
+    return inv_1_exp2(x * fmaf(c * kGelu1, x * x, c));
+}
+
 __device__ __forceinline__ float act_apply(float x, int act) {
-    if (act == CP_ACT_GELU_TANH) return x * sigmoid(2.0f * kGelu0 * (x + kGelu1 * x * x * x));
+    if (act == CP_ACT_GELU_TANH) return x * gelu_gate(x);
     if (act == CP_ACT_SILU) return x * sigmoid(x);
     if (act == CP_ACT_RELU) return x < 0.0f ? 0.0f : x;
     return x;
@@ -122,7 +132,7 @@ __device__ __forceinline__ float clamp_keep_nan(float x, float lim) { return x <
 __device__ __forceinline__ float act_grad(float x, int act) {
     if (act == CP_ACT_GELU_TANH) {
         x = clamp_keep_nan(x, 10.0f);
-        const float p = sigmoid(2.0f * kGelu0 * (x + kGelu1 * x * x * x));
+        const float p = gelu_gate(x);
         return p + 2.0f * x * p * (1.0f - p) * kGelu0 * (1.0f + 3.0f * kGelu1 * x * x);
     }
     if (act == CP_ACT_SILU) {
@@ -136,25 +146,42 @@ __device__ __forceinline__ float act_grad(float x, int act) {
 
 // ---------------------------------------------------------------- epilogue
 
-// Epilogue of one run of CNT consecutive columns of a row (fp32 sums v):
-// bias, pre-activation store, activation, residual, one rounding, store.
-// WIDE: CNT is a unit and every pointer 16-byte aligned.
+// Epilogue of one run of CNT consecutive columns of a row (fp32 sums v): bias,
+// pre-activation store, activation, residual, one rounding, store.  CNT is a
+// unit (every pointer 16-byte aligned) or 1.  Bias and residual come in as
+// loaded, so that a caller can request them early.
 template <class T, int CNT>
-__device__ __forceinline__ void finish(const GemmArgs &g, char *C, const char *bias, int row, int col, float (&v)[CNT],
-                                       bool zero) {
-    constexpr bool WIDE = CNT > 1;
+struct Raw {
+    std::conditional_t<CNT == 1, T, uint4> v;
+    __device__ __forceinline__ void load(const char *p) {
+        v = *reinterpret_cast<const std::conditional_t<CNT == 1, T, uint4> *>(p);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[CNT]) const {
+        if constexpr (CNT == 1) {
+            x[0] = to_f32(v);
+        } else {
+            union {
+                uint4 u;
+                T e[CNT];
+            } y;
+            y.u = v;
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) x[i] = to_f32(y.e[i]);
+        }
+    }
+};
+
+template <class T, int CNT>
+__device__ __forceinline__ void finish(const GemmArgs &g, char *C, int row, int col, float (&v)[CNT],
+                                       const Raw<T, CNT> *bias, const Raw<T, CNT> *res, bool zero) {
     static_assert(CNT == 1 || CNT == kUnit<T>, "columns per call");
-    auto get = [](const char *p, float(&x)[CNT]) {
-        if constexpr (WIDE) load_unit<T>(p, x);
-        else x[0] = to_f32(*reinterpret_cast<const T *>(p));
-    };
     auto put = [](char *p, const float(&x)[CNT]) {
-        if constexpr (WIDE) store_unit<T>(p, x);
+        if constexpr (CNT > 1) store_unit<T>(p, x);
         else *reinterpret_cast<T *>(p) = from_f32<T>(x[0]);
     };
     float t[CNT];
     if (bias) {
-        get(bias + (int64_t)col * sizeof(T), t);
+        bias->unpack(t);
 #pragma unroll
         for (int i = 0; i < CNT; ++i) v[i] = zero ? 0.0f : v[i] + t[i];
     }
@@ -162,8 +189,8 @@ __device__ __forceinline__ void finish(const GemmArgs &g, char *C, const char *b
     if (g.act != CP_ACT_NONE)
 #pragma unroll
         for (int i = 0; i < CNT; ++i) v[i] = act_apply(v[i], g.act);
-    if (g.res) {
-        get(g.res + ((int64_t)row * g.ldr + col) * sizeof(T), t);
+    if (res) {
+        res->unpack(t);
 #pragma unroll
         for (int i = 0; i < CNT; ++i) v[i] += t[i];
     }

@@ -72,8 +72,20 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
+// A value the compiler cannot tell from a new one: what is computed from it is
+// computed where it is used, instead of once before the loop into registers
+// that the accumulators and fragments need.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+__device__ __forceinline__ uint32_t fresh_uniform(uint32_t v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // One operand's tile of R outer indices.
-template <class T, int R, bool KC, int NW>
+template <class T, int R, bool KC, int NW, bool LEAN>
 struct Operand {
     static constexpr int ES = sizeof(T), CE = 16 / ES, BK = 128 / ES;
     static constexpr bool BF = std::is_same<T, __bf16>::value;
@@ -82,8 +94,15 @@ struct Operand {
     static constexpr int PW = LOADS >= NW ? LOADS / NW : 1;  // per wave (fewer loads than waves: some repeat one)
     static constexpr int RB = R * ES;                      // bytes of an LDS row, outer-contiguous
     static constexpr int READS = KC ? 1 : (BF ? 2 : 4);    // LDS reads of a fragment
+    // LDS rows from one load of a wave to its next.  Where that is a multiple
+    // of 16 the swizzle is the same in all of them, and so is the step in memory.
+    static constexpr int ROW_STEP = KC ? NW * 8 : NW * 1024 / RB;
+    static constexpr bool EVEN = ROW_STEP % 16 == 0;
+    // one offset register then serves all loads; a tile with registers to spare keeps one for each
+    static constexpr int OFFS = EVEN && LEAN ? 1 : PW;
     static_assert(LOADS >= NW ? LOADS % NW == 0 : NW % LOADS == 0, "loads per wave");
-    static_assert(KC || R >= 64, "bank swizzle");
+    static_assert(KC || (R >= 64 && RB <= 1024), "bank swizzle");
+    static_assert(!KC || EVEN, "loads of rows");
 
     // KC: rows r .. r + 15 of a block and chunks c, c + 2
     __device__ static int swz_kc(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (((r >> 2) & 1) << 2); }
@@ -95,12 +114,12 @@ struct Operand {
         else return ((k & 3) << 1) ^ ((k >> 3) & 1);
     }
 
-    const char *base;   // KC: first outer row at contraction index kb; outer: row kb, first column
+    const char *base;   // KC: first outer row at the first contraction index; outer: first contraction row, first column
     int64_t ld;         // bytes
     int outer;          // valid outer indices (<= R)
     int klen;           // contraction length of this workgroup
-    uint32_t off[PW];   // bytes from base of this lane's chunk in load q
-    int kc[PW];         // its first contraction index within a slab
+    uint32_t off[OFFS]; // bytes from base of this lane's chunk in load q
+    int kc;             // KC: this lane's first contraction index within a slab, the same in every load
 
     __device__ __forceinline__ static int load_id(int q, int wave) {
         return LOADS >= NW ? q * NW + wave : wave % LOADS;
@@ -112,23 +131,24 @@ struct Operand {
         outer = outer_ < R ? outer_ : R;
         klen = klen_;
 #pragma unroll
-        for (int q = 0; q < PW; ++q) {
+        for (int q = 0; q < OFFS; ++q) {
             const int o = load_id(q, wave) * 1024 + lane * 16;
             if constexpr (KC) {
                 const int r = o >> 7, c = ((o >> 4) & 7) ^ swz_kc(r);
                 off[q] = (uint32_t)r * (uint32_t)ld + (uint32_t)c * 16u;
-                kc[q] = c * CE;
+                kc = c * CE;
             } else {
                 const int k = o / RB, c = ((o % RB) >> 4) ^ swz_out(k);
                 off[q] = (uint32_t)k * (uint32_t)ld + (uint32_t)c * 16u;
-                kc[q] = k;
             }
         }
     }
 
     // Request slab `s` into LDS `lds`.  Chunks past the contraction or the
     // outer range read zeros; past the last slab all of them do, without
-    // touching memory, so that the number of loads in flight is constant.
+    // touching memory, so that the number of loads in flight is constant.  A
+    // row's last chunk is read whole: rows that are not whole chunks come only
+    // from the host's packed copies, which end in zeros.
     template <bool TRACKED>
     __device__ __forceinline__ void issue(char *lds, int s, int wave) const {
         const int k0 = s * BK, left = klen - k0;  // uniform
@@ -136,17 +156,19 @@ struct Operand {
         int64_t bytes;
         if constexpr (KC) {
             p = base + (int64_t)k0 * ES;
-            bytes = (int64_t)(outer - 1) * ld + (int64_t)left * ES;
+            bytes = (int64_t)(outer - 1) * ld + (int64_t)((left + CE - 1) / CE * CE) * ES;
         } else {
             p = base + (int64_t)k0 * ld;
-            bytes = (int64_t)((left < BK ? left : BK) - 1) * ld + (int64_t)outer * ES;
+            bytes = (int64_t)((left < BK ? left : BK) - 1) * ld + (int64_t)((outer + CE - 1) / CE * CE) * ES;
         }
         if (left <= 0) bytes = 0;
         const __amdgpu_buffer_rsrc_t r =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)bytes, kRawBuffer);
+        const uint32_t step = OFFS < PW ? fresh_uniform((uint32_t)ld * ROW_STEP) : 0;
+        const bool past = KC && kc >= left;
 #pragma unroll
         for (int q = 0; q < PW; ++q) {
-            const uint32_t v = KC && kc[q] >= left ? kOutside : off[q];
+            const uint32_t v = past ? kOutside : (OFFS < PW ? off[0] + q * step : off[OFFS < PW ? 0 : q]);
             char *dst = lds + load_id(q, wave) * 1024;
             if constexpr (TRACKED) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t *)dst, 16, v, 0, 0, 0);
             else lds_load_untracked(r, dst, v);
@@ -154,16 +176,24 @@ struct Operand {
     }
 
     // The same slab through registers, for rows that are not 16-byte aligned
-    // or not a whole number of 16-byte chunks.
+    // or not a whole number of 16-byte chunks.  Unaligned 16-byte loads cost
+    // little here (217 us aligned, 229 us with odd rows for 2048 x 4096 x 4096
+    // before whole slabs had their own branch-free path); only chunks that
+    // cross the end of a row or of the contraction are read by elements.
     __device__ __forceinline__ void fetch(uint4 (&v)[PW], int s, int wave, int lane) const {
         const int k0 = s * BK, left = klen - k0;
         const char *p = base + (KC ? (int64_t)k0 * ES : (int64_t)k0 * ld);
+        if (left >= BK && outer == R) {  // uniform
+#pragma unroll
+            for (int q = 0; q < PW; ++q) __builtin_memcpy(&v[q], p + off[q], 16);
+            return;
+        }
 #pragma unroll
         for (int q = 0; q < PW; ++q) {
             const int o = load_id(q, wave) * 1024 + lane * 16;
             int n;
-            if constexpr (KC) n = (o >> 7) < outer ? left - kc[q] : 0;
-            else n = kc[q] < left ? outer - (((o % RB) >> 4) ^ swz_out(o / RB)) * CE : 0;
+            if constexpr (KC) n = (o >> 7) < outer ? left - kc : 0;
+            else n = o / RB < left ? outer - (((o % RB) >> 4) ^ swz_out(o / RB)) * CE : 0;
             v[q] = load_partial<T>(p + off[q], n);
         }
     }
@@ -173,28 +203,35 @@ struct Operand {
             *reinterpret_cast<uint4 *>(lds + load_id(q, wave) * 1024 + lane * 16) = v[q];
     }
 
-    // Fragment of step kk (of two per slab), block of 16 outer indices from o0.
-    __device__ __forceinline__ static uint4 frag(const char *lds, int kk, int o0, int lane) {
+    // Where a lane reads its fragments, for the wave whose outer indices start
+    // at o0.  Block f and step kk only flip bits that o0 leaves zero, or add a
+    // constant: one register serves all of a slab's reads.
+    __device__ __forceinline__ static uint32_t lane_base(int o0, int lane) {
         const int g = lane >> 4;
+        if constexpr (KC) return (o0 + (lane & 15)) * 128 + ((g ^ swz_kc(lane & 15)) << 4);
+        else if constexpr (BF) {
+            const int k = 8 * g + ((lane & 15) >> 2);
+            return k * RB + ((((o0 >> 3) + ((lane & 3) >> 1)) ^ swz_out(k)) << 4) + (lane & 1) * 8;
+        } else {
+            return 4 * g * RB + ((((o0 >> 2) + ((lane & 15) >> 2)) ^ swz_out(4 * g)) << 4) + (lane & 3) * 4;
+        }
+    }
+
+    // Fragment of step kk (of two per slab), block f of 16 outer indices.
+    __device__ __forceinline__ static uint4 frag(const char *lds, uint32_t lbase, int kk, int f) {
         if constexpr (KC) {
-            // o0 is a multiple of 16, which the swizzle does not see
-            return *reinterpret_cast<const uint4 *>(lds + (o0 + (lane & 15)) * 128 +
-                                                    (((kk * 4 + g) ^ swz_kc(lane & 15)) << 4));
+            return *reinterpret_cast<const uint4 *>(lds + (lbase ^ (kk << 6)) + f * 16 * 128);
         } else if constexpr (BF) {
-            const int k = kk * 32 + 8 * g + ((lane & 15) >> 2), n = o0 + 4 * (lane & 3);
-            // the swizzle sees bits 0, 1 and 3 of k: the same for k + 4, and for any kk
-            const char *p = lds + k * RB + (((n >> 3) ^ swz_out(8 * g + ((lane & 15) >> 2))) << 4) + ((n >> 2) & 1) * 8;
+            // the swizzle sees bits 0, 1 and 3 of k: the same for k + 4, and for either kk
+            const char *p = lds + (lbase ^ (f << 5)) + kk * 32 * RB;
             const v4i16_t both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)p),
                                      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)(p + 4 * RB))};
             return *reinterpret_cast<const uint4 *>(both);
         } else {
-            const int n = o0 + (lane & 15);
+            const char *p = lds + (lbase ^ (f << 6)) + kk * 16 * RB;
             uint32_t e[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int k = kk * 16 + 4 * g + t;
-                e[t] = *reinterpret_cast<const uint32_t *>(lds + k * RB + (((n >> 2) ^ swz_out(4 * g)) << 4) + (n & 3) * 4);
-            }
+            for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const uint32_t *>(p + t * RB);
             return make_uint4(e[0], e[1], e[2], e[3]);
         }
     }
@@ -210,8 +247,11 @@ struct Product {
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
     static constexpr bool BF = std::is_same<T, __bf16>::value;
-    using OpA = Operand<T, BM, AKC, NW>;
-    using OpB = Operand<T, BN, BKC, NW>;
+    // Accumulators that take half of a wave's registers or more: addresses are
+    // recomputed rather than kept.
+    static constexpr bool LEAN = DIRECT && (FM * FN * 4 > 128 || (FM * FN * 4 == 128 && !(AKC && BKC)));
+    using OpA = Operand<T, BM, AKC, NW, LEAN>;
+    using OpB = Operand<T, BN, BKC, NW, LEAN>;
     static constexpr int BK = OpA::BK;
     static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
     static constexpr int PER = OpA::PW + OpB::PW;          // direct loads per wave and slab
@@ -220,7 +260,10 @@ struct Product {
     static constexpr int EPI_PITCH = WN + 4;               // floats of a staged output row
     static_assert(NW * 16 * EPI_PITCH * 4 <= STAGE, "epilogue staging");
     static_assert(S >= 2 && S <= 4 && (DIRECT || S == 2), "stages");
-    static_assert(WN == 32 || WN == 64, "epilogue layout");
+    static_assert(WN == 32 || WN == 64 || WN == 128, "epilogue layout");
+    // waves per SIMD the registers are budgeted for: accumulators beyond half
+    // of the 512 leave room for one
+    static constexpr int WAVES = FM * FN * 4 > 128 ? 1 : 2;
 
     __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4]) {
         const int tid = threadIdx.x, lane = tid & 63;
@@ -302,11 +345,13 @@ struct Product {
             struct Frags {
                 uint4 a[FM], b[FN];
             };
+            const uint32_t abase = OpA::lane_base(wm * WM, lane), bbase = OpB::lane_base(wn * WN, lane);
             auto load = [&](const char *s, int kk, Frags &f) {
+                const uint32_t ab = LEAN ? fresh(abase) : abase, bb = LEAN ? fresh(bbase) : bbase;
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn) f.b[fn] = OpB::frag(s + OpA::BYTES, kk, wn * WN + fn * 16, lane);
+                for (int fn = 0; fn < FN; ++fn) f.b[fn] = OpB::frag(s + OpA::BYTES, bb, kk, fn);
 #pragma unroll
-                for (int fm = 0; fm < FM; ++fm) f.a[fm] = OpA::frag(s, kk, wm * WM + fm * 16, lane);
+                for (int fm = 0; fm < FM; ++fm) f.a[fm] = OpA::frag(s, ab, kk, fm);
             };
             auto mma = [&](const Frags &f) {
 #pragma unroll
@@ -399,56 +444,93 @@ struct Product {
 
         // ---- epilogue: 16 rows at a time through this wave's part of LDS, so
         // that memory is accessed in runs of whole rows of the wave's tile ----
-        float *sh = reinterpret_cast<float *>(st[0]) + wave * 16 * EPI_PITCH;
         const int wrow = row0 + wm * WM, wcol = col0 + wn * WN;
-        float *part = g.nsplit > 1 ? g.ws + (int64_t)split * g.M * g.ldws : nullptr;
+        if (g.nsplit > 1) {
+            float *part = g.ws + (int64_t)split * g.M * g.ldws;
+            constexpr int UPR = WN / 4;
+            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
+#pragma unroll
+                for (int i = 0; i < 16 * UPR / 64; ++i) {
+                    const int u = i * 64 + lane, r = wrow + fm * 16 + u / UPR, c = (u % UPR) * 4;
+                    if (r < row_end && wcol + c < g.ldws)  // ldws is a multiple of 4
+                        *reinterpret_cast<f32x4_t *>(part + (int64_t)r * g.ldws + wcol + c) =
+                            *reinterpret_cast<const f32x4_t *>(sh + u / UPR * EPI_PITCH + c);
+                }
+            });
+        } else if (g.vec) {
+            // A lane has the same columns in all of its units.  The residual
+            // is requested AHEAD blocks early, so that its latency from memory
+            // is not paid for every 16 rows.
+            constexpr int CE = kUnit<T>, UPR = WN / CE, NU = 16 * UPR / 64, AHEAD = FM < 4 ? FM : 4;
+            static_assert(NU * 64 == 16 * UPR && 64 % UPR == 0, "units per lane");
+            const int r0 = wrow + lane / UPR, c = wcol + (lane % UPR) * CE;
+            const bool col_in = c < g.N;
+            Raw<T, CE> rb, rr[AHEAD][NU];
+            if (bias && col_in) rb.load(bias + (int64_t)c * sizeof(T));
+            auto request = [&](int fm) {
+                if (g.res)
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        const int r = r0 + fm * 16 + i * (64 / UPR);
+                        if (col_in && r < row_end)
+                            rr[fm % AHEAD][i].load(g.res + ((int64_t)r * g.ldr + c) * sizeof(T));
+                    }
+            };
+#pragma unroll
+            for (int fm = 0; fm < AHEAD; ++fm) request(fm);
+            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
+#pragma unroll
+                for (int i = 0; i < NU; ++i) {
+                    const int r = r0 + fm * 16 + i * (64 / UPR);
+                    const float *p = sh + (i * (64 / UPR) + lane / UPR) * EPI_PITCH + (lane % UPR) * CE;
+                    alignas(16) float v[CE];
+#pragma unroll
+                    for (int e = 0; e < CE; e += 4)
+                        *reinterpret_cast<f32x4_t *>(v + e) = *reinterpret_cast<const f32x4_t *>(p + e);
+                    if (col_in && r < row_end)
+                        finish<T, CE>(g, C, r, c, v, bias ? &rb : nullptr, g.res ? &rr[fm % AHEAD][i] : nullptr, zero);
+                }
+                if (fm + AHEAD < FM) request(fm + AHEAD);
+            });
+        } else {
+            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
+                for (int i = 0; i < 16 * WN / 64; ++i) {
+                    const int u = i * 64 + lane, r = wrow + fm * 16 + u / WN, c = wcol + u % WN;
+                    float v[1] = {sh[u / WN * EPI_PITCH + u % WN]};
+                    if (r < row_end && c < g.N) {
+                        Raw<T, 1> b, x;
+                        if (bias) b.load(bias + (int64_t)c * sizeof(T));
+                        if (g.res) x.load(g.res + ((int64_t)r * g.ldr + c) * sizeof(T));
+                        finish<T, 1>(g, C, r, c, v, bias ? &b : nullptr, g.res ? &x : nullptr, zero);
+                    }
+                }
+            });
+        }
+    }
+
+    // Hands each block of 16 rows of the wave's tile to f(fm, rows in LDS).
+    template <class F>
+    __device__ __forceinline__ static void stage_rows(const f32x4_t (&acc)[FM][FN], char *lds, int wave, int lane, F &&f) {
+        float *sh = reinterpret_cast<float *>(lds) + wave * 16 * EPI_PITCH;
+        auto settle = [] {  // LDS accesses of this wave only: they execute in order, the compiler must keep it
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        };
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn)
                 *reinterpret_cast<f32x4_t *>(sh + (lane & 15) * EPI_PITCH + fn * 16 + 4 * (lane >> 4)) = acc[fm][fn];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            if (part) {
-                constexpr int UPR = WN / 4;
-#pragma unroll
-                for (int i = 0; i < 16 * UPR / 64; ++i) {
-                    const int u = i * 64 + lane, r = u / UPR, c = (u % UPR) * 4;
-                    if (wrow + fm * 16 + r < row_end && wcol + c < g.ldws)  // ldws is a multiple of 4
-                        *reinterpret_cast<f32x4_t *>(part + (int64_t)(wrow + fm * 16 + r) * g.ldws + wcol + c) =
-                            *reinterpret_cast<const f32x4_t *>(sh + r * EPI_PITCH + c);
-                }
-            } else if (g.vec) {
-                constexpr int CE = kUnit<T>, UPR = WN / CE;
-#pragma unroll
-                for (int i = 0; i < 16 * UPR / 64; ++i) {
-                    const int u = i * 64 + lane, r = u / UPR, c = (u % UPR) * CE;
-                    alignas(16) float v[CE];
-#pragma unroll
-                    for (int e = 0; e < CE; e += 4)
-                        *reinterpret_cast<f32x4_t *>(v + e) =
-                            *reinterpret_cast<const f32x4_t *>(sh + r * EPI_PITCH + c + e);
-                    if (wrow + fm * 16 + r < row_end && wcol + c < g.N)
-                        finish<T, CE>(g, C, bias, wrow + fm * 16 + r, wcol + c, v, zero);
-                }
-            } else {
-                for (int i = 0; i < 16 * WN / 64; ++i) {
-                    const int u = i * 64 + lane, r = u / WN, c = u % WN;
-                    float v[1] = {sh[r * EPI_PITCH + c]};
-                    if (wrow + fm * 16 + r < row_end && wcol + c < g.N)
-                        finish<T, 1>(g, C, bias, wrow + fm * 16 + r, wcol + c, v, zero);
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            settle();
+            f(fm, sh);
+            settle();
         }
     }
 };
 
 template <class P>
-__global__ __launch_bounds__(P::NT, 2) void product_kernel(GemmArgs g) {
+__global__ __launch_bounds__(P::NT, P::WAVES) void product_kernel(GemmArgs g) {
     // one array per stage: reads of one and direct loads into another do not alias
     __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];
     __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];

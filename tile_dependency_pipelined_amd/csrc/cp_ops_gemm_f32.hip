@@ -15,14 +15,12 @@ hipError_t launch(const GemmArgs &g, int grid, hipStream_t s) {
 template <bool AKC, bool BKC>
 hipError_t launch_layout(Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s) {
     using T = float;
-
-    if (c == kTile128)
-        return direct ? launch<Product<T, 128, 128, 2, 2, 2, AKC, BKC, true>>(g, grid, s)
-                      : launch<Product<T, 128, 128, 2, 2, 2, AKC, BKC, false>>(g, grid, s);
     if constexpr (AKC)
         if (c == kTile16)
             return direct ? launch<Product<T, 16, 128, 1, 4, 4, AKC, BKC, true>>(g, grid, s)
                           : launch<Product<T, 16, 128, 1, 4, 2, AKC, BKC, false>>(g, grid, s);
+    if (!direct) return hipErrorInvalidValue;  // the host packs their operands
+    if (c == kTile128) return launch<Product<T, 128, 128, 2, 2, 2, AKC, BKC, true>>(g, grid, s);
     return hipErrorInvalidValue;
 }
 

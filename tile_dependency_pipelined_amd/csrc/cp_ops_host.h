@@ -10,11 +10,21 @@ namespace cpo {
 enum Layout : int { kNN = 0, kNT = 1, kTN = 2 };  // A and B: KC/outer, KC/KC, outer/outer
 
 // Tile configurations of the products.
-enum Config : int { kTile256 = 0, kTile128 = 1, kTile16 = 2, kConfigs = 3 };
+enum Config : int { kTile256 = 0, kTile128x256 = 1, kTile128 = 2, kTile16 = 3, kConfigs = 4 };
 struct ConfigShape {
     int bm, bn;
 };
-constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 128}, {16, 128}};
+constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {16, 128}};
+
+// A copy of a matrix with rows of whole 16-byte units, zero past the end.
+struct PackArgs {
+    const char *src;
+    char *dst;
+    int64_t ld, ldd;       // elements
+    int64_t stride, stride_d;  // from one of `count` matrices to the next
+    int32_t rows, cols, count;
+};
+hipError_t launch_pack(int dtype, const PackArgs &a, hipStream_t s);
 
 hipError_t launch_product_bf16(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
 hipError_t launch_product_f32(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);

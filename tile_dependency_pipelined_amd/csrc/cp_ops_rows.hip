@@ -8,6 +8,21 @@ namespace cpo {
 
 namespace {
 
+// ------------------------------------------------------------------- packing
+
+// 64 units of 16 bytes x 4 rows per block; the source may lie anyhow.
+template <class T>
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a, int units, int unit_blocks) {
+    constexpr int CE = kUnit<T>;
+    const int u = (blockIdx.x % unit_blocks) * 64 + (threadIdx.x & 63);
+    const int64_t r = (int64_t)(blockIdx.x / unit_blocks) * 4 + (threadIdx.x >> 6);
+    if (u >= units || r >= (int64_t)a.count * a.rows) return;
+    const int m = (int)(r / a.rows), row = (int)(r - (int64_t)m * a.rows);
+    const char *src = a.src + (m * a.stride + row * a.ld + u * CE) * (int64_t)sizeof(T);
+    *reinterpret_cast<uint4 *>(a.dst + (m * a.stride_d + row * a.ldd + u * CE) * (int64_t)sizeof(T)) =
+        load_partial<T>(src, a.cols - u * CE);
+}
+
 // ------------------------------------------------------------------- joining
 
 // Y = epilogue(sum over splits of partial); one block per row and 256 units.
@@ -42,7 +57,10 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
 #pragma unroll
         for (int i = 0; i < CNT; ++i) v[i] += p[s * step + i];
     }
-    finish<T, CNT>(g, g.C, bias, row, col, v, zero);
+    Raw<T, CNT> b, r;
+    if (bias) b.load(bias + (int64_t)col * sizeof(T));
+    if (g.res) r.load(g.res + ((int64_t)row * g.ldr + col) * sizeof(T));
+    finish<T, CNT>(g, g.C, row, col, v, bias ? &b : nullptr, g.res ? &r : nullptr, zero);
 }
 
 // --------------------------------------------- activation gradient, bias sums
@@ -67,6 +85,9 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     float sum[CNT];
 #pragma unroll
     for (int i = 0; i < CNT; ++i) sum[i] = 0.0f;
+    if (CNT == 1 && a.dz && col >= a.N && col < a.ldz)  // the rows of dZ end in zeros
+        for (int row = row0 + r; row < end; row += 8)
+            *reinterpret_cast<T *>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T)) = from_f32<T>(0.0f);
     if (col < a.N) {
 #pragma unroll 4
         for (int row = row0 + r; row < end; row += 8) {
@@ -401,6 +422,16 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a, int col_bloc
 // ------------------------------------------------------------------ launchers
 
 template <class T>
+hipError_t pack(const PackArgs &a, hipStream_t s) {
+    const int units = (a.cols + kUnit<T> - 1) / kUnit<T>;
+    const int ub = (units + 63) / 64;
+    const int64_t blocks = ((int64_t)a.count * a.rows + 3) / 4 * ub;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(pack_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, a, units, ub);
+    return hipGetLastError();
+}
+
+template <class T>
 hipError_t join(const GemmArgs &g, hipStream_t s) {
     const int unit = g.vec ? kUnit<T> : 1;
     const int per_row = (g.N + 256 * unit - 1) / (256 * unit);
@@ -486,6 +517,10 @@ hipError_t norm_backward_all(const NormArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_pack(int dtype, const PackArgs &a, hipStream_t s) {
+    return dtype == CP_BF16 ? pack<__bf16>(a, s) : pack<float>(a, s);
+}
 
 hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s) {
     return dtype == CP_BF16 ? join<__bf16>(g, s) : join<float>(g, s);

@@ -54,7 +54,7 @@ _grouped_linear_backward = _declare("cp_grouped_linear_backward", ctypes.c_int, 
 _layer_norm = _declare("cp_layer_norm", ctypes.c_int, _i32, _i64, _i64, *_MAT, _vp, _vp, _f32, *_MAT, _vp, _vp, _vp)
 _layer_norm_backward = _declare("cp_layer_norm_backward", ctypes.c_int, _i32, _i64, _i64, *_MAT, *_MAT, _vp, _vp, _vp,
                                 *_MAT, _vp, _vp, *_TAIL)
-_workspace = _declare("cp_ops_workspace", _i64, _i32, _i32, _i64, _i64, _i64, _i32)
+_workspace = _declare("cp_ops_workspace", _i64, _i32, _i32, _i64, _i64, _i64, _i32, _i32)
 _last_error = _declare("cp_ops_last_error", ctypes.c_char_p)
 
 _CODES = {torch.float32: nat.CP_F32, torch.bfloat16: nat.CP_BF16}
@@ -67,9 +67,9 @@ def _check(rc, where):
 
 
 @functools.lru_cache(maxsize=4096)
-def workspace_bytes(op, dtype, M, K, N, E=0):
+def workspace_bytes(op, dtype, M, K, N, E=0, aligned=False):
     """Bytes of scratch memory an operator takes (cp_ops_workspace)."""
-    return _check(_workspace(op, dtype, M, K, N, E), "cp_ops_workspace")
+    return _check(_workspace(op, dtype, M, K, N, E, aligned), "cp_ops_workspace")
 
 
 def _like(t, x, shape, name, dtype=None):
@@ -137,8 +137,16 @@ def _empty_weight(w, wt):
     return torch.empty(shape, dtype=w.dtype, device=w.device).transpose(-1, -2)
 
 
-def _scratch(op, code, M, K, N, E, x):
-    n = workspace_bytes(op, code, M, K, N, E)
+def _aligned(code, *mats):
+    """Whether all (pointer, rows, row length, row stride, outer stride) are whole 16-byte units."""
+    bits = 0
+    for p, rows, length, ld, outer in mats:
+        bits |= p | ((length | outer | (ld if rows > 1 else 0)) << (1 if code == nat.CP_BF16 else 2))
+    return bits % 16 == 0
+
+
+def _scratch(op, code, M, K, N, E, x, aligned=True):
+    n = workspace_bytes(op, code, M, K, N, E, aligned)
     return (torch.empty(n, dtype=torch.uint8, device=x.device) if n else None), n
 
 
@@ -185,8 +193,10 @@ def linear(x, w, bias=None, residual=None, act=ACT_NONE, need_pre=False, out=Non
     with _on(x) as stream:
         y = _output(out, x, (M, N))
         pre = torch.empty((M, N), dtype=x.dtype, device=x.device) if need_pre else None
-        ws, n = _scratch(OP_LINEAR, code, M, K, N, 0, x)
-        _check(_linear(code, M, K, N, x.data_ptr(), _rows(x, "x"), w.data_ptr(), ldw, wt, b, _ptr(residual), ldr, act,
+        xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
+        ws, n = _scratch(OP_LINEAR, code, M, K, N, 0, x,
+                         _aligned(code, (xp, M, K, ldx, 0), (wp, N if wt else K, K if wt else N, ldw, 0)))
+        _check(_linear(code, M, K, N, xp, ldx, wp, ldw, wt, b, _ptr(residual), ldr, act,
                        y.data_ptr(), _rows(y, "out"), _ptr(pre), N, _ptr(ws), n, stream), "cp_linear")
     return (y, pre) if need_pre else y
 
@@ -208,9 +218,11 @@ def linear_backward(dy, x, w, pre=None, act=ACT_NONE, need_x=True, need_w=True, 
         dx = torch.empty((M, K), dtype=dy.dtype, device=dy.device) if need_x else None
         dw = _empty_weight(w, wt) if need_w else None
         db = torch.empty(N, dtype=dy.dtype, device=dy.device) if need_bias else None
-        ws, n = _scratch(OP_LINEAR_BACKWARD, code, M, K, N, 0, dy)
-        _check(_linear_backward(code, M, K, N, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"), w.data_ptr(),
-                                ldw, wt, _ptr(pre), ldp, act, _ptr(dx), K, _ptr(dw), K if wt else N, _ptr(db), _ptr(ws),
+        dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
+        ws, n = _scratch(OP_LINEAR_BACKWARD, code, M, K, N, 0, dy,
+                         _aligned(code, (dp, M, N, ldd, 0), (xp, M, K, ldx, 0),
+                                  (wp, N if wt else K, K if wt else N, ldw, 0)))
+        _check(_linear_backward(code, M, K, N, dp, ldd, xp, ldx, wp, ldw, wt, _ptr(pre), ldp, act, _ptr(dx), K, _ptr(dw), K if wt else N, _ptr(db), _ptr(ws),
                                 n, stream), "cp_linear_backward")
     return dx, dw, db
 
@@ -247,8 +259,10 @@ def grouped_linear(x, w, offsets, bias=None, act=ACT_NONE, need_pre=False, out=N
     with _on(x) as stream:
         y = _output(out, x, (T, N))
         pre = torch.empty((T, N), dtype=x.dtype, device=x.device) if need_pre else None
-        ws, n = _scratch(OP_GROUPED_LINEAR, code, T, K, N, E, x)
-        _check(_grouped_linear(code, T, K, N, E, x.data_ptr(), _rows(x, "x"), w.data_ptr(), ldw, sw, wt,
+        xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
+        ws, n = _scratch(OP_GROUPED_LINEAR, code, T, K, N, E, x,
+                         _aligned(code, (xp, T, K, ldx, 0), (wp, N if wt else K, K if wt else N, ldw, sw if E > 1 else 0)))
+        _check(_grouped_linear(code, T, K, N, E, xp, ldx, wp, ldw, sw, wt,
                                offsets.data_ptr(), b, act, y.data_ptr(), _rows(y, "out"), _ptr(pre), N, _ptr(ws), n,
                                stream), "cp_grouped_linear")
     return (y, pre) if need_pre else y
@@ -269,9 +283,11 @@ def grouped_linear_backward(dy, x, w, offsets, pre=None, act=ACT_NONE, need_x=Tr
         dx = torch.empty((T, K), dtype=dy.dtype, device=dy.device) if need_x else None
         dw = _empty_weight(w, wt) if need_w else None
         db = torch.empty((E, N), dtype=dy.dtype, device=dy.device) if need_bias else None
-        ws, n = _scratch(OP_GROUPED_LINEAR_BACKWARD, code, T, K, N, E, dy)
-        _check(_grouped_linear_backward(code, T, K, N, E, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"),
-                                        w.data_ptr(), ldw, sw, wt, offsets.data_ptr(), _ptr(pre), ldp, act, _ptr(dx), K,
+        dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
+        ws, n = _scratch(OP_GROUPED_LINEAR_BACKWARD, code, T, K, N, E, dy,
+                         _aligned(code, (dp, T, N, ldd, 0), (xp, T, K, ldx, 0),
+                                  (wp, N if wt else K, K if wt else N, ldw, sw if E > 1 else 0)))
+        _check(_grouped_linear_backward(code, T, K, N, E, dp, ldd, xp, ldx, wp, ldw, sw, wt, offsets.data_ptr(), _ptr(pre), ldp, act, _ptr(dx), K,
                                         _ptr(dw), K if wt else N, K * N, _ptr(db), _ptr(ws), n, stream),
                "cp_grouped_linear_backward")
     return dx, dw, db
