@@ -131,6 +131,9 @@ bool few_rows(const Shape &s) {
 // 204, 91, 115 us; 128x256 238, 62, 134; 128x128 (two on a CU) 257, 62, 129.
 // A split writes and reads its partials and takes another launch.
 Choice choose(const Shape &s) {
+    // One launch and nothing but the weight's bytes to move, but its vector
+    // arithmetic grows with the rows.
+    if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows) return {kGemv, 1};
     if (few_rows(s)) {
         const int64_t tiles = max_row_tiles(s, 16) * ceil_div(s.N, 128);
         int64_t n = 2 * kComputeUnits / (tiles ? tiles : 1);
@@ -142,8 +145,8 @@ Choice choose(const Shape &s) {
         Config cfg;
         double slab, fixed;
     };
-    static const Rate bf16[] = {{kTile256, 1.5, 9.0}, {kTile128x256, 0.90, 5.0}, {kTile128, 0.98, 4.0}};
-    static const Rate f32[] = {{kTile128, 3.6, 4.0}};
+    static const Rate bf16[] = {{kTile256, 1.5, 10.0}, {kTile128x256, 0.90, 6.0}, {kTile128, 0.98, 6.0}};
+    static const Rate f32[] = {{kTile128, 3.6, 6.0}};
     const Rate *rates = s.dtype == CP_BF16 ? bf16 : f32;
     const int nrates = s.dtype == CP_BF16 ? 3 : 1;
     const double slabs = (double)slabs_of(s);
@@ -154,24 +157,17 @@ Choice choose(const Shape &s) {
         // row tiles of an average launch: each expert's last one is half empty
         const double tm = s.mode == kGroupRows ? (double)s.M / t.bm + 0.5 * s.groups : (double)ceil_div(s.M, t.bm);
         const double tiles = tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
-        for (int n = 1; n <= 16; n *= 2) {
+        for (int n = 1; n <= 16; ++n) {
             if (n > 1 && (s.mode != kDense || slabs < 4 * n)) break;
-            double rounds, slab = rates[i].slab;
+            double rounds;
             if (rates[i].cfg == kTile128) {
-                // two on a CU, taken as they come; alone on its CU a tile is faster
-                rounds = tiles * n / (2 * kComputeUnits);
-                if (rounds <= 0.5) {
-                    rounds = 1.0;
-                    slab *= 0.6;
-                } else if (rounds < 1.0) {
-                    rounds = 1.0;
-                } else {
-                    rounds += 0.25;
-                }
+                // two on a CU; what is left after full rounds runs alone on its CU, and faster
+                const double all = tiles * n / (2 * kComputeUnits), full = (double)(int64_t)all;
+                rounds = full + (all == full ? 0.0 : all - full <= 0.5 ? 0.6 : 1.0);
             } else {
                 rounds = (double)(int64_t)(tiles * n / kComputeUnits + 0.999);
             }
-            double t_us = rounds * (slab * (slabs / n) + rates[i].fixed);
+            double t_us = rounds * (rates[i].slab * (double)ceil_div((int64_t)slabs, n) + rates[i].fixed);
             if (n > 1) t_us += 4.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 4e6;
             if (t_us < least) {
                 least = t_us;
@@ -246,7 +242,7 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
     if (s.M == 0 || s.N == 0) return CP_OK;
     const int es = elem_size(s.dtype);
     const Choice c = choose(s);
-    const bool direct = c.cfg != kTile16 || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0);
+    const bool direct = (c.cfg != kTile16 && c.cfg != kGemv) || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0);
     GemmArgs g{};
     g.A = (const char *)p.A.p;
     g.B = (const char *)p.B.p;
@@ -273,6 +269,7 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
     g.ldws = (int)up(s.N, 8);
     g.vec = aligned16(p.C, s.dtype) && aligned16(p.R, s.dtype) && aligned16(p.P, s.dtype) && aligned16(p.bias) &&
             p.sc * es % 16 == 0;
+    if (c.cfg == kGemv) return launched(launch_gemv(s.dtype, s.layout == kNT, g, stream), "product of few rows");
     const ConfigShape t = kShapes[c.cfg];
     g.ntn = (int)ceil_div(s.N, t.bn);
     const int64_t ntm = max_row_tiles(s, t.bm);
@@ -505,7 +502,7 @@ int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_
         case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E, aligned != 0);
         case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0, aligned != 0);
         case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E, aligned != 0);
-        case CP_OP_LAYER_NORM_BACKWARD: return (int64_t)norm_backward_blocks(dtype, M, N) * N * 8;
+        case CP_OP_LAYER_NORM_BACKWARD: return (int64_t)norm_backward_blocks(M) * N * 8;
     }
     return fail(CP_ERR_INVALID_ARG, "operator code %d", op);
 }
@@ -593,7 +590,7 @@ int cp_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, 
     CP_TRY(check_vector(dw, dtype, "dw"));
     CP_TRY(check_vector(db, dtype, "db"));
     NormArgs a{};
-    a.blocks = norm_backward_blocks(dtype, M, N);
+    a.blocks = norm_backward_blocks(M);
     CP_TRY(check_ws(ws, ws_bytes, (int64_t)a.blocks * N * 8));
     a.x = (const char *)X;
     a.dy = (const char *)dY;

@@ -458,52 +458,60 @@ struct Product {
                 }
             });
         } else if (g.vec) {
-            // A lane has the same columns in all of its units.  The residual
-            // is requested AHEAD blocks early, so that its latency from memory
-            // is not paid for every 16 rows.
-            constexpr int CE = kUnit<T>, UPR = WN / CE, NU = 16 * UPR / 64, AHEAD = FM < 4 ? FM : 4;
-            static_assert(NU * 64 == 16 * UPR && 64 % UPR == 0, "units per lane");
-            const int r0 = wrow + lane / UPR, c = wcol + (lane % UPR) * CE;
+            finish_tile<kUnit<T>>(g, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+        } else {
+            finish_tile<1>(g, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+        }
+    }
+
+    // Epilogue and stores in runs of CNT columns.  A lane has the same columns
+    // in all of its runs.  The residual is requested AHEAD blocks of 16 rows
+    // early, so that its latency from memory is not paid for each of them.
+    template <int CNT>
+    __device__ __forceinline__ static void finish_tile(const GemmArgs &g, const f32x4_t (&acc)[FM][FN], char *lds, char *C,
+                                                       const char *bias, int wrow, int wcol, int row_end, int wave,
+                                                       int lane, bool zero) {
+        constexpr int RUNS = WN / CNT;                        // of a row
+        constexpr int STEP = RUNS < 64 ? 64 / RUNS : 1;       // rows between a lane's runs
+        constexpr int COLS = RUNS < 64 ? 1 : RUNS / 64;       // runs of a row per lane
+        constexpr int NU = 16 / STEP;
+        constexpr int AHEAD = FM < (CNT > 1 ? 4 : 1) ? FM : (CNT > 1 ? 4 : 1);
+        const int l0 = RUNS < 64 ? lane / RUNS : 0, r0 = wrow + l0;
+        const int cl = (RUNS < 64 ? lane % RUNS : lane) * CNT;
+#pragma unroll
+        for (int h = 0; h < COLS; ++h) {
+            const int c = wcol + cl + h * 64 * CNT;
             const bool col_in = c < g.N;
-            Raw<T, CE> rb, rr[AHEAD][NU];
+            Raw<T, CNT> rb, rr[AHEAD][NU];
             if (bias && col_in) rb.load(bias + (int64_t)c * sizeof(T));
             auto request = [&](int fm) {
                 if (g.res)
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
-                        const int r = r0 + fm * 16 + i * (64 / UPR);
+                        const int r = r0 + fm * 16 + i * STEP;
                         if (col_in && r < row_end)
                             rr[fm % AHEAD][i].load(g.res + ((int64_t)r * g.ldr + c) * sizeof(T));
                     }
             };
 #pragma unroll
             for (int fm = 0; fm < AHEAD; ++fm) request(fm);
-            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
+            stage_rows(acc, lds, wave, lane, [&](int fm, const float *sh) {
 #pragma unroll
                 for (int i = 0; i < NU; ++i) {
-                    const int r = r0 + fm * 16 + i * (64 / UPR);
-                    const float *p = sh + (i * (64 / UPR) + lane / UPR) * EPI_PITCH + (lane % UPR) * CE;
-                    alignas(16) float v[CE];
+                    const int r = r0 + fm * 16 + i * STEP;
+                    const float *p = sh + (i * STEP + l0) * EPI_PITCH + cl + h * 64 * CNT;
+                    alignas(16) float v[CNT];
+                    if constexpr (CNT > 1) {
 #pragma unroll
-                    for (int e = 0; e < CE; e += 4)
-                        *reinterpret_cast<f32x4_t *>(v + e) = *reinterpret_cast<const f32x4_t *>(p + e);
+                        for (int e = 0; e < CNT; e += 4)
+                            *reinterpret_cast<f32x4_t *>(v + e) = *reinterpret_cast<const f32x4_t *>(p + e);
+                    } else {
+                        v[0] = *p;
+                    }
                     if (col_in && r < row_end)
-                        finish<T, CE>(g, C, r, c, v, bias ? &rb : nullptr, g.res ? &rr[fm % AHEAD][i] : nullptr, zero);
+                        finish<T, CNT>(g, C, r, c, v, bias ? &rb : nullptr, g.res ? &rr[fm % AHEAD][i] : nullptr, zero);
                 }
                 if (fm + AHEAD < FM) request(fm + AHEAD);
-            });
-        } else {
-            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
-                for (int i = 0; i < 16 * WN / 64; ++i) {
-                    const int u = i * 64 + lane, r = wrow + fm * 16 + u / WN, c = wcol + u % WN;
-                    float v[1] = {sh[u / WN * EPI_PITCH + u % WN]};
-                    if (r < row_end && c < g.N) {
-                        Raw<T, 1> b, x;
-                        if (bias) b.load(bias + (int64_t)c * sizeof(T));
-                        if (g.res) x.load(g.res + ((int64_t)r * g.ldr + c) * sizeof(T));
-                        finish<T, 1>(g, C, r, c, v, bias ? &b : nullptr, g.res ? &x : nullptr, zero);
-                    }
-                }
             });
         }
     }

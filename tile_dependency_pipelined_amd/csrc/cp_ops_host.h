@@ -9,12 +9,14 @@ namespace cpo {
 // Which index of the operands is contiguous (see cp_ops_gemm.h).
 enum Layout : int { kNN = 0, kNT = 1, kTN = 2 };  // A and B: KC/outer, KC/KC, outer/outer
 
-// Tile configurations of the products.
-enum Config : int { kTile256 = 0, kTile128x256 = 1, kTile128 = 2, kTile16 = 3, kConfigs = 4 };
+constexpr int kGemvRows = 4;
+
+// Tile configurations of the products; kGemv: no tiles, at most kGemvRows rows.
+enum Config : int { kTile256 = 0, kTile128x256 = 1, kTile128 = 2, kTile16 = 3, kGemv = 4, kConfigs = 5 };
 struct ConfigShape {
     int bm, bn;
 };
-constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {16, 128}};
+constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {16, 128}, {kGemvRows, 1}};
 
 // A copy of a matrix with rows of whole 16-byte units, zero past the end.
 struct PackArgs {
@@ -29,6 +31,10 @@ hipError_t launch_pack(int dtype, const PackArgs &a, hipStream_t s);
 hipError_t launch_product_bf16(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
 hipError_t launch_product_f32(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
 
+// Products with at most kGemvRows rows; the weight's rows run along the
+// contraction (w_rows) or along the output.
+hipError_t launch_gemv(int dtype, bool w_rows, const GemmArgs &g, hipStream_t s);
+
 // sums the partials of a split product and runs its epilogue
 hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s);
 
@@ -41,7 +47,7 @@ struct GradArgs {
     const int32_t *off;
     int32_t groups, M, N, act, tiles, vec;
 };
-constexpr int kGradRows = 128;  // rows of a partial column sum
+constexpr int kGradRows = 64;  // rows of a partial column sum
 hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s);
 
 struct NormArgs {
@@ -54,7 +60,7 @@ struct NormArgs {
     float eps;
 };
 hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s);
-int norm_backward_blocks(int dtype, int64_t M, int64_t N);
+int norm_backward_blocks(int64_t M);  // partial sums: one per block
 hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s);
 
 }  // namespace cpo

@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
         for (int row = row0 + r; row < end; row += 8)
             *reinterpret_cast<T *>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T)) = from_f32<T>(0.0f);
     if (col < a.N) {
-#pragma unroll 4
+#pragma unroll 8
         for (int row = row0 + r; row < end; row += 8) {
             float d[CNT];
             const char *p = a.dy + ((int64_t)row * a.ldd + col) * sizeof(T);
@@ -123,40 +123,61 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     }
 }
 
-// db[e] = sum of its row tiles' partials, in order
+// db[e] = sum of its row tiles' partials: 64 columns x 4 ranges of tiles
 template <class T>
 __global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a, int col_blocks) {
-    const int e = blockIdx.x / col_blocks, col = (blockIdx.x % col_blocks) * 256 + threadIdx.x;
+    __shared__ float part[4][64];
+    const int e = blockIdx.x / col_blocks, t = threadIdx.x & 63, s = threadIdx.x >> 6;
+    const int col = (blockIdx.x % col_blocks) * 64 + t;
     int from = 0, to = (a.M + kGradRows - 1) / kGradRows;
     if (a.off) {
         int carry_end = 0, carry_tiles = 0;
         for (int base = 0;; base += 64) {
-            const GroupScan s = scan_groups(a.off, a.groups, a.M, kGradRows, base, carry_end, carry_tiles);
+            const GroupScan g = scan_groups(a.off, a.groups, a.M, kGradRows, base, carry_end, carry_tiles);
             if (e < base + 64) {
                 const int l = e - base;
-                from = l ? __builtin_amdgcn_readlane(s.tiles_end, l - 1) : carry_tiles;
-                to = __builtin_amdgcn_readlane(s.tiles_end, l);
+                from = l ? __builtin_amdgcn_readlane(g.tiles_end, l - 1) : carry_tiles;
+                to = __builtin_amdgcn_readlane(g.tiles_end, l);
                 break;
             }
-            carry_end = __builtin_amdgcn_readlane(s.end, 63);
-            carry_tiles = __builtin_amdgcn_readlane(s.tiles_end, 63);
+            carry_end = __builtin_amdgcn_readlane(g.end, 63);
+            carry_tiles = __builtin_amdgcn_readlane(g.tiles_end, 63);
         }
     }
-    if (col >= a.N) return;
+    const int per = (to - from + 3) / 4, p0 = from + s * per, p1 = p0 + per < to ? p0 + per : to;
     float v = 0.0f;
+    if (col < a.N)
 #pragma unroll 8
-    for (int t = from; t < to; ++t) v += a.ws[(int64_t)t * a.N + col];
-    reinterpret_cast<T *>(a.db)[(int64_t)e * a.N + col] = from_f32<T>(v);
+        for (int i = p0; i < p1; ++i) v += a.ws[(int64_t)i * a.N + col];
+    part[s][t] = v;
+    __syncthreads();
+    if (s == 0 && col < a.N)
+        reinterpret_cast<T *>(a.db)[(int64_t)e * a.N + col] =
+            from_f32<T>(((part[0][t] + part[1][t]) + part[2][t]) + part[3][t]);
 }
 
 // ------------------------------------------------------- layer normalisation
+
+// Sum over a wave, the same value in every lane: cross-lane adds inside the
+// vector unit (a shuffle through LDS takes several times as long).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 15, 15, true));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = dpp_add<0x111>(v);  // row_shr 1, 2, 4, 8: lane 15 of each 16 holds their sum
+    v = dpp_add<0x112>(v);
+    v = dpp_add<0x114>(v);
+    v = dpp_add<0x118>(v);
+    auto at = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    return (at(15) + at(31)) + (at(47) + at(63));
+}
 
 // Sum over the THREADS threads of a row: a wave, or a block through LDS
 // (`sh`: one float per wave; two barriers, so it can be called again at once).
 template <int THREADS>
 __device__ __forceinline__ float row_sum(float v, float *sh) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    v = wave_sum(v);
     if constexpr (THREADS > 64) {
         constexpr int W = THREADS / 64;
         if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
@@ -295,69 +316,162 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     }
 }
 
-// Backward: block b takes rows b, b + blocks, ...; a thread keeps its columns'
-// weight and bias sums in registers over all of them and stores one partial
-// per block, which norm_join_kernel adds up in block order.
+// A row (or parameter vector) as loaded, a thread's share of it.
 template <class T, int THREADS, int VPT, bool VEC>
-__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
-    constexpr int CE = kUnit<T>;
-    __shared__ float sh[16];
-    const int t = threadIdx.x;
+struct RowShare {
+    static constexpr int CE = kUnit<T>;
+    union {
+        uint4 u[VPT];
+        T e[VPT][CE];
+    };
+    __device__ __forceinline__ RowShare() {}
+    __device__ __forceinline__ void load(const char *row, int N, int t) {
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            if constexpr (VEC) {
+                const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+                u[q] = c < N ? *reinterpret_cast<const uint4 *>(row + (int64_t)c * sizeof(T)) : make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < CE; ++i) {
+                    const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                    e[q][i] = c < N ? reinterpret_cast<const T *>(row)[c] : from_f32<T>(0.0f);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int q, int i) const { return to_f32(e[q][i]); }
+    // What was unpacked so far is not kept: the next use unpacks again.
+    __device__ __forceinline__ void forget() {
+        if constexpr (VEC && sizeof(T) == 2)
+#pragma unroll
+            for (int q = 0; q < VPT; ++q)
+                asm volatile("" : "+v"(u[q].x), "+v"(u[q].y), "+v"(u[q].z), "+v"(u[q].w));
+    }
+};
+
+// Backward: SUBS rows at a time per block, THREADS threads each.  A thread
+// keeps its columns' weight and bias sums in registers over all its rows; the
+// block adds its SUBS sums up in LDS and stores one partial, which
+// norm_join_kernel adds up in block order.  The next rows are requested before
+// the current ones are reduced, so that memory is read all the time.
+template <class T, int THREADS, int SUBS, int VPT, bool VEC>
+__global__ __launch_bounds__(THREADS *SUBS) void norm_backward_kernel(NormArgs a) {
+    constexpr int CE = kUnit<T>, W = THREADS / 64, COLS = THREADS * VPT * CE;
+    __shared__ float2 sums[2][SUBS][W];
+    __shared__ float total[SUBS > 1 ? COLS : 1];
+    const int t = threadIdx.x % THREADS, sub = threadIdx.x / THREADS, wave = t >> 6;
+    using Share = RowShare<T, THREADS, VPT, VEC>;
     float dw[VPT][CE], db[VPT][CE];
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
         for (int i = 0; i < CE; ++i) dw[q][i] = db[q][i] = 0.0f;
-    for (int row = blockIdx.x; row < a.M; row += a.blocks) {
-        float x[VPT][CE], dy[VPT][CE];
-        norm_load<T, THREADS, VPT, VEC>(a.x + (int64_t)row * a.ldx * sizeof(T), a.N, t, x);
-        norm_load<T, THREADS, VPT, VEC>(a.dy + (int64_t)row * a.ldd * sizeof(T), a.N, t, dy);
-        const float mean = a.mean[row], rstd = a.rstd[row];
-#pragma unroll
-        for (int q = 0; q < VPT; ++q)
-#pragma unroll
-            for (int i = 0; i < CE; ++i) {
-                // past the row's end dy is zero, so x's value there does not count
-                x[q][i] = norm_col<T, THREADS, VEC>(q, i, t) < a.N ? (x[q][i] - mean) * rstd : 0.0f;
-                dw[q][i] += dy[q][i] * x[q][i];
-                db[q][i] += dy[q][i];
-            }
-        if (!a.y) continue;
-        if (a.w) {
-            float w[VPT][CE];
-            norm_load<T, THREADS, VPT, VEC>(a.w, a.N, t, w);
+    struct Row {
+        Share x, dy;
+        float mean, rstd;
+    } cur, next;
+    Share w;
+    if (a.w) w.load(a.w, a.N, t);
+    const int step = a.blocks * SUBS;
+    int row = blockIdx.x * SUBS + sub;
+    auto request = [&](Row &to, int r) {
+        to.x.load(a.x + (int64_t)r * a.ldx * sizeof(T), a.N, t);
+        to.dy.load(a.dy + (int64_t)r * a.ldd * sizeof(T), a.N, t);
+        to.mean = a.mean[r];
+        to.rstd = a.rstd[r];
+    };
+    // past the row's end dy is zero, so x's value there does not count
+    auto norm = [&](const Row &r, int q, int i) {
+        return norm_col<T, THREADS, VEC>(q, i, t) < a.N ? (r.x.at(q, i) - r.mean) * r.rstd : 0.0f;
+    };
+    if (row < a.M) request(next, row);
+    for (int base = blockIdx.x * SUBS, parity = 0; base < a.M; base += step, row += step, parity ^= 1) {
+        const bool live = row < a.M;  // the same in a whole wave
+        float s0 = 0.0f, s1 = 0.0f;
+        if (live) {
+            cur = next;
+            if (row + step < a.M) request(next, row + step);
 #pragma unroll
             for (int q = 0; q < VPT; ++q)
 #pragma unroll
-                for (int i = 0; i < CE; ++i) dy[q][i] *= w[q][i];
+                for (int i = 0; i < CE; ++i) {
+                    const float d = cur.dy.at(q, i), xh = norm(cur, q, i), g = a.w ? d * w.at(q, i) : d;
+                    dw[q][i] += d * xh;
+                    db[q][i] += d;
+                    s0 += g;
+                    s1 += g * xh;
+                }
         }
-        float s0 = 0.0f, s1 = 0.0f;
+        if (!a.y) continue;
+        s0 = wave_sum(s0);
+        s1 = wave_sum(s1);
+        if constexpr (W > 1) {
+            // the other parity's slots are written again only after the next barrier
+            if ((t & 63) == 0) sums[parity][sub][wave] = make_float2(s0, s1);
+            __syncthreads();
+            s0 = s1 = 0.0f;
 #pragma unroll
-        for (int q = 0; q < VPT; ++q)
-#pragma unroll
-            for (int i = 0; i < CE; ++i) {
-                s0 += dy[q][i];
-                s1 += dy[q][i] * x[q][i];
+            for (int i = 0; i < W; ++i) {
+                s0 += sums[parity][sub][i].x;
+                s1 += sums[parity][sub][i].y;
             }
-        s0 = row_sum<THREADS>(s0, sh) / (float)a.N;
-        s1 = row_sum<THREADS>(s1, sh) / (float)a.N;
+        }
+        if (live) {
+            s0 /= (float)a.N;
+            s1 /= (float)a.N;
+            // xh and g are computed a second time: kept, they would take more
+            // registers than there are
+            cur.x.forget();
+            cur.dy.forget();
+            w.forget();
+            char *out = a.y + (int64_t)row * a.ldy * sizeof(T);
 #pragma unroll
-        for (int q = 0; q < VPT; ++q)
+            for (int q = 0; q < VPT; ++q) {
+                float v[1][CE];
 #pragma unroll
-            for (int i = 0; i < CE; ++i) dy[q][i] = rstd * (dy[q][i] - s0 - x[q][i] * s1);
-        norm_store<T, THREADS, VPT, VEC>(a.y + (int64_t)row * a.ldy * sizeof(T), a.N, t, dy);
+                for (int i = 0; i < CE; ++i) {
+                    const float g = a.w ? cur.dy.at(q, i) * w.at(q, i) : cur.dy.at(q, i);
+                    v[0][i] = cur.rstd * (g - s0 - norm(cur, q, i) * s1);
+                }
+                if constexpr (VEC) {
+                    const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+                    if (c < a.N) store_unit<T>(out + (int64_t)c * sizeof(T), v[0]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < CE; ++i) {
+                        const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                        if (c < a.N) reinterpret_cast<T *>(out)[c] = from_f32<T>(v[0][i]);
+                    }
+                }
+            }
+        }
     }
-    float *pw = a.ws + (int64_t)blockIdx.x * a.N, *pb = pw + (int64_t)a.blocks * a.N;
+    auto flush = [&](const float(&v)[VPT][CE], float *dst) {
 #pragma unroll
-    for (int q = 0; q < VPT; ++q)
+        for (int s = 0; s < SUBS; ++s) {
+            if (s > 0) __syncthreads();
+            if (sub == s)
 #pragma unroll
-        for (int i = 0; i < CE; ++i) {
-            const int c = norm_col<T, THREADS, VEC>(q, i, t);
-            if (c < a.N) {
-                if (a.dw) pw[c] = dw[q][i];
-                if (a.db) pb[c] = db[q][i];
-            }
+                for (int q = 0; q < VPT; ++q)
+#pragma unroll
+                    for (int i = 0; i < CE; ++i) {
+                        const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                        float sum = v[q][i];
+                        if constexpr (SUBS > 1)
+                            if (s > 0) sum += total[c];
+                        if (s + 1 == SUBS) {
+                            if (c < a.N) dst[c] = sum;
+                        } else if constexpr (SUBS > 1) {
+                            total[c] = sum;
+                        }
+                    }
         }
+        if (SUBS > 1) __syncthreads();
+    };
+    float *pw = a.ws + (int64_t)blockIdx.x * a.N;
+    if (a.dw) flush(dw, pw);
+    if (a.db) flush(db, pw + (int64_t)a.blocks * a.N);
 }
 
 // Rows too long for registers: dX by rows ...
@@ -400,23 +514,25 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs a, int col_b
     a.ws[(int64_t)(a.blocks + blk) * a.N + c] = db;
 }
 
-// dw and db from the blocks' partials: 64 columns x 4 ranges of blocks
+// dw and db from the blocks' partials: 64 columns x 16 ranges of blocks
 template <class T>
-__global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a, int col_blocks) {
-    __shared__ float part[4][64];
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int col_blocks) {
+    __shared__ float part[16][64];
     const int which = blockIdx.x / col_blocks;
     char *dst = which ? a.db : a.dw;
     if (!dst) return;  // whole blocks
     const int t = threadIdx.x & 63, s = threadIdx.x >> 6, c = (blockIdx.x % col_blocks) * 64 + t;
-    const int per = (a.blocks + 3) / 4, to = (s + 1) * per < a.blocks ? (s + 1) * per : a.blocks;
+    const int per = (a.blocks + 15) / 16, to = (s + 1) * per < a.blocks ? (s + 1) * per : a.blocks;
     float v = 0.0f;
     if (c < a.N)
 #pragma unroll 8
         for (int b = s * per; b < to; ++b) v += a.ws[((int64_t)which * a.blocks + b) * a.N + c];
     part[s][t] = v;
     __syncthreads();
-    if (s == 0 && c < a.N)
-        reinterpret_cast<T *>(dst)[c] = from_f32<T>(((part[0][t] + part[1][t]) + part[2][t]) + part[3][t]);
+    if (s > 0 || c >= a.N) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += part[i][t];
+    reinterpret_cast<T *>(dst)[c] = from_f32<T>(v);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -451,7 +567,7 @@ hipError_t grad(const GradArgs &a, hipStream_t s) {
         else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, 1>), grid, dim3(256), 0, s, a, cols);
     }
     if (a.db) {
-        const int cb = (a.N + 255) / 256;
+        const int cb = (a.N + 63) / 64;
         hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), dim3((unsigned)(a.groups * cb)), dim3(256), 0, s, a, cb);
     }
     return hipGetLastError();
@@ -472,7 +588,8 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
     CPO_NORM(256, 1)
     CPO_NORM(256, 2)
     CPO_NORM(256, 4)
-    CPO_NORM(1024, 2)
+    CPO_NORM(512, 3)
+    CPO_NORM(512, 4)
     CPO_NORM(1024, 4)
 #undef CPO_NORM
     hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_long_kernel<T>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
@@ -481,20 +598,27 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
 
 template <class T, bool VEC>
 hipError_t norm_backward(const NormArgs &a, hipStream_t s) {
-    constexpr int CE = kUnit<T>;
-#define CPO_NORM(THREADS, VPT)                                                                                        \
-    if (a.N <= THREADS * VPT * CE) {                                                                                  \
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_kernel<T, THREADS, VPT, VEC>), dim3((unsigned)a.blocks),     \
-                           dim3(THREADS), 0, s, a);                                                                   \
-        return hipGetLastError();                                                                                     \
+    // Threads of a row, rows at a time per block, units per thread: one block
+    // per CU leaves the fewest partials, and the rows at a time make up the
+    // waves that keep memory busy, as far as the registers go.
+#define CPO_LAUNCH(THREADS, SUBS, VPT)                                                                              \
+    if (a.N <= THREADS * VPT * kUnit<T>) {                                                                          \
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_kernel<T, THREADS, SUBS, VPT, VEC>), dim3((unsigned)a.blocks), \
+                           dim3(THREADS * SUBS), 0, s, a);                                                          \
+        return hipGetLastError();                                                                                   \
     }
-    CPO_NORM(64, 1)
-    CPO_NORM(128, 1)
-    CPO_NORM(256, 1)
-    CPO_NORM(256, 2)
-    CPO_NORM(256, 4)
-    CPO_NORM(1024, 2)
-#undef CPO_NORM
+    CPO_LAUNCH(64, 16, 1)
+    CPO_LAUNCH(128, 8, 1)
+    CPO_LAUNCH(256, 4, 1)
+    if constexpr (VEC || sizeof(T) == 4) {
+        CPO_LAUNCH(256, 4, 2)
+        CPO_LAUNCH(512, 2, 2)
+        CPO_LAUNCH(1024, 1, 2)
+    } else {  // single bf16 elements take a register each
+        CPO_LAUNCH(512, 2, 1)
+        CPO_LAUNCH(1024, 1, 1)
+    }
+#undef CPO_LAUNCH
     const int cb = (a.N + 255) / 256;
     if (a.dw || a.db)
         hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_columns_kernel<T>), dim3((unsigned)(a.blocks * cb)), dim3(256), 0, s, a, cb);
@@ -511,7 +635,7 @@ hipError_t norm_backward_all(const NormArgs &a, hipStream_t s) {
     }
     if (a.dw || a.db) {
         const int cb = (a.N + 63) / 64;
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_join_kernel<T>), dim3((unsigned)(2 * cb)), dim3(256), 0, s, a, cb);
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_join_kernel<T>), dim3((unsigned)(2 * cb)), dim3(1024), 0, s, a, cb);
     }
     return hipGetLastError();
 }
@@ -535,7 +659,7 @@ hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s) {
     return a.vec ? norm<float, true>(a, s) : norm<float, false>(a, s);
 }
 
-int norm_backward_blocks(int, int64_t M, int64_t) { return (int)(M < 512 ? M : 512); }
+int norm_backward_blocks(int64_t M) { return (int)(M < 256 ? M : 256); }
 
 hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s) {
     return dtype == CP_BF16 ? norm_backward_all<__bf16>(a, s) : norm_backward_all<float>(a, s);

@@ -120,10 +120,8 @@ def _weight(w, name):
                      f"(strides {w.stride()}); call .contiguous()")
 
 
-def _vector(b, x, shape, name):
-    if b is None:
-        return None
-    _like(b, x, shape, name)
+def _vector(b, x, shape, name, dtype=None):
+    _like(b, x, shape, name, dtype)
     if not b.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return b.data_ptr()
@@ -137,44 +135,23 @@ def _empty_weight(w, wt):
     return torch.empty(shape, dtype=w.dtype, device=w.device).transpose(-1, -2)
 
 
-def _aligned(code, *mats):
-    """Whether all (pointer, rows, row length, row stride, outer stride) are whole 16-byte units."""
-    bits = 0
-    for p, rows, length, ld, outer in mats:
-        bits |= p | ((length | outer | (ld if rows > 1 else 0)) << (1 if code == nat.CP_BF16 else 2))
-    return bits % 16 == 0
+def _elsewhere(x):
+    """Whether the tensor's device is not the current one."""
+    return x.get_device() != torch.cuda.current_device()
 
 
-def _scratch(op, code, M, K, N, E, x, aligned=True):
-    n = workspace_bytes(op, code, M, K, N, E, aligned)
-    return (torch.empty(n, dtype=torch.uint8, device=x.device) if n else None), n
-
-
-class _on:
-    """The tensor's device made current, if it is not already."""
-
-    def __init__(self, x):
-        i = x.device.index
-        self.guard = torch.cuda.device(i) if i != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.guard.__exit__(*exc)
+# The current stream's handle without a stream object around it: the calls below
+# cost a few microseconds each, and the object alone takes three.
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _output(out, x, shape, name="out"):
-    if out is None:
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
-    return _like(out, x, shape, name)
+def _scratch(op, code, M, K, N, E, x, aligned):
+    n = workspace_bytes(op, code, M, K, N, E, aligned)
+    return (torch.empty(n, dtype=torch.uint8, device=x.device) if n else None), n
 
 
 def linear(x, w, bias=None, residual=None, act=ACT_NONE, need_pre=False, out=None):
@@ -182,22 +159,25 @@ def linear(x, w, bias=None, residual=None, act=ACT_NONE, need_pre=False, out=Non
     With need_pre returns (y, x w + bias), the second for linear_backward.  `out`
     may be the residual itself."""
     code = _first(x, 2, "x")
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return linear(x, w, bias, residual, act, need_pre, out)
     M, K = x.shape
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a matrix")
     N = w.shape[1]
     _like(w, x, (K, N), "w")
     ldw, wt = _weight(w, "w")
-    b = _vector(bias, x, (N,), "bias")
+    b = None if bias is None else _vector(bias, x, (N,), "bias")
     ldr = 0 if residual is None else _rows(_like(residual, x, (M, N), "residual"), "residual")
-    with _on(x) as stream:
-        y = _output(out, x, (M, N))
-        pre = torch.empty((M, N), dtype=x.dtype, device=x.device) if need_pre else None
-        xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
-        ws, n = _scratch(OP_LINEAR, code, M, K, N, 0, x,
-                         _aligned(code, (xp, M, K, ldx, 0), (wp, N if wt else K, K if wt else N, ldw, 0)))
-        _check(_linear(code, M, K, N, xp, ldx, wp, ldw, wt, b, _ptr(residual), ldr, act,
-                       y.data_ptr(), _rows(y, "out"), _ptr(pre), N, _ptr(ws), n, stream), "cp_linear")
+    y = x.new_empty((M, N)) if out is None else _like(out, x, (M, N), "out")
+    pre = torch.empty_like(y, memory_format=torch.contiguous_format) if need_pre else None
+    xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
+    es = x.element_size()
+    ws, n = _scratch(OP_LINEAR, code, M, K, N, 0, x, not ((xp | wp | (ldx | K | ldw | N) * es) & 15))
+    _check(_linear(code, M, K, N, xp, ldx, wp, ldw, wt, b, _ptr(residual), ldr, act, y.data_ptr(),
+                   N if out is None else _rows(y, "out"), _ptr(pre), N, _ptr(ws), n, _stream(x.get_device())),
+           "cp_linear")
     return (y, pre) if need_pre else y
 
 
@@ -206,6 +186,9 @@ def linear_backward(dy, x, w, pre=None, act=ACT_NONE, need_x=True, need_w=True, 
     for.  `pre` is what linear returned with need_pre (not needed without an
     activation).  The residual's gradient is dy."""
     code = _first(dy, 2, "dy")
+    if _elsewhere(dy):
+        with torch.cuda.device(dy.device):
+            return linear_backward(dy, x, w, pre, act, need_x, need_w, need_bias)
     M, N = dy.shape
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a matrix")
@@ -214,16 +197,14 @@ def linear_backward(dy, x, w, pre=None, act=ACT_NONE, need_x=True, need_w=True, 
     _like(x, dy, (M, K), "x")
     ldw, wt = _weight(w, "w")
     ldp = _backward_pre(pre, dy, act)
-    with _on(dy) as stream:
-        dx = torch.empty((M, K), dtype=dy.dtype, device=dy.device) if need_x else None
-        dw = _empty_weight(w, wt) if need_w else None
-        db = torch.empty(N, dtype=dy.dtype, device=dy.device) if need_bias else None
-        dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
-        ws, n = _scratch(OP_LINEAR_BACKWARD, code, M, K, N, 0, dy,
-                         _aligned(code, (dp, M, N, ldd, 0), (xp, M, K, ldx, 0),
-                                  (wp, N if wt else K, K if wt else N, ldw, 0)))
-        _check(_linear_backward(code, M, K, N, dp, ldd, xp, ldx, wp, ldw, wt, _ptr(pre), ldp, act, _ptr(dx), K, _ptr(dw), K if wt else N, _ptr(db), _ptr(ws),
-                                n, stream), "cp_linear_backward")
+    dx = dy.new_empty((M, K)) if need_x else None
+    dw = _empty_weight(w, wt) if need_w else None
+    db = dy.new_empty(N) if need_bias else None
+    dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
+    ws, n = _scratch(OP_LINEAR_BACKWARD, code, M, K, N, 0, dy,
+                     not ((dp | xp | wp | (ldd | ldx | ldw | K | N) * dy.element_size()) & 15))
+    _check(_linear_backward(code, M, K, N, dp, ldd, xp, ldx, wp, ldw, wt, _ptr(pre), ldp, act, _ptr(dx), K, _ptr(dw),
+                            K if wt else N, _ptr(db), _ptr(ws), n, _stream(dy.get_device())), "cp_linear_backward")
     return dx, dw, db
 
 
@@ -250,21 +231,23 @@ def grouped_linear(x, w, offsets, bias=None, act=ACT_NONE, need_pre=False, out=N
     bias [E][N]; expert e has rows offsets[e] .. offsets[e + 1] - 1 (int32, on
     the device, never read by the host).  Rows from offsets[E] on give zeros."""
     code = _first(x, 2, "x")
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return grouped_linear(x, w, offsets, bias, act, need_pre, out)
     E, sw = _experts(w, x, offsets)
     T, K = x.shape
     N = w.shape[2]
     _like(w, x, (E, K, N), "w")
     ldw, wt = _weight(w, "w")
-    b = _vector(bias, x, (E, N), "bias")
-    with _on(x) as stream:
-        y = _output(out, x, (T, N))
-        pre = torch.empty((T, N), dtype=x.dtype, device=x.device) if need_pre else None
-        xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
-        ws, n = _scratch(OP_GROUPED_LINEAR, code, T, K, N, E, x,
-                         _aligned(code, (xp, T, K, ldx, 0), (wp, N if wt else K, K if wt else N, ldw, sw if E > 1 else 0)))
-        _check(_grouped_linear(code, T, K, N, E, xp, ldx, wp, ldw, sw, wt,
-                               offsets.data_ptr(), b, act, y.data_ptr(), _rows(y, "out"), _ptr(pre), N, _ptr(ws), n,
-                               stream), "cp_grouped_linear")
+    b = None if bias is None else _vector(bias, x, (E, N), "bias")
+    y = x.new_empty((T, N)) if out is None else _like(out, x, (T, N), "out")
+    pre = torch.empty_like(y, memory_format=torch.contiguous_format) if need_pre else None
+    xp, wp, ldx = x.data_ptr(), w.data_ptr(), _rows(x, "x")
+    ws, n = _scratch(OP_GROUPED_LINEAR, code, T, K, N, E, x,
+                     not ((xp | wp | (ldx | K | ldw | N | sw) * x.element_size()) & 15))
+    _check(_grouped_linear(code, T, K, N, E, xp, ldx, wp, ldw, sw, wt, offsets.data_ptr(), b, act, y.data_ptr(),
+                           N if out is None else _rows(y, "out"), _ptr(pre), N, _ptr(ws), n, _stream(x.get_device())),
+           "cp_grouped_linear")
     return (y, pre) if need_pre else y
 
 
@@ -272,6 +255,9 @@ def grouped_linear_backward(dy, x, w, offsets, pre=None, act=ACT_NONE, need_x=Tr
     """Gradients (dx, dw, db) of grouped_linear for dy [T][N]; zeros for experts
     without rows and for rows without an expert."""
     code = _first(dy, 2, "dy")
+    if _elsewhere(dy):
+        with torch.cuda.device(dy.device):
+            return grouped_linear_backward(dy, x, w, offsets, pre, act, need_x, need_w, need_bias)
     E, sw = _experts(w, dy, offsets)
     T, N = dy.shape
     K = w.shape[1]
@@ -279,17 +265,15 @@ def grouped_linear_backward(dy, x, w, offsets, pre=None, act=ACT_NONE, need_x=Tr
     _like(x, dy, (T, K), "x")
     ldw, wt = _weight(w, "w")
     ldp = _backward_pre(pre, dy, act)
-    with _on(dy) as stream:
-        dx = torch.empty((T, K), dtype=dy.dtype, device=dy.device) if need_x else None
-        dw = _empty_weight(w, wt) if need_w else None
-        db = torch.empty((E, N), dtype=dy.dtype, device=dy.device) if need_bias else None
-        dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
-        ws, n = _scratch(OP_GROUPED_LINEAR_BACKWARD, code, T, K, N, E, dy,
-                         _aligned(code, (dp, T, N, ldd, 0), (xp, T, K, ldx, 0),
-                                  (wp, N if wt else K, K if wt else N, ldw, sw if E > 1 else 0)))
-        _check(_grouped_linear_backward(code, T, K, N, E, dp, ldd, xp, ldx, wp, ldw, sw, wt, offsets.data_ptr(), _ptr(pre), ldp, act, _ptr(dx), K,
-                                        _ptr(dw), K if wt else N, K * N, _ptr(db), _ptr(ws), n, stream),
-               "cp_grouped_linear_backward")
+    dx = dy.new_empty((T, K)) if need_x else None
+    dw = _empty_weight(w, wt) if need_w else None
+    db = dy.new_empty((E, N)) if need_bias else None
+    dp, xp, wp, ldd, ldx = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _rows(dy, "dy"), _rows(x, "x")
+    ws, n = _scratch(OP_GROUPED_LINEAR_BACKWARD, code, T, K, N, E, dy,
+                     not ((dp | xp | wp | (ldd | ldx | ldw | K | N | sw) * dy.element_size()) & 15))
+    _check(_grouped_linear_backward(code, T, K, N, E, dp, ldd, xp, ldx, wp, ldw, sw, wt, offsets.data_ptr(), _ptr(pre),
+                                    ldp, act, _ptr(dx), K, _ptr(dw), K if wt else N, K * N, _ptr(db), _ptr(ws), n,
+                                    _stream(dy.get_device())), "cp_grouped_linear_backward")
     return dx, dw, db
 
 
@@ -297,32 +281,36 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     """(y, mean, rstd) with y = (x - mean) rstd weight + bias over the rows of
     x [M][N]; mean and rstd are float32 [M].  `out` may be x."""
     code = _first(x, 2, "x")
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return layer_norm(x, weight, bias, eps, out)
     M, N = x.shape
-    w, b = _vector(weight, x, (N,), "weight"), _vector(bias, x, (N,), "bias")
-    with _on(x) as stream:
-        y = _output(out, x, (M, N))
-        stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
-        _check(_layer_norm(code, M, N, x.data_ptr(), _rows(x, "x"), w, b, eps, y.data_ptr(), _rows(y, "out"),
-                           stats.data_ptr(), stats.data_ptr() + 4 * M, stream), "cp_layer_norm")
-    return y, stats[0], stats[1]
+    w = None if weight is None else _vector(weight, x, (N,), "weight")
+    b = None if bias is None else _vector(bias, x, (N,), "bias")
+    y = x.new_empty((M, N)) if out is None else _like(out, x, (M, N), "out")
+    mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device).unbind()
+    _check(_layer_norm(code, M, N, x.data_ptr(), _rows(x, "x"), w, b, eps, y.data_ptr(),
+                       N if out is None else _rows(y, "out"), mean.data_ptr(), rstd.data_ptr(),
+                       _stream(x.get_device())), "cp_layer_norm")
+    return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, need_x=True, need_weight=True, need_bias=True):
     """Gradients (dx, dweight, dbias) of layer_norm for dy [M][N], from the mean
     and rstd it returned; None for those not asked for."""
     code = _first(dy, 2, "dy")
+    if _elsewhere(dy):
+        with torch.cuda.device(dy.device):
+            return layer_norm_backward(dy, x, mean, rstd, weight, need_x, need_weight, need_bias)
     M, N = dy.shape
     _like(x, dy, (M, N), "x")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if not _like(t, dy, (M,), name, torch.float32).is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    w = _vector(weight, dy, (N,), "weight")
-    with _on(dy) as stream:
-        dx = torch.empty((M, N), dtype=dy.dtype, device=dy.device) if need_x else None
-        dw = torch.empty(N, dtype=dy.dtype, device=dy.device) if need_weight else None
-        db = torch.empty(N, dtype=dy.dtype, device=dy.device) if need_bias else None
-        ws, n = _scratch(OP_LAYER_NORM_BACKWARD, code, M, 0, N, 0, dy)
-        _check(_layer_norm_backward(code, M, N, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"),
-                                    mean.data_ptr(), rstd.data_ptr(), w, _ptr(dx), N, _ptr(dw), _ptr(db), _ptr(ws), n,
-                                    stream), "cp_layer_norm_backward")
+    m, r = _vector(mean, dy, (M,), "mean", torch.float32), _vector(rstd, dy, (M,), "rstd", torch.float32)
+    w = None if weight is None else _vector(weight, dy, (N,), "weight")
+    dx = dy.new_empty((M, N)) if need_x else None
+    dw = dy.new_empty(N) if need_weight else None
+    db = dy.new_empty(N) if need_bias else None
+    ws, n = _scratch(OP_LAYER_NORM_BACKWARD, code, M, 0, N, 0, dy, True)
+    _check(_layer_norm_backward(code, M, N, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"), m, r, w,
+                                _ptr(dx), N, _ptr(dw), _ptr(db), _ptr(ws), n, _stream(dy.get_device())),
+           "cp_layer_norm_backward")
     return dx, dw, db
