@@ -131,9 +131,10 @@ bool few_rows(const Shape &s) {
 // 204, 91, 115 us; 128x256 238, 62, 134; 128x128 (two on a CU) 257, 62, 129.
 // A split writes and reads its partials and takes another launch.
 Choice choose(const Shape &s) {
-    // One launch and nothing but the weight's bytes to move, but its vector
-    // arithmetic grows with the rows.
-    if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows) return {kGemv, 1};
+    // (both sides measured: cp_ops_gemv.hip)
+    if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows &&
+        (s.layout == kNT || s.K * s.N * elem_size(s.dtype) <= kGemvColumnBytes))
+        return {kGemv, 1};
     if (few_rows(s)) {
         const int64_t tiles = max_row_tiles(s, 16) * ceil_div(s.N, 128);
         int64_t n = 2 * kComputeUnits / (tiles ? tiles : 1);

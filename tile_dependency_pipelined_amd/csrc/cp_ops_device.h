@@ -171,30 +171,58 @@ struct Raw {
     }
 };
 
-template <class T, int CNT>
-__device__ __forceinline__ void finish(const GemmArgs &g, char *C, int row, int col, float (&v)[CNT],
-                                       const Raw<T, CNT> *bias, const Raw<T, CNT> *res, bool zero) {
-    static_assert(CNT == 1 || CNT == kUnit<T>, "columns per call");
-    auto put = [](char *p, const float(&x)[CNT]) {
-        if constexpr (CNT > 1) store_unit<T>(p, x);
-        else *reinterpret_cast<T *>(p) = from_f32<T>(x[0]);
+// NU runs at once, at rows row, row + step, ..: what the call asks for is
+// branched on once for all of them.  Run i is stored if `inside` (uniform) or
+// if the column is in range and its row is below row_end.
+template <class T, int CNT, int NU>
+__device__ __forceinline__ void finish(const GemmArgs &g, char *C, int row, int step, int col, float (&v)[NU][CNT],
+                                       const Raw<T, CNT> *bias, const Raw<T, CNT> *res, bool zero, bool inside,
+                                       bool col_in, int row_end) {
+    static_assert(CNT == 1 || CNT == kUnit<T>, "columns per run");
+    auto put = [&](char *base, int64_t ld) {
+        char *p = base + ((int64_t)row * ld + col) * sizeof(T);
+        auto one = [&](int i) {
+            char *q = p + (int64_t)i * step * ld * sizeof(T);
+            if constexpr (CNT > 1) store_unit<T>(q, v[i]);
+            else *reinterpret_cast<T *>(q) = from_f32<T>(v[i][0]);
+        };
+        if (inside) {
+#pragma unroll
+            for (int i = 0; i < NU; ++i) one(i);
+        } else if (col_in) {
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+                if (row + i * step < row_end) one(i);
+        }
     };
-    float t[CNT];
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[i][j] = f(v[i][j]);
+    };
     if (bias) {
+        float t[CNT];
         bias->unpack(t);
 #pragma unroll
-        for (int i = 0; i < CNT; ++i) v[i] = zero ? 0.0f : v[i] + t[i];
-    }
-    if (g.pre) put(g.pre + ((int64_t)row * g.ldp + col) * sizeof(T), v);
-    if (g.act != CP_ACT_NONE)
+        for (int i = 0; i < NU; ++i)
 #pragma unroll
-        for (int i = 0; i < CNT; ++i) v[i] = act_apply(v[i], g.act);
+            for (int j = 0; j < CNT; ++j) v[i][j] = zero ? 0.0f : v[i][j] + t[j];
+    }
+    if (g.pre) put(g.pre, g.ldp);
+    if (g.act == CP_ACT_GELU_TANH) each([](float x) { return act_apply(x, CP_ACT_GELU_TANH); });
+    else if (g.act == CP_ACT_SILU) each([](float x) { return act_apply(x, CP_ACT_SILU); });
+    else if (g.act == CP_ACT_RELU) each([](float x) { return act_apply(x, CP_ACT_RELU); });
     if (res) {
-        res->unpack(t);
 #pragma unroll
-        for (int i = 0; i < CNT; ++i) v[i] += t[i];
+        for (int i = 0; i < NU; ++i) {
+            float t[CNT];
+            res[i].unpack(t);
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[i][j] += t[j];
+        }
     }
-    put(C + ((int64_t)row * g.ldc + col) * sizeof(T), v);
+    put(C, g.ldc);
 }
 
 // ------------------------------------------------------------- expert spans

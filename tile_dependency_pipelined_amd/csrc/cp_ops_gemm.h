@@ -475,9 +475,10 @@ struct Product {
         constexpr int STEP = RUNS < 64 ? 64 / RUNS : 1;       // rows between a lane's runs
         constexpr int COLS = RUNS < 64 ? 1 : RUNS / 64;       // runs of a row per lane
         constexpr int NU = 16 / STEP;
-        constexpr int AHEAD = FM < (CNT > 1 ? 4 : 1) ? FM : (CNT > 1 ? 4 : 1);
+        constexpr int AHEAD = FM < (CNT > 1 ? 4 : 2) ? FM : (CNT > 1 ? 4 : 2);
         const int l0 = RUNS < 64 ? lane / RUNS : 0, r0 = wrow + l0;
         const int cl = (RUNS < 64 ? lane % RUNS : lane) * CNT;
+        const bool inside = wrow + WM <= row_end && wcol + WN <= g.N;  // uniform
 #pragma unroll
         for (int h = 0; h < COLS; ++h) {
             const int c = wcol + cl + h * 64 * CNT;
@@ -485,32 +486,35 @@ struct Product {
             Raw<T, CNT> rb, rr[AHEAD][NU];
             if (bias && col_in) rb.load(bias + (int64_t)c * sizeof(T));
             auto request = [&](int fm) {
-                if (g.res)
+                if (!g.res) return;
+                const char *p = g.res + ((int64_t)(r0 + fm * 16) * g.ldr + c) * sizeof(T);
+                if (inside) {
 #pragma unroll
-                    for (int i = 0; i < NU; ++i) {
-                        const int r = r0 + fm * 16 + i * STEP;
-                        if (col_in && r < row_end)
-                            rr[fm % AHEAD][i].load(g.res + ((int64_t)r * g.ldr + c) * sizeof(T));
-                    }
+                    for (int i = 0; i < NU; ++i) rr[fm % AHEAD][i].load(p + (int64_t)i * STEP * g.ldr * sizeof(T));
+                } else if (col_in) {
+#pragma unroll
+                    for (int i = 0; i < NU; ++i)
+                        if (r0 + fm * 16 + i * STEP < row_end)
+                            rr[fm % AHEAD][i].load(p + (int64_t)i * STEP * g.ldr * sizeof(T));
+                }
             };
 #pragma unroll
             for (int fm = 0; fm < AHEAD; ++fm) request(fm);
             stage_rows(acc, lds, wave, lane, [&](int fm, const float *sh) {
+                alignas(16) float v[NU][CNT];
 #pragma unroll
                 for (int i = 0; i < NU; ++i) {
-                    const int r = r0 + fm * 16 + i * STEP;
                     const float *p = sh + (i * STEP + l0) * EPI_PITCH + cl + h * 64 * CNT;
-                    alignas(16) float v[CNT];
                     if constexpr (CNT > 1) {
 #pragma unroll
                         for (int e = 0; e < CNT; e += 4)
-                            *reinterpret_cast<f32x4_t *>(v + e) = *reinterpret_cast<const f32x4_t *>(p + e);
+                            *reinterpret_cast<f32x4_t *>(v[i] + e) = *reinterpret_cast<const f32x4_t *>(p + e);
                     } else {
-                        v[0] = *p;
+                        v[i][0] = *p;
                     }
-                    if (col_in && r < row_end)
-                        finish<T, CNT>(g, C, r, c, v, bias ? &rb : nullptr, g.res ? &rr[fm % AHEAD][i] : nullptr, zero);
                 }
+                finish<T, CNT, NU>(g, C, r0 + fm * 16, STEP, c, v, bias ? &rb : nullptr,
+                                   g.res ? rr[fm % AHEAD] : nullptr, zero, inside, col_in, row_end);
                 if (fm + AHEAD < FM) request(fm + AHEAD);
             });
         }

@@ -1,7 +1,9 @@
-// cp_ops_gemv.hip -- products with at most four rows (a decode step), bound by
+// cp_ops_gemv.hip -- products of one or two rows (a decode step), bound by
 // reading the weight once: no LDS tiles and no matrix instructions, every lane
 // loads 16 bytes of the weight at a time, many loads in flight, and multiplies
-// them with the few rows in fp32.  One launch, no partial results in memory.
+// them with the rows in fp32.  One launch and no partial results in memory,
+// where the 16-row tiles split the contraction and take a second launch to add
+// it up.
 #include "cp_ops_host.h"
 
 namespace cpo {
@@ -34,16 +36,19 @@ __device__ __forceinline__ void unpack(uint4 u, float (&v)[kUnit<T>]) {
 template <class T>
 __device__ __forceinline__ void finish_one(const GemmArgs &g, int row, int col, float sum) {
     Raw<T, 1> b, r;
-    float v[1] = {sum};
+    float v[1][1] = {{sum}};
     if (g.bias) b.load(g.bias + (int64_t)col * sizeof(T));
     if (g.res) r.load(g.res + ((int64_t)row * g.ldr + col) * sizeof(T));
-    finish<T, 1>(g, g.C, row, col, v, g.bias ? &b : nullptr, g.res ? &r : nullptr, false);
+    finish<T, 1, 1>(g, g.C, row, 0, col, v, g.bias ? &b : nullptr, g.res ? &r : nullptr, false, true, true, 0);
 }
 
 // Weight stored [K][N].  A block takes L lanes x 16 bytes of columns and all of
 // K: its 16 waves take 64 / L rows each in turn, so nothing has to be summed
 // across blocks.  The columns per block are few enough for the blocks to fill
-// the device; blocks next to each other share cache lines and an XCD.
+// the device; blocks next to each other share cache lines and an XCD.  Reading
+// 32 or 64 bytes of a row at a time costs bandwidth, so this pays while the
+// launch saved counts: bf16 1 x 4096 x 4096 11.4 us (16-row tiles 15.5), 1 x
+// 8192 x 8192 33.9 (31.5), 1 x 28672 x 8192 128 (90).
 template <class T, int MR, int L>
 __global__ __launch_bounds__(1024) void gemv_columns_kernel(GemmArgs g) {
     constexpr int CE = kUnit<T>, W = 16, RPI = 64 / L, U = MR == 1 ? 8 : 4, O = MR * L * CE;
@@ -110,7 +115,9 @@ __global__ __launch_bounds__(1024) void gemv_columns_kernel(GemmArgs g) {
 }
 
 // Weight stored [N][K]: `per` waves (1 or 4) to an output column, 64 lanes x 16
-// bytes along K.
+// bytes along K.  bf16 1 x 4096 x 4096 9.4 us, 1 x 8192 x 8192 27.0 (5.0 TB/s);
+// with four rows 45 us there, as the rows are read again for every column,
+// where the 16-row tiles take 28.
 template <class T, int MR>
 __global__ __launch_bounds__(256) void gemv_rows_kernel(GemmArgs g, int per) {
     constexpr int CE = kUnit<T>, U = 4;
@@ -199,9 +206,7 @@ hipError_t gemv(bool w_rows, const GemmArgs &g, hipStream_t s) {
 
 template <class T>
 hipError_t gemv_rows(bool w_rows, const GemmArgs &g, hipStream_t s) {
-    if (g.M == 1) return gemv<T, 1>(w_rows, g, s);
-    if (g.M == 2) return gemv<T, 2>(w_rows, g, s);
-    return gemv<T, 4>(w_rows, g, s);
+    return g.M == 1 ? gemv<T, 1>(w_rows, g, s) : gemv<T, 2>(w_rows, g, s);
 }
 
 }  // namespace

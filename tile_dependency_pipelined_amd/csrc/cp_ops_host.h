@@ -9,7 +9,8 @@ namespace cpo {
 // Which index of the operands is contiguous (see cp_ops_gemm.h).
 enum Layout : int { kNN = 0, kNT = 1, kTN = 2 };  // A and B: KC/outer, KC/KC, outer/outer
 
-constexpr int kGemvRows = 4;
+constexpr int kGemvRows = 2;
+constexpr int64_t kGemvColumnBytes = 64 << 20;  // weights stored [K][N] up to this size
 
 // Tile configurations of the products; kGemv: no tiles, at most kGemvRows rows.
 enum Config : int { kTile256 = 0, kTile128x256 = 1, kTile128 = 2, kTile16 = 3, kGemv = 4, kConfigs = 5 };

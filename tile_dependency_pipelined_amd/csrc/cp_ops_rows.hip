@@ -47,20 +47,20 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
         if (!zero) bias += (int64_t)e * g.N * sizeof(T);
     }
     if (col >= g.N) return;
-    float v[CNT];
+    float v[1][CNT];
 #pragma unroll
-    for (int i = 0; i < CNT; ++i) v[i] = 0.0f;
+    for (int i = 0; i < CNT; ++i) v[0][i] = 0.0f;
     const float *p = g.ws + (int64_t)row * g.ldws + col;
     const int64_t step = (int64_t)g.M * g.ldws;
 #pragma unroll 4
     for (int s = 0; s < g.nsplit; ++s) {
 #pragma unroll
-        for (int i = 0; i < CNT; ++i) v[i] += p[s * step + i];
+        for (int i = 0; i < CNT; ++i) v[0][i] += p[s * step + i];
     }
     Raw<T, CNT> b, r;
     if (bias) b.load(bias + (int64_t)col * sizeof(T));
     if (g.res) r.load(g.res + ((int64_t)row * g.ldr + col) * sizeof(T));
-    finish<T, CNT>(g, g.C, row, col, v, bias ? &b : nullptr, g.res ? &r : nullptr, zero);
+    finish<T, CNT, 1>(g, g.C, row, 0, col, v, bias ? &b : nullptr, g.res ? &r : nullptr, zero, true, true, 0);
 }
 
 // --------------------------------------------- activation gradient, bias sums
