@@ -124,12 +124,35 @@ bool few_rows(const Shape &s) {
     return s.layout != kTN && (s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M) <= 16;
 }
 
-// Time of a product in microseconds for each configuration that fits, from the
-// rounds of tiles the device takes and, per tile, a time per slab and one for
-// prologue and epilogue.  Measured on 2048 x 8192 x 8192, 2048 x 4096 x 4096
-// and 8192 x 4096 x 2048 (rows x columns x contraction), bf16: 256x256 tiles
-// 204, 91, 115 us; 128x256 238, 62, 134; 128x128 (two on a CU) 257, 62, 129.
-// A split writes and reads its partials and takes another launch.
+// Time in microseconds of one launch of `tiles` tiles with `slabs` slabs each,
+// from the rounds the device takes: a time per slab, which grows with the share
+// of the CUs that are busy (they share memory and power), and a fixed time.
+// Fitted to bf16 products with the weights coming from memory (rows x columns x
+// contraction, microseconds for 256x256 | 128x256 | 128x128 | 64x128 | 64x64 tiles):
+//   512 x 2048 x 1024            | 14 | 9.4 | 7.5
+//   256 x 4096 x 4096    83 | 51 | 42 | 24 | 17
+//   512 x 4096 x 4096    83 | 50 | 42 | 25 | 28
+//   1024 x 4096 x 4096   83 | 50 | 44     1024 x 8192 x 8192 176 | 118 | 137
+//   2048 x 4096 x 4096   84 | 62 | 63     2048 x 8192 x 8192 213 | 248 | 268
+//   4096 x 4096 x 4096  107 | 125 | 137   8192 x 4096 x 2048 114 | 130 | 130
+// and to fp32: 512 x 2048 x 1024 64 us with 128x128, 36 with 64x128, 23 with 64x64.
+double launch_time(Config c, int dtype, double tiles, double slabs) {
+    const double cus = tiles / kComputeUnits;  // tiles per CU
+    const double busy = cus < 1.0 ? cus : 1.0;
+    const double rounds = (double)(int64_t)(cus + 0.999);
+    if (dtype == CP_F32)  // matrix-bound: several tiles on a CU take as many times as long
+        return rounds * (c == kTile128 ? 1.9 : c == kTile64x128 ? 0.95 : 0.49) * slabs + 6.0;
+    if (c == kTile256) return rounds * ((1.12 + 0.43 * busy) * slabs + 10.0);
+    if (c == kTile128x256) return rounds * ((0.66 + 0.21 * busy) * slabs + 7.0);
+    // two on a CU; a CU that is left with one runs it faster
+    const double one = c == kTile128 ? 0.58 : c == kTile64x128 ? 0.31 : 0.19;
+    const double two = c == kTile128 ? 0.97 : c == kTile64x128 ? 0.57 : 0.37;
+    const double full = (double)(int64_t)(cus / 2.0), rest = cus - 2.0 * full;
+    double t = full * (two * slabs + 4.0);
+    if (rest > 0.0) t += (one + (rest > 1.0 ? (two - one) * (rest - 1.0) : 0.0)) * slabs + 5.0;
+    return t;
+}
+
 Choice choose(const Shape &s) {
     // (both sides measured: cp_ops_gemv.hip)
     if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows &&
@@ -142,37 +165,29 @@ Choice choose(const Shape &s) {
         if (n > 32) n = 32;
         return {kTile16, n < 1 ? 1 : (int)n};
     }
-    struct Rate {
-        Config cfg;
-        double slab, fixed;
-    };
-    static const Rate bf16[] = {{kTile256, 1.5, 10.0}, {kTile128x256, 0.90, 6.0}, {kTile128, 0.98, 6.0}};
-    static const Rate f32[] = {{kTile128, 3.6, 6.0}};
-    const Rate *rates = s.dtype == CP_BF16 ? bf16 : f32;
-    const int nrates = s.dtype == CP_BF16 ? 3 : 1;
-    const double slabs = (double)slabs_of(s);
+    const Config all[] = {kTile256, kTile128x256, kTile128, kTile64x128, kTile64};
+    const int64_t slabs = slabs_of(s);
     Choice best{kTile128, 1};
     double least = 1e300;
-    for (int i = 0; i < nrates; ++i) {
-        const ConfigShape t = kShapes[rates[i].cfg];
+    for (const Config c : all) {
+        if (s.dtype == CP_F32 && c < kTile128) continue;
+        const ConfigShape t = kShapes[c];
         // row tiles of an average launch: each expert's last one is half empty
         const double tm = s.mode == kGroupRows ? (double)s.M / t.bm + 0.5 * s.groups : (double)ceil_div(s.M, t.bm);
         const double tiles = tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && (s.mode != kDense || slabs < 4 * n)) break;
-            double rounds;
-            if (rates[i].cfg == kTile128) {
-                // two on a CU; what is left after full rounds runs alone on its CU, and faster
-                const double all = tiles * n / (2 * kComputeUnits), full = (double)(int64_t)all;
-                rounds = full + (all == full ? 0.0 : all - full <= 0.5 ? 0.6 : 1.0);
-            } else {
-                rounds = (double)(int64_t)(tiles * n / kComputeUnits + 0.999);
-            }
-            double t_us = rounds * (rates[i].slab * (double)ceil_div((int64_t)slabs, n) + rates[i].fixed);
-            if (n > 1) t_us += 4.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 4e6;
-            if (t_us < least) {
-                least = t_us;
-                best = {rates[i].cfg, n};
+            double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n));
+            // Each expert's weights are read by few tiles: the smaller the
+            // tile, the more of them wait for the same memory (8192 x 4096 x
+            // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
+            // 128x256, 183 with 128x128, which a single weight takes 130 us).
+            if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
+            // A split writes and reads its partials and takes another launch.
+            if (n > 1) us += 4.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 4e6;
+            if (us < least) {
+                least = us;
+                best = {c, n};
             }
         }
     }

@@ -23,6 +23,8 @@ hipError_t launch_layout(Config c, bool direct, const GemmArgs &g, int grid, hip
     if (c == kTile256) return launch<Product<T, 256, 256, 2, 4, 2, AKC, BKC, true>>(g, grid, s);
     if (c == kTile128x256) return launch<Product<T, 128, 256, 2, 4, 3, AKC, BKC, true>>(g, grid, s);
     if (c == kTile128) return launch<Product<T, 128, 128, 2, 2, 2, AKC, BKC, true>>(g, grid, s);
+    if (c == kTile64x128) return launch<Product<T, 64, 128, 2, 2, 3, AKC, BKC, true>>(g, grid, s);
+    if (c == kTile64) return launch<Product<T, 64, 64, 2, 2, 4, AKC, BKC, true>>(g, grid, s);
     return hipErrorInvalidValue;
 }
 

@@ -13,11 +13,11 @@ constexpr int kGemvRows = 2;
 constexpr int64_t kGemvColumnBytes = 64 << 20;  // weights stored [K][N] up to this size
 
 // Tile configurations of the products; kGemv: no tiles, at most kGemvRows rows.
-enum Config : int { kTile256 = 0, kTile128x256 = 1, kTile128 = 2, kTile16 = 3, kGemv = 4, kConfigs = 5 };
+enum Config : int { kTile256, kTile128x256, kTile128, kTile64x128, kTile64, kTile16, kGemv, kConfigs };
 struct ConfigShape {
     int bm, bn;
 };
-constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {16, 128}, {kGemvRows, 1}};
+constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}, {16, 128}, {kGemvRows, 1}};
 
 // A copy of a matrix with rows of whole 16-byte units, zero past the end.
 struct PackArgs {
