@@ -183,8 +183,9 @@ Choice choose(const Shape &s) {
             // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
             // 128x256, 183 with 128x128, which a single weight takes 130 us).
             if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
-            // A split writes and reads its partials and takes another launch.
-            if (n > 1) us += 4.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 4e6;
+            // A split writes and reads its partials, mostly in the caches, and
+            // takes another launch.
+            if (n > 1) us += 3.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 8e6;
             if (us < least) {
                 least = us;
                 best = {c, n};
@@ -223,28 +224,34 @@ struct Arena {
 };
 
 // Rows of whole 16-byte chunks, as the direct loads need them: the matrix
-// itself if it has them, otherwise a copy.  A copy moves the matrix twice; the
-// kernel that reads unaligned rows through registers instead took 208 us for
-// 2048 x 4096 x 4096 with odd rows, where the aligned one takes 62 and the copies 25.
-int packed(Mat &m, int64_t *stride, int count, int dtype, Arena &ws, hipStream_t stream) {
-    const int64_t es = elem_size(dtype);
-    if (m.rows == 0 || m.cols == 0) return CP_OK;
-    if (aligned16(m, dtype) && (!stride || *stride * es % 16 == 0)) return CP_OK;
+// itself if it has them, otherwise a copy, made by the launch that ends the
+// list.  A copy moves the matrix twice; a kernel that read unaligned rows
+// through registers instead took 200 us for 2048 x 4096 x 4096 with odd rows,
+// where the aligned one takes 62 and the copies about 25.
+struct Packs {
     PackArgs a{};
-    a.src = (const char *)m.p;
-    a.dst = ws.take(packed_bytes(dtype, m.rows, m.cols, count));
-    a.ld = m.ld;
-    a.ldd = up(m.cols, 8);
-    a.stride = stride ? *stride : 0;
-    a.stride_d = m.rows * a.ldd;
-    a.rows = (int)m.rows;
-    a.cols = (int)m.cols;
-    a.count = count;
-    m.p = a.dst;
-    m.ld = a.ldd;
-    if (stride) *stride = a.stride_d;
-    return launched(launch_pack(dtype, a, stream), "pack");
-}
+    int dtype;
+    Arena &mem;
+
+    void add(Mat &m, int64_t *stride, int count) {
+        if (m.rows == 0 || m.cols == 0) return;
+        if (aligned16(m, dtype) && (!stride || *stride * elem_size(dtype) % 16 == 0)) return;
+        PackArgs::One &o = a.one[a.n++];
+        o.src = (const char *)m.p;
+        o.dst = mem.take(packed_bytes(dtype, m.rows, m.cols, count));
+        o.ld = m.ld;
+        o.ldd = up(m.cols, 8);
+        o.stride = stride ? *stride : 0;
+        o.stride_d = m.rows * o.ldd;
+        o.rows = (int)m.rows;
+        o.cols = (int)m.cols;
+        o.count = count;
+        m.p = o.dst;
+        m.ld = o.ldd;
+        if (stride) *stride = o.stride_d;
+    }
+    int launch(hipStream_t s) { return a.n ? launched(launch_pack(dtype, a, s), "pack") : CP_OK; }
+};
 
 int64_t split_bytes(const Shape &s) {
     if (s.M == 0 || s.N == 0) return 0;
@@ -408,8 +415,10 @@ int forward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X, in
     Arena mem{(char *)ws};
     void *split = mem.take(split_bytes(p.s));
     if (!few_rows(p.s)) {
-        CP_TRY(packed(p.A, nullptr, 1, dtype, mem, (hipStream_t)stream));
-        CP_TRY(packed(p.B, &p.sb, E ? E : 1, dtype, mem, (hipStream_t)stream));
+        Packs packs{{}, dtype, mem};
+        packs.add(p.A, nullptr, 1);
+        packs.add(p.B, &p.sb, E ? E : 1);
+        CP_TRY(packs.launch((hipStream_t)stream));
     }
     return run_product(p, split, (hipStream_t)stream);
 }
@@ -473,10 +482,13 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     }
     const Shape sx = dx_shape(dtype, M, K, N, E, wt), sw = dw_shape(dtype, M, K, N, E, wt);
     int64_t sb = E > 1 ? stride_w : 0;
-    // dZ is in aligned rows already, zero past their end
-    if (act == CP_ACT_NONE && (dW || (dX && !few_rows(sx)))) CP_TRY(packed(dz, nullptr, 1, dtype, mem, s));
+    Packs packs{{}, dtype, mem};
+    // (with an activation, dZ is in aligned rows already, zero past their end)
+    if (act == CP_ACT_NONE && (dW || (dX && !few_rows(sx)))) packs.add(dz, nullptr, 1);
+    if (dX && !few_rows(sx)) packs.add(w, &sb, E ? E : 1);
+    if (dW) packs.add(x, nullptr, 1);
+    CP_TRY(packs.launch(s));
     if (dX) {
-        if (!few_rows(sx)) CP_TRY(packed(w, &sb, E ? E : 1, dtype, mem, s));
         Product p{};
         p.s = sx;
         p.A = dz;
@@ -487,7 +499,6 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         CP_TRY(run_product(p, split, s));
     }
     if (dW) {
-        CP_TRY(packed(x, nullptr, 1, dtype, mem, s));
         Product p{};
         p.s = sw;
         p.A = wt ? dz : x;

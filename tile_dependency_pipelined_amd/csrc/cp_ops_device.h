@@ -125,20 +125,20 @@ __device__ __forceinline__ float act_apply(float x, int act) {
     return x;
 }
 
-__device__ __forceinline__ float clamp_keep_nan(float x, float lim) { return x < -lim ? -lim : (x > lim ? lim : x); }
+__device__ __forceinline__ float clamp_keep_nan(float x, float lim) { return fabsf(x) > lim ? copysignf(lim, x) : x; }
 
 // Derivative.  Beyond the clamps it is 0 or 1 to fp32 precision; without them
 // x^2 could overflow and 0 * inf give NaN for a finite x.
 __device__ __forceinline__ float act_grad(float x, int act) {
-    if (act == CP_ACT_GELU_TANH) {
+    if (act == CP_ACT_GELU_TANH) {  // p + p (1 - p) 2 x u'(x), u' = sqrt(2/pi) (1 + 3 * 0.044715 x^2)
         x = clamp_keep_nan(x, 10.0f);
         const float p = gelu_gate(x);
-        return p + 2.0f * x * p * (1.0f - p) * kGelu0 * (1.0f + 3.0f * kGelu1 * x * x);
+        return p * fmaf(1.0f - p, x * fmaf(6.0f * kGelu0 * kGelu1, x * x, 2.0f * kGelu0), 1.0f);
     }
     if (act == CP_ACT_SILU) {
         x = clamp_keep_nan(x, 80.0f);
         const float p = sigmoid(x);
-        return p + x * p * (1.0f - p);
+        return p * fmaf(1.0f - p, x, 1.0f);
     }
     if (act == CP_ACT_RELU) return x > 0.0f ? 1.0f : (x == x ? 0.0f : x);
     return 1.0f;
@@ -236,6 +236,19 @@ struct GroupScan {
     int tiles_end;   // tiles of `tile` rows up to and including this lane's expert
 };
 
+// Inclusive scan over the wave with cross-lane moves inside the vector unit (a
+// scan by shuffles, twelve dependent LDS round trips, took longer than the
+// offsets' loads).  The values are not negative: 0 is neutral.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr 1, 2, 4, 8: within 16 lanes
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // lane 15 to the next 16, 47 likewise
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // lane 31 to the upper half
+}
+
 __device__ __forceinline__ GroupScan scan_groups(const int32_t *off, int groups, int rows, int tile, int base,
                                                  int carry_end, int carry_tiles) {
     const int lane = threadIdx.x & 63, e = base + lane;
@@ -245,19 +258,11 @@ __device__ __forceinline__ GroupScan scan_groups(const int32_t *off, int groups,
         end = end < 0 ? 0 : (end > rows ? rows : end);
     }
     end = end > carry_end ? end : carry_end;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(end, d);
-        if (lane >= d) end = o > end ? o : end;
-    }
+    end = wave_scan(end, [](int a, int b) { return a > b ? a : b; });
     int start = __shfl_up(end, 1);
     if (lane == 0) start = carry_end;
     int tiles = e <= groups ? (end - start + tile - 1) / tile : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(tiles, d);
-        if (lane >= d) tiles += o;
-    }
+    tiles = wave_scan(tiles, [](int a, int b) { return a + b; });
     return {start, end, tiles + carry_tiles};
 }
 

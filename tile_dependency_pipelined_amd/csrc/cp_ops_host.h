@@ -19,13 +19,17 @@ struct ConfigShape {
 };
 constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}, {16, 128}, {kGemvRows, 1}};
 
-// A copy of a matrix with rows of whole 16-byte units, zero past the end.
+// Copies of up to three matrices (or stacks of `count`) with rows of whole
+// 16-byte units, zero past the end.
 struct PackArgs {
-    const char *src;
-    char *dst;
-    int64_t ld, ldd;       // elements
-    int64_t stride, stride_d;  // from one of `count` matrices to the next
-    int32_t rows, cols, count;
+    struct One {
+        const char *src;
+        char *dst;
+        int64_t ld, ldd;           // elements
+        int64_t stride, stride_d;  // from one of `count` matrices to the next
+        int32_t rows, cols, count;
+    } one[3];
+    int32_t n;
 };
 hipError_t launch_pack(int dtype, const PackArgs &a, hipStream_t s);
 
@@ -48,7 +52,7 @@ struct GradArgs {
     const int32_t *off;
     int32_t groups, M, N, act, tiles, vec;
 };
-constexpr int kGradRows = 64;  // rows of a partial column sum
+constexpr int kGradRows = 32;  // rows of a partial column sum
 hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s);
 
 struct NormArgs {

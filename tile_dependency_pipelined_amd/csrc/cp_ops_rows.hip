@@ -11,16 +11,23 @@ namespace {
 // ------------------------------------------------------------------- packing
 
 // 64 units of 16 bytes x 4 rows per block; the source may lie anyhow.
+struct PackGrid {
+    int unit_blocks[3], end[3];  // of each copy: blocks along a row, last block + 1
+};
 template <class T>
-__global__ __launch_bounds__(256) void pack_kernel(PackArgs a, int units, int unit_blocks) {
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a, PackGrid g) {
     constexpr int CE = kUnit<T>;
-    const int u = (blockIdx.x % unit_blocks) * 64 + (threadIdx.x & 63);
-    const int64_t r = (int64_t)(blockIdx.x / unit_blocks) * 4 + (threadIdx.x >> 6);
-    if (u >= units || r >= (int64_t)a.count * a.rows) return;
-    const int m = (int)(r / a.rows), row = (int)(r - (int64_t)m * a.rows);
-    const char *src = a.src + (m * a.stride + row * a.ld + u * CE) * (int64_t)sizeof(T);
-    *reinterpret_cast<uint4 *>(a.dst + (m * a.stride_d + row * a.ldd + u * CE) * (int64_t)sizeof(T)) =
-        load_partial<T>(src, a.cols - u * CE);
+    int b = blockIdx.x, i = 0;
+    while (i < 2 && b >= g.end[i]) ++i;
+    if (i > 0) b -= g.end[i - 1];
+    const PackArgs::One o = a.one[i];
+    const int u = (b % g.unit_blocks[i]) * 64 + (threadIdx.x & 63);
+    const int64_t r = (int64_t)(b / g.unit_blocks[i]) * 4 + (threadIdx.x >> 6);
+    if (u * CE >= o.cols || r >= (int64_t)o.count * o.rows) return;
+    const int m = (int)(r / o.rows), row = (int)(r - (int64_t)m * o.rows);
+    const char *src = o.src + (m * o.stride + row * o.ld + u * CE) * (int64_t)sizeof(T);
+    *reinterpret_cast<uint4 *>(o.dst + (m * o.stride_d + row * o.ldd + u * CE) * (int64_t)sizeof(T)) =
+        load_partial<T>(src, o.cols - u * CE);
 }
 
 // ------------------------------------------------------------------- joining
@@ -89,26 +96,41 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
         for (int row = row0 + r; row < end; row += 8)
             *reinterpret_cast<T *>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T)) = from_f32<T>(0.0f);
     if (col < a.N) {
-#pragma unroll 8
-        for (int row = row0 + r; row < end; row += 8) {
-            float d[CNT];
-            const char *p = a.dy + ((int64_t)row * a.ldd + col) * sizeof(T);
-            if constexpr (CNT > 1) load_unit<T>(p, d);
-            else d[0] = to_f32(*reinterpret_cast<const T *>(p));
-            if (a.dz) {
-                float z[CNT];
-                const char *q = a.pre + ((int64_t)row * a.ldp + col) * sizeof(T);
-                if constexpr (CNT > 1) load_unit<T>(q, z);
-                else z[0] = to_f32(*reinterpret_cast<const T *>(q));
+        // all rows are requested before the first one's dZ is stored
+        constexpr int R = kGradRows / 8;
+        Raw<T, CNT> dy[R], z[R];
 #pragma unroll
-                for (int i = 0; i < CNT; ++i) d[i] *= act_grad(z[i], a.act);
-                char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
-                if constexpr (CNT > 1) store_unit<T>(o, d);
-                else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
-            }
-#pragma unroll
-            for (int i = 0; i < CNT; ++i) sum[i] += d[i];
+        for (int i = 0; i < R; ++i) {
+            const int row = row0 + r + 8 * i;
+            if (row >= end) break;
+            dy[i].load(a.dy + ((int64_t)row * a.ldd + col) * sizeof(T));
+            if (a.dz) z[i].load(a.pre + ((int64_t)row * a.ldp + col) * sizeof(T));
         }
+        auto rows = [&](auto ACT) {
+            constexpr int act = decltype(ACT)::value;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = row0 + r + 8 * i;
+                if (row >= end) break;
+                float d[CNT];
+                dy[i].unpack(d);
+                if constexpr (act != CP_ACT_NONE) {
+                    float x[CNT];
+                    z[i].unpack(x);
+#pragma unroll
+                    for (int j = 0; j < CNT; ++j) d[j] *= act_grad(x[j], act);
+                    char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
+                    if constexpr (CNT > 1) store_unit<T>(o, d);
+                    else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
+                }
+#pragma unroll
+                for (int j = 0; j < CNT; ++j) sum[j] += d[j];
+            }
+        };
+        if (!a.dz) rows(std::integral_constant<int, CP_ACT_NONE>{});
+        else if (a.act == CP_ACT_GELU_TANH) rows(std::integral_constant<int, CP_ACT_GELU_TANH>{});
+        else if (a.act == CP_ACT_SILU) rows(std::integral_constant<int, CP_ACT_SILU>{});
+        else rows(std::integral_constant<int, CP_ACT_RELU>{});
     }
     if (!a.db) return;
 #pragma unroll
@@ -539,11 +561,17 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int col_blo
 
 template <class T>
 hipError_t pack(const PackArgs &a, hipStream_t s) {
-    const int units = (a.cols + kUnit<T> - 1) / kUnit<T>;
-    const int ub = (units + 63) / 64;
-    const int64_t blocks = ((int64_t)a.count * a.rows + 3) / 4 * ub;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(pack_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, a, units, ub);
+    PackGrid g{};
+    int64_t blocks = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (i < a.n) {
+            g.unit_blocks[i] = (a.one[i].cols + 64 * kUnit<T> - 1) / (64 * kUnit<T>);
+            blocks += ((int64_t)a.one[i].count * a.one[i].rows + 3) / 4 * g.unit_blocks[i];
+            if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        }
+        g.end[i] = (int)blocks;
+    }
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(pack_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, a, g);
     return hipGetLastError();
 }
 
