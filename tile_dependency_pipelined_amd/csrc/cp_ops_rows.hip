@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
 
 // 32 column units x 8 rows per pass; each block one row tile (kGradRows rows of
 // one expert) and 32 units of columns.
-template <class T, int CNT>
+template <class T, int CNT, int ACT>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     __shared__ float part[8][32 * CNT];
     const int ct = blockIdx.x % col_blocks, rt = blockIdx.x / col_blocks;
@@ -92,45 +92,39 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     float sum[CNT];
 #pragma unroll
     for (int i = 0; i < CNT; ++i) sum[i] = 0.0f;
-    if (CNT == 1 && a.dz && col >= a.N && col < a.ldz)  // the rows of dZ end in zeros
+    if (CNT == 1 && ACT != CP_ACT_NONE && col >= a.N && col < a.ldz)  // the rows of dZ end in zeros
         for (int row = row0 + r; row < end; row += 8)
             *reinterpret_cast<T *>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T)) = from_f32<T>(0.0f);
     if (col < a.N) {
-        // all rows are requested before the first one's dZ is stored
+        // All rows are requested before the first one's dZ is stored, without
+        // a branch in between (past the end the last row, again): with one
+        // the compiler waited for each load.
         constexpr int R = kGradRows / 8;
         Raw<T, CNT> dy[R], z[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            const int row = row0 + r + 8 * i < end ? row0 + r + 8 * i : end - 1;
+            dy[i].load(a.dy + ((int64_t)row * a.ldd + col) * sizeof(T));
+            if constexpr (ACT != CP_ACT_NONE) z[i].load(a.pre + ((int64_t)row * a.ldp + col) * sizeof(T));
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
             const int row = row0 + r + 8 * i;
             if (row >= end) break;
-            dy[i].load(a.dy + ((int64_t)row * a.ldd + col) * sizeof(T));
-            if (a.dz) z[i].load(a.pre + ((int64_t)row * a.ldp + col) * sizeof(T));
-        }
-        auto rows = [&](auto ACT) {
-            constexpr int act = decltype(ACT)::value;
+            float d[CNT];
+            dy[i].unpack(d);
+            if constexpr (ACT != CP_ACT_NONE) {
+                float x[CNT];
+                z[i].unpack(x);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int row = row0 + r + 8 * i;
-                if (row >= end) break;
-                float d[CNT];
-                dy[i].unpack(d);
-                if constexpr (act != CP_ACT_NONE) {
-                    float x[CNT];
-                    z[i].unpack(x);
-#pragma unroll
-                    for (int j = 0; j < CNT; ++j) d[j] *= act_grad(x[j], act);
-                    char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
-                    if constexpr (CNT > 1) store_unit<T>(o, d);
-                    else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
-                }
-#pragma unroll
-                for (int j = 0; j < CNT; ++j) sum[j] += d[j];
+                for (int j = 0; j < CNT; ++j) d[j] *= act_grad(x[j], ACT);
+                char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
+                if constexpr (CNT > 1) store_unit<T>(o, d);
+                else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
             }
-        };
-        if (!a.dz) rows(std::integral_constant<int, CP_ACT_NONE>{});
-        else if (a.act == CP_ACT_GELU_TANH) rows(std::integral_constant<int, CP_ACT_GELU_TANH>{});
-        else if (a.act == CP_ACT_SILU) rows(std::integral_constant<int, CP_ACT_SILU>{});
-        else rows(std::integral_constant<int, CP_ACT_RELU>{});
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) sum[j] += d[j];
+        }
     }
     if (!a.db) return;
 #pragma unroll
@@ -591,8 +585,15 @@ hipError_t grad(const GradArgs &a, hipStream_t s) {
     const int cols = (a.N + 32 * unit - 1) / (32 * unit);
     if (a.tiles > 0) {
         const dim3 grid((unsigned)(a.tiles * cols));
-        if (a.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, kUnit<T>>), grid, dim3(256), 0, s, a, cols);
-        else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, 1>), grid, dim3(256), 0, s, a, cols);
+        auto launch = [&](auto ACT) {
+            constexpr int act = decltype(ACT)::value;
+            if (a.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, kUnit<T>, act>), grid, dim3(256), 0, s, a, cols);
+            else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, 1, act>), grid, dim3(256), 0, s, a, cols);
+        };
+        if (a.act == CP_ACT_NONE) launch(std::integral_constant<int, CP_ACT_NONE>{});
+        else if (a.act == CP_ACT_GELU_TANH) launch(std::integral_constant<int, CP_ACT_GELU_TANH>{});
+        else if (a.act == CP_ACT_SILU) launch(std::integral_constant<int, CP_ACT_SILU>{});
+        else launch(std::integral_constant<int, CP_ACT_RELU>{});
     }
     if (a.db) {
         const int cb = (a.N + 63) / 64;
