@@ -23,7 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcpchain.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = [os.path.join(CSRC, n) for n in ("cp_kernels.hip", "cp_chain.cpp", "cp_ops_gemm_bf16.hip",
-                                           "cp_ops_gemm_f32.hip", "cp_ops_gemv.hip", "cp_ops_rows.hip", "cp_ops.cpp")]
+                                           "cp_ops_gemm_f32.hip", "cp_ops_gradients_bf16.hip",
+                                           "cp_ops_gradients_f32.hip", "cp_ops_gemv.hip", "cp_ops_rows.hip",
+                                           "cp_ops.cpp")]
 ARCH = os.environ.get("CP_OFFLOAD_ARCH", "gfx950")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 

@@ -99,6 +99,10 @@ struct Shape {
     int mode;
     int64_t M, N, K;  // rows and columns of C, contraction; kGroupRows: M over all experts; kGroupSum: K over all
     int groups;
+    bool operator==(const Shape &o) const {
+        return dtype == o.dtype && layout == o.layout && mode == o.mode && M == o.M && N == o.N && K == o.K &&
+               groups == o.groups;
+    }
 };
 
 struct Choice {
@@ -122,6 +126,13 @@ int64_t slabs_of(const Shape &s) {
 // split, so that the loads in flight are worth their latency.
 bool few_rows(const Shape &s) {
     return s.layout != kTN && (s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M) <= 16;
+}
+
+// Tiles of an average launch: each expert's last row tile is half empty.
+double average_tiles(const Shape &s, Config c) {
+    const ConfigShape t = kShapes[c];
+    const double tm = s.mode == kGroupRows ? (double)s.M / t.bm + 0.5 * s.groups : (double)ceil_div(s.M, t.bm);
+    return tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
 }
 
 // Time in microseconds of one launch of `tiles` tiles with `slabs` slabs each,
@@ -153,7 +164,7 @@ double launch_time(Config c, int dtype, double tiles, double slabs) {
     return t;
 }
 
-Choice choose(const Shape &s) {
+Choice choose_now(const Shape &s) {
     // (both sides measured: cp_ops_gemv.hip)
     if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows &&
         (s.layout == kNT || s.K * s.N * elem_size(s.dtype) <= kGemvColumnBytes))
@@ -171,10 +182,7 @@ Choice choose(const Shape &s) {
     double least = 1e300;
     for (const Config c : all) {
         if (s.dtype == CP_F32 && c < kTile128) continue;
-        const ConfigShape t = kShapes[c];
-        // row tiles of an average launch: each expert's last one is half empty
-        const double tm = s.mode == kGroupRows ? (double)s.M / t.bm + 0.5 * s.groups : (double)ceil_div(s.M, t.bm);
-        const double tiles = tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
+        const double tiles = average_tiles(s, c);
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && (s.mode != kDense || slabs < 4 * n)) break;
             double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n));
@@ -193,6 +201,22 @@ Choice choose(const Shape &s) {
         }
     }
     return best;
+}
+
+// The same for the shapes of this thread's recent calls: weighing all tiles and
+// splits takes about a microsecond, several times in a call.
+Choice choose(const Shape &s) {
+    struct Entry {
+        Shape s{-1, kNN, 0, 0, 0, 0, 0};
+        Choice c{};
+    };
+    static thread_local Entry cache[64];
+    uint64_t h = (uint64_t)s.M * 0x9E3779B97F4A7C15ull + (uint64_t)s.N;
+    h = h * 0x9E3779B97F4A7C15ull + (uint64_t)s.K;
+    h = h * 0x9E3779B97F4A7C15ull + (uint64_t)(s.layout * 64 + s.mode * 8 + s.dtype) + (uint64_t)s.groups * 1024;
+    Entry &e = cache[(h * 0x9E3779B97F4A7C15ull) >> 58];
+    if (!(e.s == s)) e = {s, choose_now(s)};
+    return e.c;
 }
 
 // ------------------------------------------------------------------ products
@@ -259,14 +283,12 @@ int64_t split_bytes(const Shape &s) {
     return c.nsplit > 1 ? (int64_t)c.nsplit * s.M * up(s.N, 8) * 4 : 0;
 }
 
-// `split`: room for split_bytes().  The operands are aligned unless few_rows().
-int run_product(const Product &p, void *split, hipStream_t stream) {
+// The launch of a product with this choice; its operands are aligned unless it
+// is of few rows.  Returns the number of workgroups, or an error.
+int64_t launch_args(const Product &p, const Choice &c, void *split, GemmArgs &g) {
     const Shape &s = p.s;
-    if (s.M == 0 || s.N == 0) return CP_OK;
     const int es = elem_size(s.dtype);
-    const Choice c = choose(s);
-    const bool direct = (c.cfg != kTile16 && c.cfg != kGemv) || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) && p.sb * es % 16 == 0);
-    GemmArgs g{};
+    g = GemmArgs{};
     g.A = (const char *)p.A.p;
     g.B = (const char *)p.B.p;
     g.C = (char *)p.C.p;
@@ -292,18 +314,78 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
     g.ldws = (int)up(s.N, 8);
     g.vec = aligned16(p.C, s.dtype) && aligned16(p.R, s.dtype) && aligned16(p.P, s.dtype) && aligned16(p.bias) &&
             p.sc * es % 16 == 0;
-    if (c.cfg == kGemv) return launched(launch_gemv(s.dtype, s.layout == kNT, g, stream), "product of few rows");
     const ConfigShape t = kShapes[c.cfg];
-    g.ntn = (int)ceil_div(s.N, t.bn);
-    const int64_t ntm = max_row_tiles(s, t.bm);
+    const int64_t ntm = max_row_tiles(s, t.bm), ntn = ceil_div(s.N, t.bn);
+    const int64_t grid = ntm * ntn * c.nsplit * (s.mode == kGroupSum ? s.groups : 1);
+    if (grid > 0x3FFFFFFF) return fail(CP_ERR_SHAPE, "too many tiles (%lld)", (long long)grid);
     g.ntm = (int)ntm;
-    const int64_t grid = ntm * g.ntn * c.nsplit * (s.mode == kGroupSum ? s.groups : 1);
-    if (grid > 0x7FFFFFFF) return fail(CP_ERR_SHAPE, "too many tiles (%lld)", (long long)grid);
+    g.ntn = (int)ntn;
+    return grid;
+}
+
+// `split`: room for split_bytes().
+int run_product(const Product &p, void *split, hipStream_t stream) {
+    const Shape &s = p.s;
+    if (s.M == 0 || s.N == 0) return CP_OK;
+    const Choice c = choose(s);
+    GemmArgs g;
+    const int64_t grid = launch_args(p, c, split, g);
+    if (grid < 0) return (int)grid;
+    if (c.cfg == kGemv) return launched(launch_gemv(s.dtype, s.layout == kNT, g, stream), "product of few rows");
+    const bool direct = c.cfg != kTile16 || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) &&
+                                             p.sb * elem_size(s.dtype) % 16 == 0);
     CP_TRY(launched(s.dtype == CP_BF16 ? launch_product_bf16(s.layout, c.cfg, direct, g, (int)grid, stream)
                                        : launch_product_f32(s.layout, c.cfg, direct, g, (int)grid, stream),
                     "product"));
     if (c.nsplit > 1) CP_TRY(launched(launch_join(s.dtype, g, stream), "join"));
     return CP_OK;
+}
+
+// Time of dX's and dW's tiles in one launch: each slot of the device takes dX's
+// first, then dW's as it comes free.
+double gradients_time(const Shape &x, const Shape &w, Config c) {
+    const int slots = kComputeUnits * (x.dtype == CP_BF16 && c >= kTile128 ? 2 : 1);
+    const double penalty = x.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0;
+    const double tx = penalty * launch_time(c, x.dtype, slots, (double)slabs_of(x));
+    const double tw = penalty * launch_time(c, w.dtype, slots, (double)slabs_of(w));
+    const int64_t nx = (int64_t)(average_tiles(x, c) + 0.5), nw = (int64_t)(average_tiles(w, c) + 0.5);
+    const double t0 = (double)(nx / slots) * tx;  // most slots are done with dX
+    const double late = (double)(nx % slots);     // these have one more of its tiles
+    const double t1 = late > 0.0 ? t0 + tx : t0;
+    // the earliest end by which all of dW's tiles fit; from a bound below it
+    const double least = ((slots - late) * t0 + late * t1 + (double)nw * tw) / slots;
+    double k0 = (double)(int64_t)((least - t0) / tw), k1 = (double)(int64_t)((least - t1) / tw);
+    if (k0 < 1.0) k0 = 1.0;
+    if (k1 < 1.0) k1 = 1.0;
+    for (;;) {
+        const double e0 = t0 + k0 * tw, e1 = t1 + k1 * tw, end = e0 < e1 ? e0 : e1;
+        const double early = (double)(int64_t)((end - t0) / tw + 1e-6), after = (double)(int64_t)((end - t1) / tw + 1e-6);
+        if ((slots - late) * early + late * (after > 0.0 ? after : 0.0) >= (double)nw) return end > t1 ? end : t1;
+        (e0 < e1 ? k0 : k1) += 1.0;
+    }
+}
+
+// The configuration of one launch for both gradients, or kConfigs if two are
+// better (4099 x 2048 x 4096 over 8 experts, bf16: 210 us in two, 171 in one).
+Config choose_gradients(const Shape &x, const Shape &w) {
+    if (few_rows(x)) return kConfigs;
+    const Choice cx = choose(x), cw = choose(w);
+    if (cx.nsplit > 1 || cw.nsplit > 1) return kConfigs;
+    auto alone = [](const Shape &s, Config c) {
+        return (s.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0) *
+               launch_time(c, s.dtype, average_tiles(s, c), (double)slabs_of(s));
+    };
+    double least = alone(x, cx.cfg) + alone(w, cw.cfg);
+    Config best = kConfigs;
+    for (const Config c : {kTile256, kTile128x256, kTile128, kTile64x128, kTile64}) {
+        if (x.dtype == CP_F32 && c < kTile128) continue;
+        const double us = gradients_time(x, w, c) - 3.0;  // a launch less
+        if (us < least) {
+            least = us;
+            best = c;
+        }
+    }
+    return best;
 }
 
 // ------------------------------------------------- the linear layers, dense and
@@ -458,8 +540,8 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     void *split = mem.take(backward_split_bytes(dtype, M, K, N, E));
     Mat dz = dy;
     if (act != CP_ACT_NONE) dz = {mem.take(packed_bytes(dtype, M, N, 1)), M, N, up(N, 8)};
+    GradArgs a{};
     if (N > 0 && (act != CP_ACT_NONE || db)) {
-        GradArgs a{};
         a.dy = (const char *)dy.p;
         a.ldd = dy.ld;
         if (act != CP_ACT_NONE) {
@@ -488,26 +570,32 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     if (dX && !few_rows(sx)) packs.add(w, &sb, E ? E : 1);
     if (dW) packs.add(x, nullptr, 1);
     CP_TRY(packs.launch(s));
-    if (dX) {
-        Product p{};
-        p.s = sx;
-        p.A = dz;
-        p.B = w;
-        p.C = dx;
-        p.sb = sb;
-        p.off = off;
-        CP_TRY(run_product(p, split, s));
+    Product px{}, pw{};
+    px.s = sx;
+    px.A = dz;
+    px.B = w;
+    px.C = dx;
+    px.sb = sb;
+    px.off = off;
+    pw.s = sw;
+    pw.A = wt ? dz : x;
+    pw.B = wt ? x : dz;
+    pw.C = dw;
+    pw.sc = E > 1 ? stride_dw : 0;
+    pw.off = off;
+    const Config both = dX && dW && M > 0 && K > 0 && N > 0 ? choose_gradients(sx, sw) : kConfigs;
+    if (both != kConfigs) {
+        GemmArgs gx, gw;
+        const int64_t nx = launch_args(px, {both, 1}, split, gx), nw = launch_args(pw, {both, 1}, split, gw);
+        if (nx < 0 || nw < 0) return (int)(nx < 0 ? nx : nw);
+        const int nd = db ? grad_join_blocks(a) : 0;
+        return launched((dtype == CP_BF16 ? launch_gradients_bf16 : launch_gradients_f32)(sx.layout, both, gx, (int)nx, gw,
+                                                                                         (int)nw, a, nd, s),
+                        "gradients");
     }
-    if (dW) {
-        Product p{};
-        p.s = sw;
-        p.A = wt ? dz : x;
-        p.B = wt ? x : dz;
-        p.C = dw;
-        p.sc = E > 1 ? stride_dw : 0;
-        p.off = off;
-        CP_TRY(run_product(p, split, s));
-    }
+    if (db && N > 0) CP_TRY(launched(launch_grad_join(dtype, a, s), "bias gradient"));
+    if (dX) CP_TRY(run_product(px, split, s));
+    if (dW) CP_TRY(run_product(pw, split, s));
     return CP_OK;
 }
 

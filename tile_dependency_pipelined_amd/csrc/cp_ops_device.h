@@ -318,4 +318,51 @@ __device__ __forceinline__ int xcd_remap(int b, int n) {
     return x * q + (x < r ? x : r) + (b >> 3);
 }
 
+// dZ = dY act'(pre) and column sums of it per expert (dense: groups = 1, off null)
+struct GradArgs {
+    const char *dy, *pre;
+    char *dz, *db;
+    float *ws;             // [row tiles][N] partial column sums
+    int64_t ldd, ldp, ldz;
+    const int32_t *off;
+    int32_t groups, M, N, act, tiles, vec;
+};
+constexpr int kGradRows = 32;  // rows of a partial column sum
+
+// db[e] = sum of its row tiles' partials (GradArgs): 64 columns x NT / 64
+// ranges of tiles per block.
+template <class T, int NT>
+__device__ __forceinline__ void join_columns(const GradArgs &a, int b, float *part) {
+    constexpr int R = NT / 64;
+    const int col_blocks = (a.N + 63) / 64;
+    const int e = b / col_blocks, t = threadIdx.x & 63, s = threadIdx.x >> 6;
+    const int col = (b % col_blocks) * 64 + t;
+    int from = 0, to = (a.M + kGradRows - 1) / kGradRows;
+    if (a.off) {
+        int carry_end = 0, carry_tiles = 0;
+        for (int base = 0;; base += 64) {
+            const GroupScan g = scan_groups(a.off, a.groups, a.M, kGradRows, base, carry_end, carry_tiles);
+            if (e < base + 64) {
+                const int l = e - base;
+                from = l ? __builtin_amdgcn_readlane(g.tiles_end, l - 1) : carry_tiles;
+                to = __builtin_amdgcn_readlane(g.tiles_end, l);
+                break;
+            }
+            carry_end = __builtin_amdgcn_readlane(g.end, 63);
+            carry_tiles = __builtin_amdgcn_readlane(g.tiles_end, 63);
+        }
+    }
+    const int per = (to - from + R - 1) / R, p0 = from + s * per, p1 = p0 + per < to ? p0 + per : to;
+    float v = 0.0f;
+    if (col < a.N)
+#pragma unroll 8
+        for (int i = p0; i < p1; ++i) v += a.ws[(int64_t)i * a.N + col];
+    part[s * 64 + t] = v;
+    __syncthreads();
+    if (s > 0 || col >= a.N) return;
+#pragma unroll
+    for (int i = 1; i < R; ++i) v += part[i * 64 + t];
+    reinterpret_cast<T *>(a.db)[(int64_t)e * a.N + col] = from_f32<T>(v);
+}
+
 }  // namespace cpo

@@ -25,7 +25,7 @@
 #pragma once
 #include <type_traits>
 
-#include "cp_ops_device.h"
+#include "cp_ops_host.h"
 
 namespace cpo {
 
@@ -265,13 +265,14 @@ struct Product {
     // of the 512 leave room for one
     static constexpr int WAVES = FM * FN * 4 > 128 ? 1 : 2;
 
-    __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4]) {
+    // `b`: which of the launch's workgroups for this product.
+    __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4], int b) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
 
         // ---- which tile ----
-        int ntm = g.ntm, b = blockIdx.x, expert = 0, row0, row_end = g.M, k_first = 0, klen = g.K;
+        int ntm = g.ntm, expert = 0, row0, row_end = g.M, k_first = 0, klen = g.K;
         GroupScan scan{};
         if (g.mode == kGroupRows) ntm = count_tiles(g.off, g.groups, g.M, BM, scan);
         const int tiles = ntm * g.ntn;
@@ -541,15 +542,82 @@ struct Product {
     }
 };
 
+// The stages in LDS: one array each, as reads of one and direct loads into
+// another do not alias.
+#define CPO_STAGES(P)                                                                      \
+    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];                           \
+    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];                           \
+    __shared__ __attribute__((aligned(1024))) char s2[P::S > 2 ? P::STAGE : 16];           \
+    __shared__ __attribute__((aligned(1024))) char s3[P::S > 3 ? P::STAGE : 16];           \
+    char *const st[4] = {s0, s1, s2, s3}
+
 template <class P>
 __global__ __launch_bounds__(P::NT, P::WAVES) void product_kernel(GemmArgs g) {
-    // one array per stage: reads of one and direct loads into another do not alias
-    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];
-    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];
-    __shared__ __attribute__((aligned(1024))) char s2[P::S > 2 ? P::STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) char s3[P::S > 3 ? P::STAGE : 16];
-    char *const st[4] = {s0, s1, s2, s3};
-    P::run(g, st);
+    CPO_STAGES(P);
+    P::run(g, st, blockIdx.x);
+}
+
+// A layer's gradients in one launch: the tiles of dX (nx workgroups), of dW
+// (nw), and the bias sums (the rest).  What one of them leaves of the device
+// in its last round, the next one's tiles take.
+template <class PX, class PW>
+__global__ __launch_bounds__(PX::NT, PX::WAVES) void gradients_kernel(GemmArgs x, GemmArgs w, GradArgs d, int nx, int nw) {
+    static_assert(PX::NT == PW::NT && PX::STAGE == PW::STAGE && PX::S == PW::S, "one shape of workgroup");
+    CPO_STAGES(PX);
+    const int b = blockIdx.x;
+    if (b < nx) PX::run(x, st, b);
+    else if (b < nx + nw) PW::run(w, st, b - nx);
+    else join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
+}
+
+// The tile configurations with direct loads, by type.
+template <class T, bool AKC, bool BKC, int CFG>
+struct TileOf;
+template <class T, bool A, bool B> struct TileOf<T, A, B, kTile256> { using P = Product<T, 256, 256, 2, 4, 2, A, B, true>; };
+template <class T, bool A, bool B> struct TileOf<T, A, B, kTile128x256> { using P = Product<T, 128, 256, 2, 4, 3, A, B, true>; };
+template <class T, bool A, bool B> struct TileOf<T, A, B, kTile128> { using P = Product<T, 128, 128, 2, 2, 2, A, B, true>; };
+template <class T, bool A, bool B> struct TileOf<T, A, B, kTile64x128> { using P = Product<T, 64, 128, 2, 2, 3, A, B, true>; };
+template <class T, bool A, bool B> struct TileOf<T, A, B, kTile64> { using P = Product<T, 64, 64, 2, 2, 4, A, B, true>; };
+
+// f(integral_constant) of a configuration that this type has
+template <class T, class F>
+hipError_t with_tile(Config c, F &&f) {
+    if constexpr (sizeof(T) == 2) {
+        if (c == kTile256) return f(ic<kTile256>{});
+        if (c == kTile128x256) return f(ic<kTile128x256>{});
+    }
+    if (c == kTile128) return f(ic<kTile128>{});
+    if (c == kTile64x128) return f(ic<kTile64x128>{});
+    if (c == kTile64) return f(ic<kTile64>{});
+    return hipErrorInvalidValue;
+}
+
+template <class T, bool AKC, bool BKC>
+hipError_t launch_layout(Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s) {
+    auto launch = [&](auto P) {
+        using K = typename decltype(P)::P;
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<K>), dim3(grid), dim3(K::NT), 0, s, g);
+        return hipGetLastError();
+    };
+    if constexpr (AKC)
+        if (c == kTile16) {
+            struct Direct { using P = Product<T, 16, 128, 1, 4, 4, AKC, BKC, true>; };
+            struct Staged { using P = Product<T, 16, 128, 1, 4, 2, AKC, BKC, false>; };
+            return direct ? launch(Direct{}) : launch(Staged{});
+        }
+    if (!direct) return hipErrorInvalidValue;  // the host packs their operands
+    return with_tile<T>(c, [&](auto C) { return launch(TileOf<T, AKC, BKC, decltype(C)::value>{}); });
+}
+
+template <class T, bool BKC>
+hipError_t launch_gradients_layout(Config c, const GemmArgs &x, int nx, const GemmArgs &w, int nw, const GradArgs &d, int nd,
+                                   hipStream_t s) {
+    return with_tile<T>(c, [&](auto C) {
+        using PX = typename TileOf<T, true, BKC, decltype(C)::value>::P;
+        using PW = typename TileOf<T, false, false, decltype(C)::value>::P;
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(gradients_kernel<PX, PW>), dim3(nx + nw + nd), dim3(PX::NT), 0, s, x, w, d, nx, nw);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace cpo

@@ -36,6 +36,13 @@ hipError_t launch_pack(int dtype, const PackArgs &a, hipStream_t s);
 hipError_t launch_product_bf16(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
 hipError_t launch_product_f32(Layout l, Config c, bool direct, const GemmArgs &g, int grid, hipStream_t s);
 
+// dX (x, nx workgroups), dW (w, nw) and bias sums (d, nd) of a layer with tiles of
+// one configuration; x's A and w's operands as in Layout, lx is kNN or kNT.
+hipError_t launch_gradients_bf16(Layout lx, Config c, const GemmArgs &x, int nx, const GemmArgs &w, int nw, const GradArgs &d,
+                                 int nd, hipStream_t s);
+hipError_t launch_gradients_f32(Layout lx, Config c, const GemmArgs &x, int nx, const GemmArgs &w, int nw, const GradArgs &d,
+                                int nd, hipStream_t s);
+
 // Products with at most kGemvRows rows; the weight's rows run along the
 // contraction (w_rows) or along the output.
 hipError_t launch_gemv(int dtype, bool w_rows, const GemmArgs &g, hipStream_t s);
@@ -43,17 +50,10 @@ hipError_t launch_gemv(int dtype, bool w_rows, const GemmArgs &g, hipStream_t s)
 // sums the partials of a split product and runs its epilogue
 hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s);
 
-// dZ = dY act'(pre) and column sums of it per expert (dense: groups = 1, off null)
-struct GradArgs {
-    const char *dy, *pre;
-    char *dz, *db;
-    float *ws;             // [row tiles][N] partial column sums
-    int64_t ldd, ldp, ldz;
-    const int32_t *off;
-    int32_t groups, M, N, act, tiles, vec;
-};
-constexpr int kGradRows = 32;  // rows of a partial column sum
+// dZ and the partial column sums; then the bias gradient from those.
+inline int grad_join_blocks(const GradArgs &a) { return a.groups * ((a.N + 63) / 64); }
 hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s);
+hipError_t launch_grad_join(int dtype, const GradArgs &a, hipStream_t s);
 
 struct NormArgs {
     const char *x, *dy, *w, *b;

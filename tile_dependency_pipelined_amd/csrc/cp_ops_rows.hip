@@ -139,37 +139,10 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     }
 }
 
-// db[e] = sum of its row tiles' partials: 64 columns x 4 ranges of tiles
 template <class T>
-__global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a, int col_blocks) {
-    __shared__ float part[4][64];
-    const int e = blockIdx.x / col_blocks, t = threadIdx.x & 63, s = threadIdx.x >> 6;
-    const int col = (blockIdx.x % col_blocks) * 64 + t;
-    int from = 0, to = (a.M + kGradRows - 1) / kGradRows;
-    if (a.off) {
-        int carry_end = 0, carry_tiles = 0;
-        for (int base = 0;; base += 64) {
-            const GroupScan g = scan_groups(a.off, a.groups, a.M, kGradRows, base, carry_end, carry_tiles);
-            if (e < base + 64) {
-                const int l = e - base;
-                from = l ? __builtin_amdgcn_readlane(g.tiles_end, l - 1) : carry_tiles;
-                to = __builtin_amdgcn_readlane(g.tiles_end, l);
-                break;
-            }
-            carry_end = __builtin_amdgcn_readlane(g.end, 63);
-            carry_tiles = __builtin_amdgcn_readlane(g.tiles_end, 63);
-        }
-    }
-    const int per = (to - from + 3) / 4, p0 = from + s * per, p1 = p0 + per < to ? p0 + per : to;
-    float v = 0.0f;
-    if (col < a.N)
-#pragma unroll 8
-        for (int i = p0; i < p1; ++i) v += a.ws[(int64_t)i * a.N + col];
-    part[s][t] = v;
-    __syncthreads();
-    if (s == 0 && col < a.N)
-        reinterpret_cast<T *>(a.db)[(int64_t)e * a.N + col] =
-            from_f32<T>(((part[0][t] + part[1][t]) + part[2][t]) + part[3][t]);
+__global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a) {
+    __shared__ float part[256];
+    join_columns<T, 256>(a, blockIdx.x, part);
 }
 
 // ------------------------------------------------------- layer normalisation
@@ -595,10 +568,12 @@ hipError_t grad(const GradArgs &a, hipStream_t s) {
         else if (a.act == CP_ACT_SILU) launch(std::integral_constant<int, CP_ACT_SILU>{});
         else launch(std::integral_constant<int, CP_ACT_RELU>{});
     }
-    if (a.db) {
-        const int cb = (a.N + 63) / 64;
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), dim3((unsigned)(a.groups * cb)), dim3(256), 0, s, a, cb);
-    }
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t grad_join(const GradArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), dim3((unsigned)grad_join_blocks(a)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -681,6 +656,10 @@ hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s) {
 
 hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s) {
     return dtype == CP_BF16 ? grad<__bf16>(a, s) : grad<float>(a, s);
+}
+
+hipError_t launch_grad_join(int dtype, const GradArgs &a, hipStream_t s) {
+    return dtype == CP_BF16 ? grad_join<__bf16>(a, s) : grad_join<float>(a, s);
 }
 
 hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s) {
