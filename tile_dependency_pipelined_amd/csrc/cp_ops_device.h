@@ -279,10 +279,11 @@ __device__ __forceinline__ int count_tiles(const int32_t *off, int groups, int r
 
 struct RowTile {
     int expert;      // == groups: rows without an expert
-    int row0, end;   // first row, end of the expert's rows
+    int row0, end;   // the expert's rows
+    int before;      // row tiles of the experts before it
 };
 
-// The expert and rows of row tile t (0 <= t < count_tiles).  `s` is what
+// The expert whose rows row tile t (0 <= t < count_tiles) takes.  `s` is what
 // count_tiles left: with fewer than 64 experts it is the only chunk.
 __device__ __forceinline__ RowTile find_tile(const int32_t *off, int groups, int rows, int tile, int t, GroupScan s) {
     int carry_end = 0, carry_tiles = 0;
@@ -293,7 +294,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t *off, int groups, int
             const int l = hit ? __builtin_ctzll(hit) : 63;
             const int before = l ? __builtin_amdgcn_readlane(s.tiles_end, l - 1) : carry_tiles;
             const int start = __builtin_amdgcn_readlane(s.start, l);
-            return {base + l, start + (t - before) * tile, __builtin_amdgcn_readlane(s.end, l)};
+            return {base + l, start, __builtin_amdgcn_readlane(s.end, l), before};
         }
         carry_end = __builtin_amdgcn_readlane(s.end, 63);
         carry_tiles = __builtin_amdgcn_readlane(s.tiles_end, 63);
@@ -306,7 +307,7 @@ __device__ __forceinline__ RowTile expert_rows(const int32_t *off, int groups, i
     for (int base = 0;; base += 64) {
         const GroupScan s = scan_groups(off, groups, rows, 1, base, carry_end, 0);
         if (e < base + 64)
-            return {e, __builtin_amdgcn_readlane(s.start, e - base), __builtin_amdgcn_readlane(s.end, e - base)};
+            return {e, __builtin_amdgcn_readlane(s.start, e - base), __builtin_amdgcn_readlane(s.end, e - base), 0};
         carry_end = __builtin_amdgcn_readlane(s.end, 63);
     }
 }

@@ -286,24 +286,18 @@ struct Product {
             split = b / tiles;
             b -= split * tiles;
         }
-        // Bands of 8 row tiles, row tiles fastest: the ~32 tiles an XCD works
-        // on at a time form a near-square block, which reads least into its L2.
-        constexpr int BAND = 8;
-        const int band = b / (BAND * g.ntn), inband = b - band * BAND * g.ntn;
-        const int left_rows = ntm - band * BAND, high = left_rows < BAND ? left_rows : BAND;
-        int nt = inband / high, mt = band * BAND + inband % high;
-        mt = __builtin_amdgcn_readfirstlane(mt);
-        nt = __builtin_amdgcn_readfirstlane(nt);
-        row0 = mt * BM;
-        const int col0 = nt * BN;
         const char *A = g.A, *B = g.B, *bias = g.bias;
         char *C = g.C;
         bool zero = false;
+        int first = 0;  // rows before the expert's
         if (g.mode == kGroupRows) {
-            const RowTile t = find_tile(g.off, g.groups, g.M, BM, mt, scan);
+            // expert by expert: its tiles are next to each other
+            const RowTile t = find_tile(g.off, g.groups, g.M, BM, b / g.ntn, scan);
             expert = t.expert;
-            row0 = t.row0;
+            first = t.row0;
             row_end = t.end;
+            b -= t.before * g.ntn;
+            ntm = (t.end - t.row0 + BM - 1) / BM;
             zero = expert == g.groups;  // rows without an expert
             if (zero) {
                 klen = 0;
@@ -317,6 +311,15 @@ struct Product {
             klen = t.end - t.row0;
             C += (int64_t)expert * g.sc * sizeof(T);
         }
+        // Bands of 8 row tiles, row tiles fastest: the ~32 tiles an XCD works
+        // on at a time form a near-square block, which reads least into its L2.
+        constexpr int BAND = 8;
+        const int band = b / (BAND * g.ntn), inband = b - band * BAND * g.ntn;
+        const int left_rows = ntm - band * BAND, high = left_rows < BAND ? left_rows : BAND;
+        const int nt = __builtin_amdgcn_readfirstlane(inband / high);
+        const int mt = __builtin_amdgcn_readfirstlane(band * BAND + inband % high);
+        const int col0 = nt * BN;
+        row0 = first + mt * BM;
         if (g.nsplit > 1) {  // whole slabs per split
             const int slabs = (klen + BK - 1) / BK, per = (slabs + g.nsplit - 1) / g.nsplit;
             const int from = split * per * BK;

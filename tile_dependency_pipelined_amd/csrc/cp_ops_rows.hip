@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
         if (rt >= count_tiles(a.off, a.groups, a.M, kGradRows, s)) return;
         const RowTile t = find_tile(a.off, a.groups, a.M, kGradRows, rt, s);
         if (t.expert == a.groups) return;  // their dZ is never read
-        row0 = t.row0;
+        row0 = t.row0 + (rt - t.before) * kGradRows;
         end = t.end;
     }
     if (end > row0 + kGradRows) end = row0 + kGradRows;
