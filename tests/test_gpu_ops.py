@@ -287,7 +287,8 @@ def test_grouped(ops, case, kn, name):
 
 
 NORM = [(1, 1), (1, 8), (3, 7), (5, 64), (2, 512), (9, 513), (4, 1024), (7, 1000), (1, 8192), (600, 264), (33, 4099),
-        (3, 8193), (2, 16384), (2, 20001), (3, 40000), (0, 16), (1100, 40)]
+        (3, 8193), (2, 16384), (2, 20001), (3, 40000), (0, 16), (1100, 40), (1, 9000), (1, 16392), (1, 33000), (16, 512),
+        (17, 482), (2, 4096), (2, 4097), (40, 12296), (5, 6000), (260, 5000)]
 
 
 @pytest.mark.parametrize("name", ["bf16", "f32"])
@@ -456,6 +457,52 @@ def test_streams_and_graphs(ops):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want)), rep
+
+
+def test_rows_beyond_32_bits(ops):
+    """Row and expert offsets past 2^31 elements: only the last rows and the last expert hold values, and
+    theirs are the only results that are not zero."""
+    say("offsets past 32 bits")
+    g = torch.Generator().manual_seed(17)
+    d = torch.bfloat16
+    M, K, N = 530_000, 4096, 8   # x: 2.17e9 elements
+    x = torch.zeros(M, K, dtype=d, device="cuda")
+    tail = data(g, 3, K, dtype=d)
+    x[-3:] = tail.to("cuda", d)
+    w = data(g, K, N, dtype=d, std=K ** -0.5)
+    want = tail @ w
+    tol = (K + 8) * E32 * (tail.abs() @ w.abs()) + 1.01 * U["bf16"] * want.abs()
+    y = ops.linear(x, w.to("cuda", d))
+    close(y[-3:], want, tol, "linear")
+    assert not y[:-3].any()
+    off = torch.tensor([0, 5, M], dtype=torch.int32, device="cuda")
+    we = torch.stack([torch.zeros_like(w), w]).to("cuda", d)
+    close(ops.grouped_linear(x, we, off)[-3:], want, tol, "grouped rows")
+    n = ops.layer_norm(x)[0]
+    xh = (tail - tail.mean(1, keepdim=True)) / (tail.var(1, unbiased=False, keepdim=True) + 1e-5).sqrt()
+    assert (n[-3:].double().cpu() - xh).abs().max() < 4 * U["bf16"] * xh.abs().max()
+    assert not n[:-3].any()
+    dy = torch.zeros(M, N, dtype=d, device="cuda")
+    dt_ = data(g, 3, N, dtype=d)
+    dy[-3:] = dt_.to("cuda", d)
+    dx, dw, db = ops.linear_backward(dy, x, w.to("cuda", d))
+    check_backward(tail, w, dt_, torch.zeros_like(dt_), "none", "bf16", dx[-3:], None, None)
+    want = tail.t() @ dt_
+    close(dw, want, (M + 8) * E32 * (tail.abs().t() @ dt_.abs()) + 1.01 * U["bf16"] * want.abs(), "dw")
+    assert not dx[:-3].any()
+    del x, n, dx, y
+    E, K, N = 35, 8192, 8192     # w: 2.35e9 elements
+    we = torch.zeros(E, K, N, dtype=d, device="cuda")
+    w = torch.randn(K, N, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") * K ** -0.5
+    we[-1] = w.to(d)
+    xs = data(g, 4, K, dtype=d)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = 4
+    got = ops.grouped_linear(xs.to("cuda", d), we, off)
+    wd = we[-1].double()
+    xd = xs.cuda()
+    want = xd @ wd
+    close(got, want.cpu(), ((K + 8) * E32 * (xd.abs() @ wd.abs()) + 1.01 * U["bf16"] * want.abs()).cpu(), "last expert")
 
 
 def test_refusals(ops):

@@ -437,6 +437,12 @@ int64_t backward_ws(int dtype, int64_t M, int64_t K, int64_t N, int E, bool alig
     return n;
 }
 
+// Partial sums of the norm's backward pass, unless one block has it all.
+int64_t norm_ws(int64_t M, int64_t N) {
+    const int blocks = norm_backward_blocks(M, N);
+    return blocks > 1 ? (int64_t)blocks * N * 8 : 0;
+}
+
 int check_ws(const void *ws, int64_t have, int64_t need) {
     if (need == 0) return CP_OK;
     if (!ws || have < need)
@@ -617,7 +623,7 @@ int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_
         case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E, aligned != 0);
         case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0, aligned != 0);
         case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E, aligned != 0);
-        case CP_OP_LAYER_NORM_BACKWARD: return (int64_t)norm_backward_blocks(M) * N * 8;
+        case CP_OP_LAYER_NORM_BACKWARD: return norm_ws(M, N);
     }
     return fail(CP_ERR_INVALID_ARG, "operator code %d", op);
 }
@@ -705,8 +711,8 @@ int cp_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, 
     CP_TRY(check_vector(dw, dtype, "dw"));
     CP_TRY(check_vector(db, dtype, "db"));
     NormArgs a{};
-    a.blocks = norm_backward_blocks(M);
-    CP_TRY(check_ws(ws, ws_bytes, (int64_t)a.blocks * N * 8));
+    a.blocks = norm_backward_blocks(M, N);
+    CP_TRY(check_ws(ws, ws_bytes, norm_ws(M, N)));
     a.x = (const char *)X;
     a.dy = (const char *)dY;
     a.w = (const char *)w;

@@ -65,7 +65,8 @@ struct NormArgs {
     float eps;
 };
 hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s);
-int norm_backward_blocks(int64_t M);  // partial sums: one per block
+constexpr int64_t kNormOneBlock = 8192;  // elements that one block takes on its own (such rows fit its registers)
+int norm_backward_blocks(int64_t M, int64_t N);  // partial sums: one per block
 hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s);
 
 }  // namespace cpo

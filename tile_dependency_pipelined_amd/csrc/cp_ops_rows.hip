@@ -436,7 +436,7 @@ __global__ __launch_bounds__(THREADS *SUBS) void norm_backward_kernel(NormArgs a
             }
         }
     }
-    auto flush = [&](const float(&v)[VPT][CE], float *dst) {
+    auto flush = [&](const float(&v)[VPT][CE], float *dst, char *out) {
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
             if (s > 0) __syncthreads();
@@ -450,7 +450,10 @@ __global__ __launch_bounds__(THREADS *SUBS) void norm_backward_kernel(NormArgs a
                         if constexpr (SUBS > 1)
                             if (s > 0) sum += total[c];
                         if (s + 1 == SUBS) {
-                            if (c < a.N) dst[c] = sum;
+                            if (c < a.N) {
+                                if (a.blocks == 1) reinterpret_cast<T *>(out)[c] = from_f32<T>(sum);
+                                else dst[c] = sum;
+                            }
                         } else if constexpr (SUBS > 1) {
                             total[c] = sum;
                         }
@@ -459,8 +462,8 @@ __global__ __launch_bounds__(THREADS *SUBS) void norm_backward_kernel(NormArgs a
         if (SUBS > 1) __syncthreads();
     };
     float *pw = a.ws + (int64_t)blockIdx.x * a.N;
-    if (a.dw) flush(dw, pw);
-    if (a.db) flush(db, pw + (int64_t)a.blocks * a.N);
+    if (a.dw) flush(dw, pw, a.dw);
+    if (a.db) flush(db, pw + (int64_t)a.blocks * a.N, a.db);
 }
 
 // Rows too long for registers: dX by rows ...
@@ -637,7 +640,7 @@ hipError_t norm_backward_all(const NormArgs &a, hipStream_t s) {
         const hipError_t e = a.vec ? norm_backward<T, true>(a, s) : norm_backward<T, false>(a, s);
         if (e != hipSuccess) return e;
     }
-    if (a.dw || a.db) {
+    if ((a.dw || a.db) && a.blocks != 1) {
         const int cb = (a.N + 63) / 64;
         hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_join_kernel<T>), dim3((unsigned)(2 * cb)), dim3(1024), 0, s, a, cb);
     }
@@ -667,7 +670,13 @@ hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s) {
     return a.vec ? norm<float, true>(a, s) : norm<float, false>(a, s);
 }
 
-int norm_backward_blocks(int64_t M) { return (int)(M < 256 ? M : 256); }
+// One block, which stores the sums itself, where two launches would take longer
+// than its rows; otherwise at least two.
+int norm_backward_blocks(int64_t M, int64_t N) {
+    if (M == 0) return 0;
+    if (M * N <= kNormOneBlock) return 1;
+    return (int)(M < 2 ? 2 : M < 256 ? M : 256);
+}
 
 hipError_t launch_norm_backward(int dtype, const NormArgs &a, hipStream_t s) {
     return dtype == CP_BF16 ? norm_backward_all<__bf16>(a, s) : norm_backward_all<float>(a, s);
