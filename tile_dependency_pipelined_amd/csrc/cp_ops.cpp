@@ -566,6 +566,7 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         const Shape rows{dtype, kNN, E ? kGroupRows : kDense, M, N, K, E};
         a.tiles = (int)max_row_tiles(rows, kGradRows);
         a.vec = aligned16(dy, dtype) && (act == CP_ACT_NONE || aligned16(z, dtype));
+        a.final = !E && a.tiles == 1;
         CP_TRY(launched(launch_grad(dtype, a, s), "activation gradient"));
     }
     const Shape sx = dx_shape(dtype, M, K, N, E, wt), sw = dw_shape(dtype, M, K, N, E, wt);
@@ -594,12 +595,12 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         GemmArgs gx, gw;
         const int64_t nx = launch_args(px, {both, 1}, split, gx), nw = launch_args(pw, {both, 1}, split, gw);
         if (nx < 0 || nw < 0) return (int)(nx < 0 ? nx : nw);
-        const int nd = db ? grad_join_blocks(a) : 0;
+        const int nd = db && !a.final ? grad_join_blocks(a) : 0;
         return launched((dtype == CP_BF16 ? launch_gradients_bf16 : launch_gradients_f32)(sx.layout, both, gx, (int)nx, gw,
                                                                                          (int)nw, a, nd, s),
                         "gradients");
     }
-    if (db && N > 0) CP_TRY(launched(launch_grad_join(dtype, a, s), "bias gradient"));
+    if (db && N > 0 && !a.final) CP_TRY(launched(launch_grad_join(dtype, a, s), "bias gradient"));
     if (dX) CP_TRY(run_product(px, split, s));
     if (dW) CP_TRY(run_product(pw, split, s));
     return CP_OK;

@@ -327,6 +327,7 @@ struct GradArgs {
     int64_t ldd, ldp, ldz;
     const int32_t *off;
     int32_t groups, M, N, act, tiles, vec;
+    int32_t final;         // the only row tile: its sums are db
 };
 constexpr int kGradRows = 32;  // rows of a partial column sum
 

@@ -135,7 +135,9 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += part[i][c];
-        if (gc < a.N) a.ws[(int64_t)rt * a.N + gc] = v;
+        if (gc >= a.N) continue;
+        if (a.final) reinterpret_cast<T *>(a.db)[gc] = from_f32<T>(v);
+        else a.ws[(int64_t)rt * a.N + gc] = v;
     }
 }
 
