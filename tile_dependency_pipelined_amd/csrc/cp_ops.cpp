@@ -365,17 +365,23 @@ double gradients_time(const Shape &x, const Shape &w, Config c) {
     }
 }
 
+// Time of dX alone where it has few rows (its weights' bytes).
+double few_rows_time(const Shape &x, const Choice &c) {
+    const double experts = x.mode == kGroupRows ? (double)(x.M < x.groups ? x.M : x.groups) : 1.0;
+    return 6.0 + experts * (double)x.N * (double)x.K * elem_size(x.dtype) / 4.8e6 + (c.nsplit > 1 ? 4.0 : 0.0);
+}
+
 // The configuration of one launch for both gradients, or kConfigs if two are
 // better (4099 x 2048 x 4096 over 8 experts, bf16: 210 us in two, 171 in one).
 Config choose_gradients(const Shape &x, const Shape &w) {
-    if (few_rows(x)) return kConfigs;
     const Choice cx = choose(x), cw = choose(w);
-    if (cx.nsplit > 1 || cw.nsplit > 1) return kConfigs;
+    const bool few = few_rows(x);
+    if ((!few && cx.nsplit > 1) || cw.nsplit > 1) return kConfigs;
     auto alone = [](const Shape &s, Config c) {
         return (s.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0) *
                launch_time(c, s.dtype, average_tiles(s, c), (double)slabs_of(s));
     };
-    double least = alone(x, cx.cfg) + alone(w, cw.cfg);
+    double least = (few ? few_rows_time(x, cx) : alone(x, cx.cfg)) + alone(w, cw.cfg);
     Config best = kConfigs;
     for (const Config c : {kTile256, kTile128x256, kTile128, kTile64x128, kTile64}) {
         if (x.dtype == CP_F32 && c < kTile128) continue;
@@ -590,7 +596,9 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     pw.C = dw;
     pw.sc = E > 1 ? stride_dw : 0;
     pw.off = off;
-    const Config both = dX && dW && M > 0 && K > 0 && N > 0 ? choose_gradients(sx, sw) : kConfigs;
+    // (of few rows, dX is not worth a copy of W)
+    const bool w_ready = !few_rows(sx) || (aligned16(w, dtype) && sb * es % 16 == 0);
+    const Config both = dX && dW && M > 0 && K > 0 && N > 0 && w_ready ? choose_gradients(sx, sw) : kConfigs;
     if (both != kConfigs) {
         GemmArgs gx, gw;
         const int64_t nx = launch_args(px, {both, 1}, split, gx), nw = launch_args(pw, {both, 1}, split, gw);

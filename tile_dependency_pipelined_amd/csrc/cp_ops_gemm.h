@@ -125,7 +125,10 @@ struct Operand {
         return LOADS >= NW ? q * NW + wave : wave % LOADS;
     }
 
-    __device__ __forceinline__ void init(const char *b, int64_t ld_elems, int outer_, int klen_, int wave, int lane) {
+    // `again`: rows past the last one read that again (their results are not
+    // stored) instead of zeros.
+    __device__ __forceinline__ void init(const char *b, int64_t ld_elems, int outer_, int klen_, int wave, int lane,
+                                         bool again) {
         base = b;
         ld = ld_elems * ES;
         outer = outer_ < R ? outer_ : R;
@@ -135,7 +138,7 @@ struct Operand {
             const int o = load_id(q, wave) * 1024 + lane * 16;
             if constexpr (KC) {
                 const int r = o >> 7, c = ((o >> 4) & 7) ^ swz_kc(r);
-                off[q] = (uint32_t)r * (uint32_t)ld + (uint32_t)c * 16u;
+                off[q] = (uint32_t)(again && r >= outer ? outer - 1 : r) * (uint32_t)ld + (uint32_t)c * 16u;
                 kc = c * CE;
             } else {
                 const int k = o / RB, c = ((o % RB) >> 4) ^ swz_out(k);
@@ -183,7 +186,7 @@ struct Operand {
     __device__ __forceinline__ void fetch(uint4 (&v)[PW], int s, int wave, int lane) const {
         const int k0 = s * BK, left = klen - k0;
         const char *p = base + (KC ? (int64_t)k0 * ES : (int64_t)k0 * ld);
-        if (left >= BK && outer == R) {  // uniform
+        if (left >= BK && (KC || outer == R)) {  // uniform
 #pragma unroll
             for (int q = 0; q < PW; ++q) __builtin_memcpy(&v[q], p + off[q], 16);
             return;
@@ -192,7 +195,7 @@ struct Operand {
         for (int q = 0; q < PW; ++q) {
             const int o = load_id(q, wave) * 1024 + lane * 16;
             int n;
-            if constexpr (KC) n = (o >> 7) < outer ? left - kc : 0;
+            if constexpr (KC) n = left - kc;
             else n = o / RB < left ? outer - (((o % RB) >> 4) ^ swz_out(o / RB)) * CE : 0;
             v[q] = load_partial<T>(p + off[q], n);
         }
@@ -343,9 +346,9 @@ struct Product {
             OpA a;
             OpB w;
             a.init(A + ((AKC ? (int64_t)row0 * g.lda + k_first : (int64_t)k_first * g.lda + row0)) * (int64_t)sizeof(T),
-                   g.lda, row_end - row0, klen, wave, lane);
+                   g.lda, row_end - row0, klen, wave, lane, !DIRECT);
             w.init(B + ((BKC ? (int64_t)col0 * g.ldb + k_first : (int64_t)k_first * g.ldb + col0)) * (int64_t)sizeof(T),
-                   g.ldb, g.N - col0, klen, wave, lane);
+                   g.ldb, g.N - col0, klen, wave, lane, !DIRECT);
             struct Frags {
                 uint4 a[FM], b[FN];
             };
@@ -418,16 +421,23 @@ struct Product {
                     if (slab < nk) step(ic<2>{}, slab++);
                 wait_vm<0>();  // the trailing requests land before the LDS is reused
             } else {
-                uint4 ra[OpA::PW], rb[OpB::PW];
-                a.fetch(ra, 0, wave, lane);
-                w.fetch(rb, 0, wave, lane);
-                auto step = [&](char *s, int slab) {
-                    OpA::put(s, ra, wave, lane);
-                    OpB::put(s + OpA::BYTES, rb, wave, lane);
+                // Four slabs in registers on their way to two stages.
+                uint4 ra[4][OpA::PW], rb[4][OpB::PW];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (u < nk) {
+                        a.fetch(ra[u], u, wave, lane);
+                        w.fetch(rb[u], u, wave, lane);
+                    }
+                auto step = [&](auto U, int slab) {
+                    constexpr int u = decltype(U)::value;
+                    char *s = st[u & 1];
+                    OpA::put(s, ra[u], wave, lane);
+                    OpB::put(s + OpA::BYTES, rb[u], wave, lane);
                     __syncthreads();  // also: every wave is done with the other stage's previous slab
-                    if (slab + 1 < nk) {
-                        a.fetch(ra, slab + 1, wave, lane);
-                        w.fetch(rb, slab + 1, wave, lane);
+                    if (slab + 4 < nk) {
+                        a.fetch(ra[u], slab + 4, wave, lane);
+                        w.fetch(rb[u], slab + 4, wave, lane);
                     }
                     Frags f0;
 #pragma unroll
@@ -437,11 +447,15 @@ struct Product {
                     }
                 };
                 int slab = 0;
-                for (; slab + 2 <= nk; slab += 2) {
-                    step(st[0], slab);
-                    step(st[1], slab + 1);
+                for (; slab + 4 <= nk; slab += 4) {
+                    step(ic<0>{}, slab);
+                    step(ic<1>{}, slab + 1);
+                    step(ic<2>{}, slab + 2);
+                    step(ic<3>{}, slab + 3);
                 }
-                if (slab < nk) step(st[0], slab);
+                if (slab < nk) step(ic<0>{}, slab++);
+                if (slab < nk) step(ic<1>{}, slab++);
+                if (slab < nk) step(ic<2>{}, slab++);
             }
             __syncthreads();  // every wave is done with the stages
         }
