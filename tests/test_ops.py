@@ -1,6 +1,7 @@
 """Host tests of the feed-forward operators' C ABI: every declared symbol is
 bound, constants agree with the binding, workspace sizes are host-only, and bad
 arguments give the documented codes before anything is launched."""
+import ctypes
 import os
 import re
 
@@ -12,6 +13,16 @@ HEADER = os.path.join(ROOT, "include", "cp_ops.h")
 nat = pytest.importorskip("tile_dependency_pipelined_amd.native",
                           reason="libcpchain.so not built (python -m tile_dependency_pipelined_amd.build)")
 from tile_dependency_pipelined_amd import ops  # noqa: E402
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_mat, _sizes, _tail = (_vp, _i64), (_i32, _i64, _i64, _i64), (_vp, _i64, _vp)
+for _name, _args in (
+        ("cp_linear", (*_sizes, *_mat, *_mat, _i32, _vp, *_mat, _i32, *_mat, *_mat, *_tail)),
+        ("cp_linear_backward", (*_sizes, *_mat, *_mat, *_mat, _i32, *_mat, _i32, *_mat, *_mat, _vp, *_tail)),
+        ("cp_grouped_linear", (*_sizes, _i32, *_mat, *_mat, _i64, _i32, _vp, _vp, _i32, *_mat, *_mat, *_tail)),
+        ("cp_layer_norm", (_i32, _i64, _i64, *_mat, _vp, _vp, ctypes.c_float, *_mat, _vp, _vp, _vp)),
+        ("cp_layer_norm_backward", (_i32, _i64, _i64, *_mat, *_mat, _vp, _vp, _vp, *_mat, _vp, _vp, *_tail))):
+    getattr(nat.lib(), _name).argtypes = _args
 
 P = 1 << 20  # a plausible, aligned address that no call below may touch
 

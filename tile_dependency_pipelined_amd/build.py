@@ -1,4 +1,5 @@
-"""Build the HIP library libcpchain.so in-tree for gfx950 (MI355X).
+"""Build the HIP library libcpchain.so in-tree for gfx950 (MI355X), and the Python
+module of the feed-forward operators beside it.
 
     python -m tile_dependency_pipelined_amd.build
 
@@ -14,6 +15,7 @@ import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +28,9 @@ SOURCES = [os.path.join(CSRC, n) for n in ("cp_kernels.hip", "cp_chain.cpp", "cp
                                            "cp_ops_gemm_f32.hip", "cp_ops_gradients_bf16.hip",
                                            "cp_ops_gradients_f32.hip", "cp_ops_gemv.hip", "cp_ops_rows.hip",
                                            "cp_ops.cpp")]
+# Python module of the feed-forward operators (torch tensors in and out), linked to LIB
+TORCH_MODULE = os.path.join(PKG, "_cp_ops_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "cp_ops_torch.cpp")
 ARCH = os.environ.get("CP_OFFLOAD_ARCH", "gfx950")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
@@ -41,6 +46,21 @@ def torch_lib_dir():
         return None
     d = os.path.join(list(spec.submodule_search_locations)[0], "lib")
     return d if os.path.exists(os.path.join(d, "libamdhip64.so")) else None
+
+
+def build_torch_module(tdir: str, verbose: bool = True) -> str:
+    """The operators' binding, host code only, against the importable torch."""
+    inc = os.path.join(os.path.dirname(tdir), "include")
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(ROCM, "include"),
+           "-o", TORCH_MODULE + ".tmp", TORCH_SOURCE, "-L" + tdir, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_hip", LIB, "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + tdir]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(TORCH_MODULE + ".tmp", TORCH_MODULE)
+    return TORCH_MODULE
 
 
 def build(verbose: bool = True, extra=None) -> str:
@@ -67,11 +87,13 @@ def build(verbose: bool = True, extra=None) -> str:
     else:
         rl = os.path.join(ROCM, "lib")
         runtime = ["-L" + rl, "-lamdhip64", "-Wl,-rpath," + rl]
-    cmd = ["g++", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objs + runtime + ["-Wl,--no-undefined"]
+    cmd = ["g++", "-shared", "-fPIC", "-Wl,-soname,libcpchain.so", "-o", LIB + ".tmp"] + objs + runtime + ["-Wl,--no-undefined"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    if tdir:
+        build_torch_module(tdir, verbose)
     if verbose:
         print(f"built {LIB} in {time.time() - t0:.1f}s (HIP runtime: {tdir or ROCM})", flush=True)
     return LIB
