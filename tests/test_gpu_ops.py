@@ -236,6 +236,7 @@ OFFSETS = {  # rows, offsets
     "sixty_four": (100, [0] + [min(100, 2 * i) for i in range(64)]),
     "malformed": (90, [5, 30, 10, 200, 60, -3]),
     "wide": (700, [0, 260, 300, 650, 700]),
+    "long": (3000, [0, 1500, 1500, 2990]),
 }
 
 

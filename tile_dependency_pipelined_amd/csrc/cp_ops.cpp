@@ -117,6 +117,9 @@ int64_t max_row_tiles(const Shape &s, int bm) {
     return (s.M + used * (bm - 1)) / bm;
 }
 
+// Rows of all the results together.
+int64_t result_rows(const Shape &s) { return s.M * (s.mode == kGroupSum ? s.groups : 1); }
+
 int64_t slabs_of(const Shape &s) {
     return ceil_div(s.mode == kGroupSum ? ceil_div(s.K, s.groups) : s.K, 128 / elem_size(s.dtype));
 }
@@ -184,7 +187,7 @@ Choice choose_now(const Shape &s) {
         if (s.dtype == CP_F32 && c < kTile128) continue;
         const double tiles = average_tiles(s, c);
         for (int n = 1; n <= 16; ++n) {
-            if (n > 1 && (s.mode != kDense || slabs < 4 * n)) break;
+            if (n > 1 && slabs < 4 * n) break;
             double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n));
             // Each expert's weights are read by few tiles: the smaller the
             // tile, the more of them wait for the same memory (8192 x 4096 x
@@ -193,7 +196,7 @@ Choice choose_now(const Shape &s) {
             if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
             // A split writes and reads its partials, mostly in the caches, and
             // takes another launch.
-            if (n > 1) us += 3.0 + 2.0 * n * (double)s.M * (double)s.N * 4.0 / 8e6;
+            if (n > 1) us += 3.0 + 2.0 * n * (double)result_rows(s) * (double)s.N * 4.0 / 8e6;
             if (us < least) {
                 least = us;
                 best = {c, n};
@@ -280,7 +283,7 @@ struct Packs {
 int64_t split_bytes(const Shape &s) {
     if (s.M == 0 || s.N == 0) return 0;
     const Choice c = choose(s);
-    return c.nsplit > 1 ? (int64_t)c.nsplit * s.M * up(s.N, 8) * 4 : 0;
+    return c.nsplit > 1 ? (int64_t)c.nsplit * result_rows(s) * up(s.N, 8) * 4 : 0;
 }
 
 // The launch of a product with this choice; its operands are aligned unless it

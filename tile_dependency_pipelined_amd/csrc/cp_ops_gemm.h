@@ -280,15 +280,15 @@ struct Product {
         if (g.mode == kGroupRows) ntm = count_tiles(g.off, g.groups, g.M, BM, scan);
         const int tiles = ntm * g.ntn;
         int split = 0;
-        if (g.mode == kGroupSum) {
-            expert = b / tiles;   // experts one after the other, each spread over all XCDs
-            b = xcd_remap(b - expert * tiles, tiles);
-        } else {
-            if (b >= tiles * g.nsplit) return;  // the grid is sized for the most tiles there can be
-            b = xcd_remap(b, tiles * g.nsplit);
-            split = b / tiles;
-            b -= split * tiles;
+        if (g.mode == kGroupSum) {  // experts one after the other, each spread over all XCDs
+            expert = b / (tiles * g.nsplit);
+            b -= expert * tiles * g.nsplit;
+        } else if (b >= tiles * g.nsplit) {
+            return;  // the grid is sized for the most tiles there can be
         }
+        b = xcd_remap(b, tiles * g.nsplit);
+        split = b / tiles;
+        b -= split * tiles;
         const char *A = g.A, *B = g.B, *bias = g.bias;
         char *C = g.C;
         bool zero = false;
@@ -464,7 +464,9 @@ struct Product {
         // that memory is accessed in runs of whole rows of the wave's tile ----
         const int wrow = row0 + wm * WM, wcol = col0 + wn * WN;
         if (g.nsplit > 1) {
-            float *part = g.ws + (int64_t)split * g.M * g.ldws;
+            // (kGroupSum: the experts' rows one after the other)
+            const int64_t above = g.mode == kGroupSum ? (int64_t)split * g.groups + expert : split;
+            float *part = g.ws + above * g.M * g.ldws;
             constexpr int UPR = WN / 4;
             stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
 #pragma unroll

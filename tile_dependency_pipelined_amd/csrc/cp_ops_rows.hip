@@ -35,8 +35,10 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a, PackGrid g) {
 // Y = epilogue(sum over splits of partial); one block per row and 256 units.
 template <class T, int CNT>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_row) {
-    const int row = blockIdx.x / blocks_per_row;
+    const int all = blockIdx.x / blocks_per_row;  // row of the partials
+    const int expert = g.mode == kGroupSum ? all / g.M : 0, row = all - expert * g.M;
     const int col = ((blockIdx.x % blocks_per_row) * 256 + threadIdx.x) * CNT;
+    char *C = g.C + (int64_t)expert * g.sc * sizeof(T);
     const char *bias = g.bias;
     bool zero = false;
     if (g.mode == kGroupRows && bias) {  // the row's expert
@@ -57,8 +59,8 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
     float v[1][CNT];
 #pragma unroll
     for (int i = 0; i < CNT; ++i) v[0][i] = 0.0f;
-    const float *p = g.ws + (int64_t)row * g.ldws + col;
-    const int64_t step = (int64_t)g.M * g.ldws;
+    const float *p = g.ws + (int64_t)all * g.ldws + col;
+    const int64_t step = (int64_t)g.M * g.ldws * (g.mode == kGroupSum ? g.groups : 1);
 #pragma unroll 4
     for (int s = 0; s < g.nsplit; ++s) {
 #pragma unroll
@@ -67,15 +69,17 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
     Raw<T, CNT> b, r;
     if (bias) b.load(bias + (int64_t)col * sizeof(T));
     if (g.res) r.load(g.res + ((int64_t)row * g.ldr + col) * sizeof(T));
-    finish<T, CNT, 1>(g, g.C, row, 0, col, v, bias ? &b : nullptr, g.res ? &r : nullptr, zero, true, true, 0);
+    finish<T, CNT, 1>(g, C, row, 0, col, v, bias ? &b : nullptr, g.res ? &r : nullptr, zero, true, true, 0);
 }
 
 // --------------------------------------------- activation gradient, bias sums
 
-// 32 column units x 8 rows per pass; each block one row tile (kGradRows rows of
-// one expert) and 32 units of columns.
-template <class T, int CNT, int ACT>
+// 32 units of columns x 8 rows per pass; each block one row tile (kGradRows rows
+// of one expert) and 32 units.  Rows that are not aligned are read by unaligned
+// units (VEC false; only a row's last unit by elements), dZ's rows always are.
+template <class T, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
+    constexpr int CNT = kUnit<T>;
     __shared__ float part[8][32 * CNT];
     const int ct = blockIdx.x % col_blocks, rt = blockIdx.x / col_blocks;
     int row0 = rt * kGradRows, end = a.M;
@@ -92,21 +96,30 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
     float sum[CNT];
 #pragma unroll
     for (int i = 0; i < CNT; ++i) sum[i] = 0.0f;
-    if (CNT == 1 && ACT != CP_ACT_NONE && col >= a.N && col < a.ldz)  // the rows of dZ end in zeros
-        for (int row = row0 + r; row < end; row += 8)
-            *reinterpret_cast<T *>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T)) = from_f32<T>(0.0f);
     if (col < a.N) {
         // All rows are requested before the first one's dZ is stored, without
         // a branch in between (past the end the last row, again): with one
         // the compiler waited for each load.
         constexpr int R = kGradRows / 8;
         Raw<T, CNT> dy[R], z[R];
+        auto request = [&](auto &&get) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = row0 + r + 8 * i < end ? row0 + r + 8 * i : end - 1;
-            dy[i].load(a.dy + ((int64_t)row * a.ldd + col) * sizeof(T));
-            if constexpr (ACT != CP_ACT_NONE) z[i].load(a.pre + ((int64_t)row * a.ldp + col) * sizeof(T));
-        }
+            for (int i = 0; i < R; ++i) {
+                const int row = row0 + r + 8 * i < end ? row0 + r + 8 * i : end - 1;
+                dy[i].v = get(a.dy + ((int64_t)row * a.ldd + col) * sizeof(T));
+                if constexpr (ACT != CP_ACT_NONE) z[i].v = get(a.pre + ((int64_t)row * a.ldp + col) * sizeof(T));
+            }
+        };
+        if constexpr (VEC)
+            request([](const char *p) { return *reinterpret_cast<const uint4 *>(p); });
+        else if (col + CNT <= a.N)
+            request([](const char *p) {
+                uint4 v;
+                __builtin_memcpy(&v, p, 16);
+                return v;
+            });
+        else
+            request([&](const char *p) { return load_partial<T>(p, a.N - col); });
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int row = row0 + r + 8 * i;
@@ -116,11 +129,10 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks) {
             if constexpr (ACT != CP_ACT_NONE) {
                 float x[CNT];
                 z[i].unpack(x);
+                // (past the row's end dy is zero, so dZ's rows end in zeros)
 #pragma unroll
                 for (int j = 0; j < CNT; ++j) d[j] *= act_grad(x[j], ACT);
-                char *o = a.dz + ((int64_t)row * a.ldz + col) * sizeof(T);
-                if constexpr (CNT > 1) store_unit<T>(o, d);
-                else *reinterpret_cast<T *>(o) = from_f32<T>(d[0]);
+                store_unit<T>(a.dz + ((int64_t)row * a.ldz + col) * sizeof(T), d);
             }
 #pragma unroll
             for (int j = 0; j < CNT; ++j) sum[j] += d[j];
@@ -551,7 +563,7 @@ template <class T>
 hipError_t join(const GemmArgs &g, hipStream_t s) {
     const int unit = g.vec ? kUnit<T> : 1;
     const int per_row = (g.N + 256 * unit - 1) / (256 * unit);
-    const dim3 grid((unsigned)(g.M * per_row));
+    const dim3 grid((unsigned)((int64_t)g.M * (g.mode == kGroupSum ? g.groups : 1) * per_row));
     if (g.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, kUnit<T>>), grid, dim3(256), 0, s, g, per_row);
     else hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, 1>), grid, dim3(256), 0, s, g, per_row);
     return hipGetLastError();
@@ -559,14 +571,13 @@ hipError_t join(const GemmArgs &g, hipStream_t s) {
 
 template <class T>
 hipError_t grad(const GradArgs &a, hipStream_t s) {
-    const int unit = a.vec ? kUnit<T> : 1;
-    const int cols = (a.N + 32 * unit - 1) / (32 * unit);
+    const int cols = (a.N + 32 * kUnit<T> - 1) / (32 * kUnit<T>);
     if (a.tiles > 0) {
         const dim3 grid((unsigned)(a.tiles * cols));
         auto launch = [&](auto ACT) {
             constexpr int act = decltype(ACT)::value;
-            if (a.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, kUnit<T>, act>), grid, dim3(256), 0, s, a, cols);
-            else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, 1, act>), grid, dim3(256), 0, s, a, cols);
+            if (a.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, act, true>), grid, dim3(256), 0, s, a, cols);
+            else hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_kernel<T, act, false>), grid, dim3(256), 0, s, a, cols);
         };
         if (a.act == CP_ACT_NONE) launch(std::integral_constant<int, CP_ACT_NONE>{});
         else if (a.act == CP_ACT_GELU_TANH) launch(std::integral_constant<int, CP_ACT_GELU_TANH>{});
