@@ -240,6 +240,38 @@ struct Operand {
     }
 };
 
+// What the epilogue needs of the arguments at byte ARG of the kernel's, read
+// again: kept in scalar registers over the main loop they would spill into the
+// vector registers that the accumulators leave (the 256x256 gradients' kernel
+// then spilled those too, 119 -> 174 us for 2048 x 4096 x 4096).
+template <int ARG>
+__device__ __forceinline__ GemmArgs epilogue_args() {
+    typedef const __attribute__((address_space(4))) char *kernarg_t;
+    typedef const __attribute__((address_space(4))) GemmArgs *args_t;
+    kernarg_t p = (kernarg_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    const args_t g = (args_t)(p + ARG);
+    GemmArgs e{};
+    e.C = g->C;
+    e.bias = g->bias;
+    e.res = g->res;
+    e.pre = g->pre;
+    e.ws = g->ws;
+    e.ldc = g->ldc;
+    e.ldr = g->ldr;
+    e.ldp = g->ldp;
+    e.sc = g->sc;
+    e.groups = g->groups;
+    e.mode = g->mode;
+    e.M = g->M;
+    e.N = g->N;
+    e.act = g->act;
+    e.nsplit = g->nsplit;
+    e.ldws = g->ldws;
+    e.vec = g->vec;
+    return e;
+}
+
 // Tile BM x BN, wave grid WGM x WGN, S LDS stages.  DIRECT: loads straight to
 // LDS (16-byte aligned operands); otherwise through registers, two stages.
 template <class T_, int BM_, int BN_, int WGM_, int WGN_, int S_, bool AKC_, bool BKC_, bool DIRECT_>
@@ -268,7 +300,9 @@ struct Product {
     // of the 512 leave room for one
     static constexpr int WAVES = FM * FN * 4 > 128 ? 1 : 2;
 
-    // `b`: which of the launch's workgroups for this product.
+    // `b`: which of the launch's workgroups for this product.  `ARG`: where
+    // the kernel's arguments hold `g` (bytes).
+    template <int ARG>
     __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4], int b) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -289,8 +323,7 @@ struct Product {
         b = xcd_remap(b, tiles * g.nsplit);
         split = b / tiles;
         b -= split * tiles;
-        const char *A = g.A, *B = g.B, *bias = g.bias;
-        char *C = g.C;
+        const char *A = g.A, *B = g.B;
         bool zero = false;
         int first = 0;  // rows before the expert's
         if (g.mode == kGroupRows) {
@@ -302,17 +335,12 @@ struct Product {
             b -= t.before * g.ntn;
             ntm = (t.end - t.row0 + BM - 1) / BM;
             zero = expert == g.groups;  // rows without an expert
-            if (zero) {
-                klen = 0;
-            } else {
-                B += (int64_t)expert * g.sb * sizeof(T);
-                if (bias) bias += (int64_t)expert * g.N * sizeof(T);
-            }
+            if (zero) klen = 0;
+            else B += (int64_t)expert * g.sb * sizeof(T);
         } else if (g.mode == kGroupSum) {
             const RowTile t = expert_rows(g.off, g.groups, g.K, expert);
             k_first = t.row0;
             klen = t.end - t.row0;
-            C += (int64_t)expert * g.sc * sizeof(T);
         }
         // Bands of 8 row tiles, row tiles fastest: the ~32 tiles an XCD works
         // on at a time form a near-square block, which reads least into its L2.
@@ -462,25 +490,30 @@ struct Product {
 
         // ---- epilogue: 16 rows at a time through this wave's part of LDS, so
         // that memory is accessed in runs of whole rows of the wave's tile ----
+        const GemmArgs e = epilogue_args<ARG>();
         const int wrow = row0 + wm * WM, wcol = col0 + wn * WN;
-        if (g.nsplit > 1) {
+        char *C = e.C;
+        const char *bias = e.bias;
+        if (e.mode == kGroupSum) C += (int64_t)expert * e.sc * sizeof(T);
+        if (e.mode == kGroupRows && bias && !zero) bias += (int64_t)expert * e.N * sizeof(T);
+        if (e.nsplit > 1) {
             // (kGroupSum: the experts' rows one after the other)
-            const int64_t above = g.mode == kGroupSum ? (int64_t)split * g.groups + expert : split;
-            float *part = g.ws + above * g.M * g.ldws;
+            const int64_t above = e.mode == kGroupSum ? (int64_t)split * e.groups + expert : split;
+            float *part = e.ws + above * e.M * e.ldws;
             constexpr int UPR = WN / 4;
             stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
 #pragma unroll
                 for (int i = 0; i < 16 * UPR / 64; ++i) {
                     const int u = i * 64 + lane, r = wrow + fm * 16 + u / UPR, c = (u % UPR) * 4;
-                    if (r < row_end && wcol + c < g.ldws)  // ldws is a multiple of 4
-                        *reinterpret_cast<f32x4_t *>(part + (int64_t)r * g.ldws + wcol + c) =
+                    if (r < row_end && wcol + c < e.ldws)  // ldws is a multiple of 4
+                        *reinterpret_cast<f32x4_t *>(part + (int64_t)r * e.ldws + wcol + c) =
                             *reinterpret_cast<const f32x4_t *>(sh + u / UPR * EPI_PITCH + c);
                 }
             });
-        } else if (g.vec) {
-            finish_tile<kUnit<T>>(g, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+        } else if (e.vec) {
+            finish_tile<kUnit<T>>(e, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
         } else {
-            finish_tile<1>(g, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+            finish_tile<1>(e, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
         }
     }
 
@@ -573,7 +606,7 @@ struct Product {
 template <class P>
 __global__ __launch_bounds__(P::NT, P::WAVES) void product_kernel(GemmArgs g) {
     CPO_STAGES(P);
-    P::run(g, st, blockIdx.x);
+    P::template run<0>(g, st, blockIdx.x);
 }
 
 // A layer's gradients in one launch: the tiles of dX (nx workgroups), of dW
@@ -584,8 +617,9 @@ __global__ __launch_bounds__(PX::NT, PX::WAVES) void gradients_kernel(GemmArgs x
     static_assert(PX::NT == PW::NT && PX::STAGE == PW::STAGE && PX::S == PW::S, "one shape of workgroup");
     CPO_STAGES(PX);
     const int b = blockIdx.x;
-    if (b < nx) PX::run(x, st, b);
-    else if (b < nx + nw) PW::run(w, st, b - nx);
+    static_assert(sizeof(GemmArgs) % 8 == 0, "the second argument follows the first");
+    if (b < nx) PX::template run<0>(x, st, b);
+    else if (b < nx + nw) PW::template run<sizeof(GemmArgs)>(w, st, b - nx);
     else join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
 }
 
