@@ -540,3 +540,57 @@ def test_refusals(ops):
         with pytest.raises(kind):
             call()
             say("not refused:", i)
+
+
+# More than one round of large tiles, the last one at most half full, with
+# ragged edges: its tiles are computed in halves, some of them without a row.
+# Compared at some rows, with those on both sides of the halves' borders.
+def some_rows(M):
+    return sorted({r for r in range(0, M, 23)} | {r for k in range(0, M + 1, 128) for r in (k - 1, k) if 0 <= r < M} | {M - 1})
+
+
+@pytest.mark.parametrize("wt", [False, True])
+def test_linear_rounds(ops, wt):
+    M, K, N = 4200, 2056, 4312
+    g = torch.Generator().manual_seed(11 + wt)
+    d = torch.bfloat16
+    x, w, b, r = (data(g, *s, dtype=d, std=sd) for s, sd in (((M, K), 1), ((K, N), K ** -0.5), ((N,), 1), ((M, N), 1)))
+    dw = place(w.t().contiguous(), d, 8).t() if wt else place(w, d, 8)
+    y, pre = ops.linear(place(x, d, 8), dw, b.to("cuda", d), residual=place(r, d, 8), act=ops.ACTS["gelu_tanh"], need_pre=True)
+    s = some_rows(M)
+    z = x[s] @ w + b
+    want = act(z, "gelu_tanh") + r[s]
+    ty, tz = forward_tol(x[s], w, b, z, want, "gelu_tanh", "bf16")
+    close(y[s], want, ty + 4 * E32 * r[s].abs(), "y")
+    close(pre[s], z, tz, "pre")
+
+
+@pytest.mark.parametrize("wt", [False, True])
+def test_linear_gradient_rounds(ops, wt):
+    M, K, N = 2056, 4200, 4312
+    g = torch.Generator().manual_seed(21 + wt)
+    d = torch.bfloat16
+    x, w, dy = data(g, M, K, dtype=d), data(g, K, N, dtype=d, std=N ** -0.5), data(g, M, N, dtype=d)
+    dw_in = place(w.t().contiguous(), d, 8).t() if wt else place(w, d, 8)
+    for need_x, need_w in ((False, True), (True, True)):
+        dx, dw, _ = ops.linear_backward(place(dy, d, 8), place(x, d, 8), dw_in, need_x=need_x, need_w=need_w)
+        s = some_rows(K)
+        check_backward(x[:, s], w[s], dy, dy, "none", "bf16", None if dx is None else dx[:, s], dw[s], None)
+
+
+@pytest.mark.parametrize("wt", [False, True])
+def test_grouped_rounds(ops, wt):
+    T, K, N, off = 4400, 2056, 4312, [0, 700, 700, 1900, 3180, 4390]
+    g = torch.Generator().manual_seed(31 + wt)
+    E, d = len(off) - 1, torch.bfloat16
+    x, w, b = data(g, T, K, dtype=d), data(g, E, K, N, dtype=d, std=K ** -0.5), data(g, E, N, dtype=d)
+    doff = torch.tensor(off, dtype=torch.int32, device="cuda")
+    dwt = place(w.transpose(1, 2).contiguous(), d).transpose(1, 2) if wt else place(w, d)
+    y, pre = ops.grouped_linear(place(x, d, 8), dwt, doff, b.to("cuda", d), act=ops.ACTS["silu"], need_pre=True)
+    for e in range(E):
+        s = [off[e] + r for r in some_rows(off[e + 1] - off[e])] if off[e + 1] > off[e] else []
+        z = x[s] @ w[e] + b[e]
+        ty, tz = forward_tol(x[s], w[e], b[e], z, act(z, "silu"), "silu", "bf16")
+        close(y[s], act(z, "silu"), ty, f"y {e}")
+        close(pre[s], z, tz, f"pre {e}")
+    assert not y[off[-1]:].any() and not pre[off[-1]:].any()

@@ -27,7 +27,6 @@ int launched(hipError_t e, const char *what) {
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int kComputeUnits = 256;
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -138,7 +137,8 @@ double average_tiles(const Shape &s, Config c) {
     return tm * (double)ceil_div(s.N, t.bn) * (s.mode == kGroupSum ? s.groups : 1);
 }
 
-// Time in microseconds of one launch of `tiles` tiles with `slabs` slabs each,
+// Time in microseconds of one launch of `tiles` tiles with `slabs` slabs each
+// (`halves`: with the last round of 256x256 tiles in halves where that fits),
 // from the rounds the device takes: a time per slab, which grows with the share
 // of the CUs that are busy (they share memory and power), and a fixed time.
 // Fitted to bf16 products with the weights coming from memory (rows x columns x
@@ -150,13 +150,18 @@ double average_tiles(const Shape &s, Config c) {
 //   2048 x 4096 x 4096   84 | 62 | 63     2048 x 8192 x 8192 213 | 248 | 268
 //   4096 x 4096 x 4096  107 | 125 | 137   8192 x 4096 x 2048 114 | 130 | 130
 // and to fp32: 512 x 2048 x 1024 64 us with 128x128, 36 with 64x128, 23 with 64x64.
-double launch_time(Config c, int dtype, double tiles, double slabs) {
+double launch_time(Config c, int dtype, double tiles, double slabs, bool halves) {
     const double cus = tiles / kComputeUnits;  // tiles per CU
     const double busy = cus < 1.0 ? cus : 1.0;
     const double rounds = (double)(int64_t)(cus + 0.999);
     if (dtype == CP_F32)  // matrix-bound: several tiles on a CU take as many times as long
         return rounds * (c == kTile128 ? 1.9 : c == kTile64x128 ? 0.95 : 0.49) * slabs + 6.0;
-    if (c == kTile256) return rounds * ((1.12 + 0.43 * busy) * slabs + 10.0);
+    if (c == kTile256) {
+        const double rest = tiles - kComputeUnits * (rounds - 1.0);
+        if (halves && rounds > 1.0 && rest <= kComputeUnits / 2)
+            return (rounds - 1.0) * (1.55 * slabs + 10.0) + launch_time(kTile128x256, dtype, 2.0 * rest, slabs, false);
+        return rounds * ((1.12 + 0.43 * busy) * slabs + 10.0);
+    }
     if (c == kTile128x256) return rounds * ((0.66 + 0.21 * busy) * slabs + 7.0);
     // two on a CU; a CU that is left with one runs it faster
     const double one = c == kTile128 ? 0.58 : c == kTile64x128 ? 0.31 : 0.19;
@@ -188,7 +193,7 @@ Choice choose_now(const Shape &s) {
         const double tiles = average_tiles(s, c);
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && slabs < 4 * n) break;
-            double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n));
+            double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n), s.mode != kGroupSum);
             // Each expert's weights are read by few tiles: the smaller the
             // tile, the more of them wait for the same memory (8192 x 4096 x
             // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
@@ -287,8 +292,9 @@ int64_t split_bytes(const Shape &s) {
 }
 
 // The launch of a product with this choice; its operands are aligned unless it
-// is of few rows.  Returns the number of workgroups, or an error.
-int64_t launch_args(const Product &p, const Choice &c, void *split, GemmArgs &g) {
+// is of few rows; `alone` in its launch.  Returns the number of workgroups, or
+// an error.
+int64_t launch_args(const Product &p, const Choice &c, void *split, GemmArgs &g, bool alone) {
     const Shape &s = p.s;
     const int es = elem_size(s.dtype);
     g = GemmArgs{};
@@ -323,6 +329,8 @@ int64_t launch_args(const Product &p, const Choice &c, void *split, GemmArgs &g)
     if (grid > 0x3FFFFFFF) return fail(CP_ERR_SHAPE, "too many tiles (%lld)", (long long)grid);
     g.ntm = (int)ntm;
     g.ntn = (int)ntn;
+    if (c.cfg == kTile256 && s.mode != kGroupSum && alone)  // (kGroupRows: any number of tiles up to `grid`)
+        return grid + (s.mode == kGroupRows ? kComputeUnits / 2 : halved_tiles((int)grid));
     return grid;
 }
 
@@ -332,7 +340,7 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
     if (s.M == 0 || s.N == 0) return CP_OK;
     const Choice c = choose(s);
     GemmArgs g;
-    const int64_t grid = launch_args(p, c, split, g);
+    const int64_t grid = launch_args(p, c, split, g, true);
     if (grid < 0) return (int)grid;
     if (c.cfg == kGemv) return launched(launch_gemv(s.dtype, s.layout == kNT, g, stream), "product of few rows");
     const bool direct = c.cfg != kTile16 || (aligned16(p.A, s.dtype) && aligned16(p.B, s.dtype) &&
@@ -349,8 +357,8 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
 double gradients_time(const Shape &x, const Shape &w, Config c) {
     const int slots = kComputeUnits * (x.dtype == CP_BF16 && c >= kTile128 ? 2 : 1);
     const double penalty = x.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0;
-    const double tx = penalty * launch_time(c, x.dtype, slots, (double)slabs_of(x));
-    const double tw = penalty * launch_time(c, w.dtype, slots, (double)slabs_of(w));
+    const double tx = penalty * launch_time(c, x.dtype, slots, (double)slabs_of(x), false);
+    const double tw = penalty * launch_time(c, w.dtype, slots, (double)slabs_of(w), false);
     const int64_t nx = (int64_t)(average_tiles(x, c) + 0.5), nw = (int64_t)(average_tiles(w, c) + 0.5);
     const double t0 = (double)(nx / slots) * tx;  // most slots are done with dX
     const double late = (double)(nx % slots);     // these have one more of its tiles
@@ -382,7 +390,7 @@ Config choose_gradients(const Shape &x, const Shape &w) {
     if ((!few && cx.nsplit > 1) || cw.nsplit > 1) return kConfigs;
     auto alone = [](const Shape &s, Config c) {
         return (s.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0) *
-               launch_time(c, s.dtype, average_tiles(s, c), (double)slabs_of(s));
+               launch_time(c, s.dtype, average_tiles(s, c), (double)slabs_of(s), s.mode != kGroupSum);
     };
     double least = (few ? few_rows_time(x, cx) : alone(x, cx.cfg)) + alone(w, cw.cfg);
     Config best = kConfigs;
@@ -604,7 +612,8 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     const Config both = dX && dW && M > 0 && K > 0 && N > 0 && w_ready ? choose_gradients(sx, sw) : kConfigs;
     if (both != kConfigs) {
         GemmArgs gx, gw;
-        const int64_t nx = launch_args(px, {both, 1}, split, gx), nw = launch_args(pw, {both, 1}, split, gw);
+        const int64_t nx = launch_args(px, {both, 1}, split, gx, false),
+                      nw = launch_args(pw, {both, 1}, split, gw, false);
         if (nx < 0 || nw < 0) return (int)(nx < 0 ? nx : nw);
         const int nd = db && !a.final ? grad_join_blocks(a) : 0;
         return launched((dtype == CP_BF16 ? launch_gradients_bf16 : launch_gradients_f32)(sx.layout, both, gx, (int)nx, gw,

@@ -319,6 +319,14 @@ __device__ __forceinline__ int xcd_remap(int b, int n) {
     return x * q + (x < r ? x : r) + (b >> 3);
 }
 
+// Of `units` tiles of 256 x 256, how many are computed as two halves each: the
+// last round's, if its halves fit the device.
+constexpr int kComputeUnits = 256;
+__host__ __device__ constexpr int halved_tiles(int units) {
+    const int rest = units % kComputeUnits;
+    return 2 * rest <= kComputeUnits ? rest : 0;
+}
+
 // dZ = dY act'(pre) and column sums of it per expert (dense: groups = 1, off null)
 struct GradArgs {
     const char *dy, *pre;

@@ -272,6 +272,19 @@ __device__ __forceinline__ GemmArgs epilogue_args() {
     return e;
 }
 
+// Where a workgroup keeps its stages of A and B, and the rows of its epilogue.
+struct Stages {
+    char *a[4], *b[4], *rows;
+};
+
+// Which of a launch's tiles a workgroup computes: `unit` counts the tiles of
+// split after split, for kGroupSum those of `expert`.
+struct Place {
+    int unit, expert, half;
+    int ntm;         // row tiles
+    GroupScan scan;  // kGroupRows
+};
+
 // Tile BM x BN, wave grid WGM x WGN, S LDS stages.  DIRECT: loads straight to
 // LDS (16-byte aligned operands); otherwise through registers, two stages.
 template <class T_, int BM_, int BN_, int WGM_, int WGN_, int S_, bool AKC_, bool BKC_, bool DIRECT_>
@@ -300,40 +313,45 @@ struct Product {
     // of the 512 leave room for one
     static constexpr int WAVES = FM * FN * 4 > 128 ? 1 : 2;
 
-    // `b`: which of the launch's workgroups for this product.  `ARG`: where
-    // the kernel's arguments hold `g` (bytes).
-    template <int ARG>
-    __device__ __forceinline__ static void run(const GemmArgs &g, char *const (&st)[4], int b) {
+    // Workgroup `b`'s place in a launch with one workgroup to a tile; false if it has none.
+    __device__ __forceinline__ static bool place(const GemmArgs &g, int b, Place &p) {
+        p.ntm = g.ntm;
+        p.expert = p.half = 0;
+        if (g.mode == kGroupRows) p.ntm = count_tiles(g.off, g.groups, g.M, BM, p.scan);
+        const int units = p.ntm * g.ntn * g.nsplit;
+        if (g.mode == kGroupSum) {  // experts one after the other, each spread over all XCDs
+            p.expert = b / units;
+            b -= p.expert * units;
+        } else if (b >= units) {
+            return false;  // the grid is sized for the most tiles there can be
+        }
+        p.unit = xcd_remap(b, units);
+        return true;
+    }
+
+    // `ARG`: where the kernel's arguments hold `g` (bytes).  `TM`: rows of the
+    // tiles that `at` counts; this one is the `at.half`-th part of such a tile.
+    template <int ARG, int TM = BM>
+    __device__ __forceinline__ static void run(const GemmArgs &g, const Stages &st, const Place &at) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
 
         // ---- which tile ----
-        int ntm = g.ntm, expert = 0, row0, row_end = g.M, k_first = 0, klen = g.K;
-        GroupScan scan{};
-        if (g.mode == kGroupRows) ntm = count_tiles(g.off, g.groups, g.M, BM, scan);
-        const int tiles = ntm * g.ntn;
-        int split = 0;
-        if (g.mode == kGroupSum) {  // experts one after the other, each spread over all XCDs
-            expert = b / (tiles * g.nsplit);
-            b -= expert * tiles * g.nsplit;
-        } else if (b >= tiles * g.nsplit) {
-            return;  // the grid is sized for the most tiles there can be
-        }
-        b = xcd_remap(b, tiles * g.nsplit);
-        split = b / tiles;
-        b -= split * tiles;
+        int ntm = at.ntm, expert = at.expert, row0, row_end = g.M, k_first = 0, klen = g.K;
+        const int split = at.unit / (ntm * g.ntn);
+        int b = at.unit - split * ntm * g.ntn;
         const char *A = g.A, *B = g.B;
         bool zero = false;
         int first = 0;  // rows before the expert's
         if (g.mode == kGroupRows) {
             // expert by expert: its tiles are next to each other
-            const RowTile t = find_tile(g.off, g.groups, g.M, BM, b / g.ntn, scan);
+            const RowTile t = find_tile(g.off, g.groups, g.M, TM, b / g.ntn, at.scan);
             expert = t.expert;
             first = t.row0;
             row_end = t.end;
             b -= t.before * g.ntn;
-            ntm = (t.end - t.row0 + BM - 1) / BM;
+            ntm = (t.end - t.row0 + TM - 1) / TM;
             zero = expert == g.groups;  // rows without an expert
             if (zero) klen = 0;
             else B += (int64_t)expert * g.sb * sizeof(T);
@@ -350,7 +368,7 @@ struct Product {
         const int nt = __builtin_amdgcn_readfirstlane(inband / high);
         const int mt = __builtin_amdgcn_readfirstlane(band * BAND + inband % high);
         const int col0 = nt * BN;
-        row0 = first + mt * BM;
+        row0 = first + mt * TM + (TM > BM ? at.half * BM : 0);
         if (g.nsplit > 1) {  // whole slabs per split
             const int slabs = (klen + BK - 1) / BK, per = (slabs + g.nsplit - 1) / g.nsplit;
             const int from = split * per * BK;
@@ -362,6 +380,7 @@ struct Product {
         k_first = __builtin_amdgcn_readfirstlane(k_first);
         row0 = __builtin_amdgcn_readfirstlane(row0);
         row_end = __builtin_amdgcn_readfirstlane(row_end);
+        if (TM > BM && row0 >= row_end) return;
 
         f32x4_t acc[FM][FN];
 #pragma unroll
@@ -381,12 +400,12 @@ struct Product {
                 uint4 a[FM], b[FN];
             };
             const uint32_t abase = OpA::lane_base(wm * WM, lane), bbase = OpB::lane_base(wn * WN, lane);
-            auto load = [&](const char *s, int kk, Frags &f) {
+            auto load = [&](int u, int kk, Frags &f) {
                 const uint32_t ab = LEAN ? fresh(abase) : abase, bb = LEAN ? fresh(bbase) : bbase;
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn) f.b[fn] = OpB::frag(s + OpA::BYTES, bb, kk, fn);
+                for (int fn = 0; fn < FN; ++fn) f.b[fn] = OpB::frag(st.b[u], bb, kk, fn);
 #pragma unroll
-                for (int fm = 0; fm < FM; ++fm) f.a[fm] = OpA::frag(s, ab, kk, fm);
+                for (int fm = 0; fm < FM; ++fm) f.a[fm] = OpA::frag(st.a[u], ab, kk, fm);
             };
             auto mma = [&](const Frags &f) {
 #pragma unroll
@@ -413,28 +432,28 @@ struct Product {
                 // before a slab's last step, when every wave holds all it
                 // needs of that slab, so its stage can be refilled.
                 constexpr bool TRACKED = S == 2;
-                auto issue = [&](char *s, int slab) {
-                    a.template issue<TRACKED>(s, slab, wave);
-                    w.template issue<TRACKED>(s + OpA::BYTES, slab, wave);
+                auto issue = [&](int u, int slab) {
+                    a.template issue<TRACKED>(st.a[u], slab, wave);
+                    w.template issue<TRACKED>(st.b[u], slab, wave);
                 };
                 Frags f0, f1;
                 auto step = [&](auto U, int slab) {
                     constexpr int u = decltype(U)::value;
-                    load(st[u], 1, f1);
+                    load(u, 1, f1);
                     mma(f0);
                     interleave<0, RD, MF, 0>();
                     wait_vm<(S - 2) * PER>();
                     __syncthreads();
-                    issue(st[u], slab + S);
-                    load(st[(u + 1) % S], 0, f0);
+                    issue(u, slab + S);
+                    load((u + 1) % S, 0, f0);
                     mma(f1);
                     interleave<0, RD, MF, TRACKED ? PER : 0>();
                 };
 #pragma unroll
-                for (int u = 0; u < S; ++u) issue(st[u], u);
+                for (int u = 0; u < S; ++u) issue(u, u);
                 wait_vm<(S - 1) * PER>();
                 __syncthreads();
-                load(st[0], 0, f0);
+                load(0, 0, f0);
                 int slab = 0;
                 for (; slab + S <= nk; slab += S) {
                     step(ic<0>{}, slab);
@@ -459,9 +478,8 @@ struct Product {
                     }
                 auto step = [&](auto U, int slab) {
                     constexpr int u = decltype(U)::value;
-                    char *s = st[u & 1];
-                    OpA::put(s, ra[u], wave, lane);
-                    OpB::put(s + OpA::BYTES, rb[u], wave, lane);
+                    OpA::put(st.a[u & 1], ra[u], wave, lane);
+                    OpB::put(st.b[u & 1], rb[u], wave, lane);
                     __syncthreads();  // also: every wave is done with the other stage's previous slab
                     if (slab + 4 < nk) {
                         a.fetch(ra[u], slab + 4, wave, lane);
@@ -470,7 +488,7 @@ struct Product {
                     Frags f0;
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
-                        load(s, kk, f0);
+                        load(u & 1, kk, f0);
                         mma(f0);
                     }
                 };
@@ -501,7 +519,7 @@ struct Product {
             const int64_t above = e.mode == kGroupSum ? (int64_t)split * e.groups + expert : split;
             float *part = e.ws + above * e.M * e.ldws;
             constexpr int UPR = WN / 4;
-            stage_rows(acc, st[0], wave, lane, [&](int fm, const float *sh) {
+            stage_rows(acc, st.rows, wave, lane, [&](int fm, const float *sh) {
 #pragma unroll
                 for (int i = 0; i < 16 * UPR / 64; ++i) {
                     const int u = i * 64 + lane, r = wrow + fm * 16 + u / UPR, c = (u % UPR) * 4;
@@ -511,9 +529,9 @@ struct Product {
                 }
             });
         } else if (e.vec) {
-            finish_tile<kUnit<T>>(e, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+            finish_tile<kUnit<T>>(e, acc, st.rows, C, bias, wrow, wcol, row_end, wave, lane, zero);
         } else {
-            finish_tile<1>(e, acc, st[0], C, bias, wrow, wcol, row_end, wave, lane, zero);
+            finish_tile<1>(e, acc, st.rows, C, bias, wrow, wcol, row_end, wave, lane, zero);
         }
     }
 
@@ -601,12 +619,42 @@ struct Product {
     __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];                           \
     __shared__ __attribute__((aligned(1024))) char s2[P::S > 2 ? P::STAGE : 16];           \
     __shared__ __attribute__((aligned(1024))) char s3[P::S > 3 ? P::STAGE : 16];           \
-    char *const st[4] = {s0, s1, s2, s3}
+    const Stages st = {{s0, s1, s2, s3},                                                   \
+                       {s0 + P::OpA::BYTES, s1 + P::OpA::BYTES, s2 + P::OpA::BYTES, s3 + P::OpA::BYTES}, s0}
 
 template <class P>
 __global__ __launch_bounds__(P::NT, P::WAVES) void product_kernel(GemmArgs g) {
     CPO_STAGES(P);
-    P::template run<0>(g, st, blockIdx.x);
+    Place at;
+    if (P::place(g, blockIdx.x, at)) P::template run<0>(g, st, at);
+}
+
+// The same for 256 x 256 tiles, one to a CU, with a last round that is at most
+// half full computed as the halves (by rows, H) of its tiles, a workgroup each:
+// 8192 x 2048 x 4096 over 16 experts (2.5 rounds) 180 us with either tile alone,
+// 163 with both; 2048 x 8192 x 10240 (1.25 rounds) 375 -> 317 us.
+template <class P, class H>
+__global__ __launch_bounds__(P::NT, P::WAVES) void halving_kernel(GemmArgs g) {
+    static_assert(P::NT == H::NT && 2 * H::BM == P::BM && H::BN == P::BN && P::S == 2 && H::S == 3, "halves");
+    constexpr int HA = H::OpA::BYTES, HB = H::OpB::BYTES;
+    static_assert(P::STAGE == 2 * HB && P::STAGE == HB + 2 * HA, "stages");
+    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s2[HA];
+    Place at{};
+    at.ntm = g.mode == kGroupRows ? count_tiles(g.off, g.groups, g.M, P::BM, at.scan) : g.ntm;
+    const int units = at.ntm * g.ntn * g.nsplit, halved = halved_tiles(units), whole = units - halved;
+    const int b = blockIdx.x;
+    if (b < whole) {
+        at.unit = xcd_remap(b, whole);
+        P::template run<0>(g, Stages{{s0, s1, s0, s1}, {s0 + P::OpA::BYTES, s1 + P::OpA::BYTES, s0, s1}, s0}, at);
+    } else if (b < whole + 2 * halved) {
+        const int h = xcd_remap(b - whole, 2 * halved);
+        at.unit = whole + h / 2;
+        at.half = h & 1;
+        H::template run<0, P::BM>(
+            g, Stages{{s1 + HB, s1 + HB + HA, s2, s2}, {s0, s0 + HB, s1, s1}, s0}, at);
+    }
 }
 
 // A layer's gradients in one launch: the tiles of dX (nx workgroups), of dW
@@ -618,9 +666,12 @@ __global__ __launch_bounds__(PX::NT, PX::WAVES) void gradients_kernel(GemmArgs x
     CPO_STAGES(PX);
     const int b = blockIdx.x;
     static_assert(sizeof(GemmArgs) % 8 == 0, "the second argument follows the first");
-    if (b < nx) PX::template run<0>(x, st, b);
-    else if (b < nx + nw) PW::template run<sizeof(GemmArgs)>(w, st, b - nx);
-    else join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
+    Place at;
+    if (b < nx) {
+        if (PX::place(x, b, at)) PX::template run<0>(x, st, at);
+    } else if (b < nx + nw) {
+        if (PW::place(w, b - nx, at)) PW::template run<sizeof(GemmArgs)>(w, st, at);
+    } else join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
 }
 
 // The tile configurations with direct loads, by type.
@@ -659,7 +710,17 @@ hipError_t launch_layout(Config c, bool direct, const GemmArgs &g, int grid, hip
             return direct ? launch(Direct{}) : launch(Staged{});
         }
     if (!direct) return hipErrorInvalidValue;  // the host packs their operands
-    return with_tile<T>(c, [&](auto C) { return launch(TileOf<T, AKC, BKC, decltype(C)::value>{}); });
+    if constexpr (sizeof(T) == 2)
+        if (c == kTile256 && (AKC || g.mode != kGroupSum)) {
+            using P = typename TileOf<T, AKC, BKC, kTile256>::P;
+            using H = typename TileOf<T, AKC, BKC, kTile128x256>::P;
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(halving_kernel<P, H>), dim3(grid), dim3(P::NT), 0, s, g);
+            return hipGetLastError();
+        }
+    return with_tile<T>(c, [&](auto C) {
+        if constexpr (AKC && C == kTile256) return hipErrorInvalidValue;  // (above)
+        else return launch(TileOf<T, AKC, BKC, decltype(C)::value>{});
+    });
 }
 
 template <class T, bool BKC>
