@@ -280,9 +280,16 @@ struct Stages {
 // Which of a launch's tiles a workgroup computes: `unit` counts the tiles of
 // split after split, for kGroupSum those of `expert`.
 struct Place {
-    int unit, expert, half;
+    int unit, expert;
     int ntm;         // row tiles
     GroupScan scan;  // kGroupRows
+};
+
+// A tile: from row0 and col0, rows up to row_end, over contraction indexes
+// k_first .. k_first + klen - 1; zero: its rows belong to no expert.
+struct Tile {
+    int expert, split, row0, row_end, col0, k_first, klen;
+    bool zero;
 };
 
 // Tile BM x BN, wave grid WGM x WGN, S LDS stages.  DIRECT: loads straight to
@@ -316,7 +323,7 @@ struct Product {
     // Workgroup `b`'s place in a launch with one workgroup to a tile; false if it has none.
     __device__ __forceinline__ static bool place(const GemmArgs &g, int b, Place &p) {
         p.ntm = g.ntm;
-        p.expert = p.half = 0;
+        p.expert = 0;
         if (g.mode == kGroupRows) p.ntm = count_tiles(g.off, g.groups, g.M, BM, p.scan);
         const int units = p.ntm * g.ntn * g.nsplit;
         if (g.mode == kGroupSum) {  // experts one after the other, each spread over all XCDs
@@ -329,36 +336,31 @@ struct Product {
         return true;
     }
 
-    // `ARG`: where the kernel's arguments hold `g` (bytes).  `TM`: rows of the
-    // tiles that `at` counts; this one is the `at.half`-th part of such a tile.
-    template <int ARG, int TM = BM>
-    __device__ __forceinline__ static void run(const GemmArgs &g, const Stages &st, const Place &at) {
-        const int tid = threadIdx.x, lane = tid & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int wm = wave / WGN, wn = wave % WGN;
-
-        // ---- which tile ----
-        int ntm = at.ntm, expert = at.expert, row0, row_end = g.M, k_first = 0, klen = g.K;
-        const int split = at.unit / (ntm * g.ntn);
-        int b = at.unit - split * ntm * g.ntn;
-        const char *A = g.A, *B = g.B;
-        bool zero = false;
-        int first = 0;  // rows before the expert's
+    // The tile at `at`, of BM rows and BN columns.
+    __device__ __forceinline__ static Tile tile(const GemmArgs &g, const Place &at) {
+        Tile t;
+        int ntm = at.ntm, first = 0;  // first: rows before the expert's
+        t.expert = at.expert;
+        t.split = at.unit / (ntm * g.ntn);
+        t.row_end = g.M;
+        t.k_first = 0;
+        t.klen = g.K;
+        t.zero = false;
+        int b = at.unit - t.split * ntm * g.ntn;
         if (g.mode == kGroupRows) {
             // expert by expert: its tiles are next to each other
-            const RowTile t = find_tile(g.off, g.groups, g.M, TM, b / g.ntn, at.scan);
-            expert = t.expert;
-            first = t.row0;
-            row_end = t.end;
-            b -= t.before * g.ntn;
-            ntm = (t.end - t.row0 + TM - 1) / TM;
-            zero = expert == g.groups;  // rows without an expert
-            if (zero) klen = 0;
-            else B += (int64_t)expert * g.sb * sizeof(T);
+            const RowTile r = find_tile(g.off, g.groups, g.M, BM, b / g.ntn, at.scan);
+            t.expert = r.expert;
+            first = r.row0;
+            t.row_end = r.end;
+            b -= r.before * g.ntn;
+            ntm = (r.end - r.row0 + BM - 1) / BM;
+            t.zero = r.expert == g.groups;  // rows without an expert
+            if (t.zero) t.klen = 0;
         } else if (g.mode == kGroupSum) {
-            const RowTile t = expert_rows(g.off, g.groups, g.K, expert);
-            k_first = t.row0;
-            klen = t.end - t.row0;
+            const RowTile r = expert_rows(g.off, g.groups, g.K, t.expert);
+            t.k_first = r.row0;
+            t.klen = r.end - r.row0;
         }
         // Bands of 8 row tiles, row tiles fastest: the ~32 tiles an XCD works
         // on at a time form a near-square block, which reads least into its L2.
@@ -367,20 +369,33 @@ struct Product {
         const int left_rows = ntm - band * BAND, high = left_rows < BAND ? left_rows : BAND;
         const int nt = __builtin_amdgcn_readfirstlane(inband / high);
         const int mt = __builtin_amdgcn_readfirstlane(band * BAND + inband % high);
-        const int col0 = nt * BN;
-        row0 = first + mt * TM + (TM > BM ? at.half * BM : 0);
+        t.col0 = nt * BN;
+        t.row0 = first + mt * BM;
         if (g.nsplit > 1) {  // whole slabs per split
-            const int slabs = (klen + BK - 1) / BK, per = (slabs + g.nsplit - 1) / g.nsplit;
-            const int from = split * per * BK;
-            k_first += from;
-            klen = klen - from < per * BK ? klen - from : per * BK;
-            if (klen < 0) klen = 0;
+            const int slabs = (t.klen + BK - 1) / BK, per = (slabs + g.nsplit - 1) / g.nsplit;
+            const int from = t.split * per * BK;
+            t.k_first += from;
+            t.klen = t.klen - from < per * BK ? t.klen - from : per * BK;
+            if (t.klen < 0) t.klen = 0;
         }
-        klen = __builtin_amdgcn_readfirstlane(klen);
-        k_first = __builtin_amdgcn_readfirstlane(k_first);
-        row0 = __builtin_amdgcn_readfirstlane(row0);
-        row_end = __builtin_amdgcn_readfirstlane(row_end);
-        if (TM > BM && row0 >= row_end) return;
+        t.klen = __builtin_amdgcn_readfirstlane(t.klen);
+        t.k_first = __builtin_amdgcn_readfirstlane(t.k_first);
+        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+        t.row_end = __builtin_amdgcn_readfirstlane(t.row_end);
+        return t;
+    }
+
+    // `ARG`: where the kernel's arguments hold `g` (bytes).
+    template <int ARG>
+    __device__ __forceinline__ static void run(const GemmArgs &g, const Stages &st, const Tile &t) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / WGN, wn = wave % WGN;
+        const int expert = t.expert, split = t.split, row0 = t.row0, row_end = t.row_end, col0 = t.col0;
+        const int k_first = t.k_first, klen = t.klen;
+        const bool zero = t.zero;
+        const char *A = g.A, *B = g.B;
+        if (g.mode == kGroupRows && !zero) B += (int64_t)expert * g.sb * sizeof(T);
 
         f32x4_t acc[FM][FN];
 #pragma unroll
@@ -626,52 +641,99 @@ template <class P>
 __global__ __launch_bounds__(P::NT, P::WAVES) void product_kernel(GemmArgs g) {
     CPO_STAGES(P);
     Place at;
-    if (P::place(g, blockIdx.x, at)) P::template run<0>(g, st, at);
+    if (P::place(g, blockIdx.x, at)) P::template run<0>(g, st, P::tile(g, at));
 }
 
-// The same for 256 x 256 tiles, one to a CU, with a last round that is at most
-// half full computed as the halves (by rows, H) of its tiles, a workgroup each:
-// 8192 x 2048 x 4096 over 16 experts (2.5 rounds) 180 us with either tile alone,
-// 163 with both; 2048 x 8192 x 10240 (1.25 rounds) 375 -> 317 us.
+// 256 x 256 tiles (P), one to a CU, and their halves by rows (H), with the
+// stages of both in the same LDS: P's two of A and B, H's three of B and A.
+template <class P, class H>
+struct Halving {
+    static_assert(P::NT == H::NT && 2 * H::BM == P::BM && H::BN == P::BN && P::S == 2 && H::S == 3, "halves");
+    static constexpr int HA = H::OpA::BYTES, HB = H::OpB::BYTES;
+    static_assert(P::STAGE == 2 * HB && P::STAGE == HB + 2 * HA, "stages");
+    static constexpr int LAST = HA;
+
+    template <int ARG>
+    __device__ __forceinline__ static void run(const GemmArgs &g, char *s0, char *s1, char *s2, const Tile &t, bool half) {
+        if (half)
+            H::template run<ARG>(g, Stages{{s1 + HB, s1 + HB + HA, s2, s2}, {s0, s0 + HB, s1, s1}, s0}, t);
+        else
+            P::template run<ARG>(g, Stages{{s0, s1, s0, s1}, {s0 + P::OpA::BYTES, s1 + P::OpA::BYTES, s0, s1}, s0}, t);
+    }
+};
+#define CPO_HALVING_STAGES(P, V)                                 \
+    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE]; \
+    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE]; \
+    __shared__ __attribute__((aligned(1024))) char s2[V::LAST]
+
+// A last round that is at most half full is computed as the halves of its
+// tiles, a workgroup each: 8192 x 2048 x 4096 over 16 experts (2.5 rounds)
+// 180 us with either tile alone, 163 with both; 2048 x 8192 x 10240 (1.25
+// rounds) 375 -> 317 us.
 template <class P, class H>
 __global__ __launch_bounds__(P::NT, P::WAVES) void halving_kernel(GemmArgs g) {
-    static_assert(P::NT == H::NT && 2 * H::BM == P::BM && H::BN == P::BN && P::S == 2 && H::S == 3, "halves");
-    constexpr int HA = H::OpA::BYTES, HB = H::OpB::BYTES;
-    static_assert(P::STAGE == 2 * HB && P::STAGE == HB + 2 * HA, "stages");
-    __shared__ __attribute__((aligned(1024))) char s0[P::STAGE];
-    __shared__ __attribute__((aligned(1024))) char s1[P::STAGE];
-    __shared__ __attribute__((aligned(1024))) char s2[HA];
+    using V = Halving<P, H>;
+    CPO_HALVING_STAGES(P, V);
     Place at{};
     at.ntm = g.mode == kGroupRows ? count_tiles(g.off, g.groups, g.M, P::BM, at.scan) : g.ntm;
     const int units = at.ntm * g.ntn * g.nsplit, halved = halved_tiles(units), whole = units - halved;
     const int b = blockIdx.x;
+    int half = 0;
     if (b < whole) {
         at.unit = xcd_remap(b, whole);
-        P::template run<0>(g, Stages{{s0, s1, s0, s1}, {s0 + P::OpA::BYTES, s1 + P::OpA::BYTES, s0, s1}, s0}, at);
     } else if (b < whole + 2 * halved) {
         const int h = xcd_remap(b - whole, 2 * halved);
         at.unit = whole + h / 2;
-        at.half = h & 1;
-        H::template run<0, P::BM>(
-            g, Stages{{s1 + HB, s1 + HB + HA, s2, s2}, {s0, s0 + HB, s1, s1}, s0}, at);
+        half = h & 1;
+    } else {
+        return;
     }
+    Tile t = P::tile(g, at);
+    t.row0 += half * H::BM;
+    if (t.row0 < t.row_end) V::template run<0>(g, s0, s1, s2, t, b >= whole);
 }
 
 // A layer's gradients in one launch: the tiles of dX (nx workgroups), of dW
 // (nw), and the bias sums (the rest).  What one of them leaves of the device
 // in its last round, the next one's tiles take.
+static_assert(sizeof(GemmArgs) % 8 == 0, "the second argument follows the first");
 template <class PX, class PW>
 __global__ __launch_bounds__(PX::NT, PX::WAVES) void gradients_kernel(GemmArgs x, GemmArgs w, GradArgs d, int nx, int nw) {
     static_assert(PX::NT == PW::NT && PX::STAGE == PW::STAGE && PX::S == PW::S, "one shape of workgroup");
     CPO_STAGES(PX);
     const int b = blockIdx.x;
-    static_assert(sizeof(GemmArgs) % 8 == 0, "the second argument follows the first");
     Place at;
     if (b < nx) {
-        if (PX::place(x, b, at)) PX::template run<0>(x, st, at);
+        if (PX::place(x, b, at)) PX::template run<0>(x, st, PX::tile(x, at));
     } else if (b < nx + nw) {
-        if (PW::place(w, b - nx, at)) PW::template run<sizeof(GemmArgs)>(w, st, at);
-    } else join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
+        if (PW::place(w, b - nx, at)) PW::template run<sizeof(GemmArgs)>(w, st, PW::tile(w, at));
+    } else {
+        join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
+    }
+}
+
+// The same for 256 x 256 tiles, dX's with at most half of their rows as halves:
+// 4099 x 2048 x 4096 over 8 experts 180 -> 176 us.  (In the forward pass, where
+// an expert's tiles keep step and share what they read, this lost: 161 -> 163.)
+template <class PX, class HX, class PW>
+__global__ __launch_bounds__(PX::NT, PX::WAVES) void halving_gradients_kernel(GemmArgs x, GemmArgs w, GradArgs d, int nx, int nw) {
+    using V = Halving<PX, HX>;
+    static_assert(PX::NT == PW::NT && PX::STAGE == PW::STAGE && PX::S == PW::S, "one shape of workgroup");
+    CPO_HALVING_STAGES(PX, V);
+    const int b = blockIdx.x;
+    Place at;
+    if (b < nx) {
+        if (PX::place(x, b, at)) {
+            const Tile t = PX::tile(x, at);
+            V::template run<0>(x, s0, s1, s2, t, t.row_end - t.row0 <= HX::BM);
+        }
+    } else if (b < nx + nw) {
+        if (PW::place(w, b - nx, at))
+            PW::template run<sizeof(GemmArgs)>(
+                w, Stages{{s0, s1, s0, s1}, {s0 + PW::OpA::BYTES, s1 + PW::OpA::BYTES, s0, s1}, s0}, PW::tile(w, at));
+    } else {
+        join_columns<typename PX::T, PX::NT>(d, b - nx - nw, reinterpret_cast<float *>(s0));
+    }
 }
 
 // The tile configurations with direct loads, by type.
@@ -729,7 +791,13 @@ hipError_t launch_gradients_layout(Config c, const GemmArgs &x, int nx, const Ge
     return with_tile<T>(c, [&](auto C) {
         using PX = typename TileOf<T, true, BKC, decltype(C)::value>::P;
         using PW = typename TileOf<T, false, false, decltype(C)::value>::P;
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(gradients_kernel<PX, PW>), dim3(nx + nw + nd), dim3(PX::NT), 0, s, x, w, d, nx, nw);
+        const dim3 grid(nx + nw + nd), block(PX::NT);
+        if constexpr (C == kTile256) {
+            using HX = typename TileOf<T, true, BKC, kTile128x256>::P;
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(halving_gradients_kernel<PX, HX, PW>), grid, block, 0, s, x, w, d, nx, nw);
+        } else {
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(gradients_kernel<PX, PW>), grid, block, 0, s, x, w, d, nx, nw);
+        }
         return hipGetLastError();
     });
 }
