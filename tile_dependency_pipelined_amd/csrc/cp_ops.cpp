@@ -172,6 +172,20 @@ double launch_time(Config c, int dtype, double tiles, double slabs, bool halves)
     return t;
 }
 
+// Time of a product with tiles `c` and `n` splits.
+double product_time(const Shape &s, Config c, int n) {
+    double us = launch_time(c, s.dtype, average_tiles(s, c) * n, (double)ceil_div(slabs_of(s), n), s.mode != kGroupSum);
+    // Each expert's weights are read by few tiles: the smaller the
+    // tile, the more of them wait for the same memory (8192 x 4096 x
+    // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
+    // 128x256, 183 with 128x128, which a single weight takes 130 us).
+    if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
+    // A split writes and reads its partials, mostly in the caches, and
+    // takes another launch.
+    if (n > 1) us += 3.0 + 2.0 * n * (double)result_rows(s) * (double)s.N * 4.0 / 8e6;
+    return us;
+}
+
 Choice choose_now(const Shape &s) {
     // (both sides measured: cp_ops_gemv.hip)
     if (few_rows(s) && s.mode == kDense && s.M <= kGemvRows &&
@@ -190,18 +204,9 @@ Choice choose_now(const Shape &s) {
     double least = 1e300;
     for (const Config c : all) {
         if (s.dtype == CP_F32 && c < kTile128) continue;
-        const double tiles = average_tiles(s, c);
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && slabs < 4 * n) break;
-            double us = launch_time(c, s.dtype, tiles * n, (double)ceil_div(slabs, n), s.mode != kGroupSum);
-            // Each expert's weights are read by few tiles: the smaller the
-            // tile, the more of them wait for the same memory (8192 x 4096 x
-            // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
-            // 128x256, 183 with 128x128, which a single weight takes 130 us).
-            if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
-            // A split writes and reads its partials, mostly in the caches, and
-            // takes another launch.
-            if (n > 1) us += 3.0 + 2.0 * n * (double)result_rows(s) * (double)s.N * 4.0 / 8e6;
+            const double us = product_time(s, c, n);
             if (us < least) {
                 least = us;
                 best = {c, n};
@@ -357,9 +362,10 @@ int run_product(const Product &p, void *split, hipStream_t stream) {
 double gradients_time(const Shape &x, const Shape &w, Config c) {
     const int slots = kComputeUnits * (x.dtype == CP_BF16 && c >= kTile128 ? 2 : 1);
     const double penalty = x.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0;
-    const double tx = penalty * launch_time(c, x.dtype, slots, (double)slabs_of(x), false);
-    const double tw = penalty * launch_time(c, w.dtype, slots, (double)slabs_of(w), false);
     const int64_t nx = (int64_t)(average_tiles(x, c) + 0.5), nw = (int64_t)(average_tiles(w, c) + 0.5);
+    const double busy = nx + nw < slots ? (double)(nx + nw) : (double)slots;
+    const double tx = penalty * launch_time(c, x.dtype, busy, (double)slabs_of(x), false);
+    const double tw = penalty * launch_time(c, w.dtype, busy, (double)slabs_of(w), false);
     const double t0 = (double)(nx / slots) * tx;  // most slots are done with dX
     const double late = (double)(nx % slots);     // these have one more of its tiles
     const double t1 = late > 0.0 ? t0 + tx : t0;
@@ -383,16 +389,13 @@ double few_rows_time(const Shape &x, const Choice &c) {
 }
 
 // The configuration of one launch for both gradients, or kConfigs if two are
-// better (4099 x 2048 x 4096 over 8 experts, bf16: 210 us in two, 171 in one).
+// better.  In two and in one, whole passes, bf16, microseconds: 140 x 200 x 1728
+// 18.1 | 13.1 and 2048 x 512 x 512 20.3 | 15.7 (rather than split products); 4099 x
+// 2048 x 4096 over 8 experts, the products 210 | 171.
 Config choose_gradients(const Shape &x, const Shape &w) {
     const Choice cx = choose(x), cw = choose(w);
     const bool few = few_rows(x);
-    if ((!few && cx.nsplit > 1) || cw.nsplit > 1) return kConfigs;
-    auto alone = [](const Shape &s, Config c) {
-        return (s.mode == kGroupRows && c >= kTile128 ? 1.2 : 1.0) *
-               launch_time(c, s.dtype, average_tiles(s, c), (double)slabs_of(s), s.mode != kGroupSum);
-    };
-    double least = (few ? few_rows_time(x, cx) : alone(x, cx.cfg)) + alone(w, cw.cfg);
+    double least = (few ? few_rows_time(x, cx) : product_time(x, cx.cfg, cx.nsplit)) + product_time(w, cw.cfg, cw.nsplit);
     Config best = kConfigs;
     for (const Config c : {kTile256, kTile128x256, kTile128, kTile64x128, kTile64}) {
         if (x.dtype == CP_F32 && c < kTile128) continue;
@@ -563,6 +566,13 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
     void *split = mem.take(backward_split_bytes(dtype, M, K, N, E));
     Mat dz = dy;
     if (act != CP_ACT_NONE) dz = {mem.take(packed_bytes(dtype, M, N, 1)), M, N, up(N, 8)};
+    const Shape sx = dx_shape(dtype, M, K, N, E, wt), sw = dw_shape(dtype, M, K, N, E, wt);
+    int64_t sb = E > 1 ? stride_w : 0;
+    Packs packs{{}, dtype, mem};
+    // (with an activation, dZ is in aligned rows already, zero past their end)
+    if (act == CP_ACT_NONE && (dW || (dX && !few_rows(sx)))) packs.add(dz, nullptr, 1);
+    if (dX && !few_rows(sx)) packs.add(w, &sb, E ? E : 1);
+    if (dW) packs.add(x, nullptr, 1);
     GradArgs a{};
     if (N > 0 && (act != CP_ACT_NONE || db)) {
         a.dy = (const char *)dy.p;
@@ -584,16 +594,10 @@ int backward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *dY, 
         a.tiles = (int)max_row_tiles(rows, kGradRows);
         a.vec = aligned16(dy, dtype) && (act == CP_ACT_NONE || aligned16(z, dtype));
         a.final = !E && a.tiles == 1;
-        CP_TRY(launched(launch_grad(dtype, a, s), "activation gradient"));
+        CP_TRY(launched(launch_grad(dtype, a, packs.a, s), "activation gradient"));
+    } else {
+        CP_TRY(packs.launch(s));
     }
-    const Shape sx = dx_shape(dtype, M, K, N, E, wt), sw = dw_shape(dtype, M, K, N, E, wt);
-    int64_t sb = E > 1 ? stride_w : 0;
-    Packs packs{{}, dtype, mem};
-    // (with an activation, dZ is in aligned rows already, zero past their end)
-    if (act == CP_ACT_NONE && (dW || (dX && !few_rows(sx)))) packs.add(dz, nullptr, 1);
-    if (dX && !few_rows(sx)) packs.add(w, &sb, E ? E : 1);
-    if (dW) packs.add(x, nullptr, 1);
-    CP_TRY(packs.launch(s));
     Product px{}, pw{};
     px.s = sx;
     px.A = dz;

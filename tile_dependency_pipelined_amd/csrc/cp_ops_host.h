@@ -50,9 +50,10 @@ hipError_t launch_gemv(int dtype, bool w_rows, const GemmArgs &g, hipStream_t s)
 // sums the partials of a split product and runs its epilogue
 hipError_t launch_join(int dtype, const GemmArgs &g, hipStream_t s);
 
-// dZ and the partial column sums; then the bias gradient from those.
+// dZ and the partial column sums, in the same launch the copies; then the bias
+// gradient from those.
 inline int grad_join_blocks(const GradArgs &a) { return a.groups * ((a.N + 63) / 64); }
-hipError_t launch_grad(int dtype, const GradArgs &a, hipStream_t s);
+hipError_t launch_grad(int dtype, const GradArgs &a, const PackArgs &packs, hipStream_t s);
 hipError_t launch_grad_join(int dtype, const GradArgs &a, hipStream_t s);
 
 struct NormArgs {
