@@ -594,3 +594,35 @@ def test_grouped_rounds(ops, wt):
         close(y[s], act(z, "silu"), ty, f"y {e}")
         close(pre[s], z, tz, f"pre {e}")
     assert not y[off[-1]:].any() and not pre[off[-1]:].any()
+
+
+# Widths around the units of 16 bytes and the threads of a row, in rows that are
+# not aligned, surrounded by NaN; also in place, and nothing else is written.
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 8, 9, 15, 23, 505, 511, 517, 1025, 2047, 2051, 4095, 8185, 8193, 12287, 12289, 16383])
+def test_layer_norm_odd_widths(ops, N, name):
+    M, eps, d = 5, 1e-5, dt(name)
+    say(f"layer_norm odd width {N} {name}")
+    g = torch.Generator().manual_seed(N)
+    x, w, b = data(g, M, N, dtype=d), data(g, N, dtype=d), data(g, N, dtype=d)
+    px = place(x, d, 3, 1)
+    y, mean, rstd = ops.layer_norm(px, place(w, d, 0, 1), place(b, d, 0, 1), eps=eps)
+    mu = x.mean(1, keepdim=True)
+    var = ((x - mu) ** 2).mean(1, keepdim=True)
+    rs = (var + eps) ** -0.5
+    xh = (x - mu) * rs
+    n = (N + 16) * E32
+    off = n * x.abs().mean(1, keepdim=True)
+    rel = n + 2 * off * off / (var + eps) + 8 * E32
+    close(mean, mu[:, 0], off[:, 0] + E32 * mu[:, 0].abs(), "mean")
+    close(rstd, rs[:, 0], (rel * rs)[:, 0], "rstd")
+    want = xh * w + b
+    close(y, want, (off * rs + xh.abs() * (rel + 4 * E32)) * w.abs() + (1.01 * U[name] + 4 * E32) * want.abs()
+          + 4 * E32 * b.abs(), "y")
+    box = torch.full((M + 2, N + 3), 7.0, dtype=d, device="cuda")
+    inside = box[1:M + 1, 1:N + 1]
+    inside.copy_(px)
+    ops.layer_norm(inside, place(w, d, 0, 1), place(b, d, 0, 1), eps=eps, out=inside)
+    assert torch.equal(inside, y)
+    inside.fill_(7.0)
+    assert bool((box == 7.0).all()), "wrote outside the rows"

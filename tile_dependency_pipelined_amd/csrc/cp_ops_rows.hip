@@ -208,23 +208,55 @@ __device__ __forceinline__ int norm_col(int q, int i, int t) {
     return VEC ? (q * THREADS + t) * kUnit<T> + i : (q * kUnit<T> + i) * THREADS + t;
 }
 
+// The forward pass reads unaligned bf16 rows by 16-byte units as well: a row's
+// last unit starts early enough to end with the row, and its thread leaves to
+// the one before what they share.  (Single elements are as many loads as there
+// are columns: 4477 x 9970 150 us, 36 with units; 4477 x 4097 73 and 29.  fp32
+// gains nothing: 4096 x 9001 62 us, 76 with units.  Nor does the backward pass,
+// where the masks cost more: 912 x 49 12 us, 22 with units.)
+template <class T, bool VEC>
+constexpr bool kNormShift = !VEC && sizeof(T) == 2;
+
+// First column of unit q, and whether its element i is this thread's.
+template <class T, int THREADS>
+__device__ __forceinline__ int shifted(int q, int t, int N) {
+    const int c = (q * THREADS + t) * kUnit<T>;
+    return c + kUnit<T> <= N ? c : N - kUnit<T>;
+}
+template <class T, int THREADS, bool VEC>
+__device__ __forceinline__ bool norm_mine(int q, int i, int t, int N) {
+    if constexpr (kNormShift<T, VEC>) {
+        const int c = (q * THREADS + t) * kUnit<T>;
+        return shifted<T, THREADS>(q, t, N) + i >= c && c < N;
+    }
+    return norm_col<T, THREADS, VEC>(q, i, t) < N;
+}
+
+// (what is not this thread's: anything)
 template <class T, int THREADS, int VPT, bool VEC>
 __device__ __forceinline__ void norm_load(const char *row, int N, int t, float (&v)[VPT][kUnit<T>]) {
+    if constexpr (VEC || kNormShift<T, VEC>) {
+        uint4 u[VPT];  // all requested before the first is used
 #pragma unroll
-    for (int q = 0; q < VPT; ++q) {
-        if constexpr (VEC) {
-            const int c = norm_col<T, THREADS, VEC>(q, 0, t);
-            if (c < N) load_unit<T>(row + (int64_t)c * sizeof(T), v[q]);
-            else
+        for (int q = 0; q < VPT; ++q) {
+            u[q] = make_uint4(0, 0, 0, 0);
+            if constexpr (VEC) {
+                const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+                if (c < N) u[q] = *reinterpret_cast<const uint4 *>(row + (int64_t)c * sizeof(T));
+            } else {
+                __builtin_memcpy(&u[q], row + (int64_t)shifted<T, THREADS>(q, t, N) * sizeof(T), 16);
+            }
+        }
 #pragma unroll
-                for (int i = 0; i < kUnit<T>; ++i) v[q][i] = 0.0f;
-        } else {
+        for (int q = 0; q < VPT; ++q) load_unit<T>(&u[q], v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
 #pragma unroll
             for (int i = 0; i < kUnit<T>; ++i) {
                 const int c = norm_col<T, THREADS, VEC>(q, i, t);
                 v[q][i] = c < N ? to_f32(reinterpret_cast<const T *>(row)[c]) : 0.0f;
             }
-        }
     }
 }
 
@@ -235,6 +267,19 @@ __device__ __forceinline__ void norm_store(char *row, int N, int t, const float 
         if constexpr (VEC) {
             const int c = norm_col<T, THREADS, VEC>(q, 0, t);
             if (c < N) store_unit<T>(row + (int64_t)c * sizeof(T), v[q]);
+        } else if constexpr (kNormShift<T, VEC>) {
+            const int c = (q * THREADS + t) * kUnit<T>;
+            if (c + kUnit<T> <= N) {
+                uint4 u;
+                store_unit<T>(&u, v[q]);
+                __builtin_memcpy(row + (int64_t)c * sizeof(T), &u, 16);
+            } else if (c < N) {
+#pragma unroll
+                for (int i = 0; i < kUnit<T>; ++i) {
+                    const int at = N - kUnit<T> + i;
+                    if (at >= c) reinterpret_cast<T *>(row)[at] = from_f32<T>(v[q][i]);
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kUnit<T>; ++i) {
@@ -260,14 +305,14 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(Nor
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
-        for (int i = 0; i < CE; ++i) s += v[q][i];
+        for (int i = 0; i < CE; ++i) s += norm_mine<T, THREADS, VEC>(q, i, t, a.N) ? v[q][i] : 0.0f;
     const float mean = row_sum<THREADS>(s, sh) / (float)a.N;
     float ss = 0.0f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
         for (int i = 0; i < CE; ++i) {
-            v[q][i] = norm_col<T, THREADS, VEC>(q, i, t) < a.N ? v[q][i] - mean : 0.0f;
+            v[q][i] = norm_mine<T, THREADS, VEC>(q, i, t, a.N) ? v[q][i] - mean : 0.0f;
             ss += v[q][i] * v[q][i];
         }
     const float rstd = 1.0f / sqrtf(row_sum<THREADS>(ss, sh) / (float)a.N + a.eps);
@@ -617,9 +662,9 @@ hipError_t grad_join(const GradArgs &a, hipStream_t s) {
 
 template <class T, bool VEC>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
-    constexpr int CE = kUnit<T>;
+    constexpr int CE = kUnit<T>, least = kNormShift<T, VEC> ? CE : 1;  // a unit has to fit the row
 #define CPO_NORM(THREADS, VPT)                                                                                        \
-    if (a.N <= THREADS * VPT * CE) {                                                                                  \
+    if (a.N >= least && a.N <= THREADS * VPT * CE) {                                                                  \
         constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, ROWS = BLOCK / THREADS;                                  \
         hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, VEC>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)), \
                            dim3(BLOCK), 0, s, a);                                                                     \
