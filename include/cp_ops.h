@@ -84,9 +84,9 @@ int cp_linear_backward(int32_t dtype, int64_t M, int64_t K, int64_t N, const voi
  *   X[T][K], Y[T][N], pre[T][N] or NULL; W_e at W + e * stride_w, each as in
  *   cp_linear; bias[E][N] or NULL; offsets[E + 1]: int32, DEVICE memory
  * The host never reads the offsets.  They are meant to start at 0 and not to
- * decrease; the device takes each as the largest so far, between 0 and T, so
- * that no value reads or writes out of range.  Rows from offsets[E] on belong
- * to no expert: their Y and pre are zero.  1 <= E <= CP_OPS_MAX_GROUPS.
+ * decrease; the device takes the first as 0 and each as the largest so far,
+ * between 0 and T, so that no value reads or writes out of range.  Rows from
+ * offsets[E] on belong to no expert: their Y and pre are zero.  1 <= E <= CP_OPS_MAX_GROUPS.
  */
 int cp_grouped_linear(int32_t dtype, int64_t T, int64_t K, int64_t N, int32_t E, const void *X, int64_t ldx,
                       const void *W, int64_t ldw, int64_t stride_w, int32_t w_trans, const int32_t *offsets,

@@ -292,6 +292,15 @@ struct Tile {
     bool zero;
 };
 
+// What bounds it: a 256 x 256 tile takes 1.55 us per 64 k of bf16 with all CUs
+// busy (1385 TFLOP/s; an 8192-cubed library product reaches 1430), reads from
+// the L2 and the matrix cores together, and 8 to 12 us besides: 0.4 to find the
+// tile, 2.5 to 4 for its first slab, 3.2 to store it (6.2 with bias and GELU, 13
+// with a residual, whose 67 MB for all tiles then move at 5.1 TB/s) and 0.9 to
+// the next workgroup's start.  2048 x 8192 x 8192 with GELU and residual: 215 us.
+// 16-row tiles are bound by the weight's bytes: 13 x 8192 x 28672 in 90 us, 5.2
+// TB/s; 16 rows over 8 experts of 4096 x 4096 in 39.
+//
 // Tile BM x BN, wave grid WGM x WGN, S LDS stages.  DIRECT: loads straight to
 // LDS (16-byte aligned operands); otherwise through registers, two stages.
 template <class T_, int BM_, int BN_, int WGM_, int WGN_, int S_, bool AKC_, bool BKC_, bool DIRECT_>

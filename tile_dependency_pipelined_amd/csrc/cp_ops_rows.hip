@@ -10,7 +10,9 @@ namespace {
 
 // ------------------------------------------------------------------- packing
 
-// 64 units of 16 bytes x 4 rows per block; the source may lie anyhow.
+// 64 units of 16 bytes x 4 rows per block; the source may lie anyhow.  777 x
+// 1003 and 1003 x 2049 bf16 (5.7 MB each way) 7.6 us: the launch and the latency
+// of one load and store.
 struct PackGrid {
     int unit_blocks[3], end[3];  // of each copy: blocks along a row, last block + 1
 };
@@ -38,6 +40,7 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a, PackGrid g) {
 // ------------------------------------------------------------------- joining
 
 // Y = epilogue(sum over splits of partial); one block per row and 256 units.
+// 4 x 515 x 2048 (17 MB, in the caches) 5.1 us, mostly the launch.
 template <class T, int CNT>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_row) {
     const int all = blockIdx.x / blocks_per_row;  // row of the partials
@@ -82,6 +85,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_ro
 // 32 units of columns x 8 rows per pass; each block one row tile (kGradRows rows
 // of one expert) and 32 units.  Rows that are not aligned are read by unaligned
 // units (VEC false; only a row's last unit by elements), dZ's rows always are.
+// Bound by its bytes: 2048 x 4096 bf16 with GELU (50 MB) 11.3 us, 4.5 TB/s.
 // The blocks from `blocks` on make the copies that the products need, which
 // saves a launch: 43 x 1059 x 696, rows off 16 bytes, 12.6 -> 10.2 us.
 template <class T, int ACT, bool VEC>
@@ -291,7 +295,9 @@ __device__ __forceinline__ void norm_store(char *row, int N, int t, const float 
 }
 
 // One row per THREADS threads, held in registers: the deviation is summed from
-// the values themselves (no difference of large squares).
+// the values themselves (no difference of large squares).  Bound by its bytes,
+// read and written once: 4093 x 4099 fp32 (134 MB) 24.8 us, 5.4 TB/s; 16384 x
+// 8192 bf16 (537 MB) 108 us, 5.0 TB/s.
 template <class T, int THREADS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(NormArgs a) {
     constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, CE = kUnit<T>;
@@ -410,7 +416,8 @@ struct RowShare {
 // keeps its columns' weight and bias sums in registers over all its rows; the
 // block adds its SUBS sums up in LDS and stores one partial, which
 // norm_join_kernel adds up in block order.  The next rows are requested before
-// the current ones are reduced, so that memory is read all the time.
+// the current ones are reduced, so that memory is read all the time: 16384 x
+// 8192 bf16 (805 MB) 167 us with the join, 4.8 TB/s.
 template <class T, int THREADS, int SUBS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS *SUBS) void norm_backward_kernel(NormArgs a) {
     constexpr int CE = kUnit<T>, W = THREADS / 64, COLS = THREADS * VPT * CE;
