@@ -1,0 +1,99 @@
+"""GPU tests of the feed-forward operators at row counts whose launches would have
+2^32 threads or more with one thread or block to a fixed number of rows.  A
+grid's dimension holds fewer, so such a launch is made in parts or over two
+dimensions, and its results have to be those of any other.
+
+Sizes of up to 69 GB; inputs are random where the whole result is compared, by
+ranges of rows on the device in 64 bits, and otherwise zero but for some rows.
+Tolerances are those of test_gpu_ops.py: with e = 2^-24 and u the unit roundoff
+of the stored type, a sum of K products is off by at most (K + 8) e sum |a||b|,
+a row's mean and deviation by (N + 16) e relative, the stored value by u."""
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+E32 = 2.0 ** -24
+U = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from tile_dependency_pipelined_amd import ops as o
+    assert torch.cuda.is_available()
+    yield o
+    torch.cuda.empty_cache()
+
+
+@pytest.fixture(autouse=True)
+def free():
+    yield
+    torch.cuda.empty_cache()
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def parts(M, step=1 << 23):
+    return [slice(r, min(r + step, M)) for r in range(0, M, step)]
+
+
+def check_norm(x, w, b, eps, y, mean, rstd, name):
+    N = x.shape[1]
+    w, b = w.double(), b.double()
+    for s in parts(x.shape[0]):
+        v = x[s].double()
+        mu = v.mean(1, keepdim=True)
+        var = ((v - mu) ** 2).mean(1, keepdim=True)
+        rs = (var + eps) ** -0.5
+        n = (N + 16) * E32
+        off = n * v.abs().mean(1, keepdim=True)
+        rel = n + 2 * off * off / (var + eps) + 8 * E32
+        assert bool(((mean[s].double() - mu[:, 0]).abs() <= off[:, 0] + E32 * mu[:, 0].abs()).all()), ("mean", s)
+        assert bool(((rstd[s].double() - rs[:, 0]).abs() <= (rel * rs)[:, 0]).all()), ("rstd", s)
+        xh = (v - mu) * rs
+        want = xh * w + b
+        tol = (off * rs + xh.abs() * (rel + 4 * E32)) * w.abs() + (1.01 * U[name] + 4 * E32) * want.abs() + 4 * E32 * b.abs()
+        assert bool(((y[s].double() - want).abs() <= tol).all()), ("y", s)
+
+
+# Narrow rows: 4 elements, far more rows than blocks of 1024 threads fit a grid;
+# 8 elements (a unit of 16 bytes in bf16), more than waves fit.
+@pytest.mark.parametrize("name, M, N", [("bf16", (1 << 22) + 3, 4), ("bf16", (1 << 26) + 5, 8), ("f32", (1 << 26) + 5, 4),
+                                        ("bf16", (1 << 26) + 5, 3)])
+def test_layer_norm_of_many_rows(ops, name, M, N):
+    say(f"layer_norm {M} x {N} {name}")
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.empty(M, N, dtype=DTYPES[name], device="cuda")
+    for s in parts(M):
+        x[s] = torch.randn(x[s].shape, generator=g, device="cuda") + 2.0
+    w, b = (torch.randn(N, generator=g, device="cuda").to(x.dtype) for _ in range(2))
+    y, mean, rstd = ops.layer_norm(x, w, b, eps=1e-3)
+    check_norm(x, w, b, 1e-3, y, mean, rstd, name)
+
+
+def test_layer_norm_backward_of_many_long_rows(ops):
+    """Rows that do not fit the registers, a block of 1024 threads each."""
+    M, N, some = (1 << 22) + 3, 8193, [0, 1, (1 << 22) - 2, (1 << 22) - 1, 1 << 22, (1 << 22) + 2]
+    say(f"layer_norm_backward {M} x {N} bf16")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")  # dy as well: two inputs may be the same
+    v = torch.randn(len(some), N, generator=g, device="cuda").to(x.dtype)
+    x[some] = v
+    mean, rstd = torch.full((M,), 0.25, device="cuda"), torch.full((M,), 0.5, device="cuda")
+    dx = ops.layer_norm_backward(x, x, mean, rstd, need_weight=False, need_bias=False)[0]
+    v = v.double()
+    xh = (v - 0.25) * 0.5
+    s0, s1 = v.mean(1, keepdim=True), (v * xh).mean(1, keepdim=True)
+    want = 0.5 * (v - s0 - xh * s1)
+    n = (N + 16) * E32
+    tol = 0.5 * (n * v.abs().mean(1, keepdim=True) + xh.abs() * n * (v * xh).abs().mean(1, keepdim=True)
+                 + 8 * E32 * (v.abs() + s0.abs() + (xh * s1).abs())) + 1.01 * U["bf16"] * want.abs()
+    assert bool(((dx[some].double() - want).abs() <= tol).all())
+    dx[some] = 0.0
+    # a row of zeros has the gradient zero
+    assert not any(bool(dx[s].any()) for s in parts(M, 1 << 18))

@@ -19,6 +19,10 @@ struct ConfigShape {
 };
 constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}, {16, 128}, {kGemvRows, 1}};
 
+// Blocks of `threads` threads that a dimension of a grid can hold.  It is counted
+// in threads, in 32 bits: a launch of more wraps around without an error.
+constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+
 // Copies of up to three matrices (or stacks of `count`) with rows of whole
 // 16-byte units, zero past the end.
 struct PackArgs {

@@ -667,15 +667,35 @@ hipError_t grad_join(const GradArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// f(rows, blocks) for as many launches of `rows` rows to a block of `threads`
+// as all rows take: one, unless a grid cannot hold that many threads.
+template <class T, class F>
+hipError_t by_rows(const NormArgs &a, int rows, int threads, F &&f) {
+    const int64_t most = max_blocks(threads) * rows;
+    for (int64_t row = 0; row < a.M; row += most) {
+        NormArgs part = a;
+        part.M = (int)(a.M - row < most ? a.M - row : most);
+        if (a.x) part.x += row * a.ldx * (int64_t)sizeof(T);
+        if (a.dy) part.dy += row * a.ldd * (int64_t)sizeof(T);
+        if (a.y) part.y += row * a.ldy * (int64_t)sizeof(T);
+        if (a.mean) part.mean += row;
+        if (a.rstd) part.rstd += row;
+        f(part, dim3((unsigned)((part.M + rows - 1) / rows)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <class T, bool VEC>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
     constexpr int CE = kUnit<T>, least = kNormShift<T, VEC> ? CE : 1;  // a unit has to fit the row
 #define CPO_NORM(THREADS, VPT)                                                                                        \
     if (a.N >= least && a.N <= THREADS * VPT * CE) {                                                                  \
-        constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, ROWS = BLOCK / THREADS;                                  \
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, VEC>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)), \
-                           dim3(BLOCK), 0, s, a);                                                                     \
-        return hipGetLastError();                                                                                     \
+        constexpr int BLOCK = THREADS < 256 ? 256 : THREADS;                                                          \
+        return by_rows<T>(a, BLOCK / THREADS, BLOCK, [&](const NormArgs &part, dim3 grid) {                           \
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, VEC>), grid, dim3(BLOCK), 0, s, part);    \
+        });                                                                                                           \
     }
     CPO_NORM(64, 1)
     CPO_NORM(64, 2)
@@ -686,8 +706,9 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
     CPO_NORM(512, 4)
     CPO_NORM(1024, 4)
 #undef CPO_NORM
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_long_kernel<T>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
-    return hipGetLastError();
+    return by_rows<T>(a, 1, 1024, [&](const NormArgs &part, dim3 grid) {
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_long_kernel<T>), grid, dim3(1024), 0, s, part);
+    });
 }
 
 template <class T, bool VEC>
@@ -717,7 +738,9 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t s) {
     if (a.dw || a.db)
         hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_columns_kernel<T>), dim3((unsigned)(a.blocks * cb)), dim3(256), 0, s, a, cb);
     if (a.y)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_long_kernel<T>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+        return by_rows<T>(a, 1, 1024, [&](const NormArgs &part, dim3 grid) {
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_backward_long_kernel<T>), grid, dim3(1024), 0, s, part);
+        });
     return hipGetLastError();
 }
 
