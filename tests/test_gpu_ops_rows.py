@@ -97,3 +97,43 @@ def test_layer_norm_backward_of_many_long_rows(ops):
     dx[some] = 0.0
     # a row of zeros has the gradient zero
     assert not any(bool(dx[s].any()) for s in parts(M, 1 << 18))
+
+
+def check_product(x, w, b, y, name):
+    w, b = w.double(), b.double()
+    for s in parts(x.shape[0]):
+        v = x[s].double()
+        want = v @ w + b
+        tol = (x.shape[1] + 8) * E32 * (v.abs() @ w.abs() + b.abs()) + 1.01 * U[name] * want.abs()
+        assert bool(((y[s].double() - want).abs() <= tol).all()), s
+
+
+def test_linear_of_many_unaligned_rows(ops):
+    """The copies that put rows of 14 bytes into whole units, four rows to a block."""
+    M, K, N = (1 << 26) + 5, 7, 8
+    say(f"linear {M} x {K} x {N} bf16")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    for s in parts(M):
+        x[s] = torch.randn(x[s].shape, generator=g, device="cuda")
+    w, b = torch.randn(K, N, generator=g, device="cuda").to(x.dtype), torch.randn(N, generator=g, device="cuda").to(x.dtype)
+    check_product(x, w, b, ops.linear(x, w, b), "bf16")
+    off = torch.tensor([0, 3, M], dtype=torch.int32, device="cuda")
+    y = ops.grouped_linear(x, torch.stack([w, -w]), off, torch.stack([b, -b]))
+    check_product(x[:3], w, b, y[:3], "bf16")
+    check_product(x[3:], w, b, -y[3:], "bf16")
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_bias_gradient_of_many_rows(ops, act):
+    """A block to each 32 rows: small integers, whose sums are exact."""
+    M, N = (1 << 29) + 5, 3
+    say(f"bias gradient {M} x {N} bf16 {act}")
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    some = [0, 31, 32, 1 << 28, (1 << 29) - 1, 1 << 29, M - 1]
+    dy[some] = torch.tensor([[i + 1.0, 2.0 * i, -i - 3.0] for i in range(len(some))], device="cuda").to(dy.dtype)
+    want = dy[some].float().sum(0)
+    x, w = torch.zeros(M, 1, dtype=dy.dtype, device="cuda"), torch.zeros(1, N, dtype=dy.dtype, device="cuda")
+    pre = None if act == "none" else torch.ones(M, N, dtype=dy.dtype, device="cuda")
+    db = ops.linear_backward(dy, x, w, pre=pre, act=ops.ACTS[act], need_x=False, need_w=False)[2]
+    assert torch.equal(db.float(), want)

@@ -47,6 +47,10 @@ struct GemmArgs {
     int32_t vec;             // C, R, pre and bias can be accessed 16 bytes at a time
 };
 
+// A block's number in a launch whose grid may have a second dimension (fewer
+// than 2^31 blocks and those that fill its last row).
+__device__ __forceinline__ unsigned block_id() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ---------------------------------------------------------------- elements
 
 template <class T>

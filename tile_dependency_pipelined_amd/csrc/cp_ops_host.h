@@ -22,6 +22,12 @@ constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {
 // Blocks of `threads` threads that a dimension of a grid can hold.  It is counted
 // in threads, in 32 bits: a launch of more wraps around without an error.
 constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+// A grid of at least `blocks` (> 0) blocks, over two dimensions if one does not
+// hold them; kernels launched so take block_id() and leave alone what is past `blocks`.
+inline dim3 grid_of(int64_t blocks, int threads) {
+    const int64_t rows = (blocks + max_blocks(threads) - 1) / max_blocks(threads);
+    return dim3((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
+}
 
 // Copies of up to three matrices (or stacks of `count`) with rows of whole
 // 16-byte units, zero past the end.

@@ -17,10 +17,11 @@ struct PackGrid {
     int unit_blocks[3], end[3];  // of each copy: blocks along a row, last block + 1
 };
 template <class T>
-__device__ __forceinline__ void pack_block(const PackArgs &a, const PackGrid &g, int b) {
+__device__ __forceinline__ void pack_block(const PackArgs &a, const PackGrid &g, unsigned b) {
     constexpr int CE = kUnit<T>;
+    if (b >= (unsigned)g.end[2]) return;
     int i = 0;
-    while (i < 2 && b >= g.end[i]) ++i;
+    while (i < 2 && b >= (unsigned)g.end[i]) ++i;
     if (i > 0) b -= g.end[i - 1];
     const PackArgs::One o = a.one[i];
     const int u = (b % g.unit_blocks[i]) * 64 + (threadIdx.x & 63);
@@ -34,7 +35,7 @@ __device__ __forceinline__ void pack_block(const PackArgs &a, const PackGrid &g,
 
 template <class T>
 __global__ __launch_bounds__(256) void pack_kernel(PackArgs a, PackGrid g) {
-    pack_block<T>(a, g, blockIdx.x);
+    pack_block<T>(a, g, block_id());
 }
 
 // ------------------------------------------------------------------- joining
@@ -43,9 +44,11 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a, PackGrid g) {
 // 4 x 515 x 2048 (17 MB, in the caches) 5.1 us, mostly the launch.
 template <class T, int CNT>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, int blocks_per_row) {
-    const int all = blockIdx.x / blocks_per_row;  // row of the partials
+    const unsigned id = block_id();
+    const int all = (int)(id / blocks_per_row);  // row of the partials
+    if (all >= g.M * (g.mode == kGroupSum ? g.groups : 1)) return;
     const int expert = g.mode == kGroupSum ? all / g.M : 0, row = all - expert * g.M;
-    const int col = ((blockIdx.x % blocks_per_row) * 256 + threadIdx.x) * CNT;
+    const int col = (int)((id % blocks_per_row) * 256 + threadIdx.x) * CNT;
     char *C = g.C + (int64_t)expert * g.sc * sizeof(T);
     const char *bias = g.bias;
     bool zero = false;
@@ -92,8 +95,9 @@ template <class T, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks, int blocks, PackArgs packs, PackGrid grid) {
     constexpr int CNT = kUnit<T>;
     __shared__ float part[8][32 * CNT];
-    if ((int)blockIdx.x >= blocks) return pack_block<T>(packs, grid, blockIdx.x - blocks);
-    const int ct = blockIdx.x % col_blocks, rt = blockIdx.x / col_blocks;
+    const unsigned id = block_id();
+    if (id >= (unsigned)blocks) return pack_block<T>(packs, grid, id - blocks);
+    const int ct = (int)(id % col_blocks), rt = (int)(id / col_blocks);
     int row0 = rt * kGradRows, end = a.M;
     if (a.off) {
         GroupScan s;
@@ -168,7 +172,8 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a, int col_blocks, i
 template <class T>
 __global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a) {
     __shared__ float part[256];
-    join_columns<T, 256>(a, blockIdx.x, part);
+    const unsigned b = block_id();
+    if (b < (unsigned)(a.groups * ((a.N + 63) / 64))) join_columns<T, 256>(a, (int)b, part);
 }
 
 // ------------------------------------------------------- layer normalisation
@@ -624,7 +629,7 @@ hipError_t pack(const PackArgs &a, hipStream_t s) {
     PackGrid g;
     const int64_t blocks = pack_grid<T>(a, g);
     if (blocks < 0) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(pack_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, a, g);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(pack_kernel<T>), grid_of(blocks, 256), dim3(256), 0, s, a, g);
     return hipGetLastError();
 }
 
@@ -632,7 +637,7 @@ template <class T>
 hipError_t join(const GemmArgs &g, hipStream_t s) {
     const int unit = g.vec ? kUnit<T> : 1;
     const int per_row = (g.N + 256 * unit - 1) / (256 * unit);
-    const dim3 grid((unsigned)((int64_t)g.M * (g.mode == kGroupSum ? g.groups : 1) * per_row));
+    const dim3 grid = grid_of((int64_t)g.M * (g.mode == kGroupSum ? g.groups : 1) * per_row, 256);
     if (g.vec) hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, kUnit<T>>), grid, dim3(256), 0, s, g, per_row);
     else hipLaunchKernelGGL(HIP_KERNEL_NAME(join_kernel<T, 1>), grid, dim3(256), 0, s, g, per_row);
     return hipGetLastError();
@@ -645,7 +650,7 @@ hipError_t grad(const GradArgs &a, const PackArgs &packs, hipStream_t s) {
     const int64_t blocks = (int64_t)a.tiles * cols, more = pack_grid<T>(packs, g);
     if (more < 0 || blocks + more > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (blocks + more > 0) {
-        const dim3 grid((unsigned)(blocks + more));
+        const dim3 grid = grid_of(blocks + more, 256);
         auto launch = [&](auto ACT) {
             constexpr int act = decltype(ACT)::value;
             if (a.vec)
@@ -663,7 +668,7 @@ hipError_t grad(const GradArgs &a, const PackArgs &packs, hipStream_t s) {
 
 template <class T>
 hipError_t grad_join(const GradArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), dim3((unsigned)grad_join_blocks(a)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(grad_join_kernel<T>), grid_of(grad_join_blocks(a), 256), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
