@@ -49,7 +49,9 @@ extern "C" {
 
 /* rows, columns and leading dimensions are at most this many elements (rows
  * of the activations: 2^30), and an operator takes at most CP_OPS_MAX_GROUPS
- * experts */
+ * experts.  A product whose result has 2^23 tiles of 256 x 256 or more (fp32:
+ * 2^24 of 128 x 128; with at most 16 rows per expert: 2^24 of 16 x 128, an
+ * expert's last one counting in full) is refused with CP_ERR_SHAPE. */
 #define CP_OPS_MAX_WIDTH 4194304
 #define CP_OPS_MAX_GROUPS 4096
 

@@ -124,6 +124,21 @@ def test_linear_of_many_unaligned_rows(ops):
     check_product(x[3:], w, b, -y[3:], "bf16")
 
 
+def test_linear_of_a_billion_rows(ops):
+    """64 x 64 tiles, the cheapest for such narrow products, are more than a grid holds."""
+    M, K, N = 1 << 30, 4, 8
+    say(f"linear {M} x {K} x {N} fp32")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.zeros(M, K, device="cuda")
+    some = [0, 1, 4095, M // 2 - 1, M // 2, M - 2, M - 1]
+    x[some] = torch.randn(len(some), K, generator=g, device="cuda")
+    w, b = torch.randn(K, N, generator=g, device="cuda"), torch.zeros(N, device="cuda")
+    y = ops.linear(x, w, b)
+    check_product(x[some], w, b, y[some], "f32")
+    y[some] = 0.0
+    assert not any(bool(y[s].any()) for s in parts(M, 1 << 26))
+
+
 @pytest.mark.parametrize("act", ["none", "relu"])
 def test_bias_gradient_of_many_rows(ops, act):
     """A block to each 32 rows: small integers, whose sums are exact."""

@@ -116,6 +116,14 @@ int64_t max_row_tiles(const Shape &s, int bm) {
     return (s.M + used * (bm - 1)) / bm;
 }
 
+// Workgroups of a launch with tiles `c` and `n` splits, at most.
+int64_t workgroups(const Shape &s, Config c, int n) {
+    const int64_t tiles = max_row_tiles(s, kShapes[c].bm) * ceil_div(s.N, kShapes[c].bn) * n;
+    return tiles * (s.mode == kGroupSum ? s.groups : 1) + (c == kTile256 ? kComputeUnits / 2 : 0);  // (halves: launch_args)
+}
+// The products' kernels count a launch's workgroups in one dimension of the grid.
+bool fits_grid(int64_t n, Config c) { return n <= max_blocks(kShapes[c].threads); }
+
 // Rows of all the results together.
 int64_t result_rows(const Shape &s) { return s.M * (s.mode == kGroupSum ? s.groups : 1); }
 
@@ -205,7 +213,7 @@ Choice choose_now(const Shape &s) {
     for (const Config c : all) {
         if (s.dtype == CP_F32 && c < kTile128) continue;
         for (int n = 1; n <= 16; ++n) {
-            if (n > 1 && slabs < 4 * n) break;
+            if ((n > 1 && slabs < 4 * n) || !fits_grid(workgroups(s, c, n), c)) break;
             const double us = product_time(s, c, n);
             if (us < least) {
                 least = us;
@@ -331,7 +339,8 @@ int64_t launch_args(const Product &p, const Choice &c, void *split, GemmArgs &g,
     const ConfigShape t = kShapes[c.cfg];
     const int64_t ntm = max_row_tiles(s, t.bm), ntn = ceil_div(s.N, t.bn);
     const int64_t grid = ntm * ntn * c.nsplit * (s.mode == kGroupSum ? s.groups : 1);
-    if (grid > 0x3FFFFFFF) return fail(CP_ERR_SHAPE, "too many tiles (%lld)", (long long)grid);
+    if (c.cfg != kGemv && !fits_grid(workgroups(s, c.cfg, c.nsplit), c.cfg))
+        return fail(CP_ERR_SHAPE, "too many tiles of %d x %d (%lld)", t.bm, t.bn, (long long)grid);
     g.ntm = (int)ntm;
     g.ntn = (int)ntn;
     if (c.cfg == kTile256 && s.mode != kGroupSum && alone)  // (kGroupRows: any number of tiles up to `grid`)
@@ -399,6 +408,8 @@ Config choose_gradients(const Shape &x, const Shape &w) {
     Config best = kConfigs;
     for (const Config c : {kTile256, kTile128x256, kTile128, kTile64x128, kTile64}) {
         if (x.dtype == CP_F32 && c < kTile128) continue;
+        const int64_t sums = ceil_div(x.K, 64) * (x.groups ? x.groups : 1);  // (the bias's)
+        if (!fits_grid(workgroups(x, c, 1) + workgroups(w, c, 1) + sums, c)) continue;
         const double us = gradients_time(x, w, c) - 3.0;  // a launch less
         if (us < least) {
             least = us;

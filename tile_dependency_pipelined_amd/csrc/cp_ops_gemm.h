@@ -778,6 +778,7 @@ hipError_t launch_layout(Config c, bool direct, const GemmArgs &g, int grid, hip
         if (c == kTile16) {
             struct Direct { using P = Product<T, 16, 128, 1, 4, 4, AKC, BKC, true>; };
             struct Staged { using P = Product<T, 16, 128, 1, 4, 2, AKC, BKC, false>; };
+            static_assert(Direct::P::NT == kShapes[kTile16].threads && Staged::P::NT == Direct::P::NT, "threads");
             return direct ? launch(Direct{}) : launch(Staged{});
         }
     if (!direct) return hipErrorInvalidValue;  // the host packs their operands
@@ -800,6 +801,7 @@ hipError_t launch_gradients_layout(Config c, const GemmArgs &x, int nx, const Ge
     return with_tile<T>(c, [&](auto C) {
         using PX = typename TileOf<T, true, BKC, decltype(C)::value>::P;
         using PW = typename TileOf<T, false, false, decltype(C)::value>::P;
+        static_assert(PX::NT == kShapes[decltype(C)::value].threads, "threads");
         const dim3 grid(nx + nw + nd), block(PX::NT);
         if constexpr (C == kTile256) {
             using HX = typename TileOf<T, true, BKC, kTile128x256>::P;

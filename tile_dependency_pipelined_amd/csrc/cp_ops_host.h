@@ -15,9 +15,10 @@ constexpr int64_t kGemvColumnBytes = 64 << 20;  // weights stored [K][N] up to t
 // Tile configurations of the products; kGemv: no tiles, at most kGemvRows rows.
 enum Config : int { kTile256, kTile128x256, kTile128, kTile64x128, kTile64, kTile16, kGemv, kConfigs };
 struct ConfigShape {
-    int bm, bn;
+    int bm, bn, threads;
 };
-constexpr ConfigShape kShapes[kConfigs] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}, {16, 128}, {kGemvRows, 1}};
+constexpr ConfigShape kShapes[kConfigs] = {{256, 256, 512}, {128, 256, 512}, {128, 128, 256}, {64, 128, 256},
+                                           {64, 64, 256},   {16, 128, 256},  {kGemvRows, 1, 0}};
 
 // Blocks of `threads` threads that a dimension of a grid can hold.  It is counted
 // in threads, in 32 bits: a launch of more wraps around without an error.
