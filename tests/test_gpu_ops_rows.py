@@ -76,6 +76,23 @@ def test_layer_norm_of_many_rows(ops, name, M, N):
     check_norm(x, w, b, 1e-3, y, mean, rstd, name)
 
 
+@pytest.mark.parametrize("N", range(1, 8))
+def test_layer_norm_narrower_than_a_unit(ops, N):
+    """Rows of fewer elements than 16 bytes hold, with NaN around them, and in place."""
+    say(f"layer_norm 1003 x {N} bf16")
+    g = torch.Generator(device="cuda").manual_seed(N)
+    box = torch.full((1005, N + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x = box[1:-1, 2:2 + N]
+    x.copy_(torch.randn(1003, N, generator=g, device="cuda") + 1.0)
+    w, b = (torch.randn(N, generator=g, device="cuda").to(x.dtype) for _ in range(2))
+    y, mean, rstd = ops.layer_norm(x, w, b, eps=1e-3)
+    check_norm(x, w, b, 1e-3, y, mean, rstd, "bf16")
+    ops.layer_norm(x, w, b, eps=1e-3, out=x)
+    assert torch.equal(x, y)
+    x.fill_(float("nan"))
+    assert bool(box.isnan().all()), "wrote outside the rows"
+
+
 def test_layer_norm_backward_of_many_long_rows(ops):
     """Rows that do not fit the registers, a block of 1024 threads each."""
     M, N, some = (1 << 22) + 3, 8193, [0, 1, (1 << 22) - 2, (1 << 22) - 1, 1 << 22, (1 << 22) + 2]

@@ -223,8 +223,7 @@ __device__ __forceinline__ int norm_col(int q, int i, int t) {
 // are columns: 4477 x 9970 150 us, 36 with units; 4477 x 4097 73 and 29.  fp32
 // gains nothing: 4096 x 9001 62 us, 76 with units.  Nor does the backward pass,
 // where the masks cost more: 912 x 49 12 us, 22 with units.)
-template <class T, bool VEC>
-constexpr bool kNormShift = !VEC && sizeof(T) == 2;
+enum Access : int { kElements, kUnits, kShifted };
 
 // First column of unit q, and whether its element i is this thread's.
 template <class T, int THREADS>
@@ -232,25 +231,25 @@ __device__ __forceinline__ int shifted(int q, int t, int N) {
     const int c = (q * THREADS + t) * kUnit<T>;
     return c + kUnit<T> <= N ? c : N - kUnit<T>;
 }
-template <class T, int THREADS, bool VEC>
+template <class T, int THREADS, Access A>
 __device__ __forceinline__ bool norm_mine(int q, int i, int t, int N) {
-    if constexpr (kNormShift<T, VEC>) {
+    if constexpr (A == kShifted) {
         const int c = (q * THREADS + t) * kUnit<T>;
         return shifted<T, THREADS>(q, t, N) + i >= c && c < N;
     }
-    return norm_col<T, THREADS, VEC>(q, i, t) < N;
+    return norm_col<T, THREADS, A == kUnits>(q, i, t) < N;
 }
 
 // (what is not this thread's: anything)
-template <class T, int THREADS, int VPT, bool VEC>
+template <class T, int THREADS, int VPT, Access A>
 __device__ __forceinline__ void norm_load(const char *row, int N, int t, float (&v)[VPT][kUnit<T>]) {
-    if constexpr (VEC || kNormShift<T, VEC>) {
+    if constexpr (A != kElements) {
         uint4 u[VPT];  // all requested before the first is used
 #pragma unroll
         for (int q = 0; q < VPT; ++q) {
             u[q] = make_uint4(0, 0, 0, 0);
-            if constexpr (VEC) {
-                const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+            if constexpr (A == kUnits) {
+                const int c = norm_col<T, THREADS, A == kUnits>(q, 0, t);
                 if (c < N) u[q] = *reinterpret_cast<const uint4 *>(row + (int64_t)c * sizeof(T));
             } else {
                 __builtin_memcpy(&u[q], row + (int64_t)shifted<T, THREADS>(q, t, N) * sizeof(T), 16);
@@ -263,20 +262,20 @@ __device__ __forceinline__ void norm_load(const char *row, int N, int t, float (
         for (int q = 0; q < VPT; ++q)
 #pragma unroll
             for (int i = 0; i < kUnit<T>; ++i) {
-                const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                const int c = norm_col<T, THREADS, A == kUnits>(q, i, t);
                 v[q][i] = c < N ? to_f32(reinterpret_cast<const T *>(row)[c]) : 0.0f;
             }
     }
 }
 
-template <class T, int THREADS, int VPT, bool VEC>
+template <class T, int THREADS, int VPT, Access A>
 __device__ __forceinline__ void norm_store(char *row, int N, int t, const float (&v)[VPT][kUnit<T>]) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-        if constexpr (VEC) {
-            const int c = norm_col<T, THREADS, VEC>(q, 0, t);
+        if constexpr (A == kUnits) {
+            const int c = norm_col<T, THREADS, A == kUnits>(q, 0, t);
             if (c < N) store_unit<T>(row + (int64_t)c * sizeof(T), v[q]);
-        } else if constexpr (kNormShift<T, VEC>) {
+        } else if constexpr (A == kShifted) {
             const int c = (q * THREADS + t) * kUnit<T>;
             if (c + kUnit<T> <= N) {
                 uint4 u;
@@ -292,7 +291,7 @@ __device__ __forceinline__ void norm_store(char *row, int N, int t, const float 
         } else {
 #pragma unroll
             for (int i = 0; i < kUnit<T>; ++i) {
-                const int c = norm_col<T, THREADS, VEC>(q, i, t);
+                const int c = norm_col<T, THREADS, A == kUnits>(q, i, t);
                 if (c < N) reinterpret_cast<T *>(row)[c] = from_f32<T>(v[q][i]);
             }
         }
@@ -303,7 +302,7 @@ __device__ __forceinline__ void norm_store(char *row, int N, int t, const float 
 // the values themselves (no difference of large squares).  Bound by its bytes,
 // read and written once: 4093 x 4099 fp32 (134 MB) 24.8 us, 5.4 TB/s; 16384 x
 // 8192 bf16 (537 MB) 108 us, 5.0 TB/s.
-template <class T, int THREADS, int VPT, bool VEC>
+template <class T, int THREADS, int VPT, Access A>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(NormArgs a) {
     constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, CE = kUnit<T>;
     __shared__ float sh[16];
@@ -311,19 +310,19 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(Nor
     const int row = blockIdx.x * (BLOCK / THREADS) + threadIdx.x / THREADS;
     if (row >= a.M) return;  // whole waves; with one row per block never taken
     float v[VPT][CE];
-    norm_load<T, THREADS, VPT, VEC>(a.x + (int64_t)row * a.ldx * sizeof(T), a.N, t, v);
+    norm_load<T, THREADS, VPT, A>(a.x + (int64_t)row * a.ldx * sizeof(T), a.N, t, v);
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
-        for (int i = 0; i < CE; ++i) s += norm_mine<T, THREADS, VEC>(q, i, t, a.N) ? v[q][i] : 0.0f;
+        for (int i = 0; i < CE; ++i) s += norm_mine<T, THREADS, A>(q, i, t, a.N) ? v[q][i] : 0.0f;
     const float mean = row_sum<THREADS>(s, sh) / (float)a.N;
     float ss = 0.0f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
         for (int i = 0; i < CE; ++i) {
-            v[q][i] = norm_mine<T, THREADS, VEC>(q, i, t, a.N) ? v[q][i] - mean : 0.0f;
+            v[q][i] = norm_mine<T, THREADS, A>(q, i, t, a.N) ? v[q][i] - mean : 0.0f;
             ss += v[q][i] * v[q][i];
         }
     const float rstd = 1.0f / sqrtf(row_sum<THREADS>(ss, sh) / (float)a.N + a.eps);
@@ -337,20 +336,20 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void norm_kernel(Nor
         for (int i = 0; i < CE; ++i) v[q][i] *= rstd;
     float p[VPT][CE];
     if (a.w) {
-        norm_load<T, THREADS, VPT, VEC>(a.w, a.N, t, p);
+        norm_load<T, THREADS, VPT, A>(a.w, a.N, t, p);
 #pragma unroll
         for (int q = 0; q < VPT; ++q)
 #pragma unroll
             for (int i = 0; i < CE; ++i) v[q][i] *= p[q][i];
     }
     if (a.b) {
-        norm_load<T, THREADS, VPT, VEC>(a.b, a.N, t, p);
+        norm_load<T, THREADS, VPT, A>(a.b, a.N, t, p);
 #pragma unroll
         for (int q = 0; q < VPT; ++q)
 #pragma unroll
             for (int i = 0; i < CE; ++i) v[q][i] += p[q][i];
     }
-    norm_store<T, THREADS, VPT, VEC>(a.y + (int64_t)row * a.ldy * sizeof(T), a.N, t, v);
+    norm_store<T, THREADS, VPT, A>(a.y + (int64_t)row * a.ldy * sizeof(T), a.N, t, v);
 }
 
 // Rows too long for registers: three passes over the row (the second and third
@@ -692,16 +691,18 @@ hipError_t by_rows(const NormArgs &a, int rows, int threads, F &&f) {
     return hipSuccess;
 }
 
-template <class T, bool VEC>
-hipError_t norm(const NormArgs &a, hipStream_t s) {
-    constexpr int CE = kUnit<T>, least = kNormShift<T, VEC> ? CE : 1;  // a unit has to fit the row
-#define CPO_NORM(THREADS, VPT)                                                                                        \
-    if (a.N >= least && a.N <= THREADS * VPT * CE) {                                                                  \
-        constexpr int BLOCK = THREADS < 256 ? 256 : THREADS;                                                          \
-        return by_rows<T>(a, BLOCK / THREADS, BLOCK, [&](const NormArgs &part, dim3 grid) {                           \
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, VEC>), grid, dim3(BLOCK), 0, s, part);    \
-        });                                                                                                           \
-    }
+template <class T, int THREADS, int VPT, Access A>
+hipError_t norm_rows(const NormArgs &a, hipStream_t s) {
+    constexpr int BLOCK = THREADS < 256 ? 256 : THREADS;
+    return by_rows<T>(a, BLOCK / THREADS, BLOCK, [&](const NormArgs &part, dim3 grid) {
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_kernel<T, THREADS, VPT, A>), grid, dim3(BLOCK), 0, s, part);
+    });
+}
+
+template <class T, Access A>
+hipError_t norm_widths(const NormArgs &a, hipStream_t s) {
+#define CPO_NORM(THREADS, VPT) \
+    if (a.N <= THREADS * VPT * kUnit<T>) return norm_rows<T, THREADS, VPT, A>(a, s);
     CPO_NORM(64, 1)
     CPO_NORM(64, 2)
     CPO_NORM(256, 1)
@@ -714,6 +715,17 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
     return by_rows<T>(a, 1, 1024, [&](const NormArgs &part, dim3 grid) {
         hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_long_kernel<T>), grid, dim3(1024), 0, s, part);
     });
+}
+
+template <class T>
+hipError_t norm(const NormArgs &a, hipStream_t s) {
+    if (a.vec) return norm_widths<T, kUnits>(a, s);
+    if constexpr (sizeof(T) == 2)
+        // a unit has to fit the row; narrower ones are a wave's single elements (as
+        // rows too long for registers, a block each, 1048576 x 4 took 3279 us, 204 so)
+        return a.N < kUnit<T> ? norm_rows<T, 64, 1, kElements>(a, s) : norm_widths<T, kShifted>(a, s);
+    else
+        return norm_widths<T, kElements>(a, s);
 }
 
 template <class T, bool VEC>
@@ -781,8 +793,7 @@ hipError_t launch_grad_join(int dtype, const GradArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t s) {
-    if (dtype == CP_BF16) return a.vec ? norm<__bf16, true>(a, s) : norm<__bf16, false>(a, s);
-    return a.vec ? norm<float, true>(a, s) : norm<float, false>(a, s);
+    return dtype == CP_BF16 ? norm<__bf16>(a, s) : norm<float>(a, s);
 }
 
 // One block, which stores the sums itself, where two launches would take longer
