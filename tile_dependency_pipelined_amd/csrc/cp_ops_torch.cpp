@@ -10,6 +10,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -134,6 +135,20 @@ Tensor empty_weight(const Tensor &w, bool stored_transposed) {
     return at::empty(s, w.options()).transpose(-1, -2);
 }
 
+// The tensor to write: `out`, or a new one.
+Tensor output(PyObject *o, const Tensor &x, at::IntArrayRef shape) {
+    if (o == Py_None) return empty(x, shape);
+    const Tensor &t = like(o, x, shape, "out");
+    if (c10::GradMode::is_enabled() && t.requires_grad())
+        refuse(PyExc_RuntimeError, "out requires a gradient, which is not recorded here; pass out.detach() or call under torch.no_grad()");
+    return t;
+}
+// Autograd takes what it saved as unchanged while its version is (tensors made
+// in inference mode have none, and are never saved).
+void written(const Tensor &out) {
+    if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+}
+
 bool aligned(const Tensor &x, std::initializer_list<const Tensor *> mats, std::initializer_list<int64_t> elements) {
     uint64_t bits = 0;
     for (const Tensor *t : mats) bits |= (uint64_t)t->data_ptr();
@@ -212,13 +227,14 @@ PyObject *linear(PyObject *const *a) {
     const int act = activation(a[4]);
     const bool need_pre = truth(a[5]);
     const c10::DeviceGuard guard(x.device());
-    const Tensor y = a[6] == Py_None ? empty(x, {M, N}) : like(a[6], x, {M, N}, "out");
+    const Tensor y = output(a[6], x, {M, N});
     const int64_t ldy = rows(y, "out");
     const Tensor pre = need_pre ? empty(x, {M, N}) : Tensor();
     const Scratch ws(x, CP_OP_LINEAR, M, K, N, 0, aligned(x, {&x, &w}, {ldx, K, ldw, N}));
     check(cp_linear(code(x), M, K, N, x.data_ptr(), ldx, w.data_ptr(), ldw, wt, bias, r ? r->data_ptr() : nullptr, ldr, act,
                     y.data_ptr(), ldy, data(pre), N, data(ws.t), ws.n, stream(x)),
           "cp_linear");
+    written(y);
     return need_pre ? wrap_tuple(y, pre) : wrap(y);
 }
 
@@ -262,7 +278,7 @@ PyObject *grouped_linear(PyObject *const *a) {
     const int act = activation(a[4]);
     const bool need_pre = truth(a[5]);
     const c10::DeviceGuard guard(x.device());
-    const Tensor y = a[6] == Py_None ? empty(x, {T, N}) : like(a[6], x, {T, N}, "out");
+    const Tensor y = output(a[6], x, {T, N});
     const int64_t ldy = rows(y, "out");
     const Tensor pre = need_pre ? empty(x, {T, N}) : Tensor();
     const Scratch ws(x, CP_OP_GROUPED_LINEAR, T, K, N, E, aligned(x, {&x, &w}, {ldx, K, ldw, N, sw}));
@@ -270,6 +286,7 @@ PyObject *grouped_linear(PyObject *const *a) {
                             (const int32_t *)off->data_ptr(), bias, act, y.data_ptr(), ldy, data(pre), N, data(ws.t), ws.n,
                             stream(x)),
           "cp_grouped_linear");
+    written(y);
     return need_pre ? wrap_tuple(y, pre) : wrap(y);
 }
 
@@ -307,13 +324,14 @@ PyObject *layer_norm(PyObject *const *a) {
     const double eps = PyFloat_AsDouble(a[3]);
     if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
     const c10::DeviceGuard guard(x.device());
-    const Tensor y = a[4] == Py_None ? empty(x, {M, N}) : like(a[4], x, {M, N}, "out");
+    const Tensor y = output(a[4], x, {M, N});
     const int64_t ldy = rows(y, "out");
     const auto f32 = x.options().dtype(at::kFloat);
     const Tensor mean = at::empty({M}, f32), rstd = at::empty({M}, f32);
     check(cp_layer_norm(code(x), M, N, x.data_ptr(), ldx, w, b, (float)eps, y.data_ptr(), ldy, (float *)mean.data_ptr(),
                         (float *)rstd.data_ptr(), stream(x)),
           "cp_layer_norm");
+    written(y);
     return wrap_tuple(y, mean, rstd);
 }
 

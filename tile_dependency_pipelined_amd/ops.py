@@ -15,6 +15,12 @@ come from PyTorch's allocator on that stream, and nothing is synchronised, so
 the calls can be captured into a graph.  Rows must have unit stride; any row
 stride that does not overlap is taken, and a weight may be a transposed view of
 a stored [N][K] matrix.  Weight gradients come back in the weight's layout.
+
+No gradient is recorded, whatever the inputs require: results have no history, and
+the *_backward functions are called by the program (or by its own
+torch.autograd.Function).  A tensor given as `out` counts as changed in place,
+so a gradient that needs its old values fails; one that requires a gradient is
+refused while gradients are recorded, as for torch's own `out` arguments.
 """
 import ctypes
 import os
