@@ -22,6 +22,9 @@
  *     call gives the same bits;
  *   - `ws` is scratch memory of at least cp_ops_workspace() bytes, 256-byte
  *     aligned, with any contents; calls that may overlap need their own;
+ *   - an output shares no memory with an input or another output unless
+ *     stated; Y and pre that do are refused with CP_ERR_INVALID_ARG (rows of
+ *     one buffer may interleave);
  *   - sizes of zero are allowed unless stated: empty outputs are left alone,
  *     a sum over nothing is zero.
  */
@@ -60,7 +63,7 @@ extern "C" {
  * is given.
  *   X[M][K], W[K][N] (w_trans = 0) or stored as [N][K] (w_trans = 1),
  *   bias[N] or NULL, R[M][N] or NULL, Y[M][N], pre[M][N] or NULL
- * Y may be R (same pointer and ld).  Y must not overlap any other input.
+ * Y may be R (same pointer and ld).
  */
 int cp_linear(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *X, int64_t ldx, const void *W, int64_t ldw,
               int32_t w_trans, const void *bias, const void *R, int64_t ldr, int32_t act, void *Y, int64_t ldy,

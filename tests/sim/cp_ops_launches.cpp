@@ -4,7 +4,10 @@
 //   op dtype M K N E w_trans act parts aligned
 // (op: forward | backward; dtype as in cp_chain.h; E = 0: dense; parts: bits 1
 // dX or the residual, 2 dW, 4 db or the bias; aligned: 0 puts every matrix off 16
-// bytes) and prints the launches of each in one line, ended by the status.
+// bytes) and prints the launches of each in one line, ended by the status.  Or,
+// with addresses of the caller's choice (0: NULL),
+//   linear dtype M K N E w_trans X ldx W ldw stride_w bias offsets R ldr Y ldy pre ldp
+//   norm dtype M N X ldx w b Y ldy
 // Pointers are never followed on the host, so they are only plausible numbers.
 #include <cstdio>
 #include <cstdlib>
@@ -62,11 +65,31 @@ int main() {
     char op[32];
     int dtype, E, wt, act, parts, aligned;
     long long M, K, N;
-    while (scanf("%31s %d %lld %lld %lld %d %d %d %d %d", op, &dtype, &M, &K, &N, &E, &wt, &act, &parts, &aligned) == 10) {
+    while (scanf("%31s", op) == 1) {
+        if (op[0] == 'l' || op[0] == 'n') {
+            std::vector<long long> v(op[0] == 'l' ? 19 : 9);
+            for (long long &x : v)
+                if (scanf("%lld", &x) != 1) return 2;
+            auto p = [&](int i) { return (void *)(uintptr_t)v[i]; };
+            void *ws = (void *)(uintptr_t(1) << 54);
+            const int64_t most = int64_t(1) << 53;
+            int rc;
+            if (op[0] == 'n')
+                rc = cp_layer_norm((int)v[0], v[1], v[2], p(3), v[4], p(5), p(6), 1e-5f, p(7), v[8], nullptr, nullptr, nullptr);
+            else if (v[4])
+                rc = cp_grouped_linear((int)v[0], v[1], v[2], v[3], (int)v[4], p(6), v[7], p(8), v[9], v[10], (int)v[5],
+                                       (const int32_t *)p(12), p(11), 0, p(15), v[16], p(17), v[18], ws, most, nullptr);
+            else
+                rc = cp_linear((int)v[0], v[1], v[2], v[3], p(6), v[7], p(8), v[9], (int)v[5], p(11), p(13), v[14], 0, p(15),
+                               v[16], p(17), v[18], ws, most, nullptr);
+            printf("status=%d %s\n", rc, cp_ops_last_error());
+            continue;
+        }
+        if (scanf("%d %lld %lld %lld %d %d %d %d %d", &dtype, &M, &K, &N, &E, &wt, &act, &parts, &aligned) != 9) return 2;
         // each matrix in a space of its own
-        const uintptr_t step = uintptr_t(1) << 44, off = aligned ? 0 : (dtype == CP_BF16 ? 2 : 4);
+        const uintptr_t step = uintptr_t(1) << 54, off = aligned ? 0 : (dtype == CP_BF16 ? 2 : 4);
         auto at = [&](int i) { return (void *)(step * i + off); };
-        const int64_t ldw = wt ? K : N, most = int64_t(1) << 43;
+        const int64_t ldw = wt ? K : N, most = int64_t(1) << 53;
         int rc;
         if (op[0] == 'f' && E)
             rc = cp_grouped_linear(dtype, M, K, N, E, at(1), K, at(2), ldw, K * N, wt, (const int32_t *)(step * 3),

@@ -1,6 +1,7 @@
 """GPU tests of `out` arguments and of what autograd sees: a tensor that a call
-writes is marked as changed, and one that requires a gradient is refused while
-gradients are recorded."""
+writes is marked as changed, one that requires a gradient is refused while
+gradients are recorded, and `out` may share memory only where the operator
+allows it."""
 import sys
 
 import pytest
@@ -72,3 +73,59 @@ def test_out_made_in_inference_mode(ops, name):
     assert torch.equal(buf, want)
     buf2 = call(buf)
     assert torch.equal(buf2, want)
+
+
+def test_out_that_overlaps_an_input(ops):
+    """Refused: other workgroups still read what such a call writes."""
+    say("overlap")
+    d = torch.bfloat16
+    M = N = K = 64
+    pool = torch.zeros(4 * M, 4 * N, dtype=d, device="cuda")
+    x, w, r = (torch.randn(M, N, device="cuda").to(d) for _ in range(3))
+    b = torch.zeros(N, dtype=d, device="cuda")
+    off = torch.tensor([0, 40, 64], dtype=torch.int32, device="cuda")
+    w2 = torch.stack([w, w])
+    shifted = pool[1:M + 1, :N]
+    bad = [
+        lambda: ops.linear(x, w, out=x),
+        lambda: ops.linear(x, w, out=w),
+        lambda: ops.linear(x, w.t(), out=w),
+        lambda: ops.linear(pool[:M, :K], w, out=pool[M - 1:2 * M - 1, :N]),
+        lambda: ops.linear(pool[:M, :K], w, out=pool[:M, K - 1:K - 1 + N]),
+        lambda: ops.linear(x, w, residual=pool[:M, :N], out=shifted),
+        lambda: ops.linear(x[:1], w, b, out=b[None]),
+        lambda: ops.grouped_linear(x, w2, off, out=x),
+        lambda: ops.grouped_linear(x, w2, off, out=w2[1]),
+        lambda: ops.layer_norm(pool[:M, :N], out=shifted),
+        lambda: ops.layer_norm(x, w[0], out=w),
+        lambda: ops.layer_norm(x, None, w[63], out=w),
+    ]
+    for i, call in enumerate(bad):
+        say("overlap", i)
+        with pytest.raises(RuntimeError, match="overlap"):
+            call()
+
+
+def test_out_beside_an_input(ops):
+    """Views of one buffer that share no element, and the tensors that `out` may be."""
+    say("views side by side")
+    d = torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, N = 40, 64
+    pool = torch.randn(2 * M, 3 * N, generator=g, device="cuda").to(d)
+    w = torch.randn(N, N, generator=g, device="cuda").to(d)
+    for x, out in ((pool[:M, :N], pool[:M, N:2 * N]), (pool[:M, :N], pool[M:, :N]), (pool[::2, :N], pool[1::2, :N]),
+                   (pool[::2, :N], pool[1::2, N:2 * N])):
+        want = ops.linear(x.clone(), w)
+        ops.linear(x, w, out=out)
+        assert torch.equal(out, want)
+        want = ops.layer_norm(x.clone())[0]
+        ops.layer_norm(x, out=out)
+        assert torch.equal(out, want)
+    x, r = pool[:M, :N], pool[:M, N:2 * N]
+    want = ops.linear(x, w, residual=r.clone())
+    ops.linear(x, w, residual=r, out=r)
+    assert torch.equal(r, want)
+    want = ops.layer_norm(x.clone())[0]
+    ops.layer_norm(x, out=x)
+    assert torch.equal(x, want)

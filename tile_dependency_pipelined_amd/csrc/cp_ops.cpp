@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <numeric>
 
 #include "cp_ops_host.h"
 
@@ -82,6 +83,50 @@ bool aligned16(const Mat &m, int dtype) {
     return !m.p || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld * es % 16 == 0 && m.cols * es % 16 == 0);
 }
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Memory of a matrix, or of one in a stack of `count`: rows of `width` bytes, `ld` bytes apart.
+struct Rows {
+    uintptr_t p;
+    int64_t rows, width, ld, count = 1, stride = 0;
+    Rows(const void *at, int64_t n, int64_t bytes, int64_t step) : p((uintptr_t)at), rows(n), width(bytes), ld(step) {}
+    Rows(const Mat &m, int dtype) : Rows(m.p, m.rows, m.cols * elem_size(dtype), m.ld * elem_size(dtype)) {}
+    Rows(const void *at, int64_t bytes) : Rows(at, 1, bytes, bytes) {}
+};
+
+// Whether a and b share a byte.  Views of one buffer may interleave: of the rows
+// of a that lie within b's extent, each is compared with b's rows, whose pattern
+// is that of the row's offset modulo b's row stride and repeats.
+bool overlap_one(const Rows &a, const Rows &b) {
+    if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+    const int64_t d = (int64_t)(a.p - b.p), extent = (b.rows - 1) * b.ld + b.width;
+    if (d >= extent || d + (a.rows - 1) * a.ld + a.width <= 0) return false;
+    const int64_t from = d + a.width > 0 ? 0 : (-d - a.width) / a.ld + 1;
+    int64_t to = (extent - 1 - d) / a.ld + 1;
+    if (to > a.rows) to = a.rows;
+    const int64_t period = b.ld / std::gcd(a.ld, b.ld);
+    for (int64_t r = from; r < to && r < from + period; ++r) {
+        const int64_t x = ((d + r * a.ld) % b.ld + b.ld) % b.ld;
+        if (x < b.width || x + a.width > b.ld) return true;
+    }
+    return false;
+}
+bool overlap(const Rows &a, Rows b) {
+    if (b.count > 1) {  // the usual case at once: apart from the whole stack
+        const uintptr_t a_end = a.p + (a.rows - 1) * a.ld + a.width;
+        const uintptr_t b_end = b.p + (b.count - 1) * b.stride + (b.rows - 1) * b.ld + b.width;
+        if (a_end <= b.p || b_end <= a.p) return false;
+    }
+    for (int64_t i = 0; i < b.count; ++i, b.p += b.stride)
+        if (overlap_one(a, b)) return true;
+    return false;
+}
+
+// An output against an input, or the other output; `same`: it may be that very matrix.
+int check_apart(const char *name, const Rows &out, const char *other, const Rows &in, bool same = false) {
+    if (same && out.p == in.p && (out.ld == in.ld || out.rows <= 1)) return CP_OK;
+    if (overlap(out, in)) return fail(CP_ERR_INVALID_ARG, "%s overlaps %s", name, other);
+    return CP_OK;
+}
 
 #define CP_TRY(expr)                  \
     do {                              \
@@ -527,6 +572,19 @@ int forward(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X, in
     p.off = off;
     p.bias = bias;
     p.act = act;
+    Rows w(p.B, dtype);
+    w.count = E > 1 ? E : 1;
+    w.stride = p.sb * elem_size(dtype);
+    for (const Mat *m : {&p.C, &p.P}) {
+        const char *name = m == &p.C ? "Y" : "pre";
+        const Rows out(*m, dtype);
+        CP_TRY(check_apart(name, out, "X", Rows(p.A, dtype)));
+        CP_TRY(check_apart(name, out, "W", w));
+        CP_TRY(check_apart(name, out, "bias", Rows(bias, (E ? E : 1) * N * elem_size(dtype))));
+        CP_TRY(check_apart(name, out, "offsets", Rows(off, (E + 1) * 4)));
+        CP_TRY(check_apart(name, out, "R", Rows(p.R, dtype), m == &p.C));
+    }
+    CP_TRY(check_apart("Y", Rows(p.C, dtype), "pre", Rows(p.P, dtype)));
     const bool aligned =
         aligned16(p.A, dtype) && aligned16(p.B, dtype) && p.sb * elem_size(dtype) % 16 == 0;
     CP_TRY(check_ws(ws, ws_bytes, forward_ws(dtype, M, K, N, E, aligned)));
@@ -721,6 +779,10 @@ int cp_layer_norm(int32_t dtype, int64_t M, int64_t N, const void *X, int64_t ld
     CP_TRY(check_mat(y, dtype, "Y"));
     CP_TRY(check_vector(w, dtype, "w"));
     CP_TRY(check_vector(b, dtype, "b"));
+    const Rows out(y, dtype);
+    CP_TRY(check_apart("Y", out, "X", Rows(x, dtype), true));
+    CP_TRY(check_apart("Y", out, "w", Rows(w, N * elem_size(dtype))));
+    CP_TRY(check_apart("Y", out, "b", Rows(b, N * elem_size(dtype))));
     NormArgs a{};
     a.x = (const char *)X;
     a.w = (const char *)w;

@@ -20,7 +20,8 @@ No gradient is recorded, whatever the inputs require: results have no history, a
 the *_backward functions are called by the program (or by its own
 torch.autograd.Function).  A tensor given as `out` counts as changed in place,
 so a gradient that needs its old values fails; one that requires a gradient is
-refused while gradients are recorded, as for torch's own `out` arguments.
+refused while gradients are recorded, as for torch's own `out` arguments.  It may
+share memory with an input only where its function says so.
 """
 import ctypes
 import os
