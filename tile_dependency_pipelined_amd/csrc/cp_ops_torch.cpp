@@ -171,6 +171,7 @@ void *stream(const Tensor &x) { return (void *)c10::hip::getCurrentHIPStream(x.g
 int activation(PyObject *o) {
     const long a = PyLong_AsLong(o);
     if (a == -1 && PyErr_Occurred()) throw Raised{};
+    if (a != (int)a) refuse(PyExc_ValueError, "activation %ld is not supported", a);
     return (int)a;
 }
 bool truth(PyObject *o) {
