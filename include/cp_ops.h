@@ -40,7 +40,7 @@ extern "C" {
 #endif
 
 /* activations of the operators, besides CP_ACT_NONE and CP_ACT_GELU_TANH */
-#define CP_ACT_RELU 2 /* max(x, 0); NaN stays NaN */
+#define CP_ACT_RELU 2 /* max(x, 0), derivative 0 at 0; NaN stays NaN */
 #define CP_ACT_SILU 3 /* x / (1 + exp(-x))        */
 
 /* operator codes of cp_ops_workspace */

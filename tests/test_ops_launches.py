@@ -9,6 +9,8 @@ import time
 
 import pytest
 
+from ops_kernels import CASES
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = os.path.join(ROOT, "tests", "sim", "cp_ops_launches.cpp")
 HIPCC = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
@@ -144,3 +146,35 @@ def test_overlap_of_large_views(many):
         f"linear 1 {M} 8 8 0 0 {1 << 20} 4194303 {far} 8 0 0 0 0 0 {(1 << 20) + 16} 4194304 0 0",
     ])
     assert [s for s, _ in got] == [0, -1, 0, -1, -1, -1] and time.time() - t0 < 20
+
+
+# -------------------------------------------------- the kernels the choice picks
+
+def launches_of(out):
+    out = re.sub(r":(threads|n[xwd])=\d+|:direct=1\b|:split=1\b", "", " ".join(out))
+    return out.replace(":layout=0", ":NN").replace(":layout=1", ":NT").replace(":layout=2", ":TN")
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:10])))
+def test_choice(launches, case):
+    out, status = launches(*case[:10])
+    assert status == CP_OK and launches_of(out) == case[10]
+
+
+def test_every_kernel_is_launched():
+    """Each configuration, dense and by expert, in both types and weight layouts, alone and for both gradients at once;
+    those of a product alone also split."""
+    got = set()
+    for c in CASES:
+        for w, layout, split in re.findall(r"((?:product|gradients):\w+)(?::([NT]{2}))?(:split=\d+)?", c[10]):
+            got.add((c[1], c[5] > 0, w, layout or c[6], bool(split)))
+        if "gemv" in c[10]:
+            got.add((c[0], c[1], "gemv", c[6]))
+    tiles = {BF16: ("256x256", "128x256", "128x128", "64x128", "64x64"), F32: ("128x128", "64x128", "64x64")}
+    want = {(d, g, f"gradients:{t}", wt, False) for d in tiles for g in (False, True) for t in tiles[d] for wt in (0, 1)}
+    want |= {(d, g, f"product:{t}", layout, split) for d in tiles for g in (False, True) for t in tiles[d]
+             for layout in ("NN", "NT", "TN") for split in (False, True)}
+    want |= {(d, g, "product:16x128", layout, split) for d in tiles for g in (False, True) for layout in ("NN", "NT")
+             for split in (False, True)}
+    want |= {("forward", d, "gemv", wt) for d in tiles for wt in (0, 1)}
+    assert want <= got, sorted(want - got, key=str)
