@@ -1,6 +1,6 @@
 // cp_ops.cpp -- host side of the feed-forward operators (include/cp_ops.h):
 // argument checks, choice of tile and split, launches.  No allocation, no
-// synchronisation, no state.
+// synchronisation; a thread keeps the choices of its recent shapes (choose).
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -178,7 +178,11 @@ int64_t slabs_of(const Shape &s) {
 
 // Few rows (per expert): 16-row tiles, whose time is that of reading B.  The
 // split fills the device twice over, keeping four slabs of 64 (fp32: 32) to a
-// split, so that the loads in flight are worth their latency.
+// split, so that the loads in flight are worth their latency.  Experts count by
+// their mean, as the host does not know their rows: where one has most of them,
+// its weight is read again by each of its tiles.  64 experts of 2048 x 4096, us
+// with the rows even | half of them in one expert | nine tenths: 8 rows each 186 |
+// 199 | 39, 16 each 190 | 232 | 285; 17 each, so with larger tiles, 192 | 192 | 198.
 bool few_rows(const Shape &s) {
     return s.layout != kTN && (s.mode == kGroupRows ? ceil_div(s.M, s.groups) : s.M) <= 16;
 }
@@ -231,7 +235,8 @@ double product_time(const Shape &s, Config c, int n) {
     // Each expert's weights are read by few tiles: the smaller the
     // tile, the more of them wait for the same memory (8192 x 4096 x
     // 2048 over 16 experts: 178 us with 256x256 tiles, 169 with
-    // 128x256, 183 with 128x128, which a single weight takes 130 us).
+    // 128x256, 183 with 128x128, which a single weight takes 130 us;
+    // the smaller ones are taken to be like it).
     if (s.mode == kGroupRows && c >= kTile128) us *= 1.2;
     // A split writes and reads its partials, mostly in the caches, and
     // takes another launch.
