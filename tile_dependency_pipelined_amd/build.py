@@ -27,7 +27,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = [os.path.join(CSRC, n) for n in ("cp_kernels.hip", "cp_chain.cpp", "cp_ops_gemm_bf16.hip",
                                            "cp_ops_gemm_f32.hip", "cp_ops_gradients_bf16.hip",
                                            "cp_ops_gradients_f32.hip", "cp_ops_gemv.hip", "cp_ops_rows.hip",
-                                           "cp_ops.cpp")]
+                                           "cp_ops_route.hip", "cp_ops_exchange.hip", "cp_ops_int4.hip",
+                                           "cp_ops_clip.hip", "cp_ops.cpp", "cp_ops_experts.cpp")]
 # Python module of the feed-forward operators (torch tensors in and out), linked to LIB
 TORCH_MODULE = os.path.join(PKG, "_cp_ops_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "cp_ops_torch.cpp")

@@ -1,0 +1,174 @@
+// cp_ops_clip.hip -- the norm over all the gradients of a model and their scaling:
+// N = sqrt(sum x^2), x min(1, c / (N + 1e-6)).  Two passes over the tensors, a launch
+// each however many there are (up to 96): the tensors are cut into chunks, numbered
+// through, and their addresses ride in the launch's arguments.  Squares are added
+// in 64 bits, which hold any fp32 value's square, and in an order that only the sizes
+// set, so a norm does not depend on timing and no finite gradient overflows it.  Both
+// passes are bound by memory: 64-bit sums run at the vector unit's full rate.
+#include "cp_ops_experts.h"
+
+namespace cpo {
+
+namespace {
+
+constexpr int kClipThreads = 256;
+
+// The tensor that holds chunk c (uniform): the last that begins at or before it.
+__device__ __forceinline__ int find_tensor(const ClipArgs &a, int64_t c) {
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.t[mid].before <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+__device__ __forceinline__ bool bit(const uint32_t *w, int i) { return w[i >> 5] >> (i & 31) & 1; }
+
+// Sum over the block, every thread gets it; the order is fixed.
+template <int NT>
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[NT / 64];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v += part[w];
+    return v;
+}
+
+// Squares of n elements from p on.
+template <class T, int NT>
+__device__ __forceinline__ void add_squares(const char *p, int64_t n, double (&acc)[4]) {
+    constexpr int CE = kUnit<T>, U = 4;
+    int64_t i = (int64_t)threadIdx.x * CE;
+    for (; i + (int64_t)(U - 1) * NT * CE + CE <= n; i += (int64_t)U * NT * CE) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) __builtin_memcpy(&v[u], p + (i + (int64_t)u * NT * CE) * (int64_t)sizeof(T), 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            T e[CE];
+            __builtin_memcpy(e, &v[u], 16);
+#pragma unroll
+            for (int j = 0; j < CE; ++j) {
+                const double d = (double)to_f32(e[j]);
+                acc[j & 3] = fma(d, d, acc[j & 3]);
+            }
+        }
+    }
+    for (; i < n; i += (int64_t)NT * CE) {
+        const uint4 v = load_partial<T>(p + i * (int64_t)sizeof(T), n - i < CE ? (int)(n - i) : CE);
+        T e[CE];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int j = 0; j < CE; ++j) {
+            const double d = (double)to_f32(e[j]);
+            acc[j & 3] = fma(d, d, acc[j & 3]);
+        }
+    }
+}
+
+// y = x f over n elements; x and y may be the same memory.
+template <class T, class O, int NT>
+__device__ __forceinline__ void scale_to(const char *x, char *y, int64_t n, float f) {
+    constexpr int CE = 8;  // elements to a step
+    constexpr int UI = CE / kUnit<T>, UO = CE / kUnit<O>;
+    for (int64_t i = (int64_t)threadIdx.x * CE; i < n; i += (int64_t)NT * CE) {
+        const int left = n - i < CE ? (int)(n - i) : CE;
+        T e[CE];
+        O o[CE];
+        if (left == CE) {
+            uint4 v[UI], w[UO];
+#pragma unroll
+            for (int u = 0; u < UI; ++u) __builtin_memcpy(&v[u], x + i * (int64_t)sizeof(T) + u * 16, 16);
+            __builtin_memcpy(e, v, sizeof e);
+#pragma unroll
+            for (int j = 0; j < CE; ++j) o[j] = from_f32<O>(to_f32(e[j]) * f);
+            __builtin_memcpy(w, o, sizeof o);
+#pragma unroll
+            for (int u = 0; u < UO; ++u) __builtin_memcpy(y + i * (int64_t)sizeof(O) + u * 16, &w[u], 16);
+        } else {
+            for (int j = 0; j < left; ++j)
+                reinterpret_cast<O *>(y)[i + j] = from_f32<O>(to_f32(reinterpret_cast<const T *>(x)[i + j]) * f);
+        }
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void square_chunk(const ClipArgs &a, int64_t c, double (&acc)[4]) {
+    const int i = find_tensor(a, c);
+    const int64_t from = (c - a.t[i].before) * kClipChunk, n = a.t[i].n - from < kClipChunk ? a.t[i].n - from : kClipChunk;
+    if (bit(a.bf16_in, i)) add_squares<__bf16, NT>(a.t[i].x + from * 2, n, acc);
+    else add_squares<float, NT>(a.t[i].x + from * 4, n, acc);
+}
+
+template <int NT>
+__device__ __forceinline__ void scale_chunk(const ClipArgs &a, int64_t c, float f) {
+    const int i = find_tensor(a, c);
+    if (f == 1.0f && a.t[i].y == a.t[i].x) return;  // in place, nothing to do
+    const int64_t from = (c - a.t[i].before) * kClipChunk, n = a.t[i].n - from < kClipChunk ? a.t[i].n - from : kClipChunk;
+    const bool bi = bit(a.bf16_in, i), bo = bit(a.bf16_out, i);
+    const char *x = a.t[i].x + from * (bi ? 2 : 4);
+    char *y = a.t[i].y + from * (bo ? 2 : 4);
+    if (bi && bo) scale_to<__bf16, __bf16, NT>(x, y, n, f);
+    else if (bi) scale_to<__bf16, float, NT>(x, y, n, f);
+    else if (bo) scale_to<float, __bf16, NT>(x, y, n, f);
+    else scale_to<float, float, NT>(x, y, n, f);
+}
+
+__device__ __forceinline__ float clip_factor(float norm, float most) {
+    const float f = most / (norm + 1e-6f);
+    return f > 1.0f || most == __builtin_inff() ? 1.0f : f;  // (a norm of NaN gives NaN)
+}
+
+__global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs a) {
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) square_chunk<kClipThreads>(a, c, acc);
+    const double s = block_sum<kClipThreads>((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
+}
+
+// The partial sums, at most a few KB, are added up by every block, which spares a
+// launch in between; the chunks go last to first, as the last read are the ones
+// that the caches still hold.
+__global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs a) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < a.nall; i += kClipThreads) s += a.all[i];
+    const float norm = (float)sqrt(block_sum<kClipThreads>(s));
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+    const float f = clip_factor(norm, a.max_norm);
+    if (a.t[0].y)  // (all have an output, or none)
+        for (int64_t c = a.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) scale_chunk<kClipThreads>(a, c, f);
+}
+
+constexpr int kClipOneThreads = 1024;
+__global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs a) {
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t c = 0; c < a.chunks; ++c) square_chunk<kClipOneThreads>(a, c, acc);
+    const float norm = (float)sqrt(block_sum<kClipOneThreads>((acc[0] + acc[1]) + (acc[2] + acc[3])));
+    if (threadIdx.x == 0) *a.norm = norm;
+    const float f = clip_factor(norm, a.max_norm);
+    if (a.t[0].y)
+        for (int64_t c = 0; c < a.chunks; ++c) scale_chunk<kClipOneThreads>(a, c, f);
+}
+
+}  // namespace
+
+hipError_t launch_norm_partials(const ClipArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(norm_partials_kernel, dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_clip(const ClipArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(clip_kernel, dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_clip_one(const ClipArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(clip_one_kernel, dim3(1), dim3(kClipOneThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace cpo

@@ -1,0 +1,169 @@
+// cp_ops_experts.h -- launch arguments and launchers of the operators around a
+// feed-forward block's products: router, exchange of rows with the experts,
+// 4-bit linear layers, gradient norm and clipping.  Internal.
+#pragma once
+#include "cp_ops_host.h"
+
+namespace cpo {
+
+// ------------------------------------------------------------------- router
+
+constexpr int kRouteTokens = 64;      // tokens of a chunk: one bit each of an expert's word
+constexpr int kRouteOneBlock = 256;   // tokens that one block takes on its own
+constexpr int kRouteBlocks = 256;     // blocks of a launch at most
+
+struct RouteArgs {
+    const char *logits;
+    const uint8_t *valid;  // [T] or null
+    int64_t ld;
+    int32_t *experts, *rows, *counts, *offsets;
+    float *gates, *loss, *slopes;
+    int32_t *hist, *live;  // scratch: slots of each expert [blocks][E] and tokens with an expert [blocks]
+    float *psum;           // scratch: sums of probabilities [blocks][E]
+    int32_t T, E, k, normalize;
+    int32_t blocks, chunks;  // chunks of kRouteTokens per block
+};
+inline int route_chunks(int64_t T) {
+    const int64_t chunks = (T + kRouteTokens - 1) / kRouteTokens;
+    if (T <= kRouteOneBlock) return chunks ? (int)chunks : 1;
+    return (int)((chunks + kRouteBlocks - 1) / kRouteBlocks);
+}
+inline int route_blocks(int64_t T) {
+    const int64_t per = (int64_t)route_chunks(T) * kRouteTokens;
+    return T ? (int)((T + per - 1) / per) : 1;
+}
+inline int64_t route_ws(int64_t T, int64_t E) {
+    const int64_t blocks = route_blocks(T);
+    return blocks > 1 ? (blocks * (2 * E + 1) * 4 + 255) / 256 * 256 : 0;
+}
+hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
+
+struct RouteGradArgs {
+    const char *logits;
+    const int32_t *experts;
+    const float *dgates, *dloss, *slopes;  // dgates or dloss may be null
+    char *dlogits;
+    int64_t ld, ldd;
+    int32_t T, E, k, normalize;
+};
+hipError_t launch_route_backward(int dtype, const RouteGradArgs &a, hipStream_t s);
+
+// ----------------------------------------------------- rows to experts and back
+
+// x [T][D] and y [R][D]; token t's slots are rows[t * k + j] of y (others than
+// 0 .. R-1: no slot).  Which of the pointers are set depends on the operator.
+struct ExchangeArgs {
+    const char *x, *y, *res;
+    char *out, *dy;
+    const int32_t *rows, *end;  // *end: rows of y from there on belong to no slot
+    const float *gates;
+    float *dgates;
+    int64_t ldx, ldy, ldr, ldo, lddy;
+    int64_t T, R;
+    int32_t k, D;
+};
+hipError_t launch_dispatch(int dtype, const ExchangeArgs &a, hipStream_t s);          // x -> out [R][D]
+hipError_t launch_combine(int dtype, const ExchangeArgs &a, hipStream_t s);           // y, res -> out [T][D]
+hipError_t launch_combine_backward(int dtype, const ExchangeArgs &a, hipStream_t s);  // x = dout, y -> dy, dgates
+
+// ---------------------------------------------------------- 4-bit linear layers
+
+// Codes as the matrix instructions take them: tiles of 16 columns x 128 of K,
+// 1 KB each, a column's tiles one after another; lane l of a wave holds column
+// l % 16 and four words, word s the k = 32 s + 8 (l / 16) .. + 7, whose codes i
+// are at bits 4 (i / 2) + 16 (i % 2).  Behind them the scales [column tile]
+// [group][16], behind those the zero points, bytes, the same way.
+constexpr int kInt4Columns = 16, kInt4Depth = 128, kInt4TileBytes = 1024;
+
+struct Int4Layout {
+    int64_t ntiles, kblocks, ngroups;
+    int64_t codes, scales, zeros;  // bytes per expert
+    Int4Layout(int dtype, int64_t K, int64_t N, int64_t group, bool zero_points)
+        : ntiles((N + kInt4Columns - 1) / kInt4Columns),
+          kblocks((K + kInt4Depth - 1) / kInt4Depth),
+          ngroups((K + group - 1) / group),
+          codes(ntiles * kblocks * kInt4TileBytes),
+          scales(ntiles * ngroups * kInt4Columns * (dtype == CP_BF16 ? 2 : 4)),
+          zeros(zero_points ? ntiles * ngroups * kInt4Columns : 0) {}
+    int64_t bytes(int64_t E) const { return E * (codes + scales + zeros); }
+};
+
+struct Int4Args {
+    const char *x, *codes, *scales, *bias, *res;
+    const uint8_t *zeros;  // null: 8
+    char *y;
+    int64_t ldx, ldr, ldy;
+    int64_t sc, ss, sz;    // bytes from one expert to the next
+    const int32_t *off;    // device: groups + 1 row offsets, or null
+    int32_t experts;       // 0: dense
+    int32_t M, K, N, act;
+    int32_t ntiles, kblocks, ngroups, group;
+    int32_t ntm, ntn;      // row tiles (at most) and column sets of the launch
+};
+// Tiles of a launch: mt x 16 rows, nt x 16 columns.
+struct Int4Tiles {
+    int32_t mt, nt, ntm, ntn;
+};
+inline Int4Tiles int4_tiles(int experts, int64_t M, int64_t ntiles) {
+    Int4Tiles t;
+    const int64_t rows = experts ? (M + experts - 1) / experts : M;  // to an expert, on average
+    t.mt = rows <= 16 ? 1 : 4;
+    t.nt = t.mt > 1 ? 4 : (ntiles > 512 ? 2 : 1);
+    const int64_t bm = 16 * t.mt, used = M < experts + 1 ? M : experts + 1;
+    t.ntm = (int32_t)(experts ? (M + used * (bm - 1)) / bm : (M + bm - 1) / bm);
+    t.ntn = (int32_t)((ntiles + t.nt - 1) / t.nt);
+    return t;
+}
+hipError_t launch_int4(int dtype, const Int4Args &a, hipStream_t s);
+
+struct Int4PackArgs {
+    const uint8_t *q, *zeros;
+    const char *scales;
+    char *codes, *pscales;
+    uint8_t *pzeros;
+    int64_t K, N, E;
+    int32_t ntiles, kblocks, ngroups, scale_bytes;
+};
+hipError_t launch_int4_pack(const Int4PackArgs &a, hipStream_t s);
+
+struct Int4QuantArgs {
+    const char *w;
+    int64_t sk, sn, se;  // strides in elements
+    uint8_t *q, *zeros;  // zeros null: symmetric
+    char *scales;
+    int64_t K, N, E;
+    int32_t group, ngroups;
+};
+hipError_t launch_int4_quantize(int dtype, const Int4QuantArgs &a, hipStream_t s);
+
+// ------------------------------------------------------ gradient norm, clipping
+
+constexpr int kClipTensors = 96;    // of a launch: its arguments hold their addresses
+constexpr int kClipBlocks = 1024;   // blocks, and partial sums, of a launch
+constexpr int64_t kClipOneBlock = 1 << 16;  // elements that one block takes on its own
+
+struct ClipArgs {
+    struct One {
+        const char *x;
+        char *y;           // output, or null
+        int64_t n;
+        int64_t before;    // chunks of the tensors before it in this launch
+    } t[kClipTensors];
+    uint32_t bf16_in[(kClipTensors + 31) / 32], bf16_out[(kClipTensors + 31) / 32];
+    int32_t n, blocks;
+    int64_t chunks;
+    double *partial;       // this launch's
+    const double *all;     // of all launches
+    int32_t nall;
+    float max_norm;
+    float *norm;
+};
+constexpr int kClipChunk = 16384;   // elements a block takes at a time
+inline int64_t clip_ws(int64_t tensors) {  // partial sums of every launch
+    return (tensors + kClipTensors - 1) / kClipTensors * kClipBlocks * (int64_t)sizeof(double);
+}
+hipError_t launch_norm_partials(const ClipArgs &a, hipStream_t s);
+hipError_t launch_clip(const ClipArgs &a, hipStream_t s);
+hipError_t launch_clip_one(const ClipArgs &a, hipStream_t s);
+
+}  // namespace cpo

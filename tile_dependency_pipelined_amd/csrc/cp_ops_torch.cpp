@@ -18,6 +18,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <string>
+#include <vector>
 
 #include "cp_ops.h"
 
@@ -355,6 +356,337 @@ PyObject *layer_norm_backward(PyObject *const *a) {
     return wrap_tuple(dx, dw, db);
 }
 
+// ---- router, exchange of rows, 4-bit layers, clipping ----------------------
+
+int64_t integer(PyObject *o, const char *name) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    if (v != (int32_t)v) refuse(PyExc_ValueError, "%s = %lld is out of range", name, v);
+    return v;
+}
+double number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+
+// An int32 matrix [T][k] of a token's slots.
+const Tensor &slots(PyObject *o, const Tensor &x, const char *name) {
+    const Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kInt || t.dim() != 2 || !t.is_contiguous() || t.device() != x.device())
+        refuse(PyExc_ValueError, "%s must be a contiguous int32 matrix on %s", name, x.device().str().c_str());
+    return t;
+}
+// The last of offsets [E + 1].
+const int32_t *last_offset(PyObject *o, const Tensor &x) {
+    const Tensor &t = tensor(o, "offsets");
+    if (t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) < 1 || !t.is_contiguous() || t.device() != x.device())
+        refuse(PyExc_ValueError, "offsets must be a contiguous int32 vector on %s", x.device().str().c_str());
+    return (const int32_t *)t.data_ptr() + (t.size(0) - 1);
+}
+
+// route(logits, k, normalize, valid) -> experts, gates, rows, counts, offsets, loss, slopes
+PyObject *route(PyObject *const *a) {
+    const Tensor &x = first(a[0], "logits");
+    const int64_t T = x.size(0), E = x.size(1), k = integer(a[1], "k"), ld = rows(x, "logits");
+    const bool normalize = truth(a[2]);
+    const void *valid = a[3] == Py_None ? nullptr : vector(a[3], x, {T}, "valid", at::kBool);
+    if (E < 1 || E > CP_OPS_MAX_ROUTED || k < 1 || k > E || k > CP_OPS_MAX_CHOSEN)
+        refuse(PyExc_ValueError, "%lld of %lld experts to a token (1 to %d of at most %d)", (long long)k, (long long)E,
+               CP_OPS_MAX_CHOSEN, CP_OPS_MAX_ROUTED);
+    const c10::DeviceGuard guard(x.device());
+    const auto i32 = x.options().dtype(at::kInt), f32 = x.options().dtype(at::kFloat);
+    const Tensor experts = at::empty({T, k}, i32), gates = at::empty({T, k}, f32), places = at::empty({T, k}, i32);
+    const Tensor counts = at::empty({E}, i32), offsets = at::empty({E + 1}, i32), loss = at::empty({}, f32);
+    const Tensor slopes = at::empty({E}, f32);
+    const Scratch ws(x, CP_OP_ROUTE, T, 0, E, 0, true);
+    check(cp_route(code(x), T, (int32_t)E, (int32_t)k, normalize, x.data_ptr(), ld, (const uint8_t *)valid,
+                   (int32_t *)experts.data_ptr(), (float *)gates.data_ptr(), (int32_t *)places.data_ptr(),
+                   (int32_t *)counts.data_ptr(), (int32_t *)offsets.data_ptr(), (float *)loss.data_ptr(),
+                   (float *)slopes.data_ptr(), data(ws.t), ws.n, stream(x)),
+          "cp_route");
+    return wrap_tuple(experts, gates, places, counts, offsets, loss, slopes);
+}
+
+// route_backward(dgates, dloss, logits, experts, slopes, normalize)
+PyObject *route_backward(PyObject *const *a) {
+    const Tensor &x = first(a[2], "logits");
+    const int64_t T = x.size(0), E = x.size(1), ld = rows(x, "logits");
+    const Tensor &experts = slots(a[3], x, "experts");
+    const int64_t k = experts.size(1);
+    like(a[3], x, {T, k}, "experts", at::kInt);
+    const void *dgates = a[0] == Py_None ? nullptr : vector(a[0], x, {T, k}, "dgates", at::kFloat);
+    const void *dloss = a[1] == Py_None ? nullptr : vector(a[1], x, {}, "dloss", at::kFloat);
+    const void *slopes = dloss ? vector(a[4], x, {E}, "slopes", at::kFloat) : nullptr;
+    const bool normalize = truth(a[5]);
+    const c10::DeviceGuard guard(x.device());
+    const Tensor d = empty(x, {T, E});
+    check(cp_route_backward(code(x), T, (int32_t)E, (int32_t)k, normalize, (const float *)dgates, (const float *)dloss,
+                            x.data_ptr(), ld, (const int32_t *)experts.data_ptr(), (const float *)slopes, d.data_ptr(), E,
+                            stream(x)),
+          "cp_route_backward");
+    return wrap(d);
+}
+
+// dispatch(x, rows, offsets, out)
+PyObject *dispatch(PyObject *const *a) {
+    const Tensor &x = first(a[0], "x");
+    const int64_t T = x.size(0), D = x.size(1), ldx = rows(x, "x");
+    const Tensor &places = slots(a[1], x, "rows");
+    const int64_t k = places.size(1), R = T * k;
+    like(a[1], x, {T, k}, "rows", at::kInt);
+    const int32_t *end = last_offset(a[2], x);
+    const c10::DeviceGuard guard(x.device());
+    const Tensor out = output(a[3], x, {R, D});
+    const int64_t ldo = rows(out, "out");
+    check(cp_dispatch(code(x), T, (int32_t)k, R, D, x.data_ptr(), ldx, (const int32_t *)places.data_ptr(), end,
+                      out.data_ptr(), ldo, stream(x)),
+          "cp_dispatch");
+    written(out);
+    return wrap(out);
+}
+
+// combine(y, rows, gates, residual, out)
+PyObject *combine(PyObject *const *a) {
+    const Tensor &y = first(a[0], "y");
+    const int64_t R = y.size(0), D = y.size(1), ldy = rows(y, "y");
+    const Tensor &places = slots(a[1], y, "rows");
+    const int64_t T = places.size(0), k = places.size(1);
+    const void *gates = a[2] == Py_None ? nullptr : vector(a[2], y, {T, k}, "gates", at::kFloat);
+    const Tensor *r = a[3] == Py_None ? nullptr : &like(a[3], y, {T, D}, "residual");
+    const int64_t ldr = r ? rows(*r, "residual") : 0;
+    const c10::DeviceGuard guard(y.device());
+    const Tensor out = output(a[4], y, {T, D});
+    const int64_t ldo = rows(out, "out");
+    check(cp_combine(code(y), T, (int32_t)k, R, D, y.data_ptr(), ldy, (const int32_t *)places.data_ptr(), (const float *)gates,
+                     r ? r->data_ptr() : nullptr, ldr, out.data_ptr(), ldo, stream(y)),
+          "cp_combine");
+    written(out);
+    return wrap(out);
+}
+
+// combine_backward(dout, y, rows, offsets, gates, need_y, need_gates)
+PyObject *combine_backward(PyObject *const *a) {
+    const Tensor &d = first(a[0], "dout");
+    const int64_t T = d.size(0), D = d.size(1), ldd = rows(d, "dout");
+    const Tensor &y = tensor(a[1], "y");
+    if (y.dim() != 2) refuse(PyExc_ValueError, "y must have 2 dimensions, got %d", (int)y.dim());
+    const int64_t R = y.size(0);
+    like(a[1], d, {R, D}, "y");
+    const int64_t ldy = rows(y, "y");
+    const Tensor &places = slots(a[2], d, "rows");
+    const int64_t k = places.size(1);
+    like(a[2], d, {T, k}, "rows", at::kInt);
+    const int32_t *end = last_offset(a[3], d);
+    const void *gates = a[4] == Py_None ? nullptr : vector(a[4], d, {T, k}, "gates", at::kFloat);
+    const bool need_y = truth(a[5]), need_gates = truth(a[6]);
+    const c10::DeviceGuard guard(d.device());
+    const Tensor dy = need_y ? empty(d, {R, D}) : Tensor();
+    const Tensor dg = need_gates ? at::empty({T, k}, d.options().dtype(at::kFloat)) : Tensor();
+    check(cp_combine_backward(code(d), T, (int32_t)k, R, D, d.data_ptr(), ldd, y.data_ptr(), ldy,
+                              (const int32_t *)places.data_ptr(), end, (const float *)gates, data(dy), D, (float *)data(dg),
+                              stream(d)),
+          "cp_combine_backward");
+    return wrap_tuple(dy, dg);
+}
+
+// Experts of a stack of weights, 1 for a single matrix.
+int64_t stack(const Tensor &t, const char *name) {
+    if (t.dim() != 2 && t.dim() != 3) refuse(PyExc_ValueError, "%s must have 2 or 3 dimensions, got %d", name, (int)t.dim());
+    const int64_t E = t.dim() == 3 ? t.size(0) : 1;
+    if (E < 1 || E > CP_OPS_MAX_GROUPS) refuse(PyExc_ValueError, "%lld experts (1 to %d)", (long long)E, CP_OPS_MAX_GROUPS);
+    return E;
+}
+int64_t group_of(PyObject *o) {
+    const int64_t g = integer(o, "group_size");
+    if (g != 32 && g != 64 && (g < 128 || g % 128 || g > CP_OPS_MAX_WIDTH))
+        refuse(PyExc_ValueError, "groups of %lld (32, 64 or a multiple of 128)", (long long)g);
+    return g;
+}
+std::vector<int64_t> with_rows(const Tensor &t, int64_t rows) {
+    auto s = t.sizes().vec();
+    s[s.size() - 2] = rows;
+    return s;
+}
+
+// quantize_int4(w, group_size, symmetric) -> codes, scales, zeros
+PyObject *quantize_int4(PyObject *const *a) {
+    if (!THPVariable_Check(a[0]) || !THPVariable_Unpack(a[0]).is_cuda()) refuse(PyExc_TypeError, "w must be a device tensor");
+    const Tensor &w = THPVariable_Unpack(a[0]);
+    if (w.scalar_type() != at::kFloat && w.scalar_type() != at::kBFloat16)
+        refuse(PyExc_ValueError, "w must be float32 or bfloat16, got %s", c10::toString(w.scalar_type()));
+    const int64_t E = stack(w, "w"), g = group_of(a[1]), d = w.dim(), K = w.size(d - 2), N = w.size(d - 1);
+    const bool symmetric = truth(a[2]);
+    const c10::DeviceGuard guard(w.device());
+    const auto u8 = w.options().dtype(at::kByte);
+    const auto per = with_rows(w, (K + g - 1) / g);
+    const Tensor q = at::empty(w.sizes(), u8), scales = at::empty(per, w.options());
+    const Tensor zeros = symmetric ? Tensor() : at::empty(per, u8);
+    check(cp_int4_quantize(code(w), K, N, (int32_t)E, g, w.data_ptr(), w.stride(d - 2), w.stride(d - 1), d == 3 ? w.stride(0) : 0,
+                           (uint8_t *)q.data_ptr(), scales.data_ptr(), (uint8_t *)data(zeros), stream(w)),
+          "cp_int4_quantize");
+    return wrap_tuple(q, scales, zeros);
+}
+
+// pack_int4(codes, scales, zeros, group_size) -> bytes
+PyObject *pack_int4(PyObject *const *a) {
+    if (!THPVariable_Check(a[1]) || !THPVariable_Unpack(a[1]).is_cuda()) refuse(PyExc_TypeError, "scales must be a device tensor");
+    const Tensor &scales = THPVariable_Unpack(a[1]);
+    if (scales.scalar_type() != at::kFloat && scales.scalar_type() != at::kBFloat16)
+        refuse(PyExc_ValueError, "scales must be float32 or bfloat16, got %s", c10::toString(scales.scalar_type()));
+    const Tensor &q = tensor(a[0], "codes");
+    const int64_t E = stack(q, "codes"), g = group_of(a[3]), d = q.dim(), K = q.size(d - 2), N = q.size(d - 1);
+    const void *codes = vector(a[0], scales, q.sizes(), "codes", at::kByte);
+    const auto per = with_rows(q, (K + g - 1) / g);
+    vector(a[1], scales, per, "scales", scales.scalar_type());
+    const void *zeros = a[2] == Py_None ? nullptr : vector(a[2], scales, per, "zeros", at::kByte);
+    const int64_t n = cp_int4_bytes(code(scales), K, N, (int32_t)E, g, zeros != nullptr);
+    check(n, "cp_int4_bytes");
+    const c10::DeviceGuard guard(scales.device());
+    const Tensor packed = at::empty({n}, scales.options().dtype(at::kByte));
+    check(cp_int4_pack(code(scales), K, N, (int32_t)E, g, (const uint8_t *)codes, scales.data_ptr(), (const uint8_t *)zeros,
+                       packed.data_ptr(), stream(scales)),
+          "cp_int4_pack");
+    return wrap(packed);
+}
+
+// A packed weight's data: as many bytes as its sizes say.
+const Tensor &packed_weight(PyObject *o, const Tensor &x, int64_t K, int64_t N, int64_t E, int64_t group, bool zeros) {
+    const int64_t n = cp_int4_bytes(code(x), K, N, (int32_t)E, group, zeros);
+    check(n, "cp_int4_bytes");
+    const Tensor &t = like(o, x, {n}, "the packed weight", at::kByte);
+    if (!t.is_contiguous()) refuse(PyExc_ValueError, "the packed weight must be contiguous");
+    return t;
+}
+
+// linear_int4(x, packed, N, group, zeros, bias, residual, act, out)
+PyObject *linear_int4(PyObject *const *a) {
+    const Tensor &x = first(a[0], "x");
+    const int64_t M = x.size(0), K = x.size(1), ldx = rows(x, "x"), N = integer(a[2], "N"), g = group_of(a[3]);
+    const bool zeros = truth(a[4]);
+    const Tensor &w = packed_weight(a[1], x, K, N, 1, g, zeros);
+    const void *bias = optional_vector(a[5], x, {N}, "bias");
+    const Tensor *r = a[6] == Py_None ? nullptr : &like(a[6], x, {M, N}, "residual");
+    const int64_t ldr = r ? rows(*r, "residual") : 0;
+    const int act = activation(a[7]);
+    const c10::DeviceGuard guard(x.device());
+    const Tensor y = output(a[8], x, {M, N});
+    const int64_t ldy = rows(y, "out");
+    check(cp_linear_int4(code(x), M, K, N, x.data_ptr(), ldx, w.data_ptr(), g, zeros, bias, r ? r->data_ptr() : nullptr, ldr,
+                         act, y.data_ptr(), ldy, stream(x)),
+          "cp_linear_int4");
+    written(y);
+    return wrap(y);
+}
+
+// grouped_linear_int4(x, packed, E, N, group, zeros, offsets, bias, act, out)
+PyObject *grouped_linear_int4(PyObject *const *a) {
+    const Tensor &x = first(a[0], "x");
+    const int64_t T = x.size(0), K = x.size(1), ldx = rows(x, "x"), E = integer(a[2], "E"), N = integer(a[3], "N");
+    const int64_t g = group_of(a[4]);
+    const bool zeros = truth(a[5]);
+    const Tensor &w = packed_weight(a[1], x, K, N, E, g, zeros);
+    const void *off = vector(a[6], x, {E + 1}, "offsets", at::kInt);
+    const void *bias = optional_vector(a[7], x, {E, N}, "bias");
+    const int act = activation(a[8]);
+    const c10::DeviceGuard guard(x.device());
+    const Tensor y = output(a[9], x, {T, N});
+    const int64_t ldy = rows(y, "out");
+    check(cp_grouped_linear_int4(code(x), T, K, N, (int32_t)E, x.data_ptr(), ldx, w.data_ptr(), g, zeros, (const int32_t *)off,
+                                 bias, act, y.data_ptr(), ldy, stream(x)),
+          "cp_grouped_linear_int4");
+    written(y);
+    return wrap(y);
+}
+
+// A gradient: float32 or bfloat16 elements that fill their memory, in any order.
+const Tensor &dense(PyObject *o, const char *name) {
+    if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda()) refuse(PyExc_TypeError, "%s must be device tensors", name);
+    const Tensor &t = THPVariable_Unpack(o);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
+        refuse(PyExc_ValueError, "%s must be float32 or bfloat16, got %s", name, c10::toString(t.scalar_type()));
+    if (!t.is_non_overlapping_and_dense())
+        refuse(PyExc_ValueError, "%s must fill their memory (strides %s); call .contiguous()", name,
+               shape_text(t.strides()).c_str());
+    return t;
+}
+
+struct Sequence {
+    PyObject *s;
+    explicit Sequence(PyObject *o) : s(PySequence_Fast(o, "gradients and out must be sequences of tensors")) {
+        if (!s) throw Raised{};
+    }
+    ~Sequence() { Py_DECREF(s); }
+    Sequence(const Sequence &) = delete;
+    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(s); }
+    PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
+};
+
+// clip_grad_norm(gradients, max_norm, out, scale) -> norm; out: None for in place
+PyObject *clip_grad_norm(PyObject *const *a) {
+    const Sequence grads(a[0]);
+    const double max_norm = number(a[1]);
+    const bool scale = truth(a[3]);
+    const Py_ssize_t n = grads.size();
+    if (n == 0) refuse(PyExc_ValueError, "no gradients");
+    const Tensor &x0 = dense(grads[0], "gradients");
+    std::vector<int32_t> types(n), out_types(n);
+    std::vector<const void *> from(n);
+    std::vector<void *> to(n);
+    std::vector<int64_t> numels(n);
+    auto enter = [&](Py_ssize_t i, const Tensor &x, const Tensor &y) {
+        if (x.device() != x0.device() || y.device() != x0.device())
+            refuse(PyExc_ValueError, "gradients and out must be on one device");
+        types[i] = code(x);
+        from[i] = x.data_ptr();
+        numels[i] = x.numel();
+        out_types[i] = code(y);
+        to[i] = y.data_ptr();
+    };
+    auto writable = [](const Tensor &t) {
+        if (c10::GradMode::is_enabled() && t.requires_grad())
+            refuse(PyExc_RuntimeError, "a tensor to write requires a gradient, which is not recorded here; pass .detach() or "
+                                       "call under torch.no_grad()");
+    };
+    if (a[2] == Py_None) {
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const Tensor &x = dense(grads[i], "gradients");
+            if (scale) writable(x);
+            enter(i, x, x);
+        }
+    } else {
+        const Sequence outs(a[2]);
+        if (outs.size() != n) refuse(PyExc_ValueError, "%zd gradients and %zd outputs", n, outs.size());
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const Tensor &x = dense(grads[i], "gradients"), &y = dense(outs[i], "out");
+            bool same = x.sizes() == y.sizes();
+            for (int64_t d = 0; same && d < x.dim(); ++d)
+                same = x.numel() == 0 || x.size(d) == 1 || x.stride(d) == y.stride(d);
+            if (!same)
+                refuse(PyExc_ValueError, "out %zd must have its gradient's shape and strides: %s %s, got %s %s", i,
+                       shape_text(x.sizes()).c_str(), shape_text(x.strides()).c_str(), shape_text(y.sizes()).c_str(),
+                       shape_text(y.strides()).c_str());
+            writable(y);
+            enter(i, x, y);
+        }
+    }
+    const c10::DeviceGuard guard(x0.device());
+    const Tensor norm = at::empty({}, x0.options().dtype(at::kFloat));
+    const Scratch ws(x0, CP_OP_CLIP_GRAD_NORM, n, 0, 0, 0, true);
+    check(cp_clip_grad_norm(n, types.data(), from.data(), numels.data(), (float)max_norm, out_types.data(),
+                            scale ? to.data() : nullptr, (float *)norm.data_ptr(), data(ws.t), ws.n, stream(x0)),
+          "cp_clip_grad_norm");
+    if (scale) {
+        if (a[2] == Py_None) {
+            for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(grads[i]));
+        } else {
+            const Sequence outs(a[2]);
+            for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(outs[i]));
+        }
+    }
+    return wrap(norm);
+}
+
 // Argument count, and C++ exceptions into Python's (torch's own, out of memory
 // among them, keep their types).
 template <PyObject *(*F)(PyObject *const *), int ARGS>
@@ -389,6 +721,16 @@ PyMethodDef g_methods[] = {CP_METHOD(linear, 7),
                            CP_METHOD(grouped_linear_backward, 9),
                            CP_METHOD(layer_norm, 5),
                            CP_METHOD(layer_norm_backward, 8),
+                           CP_METHOD(route, 4),
+                           CP_METHOD(route_backward, 6),
+                           CP_METHOD(dispatch, 4),
+                           CP_METHOD(combine, 5),
+                           CP_METHOD(combine_backward, 7),
+                           CP_METHOD(quantize_int4, 3),
+                           CP_METHOD(pack_int4, 4),
+                           CP_METHOD(linear_int4, 9),
+                           CP_METHOD(grouped_linear_int4, 10),
+                           CP_METHOD(clip_grad_norm, 4),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_cp_ops_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

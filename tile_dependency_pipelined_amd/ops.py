@@ -1,10 +1,13 @@
 """Feed-forward operators on torch tensors: linear layers with a fused epilogue,
-linear layers grouped by expert, and layer normalisation, each with its
-backward pass.
+linear layers grouped by expert, layer normalisation, the router of an expert
+layer and its rows' way to the experts and back, each with its backward pass;
+linear layers with 4-bit weights; the gradients' norm and clipping.
 
     y = act(x w + b) + residual
     y_t = act(x_t w_e + b_e)            rows sorted by expert
     y = (x - mean) rstd w + b
+    out_t = sum_j g_tj y[rows_tj] + residual_t
+    w_kn = scale_gn (code_kn - zero_gn)
 
 Every arithmetic step runs in libcpchain.so (include/cp_ops.h); the module
 _cp_ops_torch checks the arguments and calls it.  There is no fallback: without the
@@ -25,6 +28,7 @@ share memory with an input only where its function says so.
 """
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch  # noqa: F401  (the module below links to its libraries)
 
@@ -39,12 +43,17 @@ except ImportError as e:
 ACT_NONE, ACT_GELU_TANH, ACT_RELU, ACT_SILU = 0, 1, 2, 3
 ACTS = {"none": ACT_NONE, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU, "silu": ACT_SILU}
 OP_LINEAR, OP_LINEAR_BACKWARD, OP_GROUPED_LINEAR, OP_GROUPED_LINEAR_BACKWARD, OP_LAYER_NORM_BACKWARD = range(5)
+OP_ROUTE, OP_CLIP_GRAD_NORM = 5, 6
 MAX_WIDTH = 4194304
 MAX_GROUPS = 4096
+MAX_ROUTED = 1024
+MAX_CHOSEN = 32
 
 # every symbol include/cp_ops.h declares
 EXPORTS = ("cp_linear", "cp_linear_backward", "cp_grouped_linear", "cp_grouped_linear_backward", "cp_layer_norm",
-           "cp_layer_norm_backward", "cp_ops_workspace", "cp_ops_last_error")
+           "cp_layer_norm_backward", "cp_route", "cp_route_backward", "cp_dispatch", "cp_combine", "cp_combine_backward",
+           "cp_int4_quantize", "cp_int4_bytes", "cp_int4_pack", "cp_linear_int4", "cp_grouped_linear_int4",
+           "cp_clip_grad_norm", "cp_ops_workspace", "cp_ops_last_error")
 
 _workspace, _last_error = nat.lib().cp_ops_workspace, nat.lib().cp_ops_last_error
 _workspace.restype = ctypes.c_int64
@@ -104,3 +113,113 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, need_x=True, need_weight
     """Gradients (dx, dweight, dbias) of layer_norm for dy [M][N], from the mean
     and rstd it returned; None for those not asked for."""
     return _native.layer_norm_backward(dy, x, mean, rstd, weight, need_x, need_weight, need_bias)
+
+
+class Routing(NamedTuple):
+    """What route returns, for T tokens, E experts and k slots to a token."""
+    experts: torch.Tensor  # int32 [T][k], largest logit first; -1: no expert
+    gates: torch.Tensor    # float32 [T][k]; 0 without an expert
+    rows: torch.Tensor     # int32 [T][k]: the slot's row in expert order; -1 without an expert
+    counts: torch.Tensor   # int32 [E]: slots of each expert
+    offsets: torch.Tensor  # int32 [E + 1]: where each expert's rows begin
+    loss: torch.Tensor     # float32 []: the balance loss
+    slopes: torch.Tensor   # float32 [E]: its derivative by any token's probability of an expert
+
+
+def route(logits, k, normalize=False, valid=None):
+    """The k experts with the largest of each token's logits [T][E], the lower
+    index first among equals, as a Routing.  Gates are their softmax
+    probabilities, with `normalize` divided by their sum.  A logit of -inf is
+    never chosen; tokens for which `valid` (bool [T]) is False have no expert.
+    The loss is E sum_e f_e P_e, f_e the share of the slots and P_e the mean
+    probability of expert e over the tokens that have an expert."""
+    return Routing._make(_native.route(logits, k, normalize, valid))
+
+
+def route_backward(dgates, dloss, logits, experts, slopes, normalize=False):
+    """Gradient of the logits for dgates (float32 [T][k]) and dloss (float32 [],
+    on the device; each may be None), from what route was given and gave.  The
+    counts are constants; slots and tokens without an expert get zeros."""
+    return _native.route_backward(dgates, dloss, logits, experts, slopes, normalize)
+
+
+def dispatch(x, rows, offsets, out=None):
+    """Rows of x [T][D] in expert order, [T k][D]: row rows[t][j] is x[t].  Rows
+    from offsets[E] on are zero.  Its gradient is combine(d, rows)."""
+    return _native.dispatch(x, rows, offsets, out)
+
+
+def combine(y, rows, gates=None, residual=None, out=None):
+    """sum_j gates[t][j] y[rows[t][j]] + residual[t]: y [T k][D] in expert order,
+    gates float32 [T][k] (None: ones).  `out` may be the residual itself."""
+    return _native.combine(y, rows, gates, residual, out)
+
+
+def combine_backward(dout, y, rows, offsets, gates=None, need_y=True, need_gates=True):
+    """Gradients (dy, dgates) of combine for dout [T][D]; None for those not asked
+    for.  Rows of dy from offsets[E] on are zero.  The residual's is dout."""
+    return _native.combine_backward(dout, y, rows, offsets, gates, need_y, need_gates)
+
+
+class Int4Weight(NamedTuple):
+    """A weight [K][N] (or [E][K][N]) of 4-bit codes, as linear_int4 reads it."""
+    data: torch.Tensor     # uint8: codes, scales and zero points, laid out by pack_int4
+    shape: tuple
+    group_size: int
+    has_zeros: bool
+    dtype: torch.dtype     # of the scales, and of the rows it is multiplied with
+
+    def to(self, device):
+        """The same on another device."""
+        return self._replace(data=self.data.to(device))
+
+
+def quantize_int4(w, group_size=128, symmetric=False):
+    """4-bit codes of a finite weight [K][N] or [E][K][N] (any strides): (codes uint8,
+    scales, zeros) with w ~ scale (code - zero), a scale and a zero point to each
+    column's group_size consecutive k.  Symmetric: zeros None, which stands for 8."""
+    return _native.quantize_int4(w, group_size, symmetric)
+
+
+def pack_int4(codes, scales, zeros: Optional[torch.Tensor] = None, group_size=128):
+    """Lays out codes (uint8 [K][N] or [E][K][N], 0 .. 15), scales (float32 or
+    bfloat16, [ceil(K / group_size)][N] per expert) and zero points (uint8, 0 .. 15,
+    shaped like the scales; None: 8) for linear_int4, once.  group_size is 32, 64 or
+    a multiple of 128."""
+    data = _native.pack_int4(codes, scales, zeros, group_size)
+    return Int4Weight(data, tuple(codes.shape), group_size, zeros is not None, scales.dtype)
+
+
+def _check_int4(x, w, dims):
+    if not isinstance(w, Int4Weight):
+        raise TypeError("w must be an Int4Weight (pack_int4)")
+    if len(w.shape) != dims:
+        raise ValueError(f"w must have {dims} dimensions, got {w.shape}")
+    if x.dtype != w.dtype or x.shape[-1] != w.shape[-2]:
+        raise ValueError(f"x must be {w.dtype} with rows of {w.shape[-2]}, got {x.dtype} {tuple(x.shape)}")
+
+
+def linear_int4(x, w, bias=None, residual=None, act=ACT_NONE, out=None):
+    """linear with a 4-bit weight (an Int4Weight [K][N]), for decoding and short
+    prompts; x of the weight's type, finite.  `out` may be the residual itself."""
+    _check_int4(x, w, 2)
+    return _native.linear_int4(x, w.data, w.shape[1], w.group_size, w.has_zeros, bias, residual, act, out)
+
+
+def grouped_linear_int4(x, w, offsets, bias=None, act=ACT_NONE, out=None):
+    """grouped_linear with 4-bit weights (an Int4Weight [E][K][N])."""
+    _check_int4(x, w, 3)
+    return _native.grouped_linear_int4(x, w.data, w.shape[0], w.shape[2], w.group_size, w.has_zeros, offsets, bias, act, out)
+
+
+def grad_norm(gradients):
+    """Root of the sum of squares over all the tensors, float32 []; sums in 64 bits."""
+    return _native.clip_grad_norm(gradients, float("inf"), None, False)
+
+
+def clip_grad_norm(gradients, max_norm, out=None):
+    """Scales the tensors (float32 and bfloat16, any mix, dense) by min(1, max_norm /
+    (norm + 1e-6)) and returns the norm they had.  In place, or into `out`: a
+    tensor of the same shape and strides for each, of either type.  Nothing is read back to the
+    host: a norm that is not finite shows in the norm and in the results."""
+    return _native.clip_grad_norm(gradients, max_norm, out, True)
