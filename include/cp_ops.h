@@ -53,6 +53,7 @@ extern "C" {
 #define CP_OP_LAYER_NORM_BACKWARD 4
 #define CP_OP_ROUTE 5          /* M: tokens, N: experts */
 #define CP_OP_CLIP_GRAD_NORM 6 /* M: tensors            */
+#define CP_OP_LINEAR_INT4 7    /* E = 0: dense          */
 
 /* rows, columns and leading dimensions are at most this many elements (rows
  * of the activations: 2^30), and an operator takes at most CP_OPS_MAX_GROUPS
@@ -222,7 +223,7 @@ int cp_combine_backward(int32_t dtype, int64_t T, int32_t k, int64_t R, int64_t 
  */
 int cp_int4_quantize(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, const void *W, int64_t stride_k,
                      int64_t stride_n, int64_t stride_e, uint8_t *codes, void *scales, uint8_t *zeros, void *stream);
-int64_t cp_int4_bytes(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, int32_t zero_points);
+int64_t cp_int4_bytes(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group);
 int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, const uint8_t *codes,
                  const void *scales, const uint8_t *zeros, void *packed, void *stream);
 
@@ -230,15 +231,16 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
  * cp_linear_int4, cp_grouped_linear_int4 -- cp_linear and cp_grouped_linear with
  * a packed weight.  Products of x with the codes are exact and added up in fp32, a
  * group at a time; the weight itself is never rounded.  x is meant to be finite and
- * below 2^115: a row with infinities gives NaN.  A product of more than 2^23 tiles
- * of 64 x 64 (or, with at most 16 rows per expert, of 16 x 16) is refused.
+ * below 2^115: a row with infinities gives NaN.  A product of more than 2^22 tiles
+ * of 64 x 64 is refused.
  */
 int cp_linear_int4(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *X, int64_t ldx, const void *packed,
-                   int64_t group, int32_t zero_points, const void *bias, const void *R, int64_t ldr, int32_t act,
-                   void *Y, int64_t ldy, void *stream);
+                   int64_t group, const void *bias, const void *R, int64_t ldr, int32_t act,
+                   void *Y, int64_t ldy, void *ws, int64_t ws_bytes, void *stream);
 int cp_grouped_linear_int4(int32_t dtype, int64_t T, int64_t K, int64_t N, int32_t E, const void *X, int64_t ldx,
-                           const void *packed, int64_t group, int32_t zero_points, const int32_t *offsets,
-                           const void *bias, int32_t act, void *Y, int64_t ldy, void *stream);
+                           const void *packed, int64_t group, const int32_t *offsets,
+                           const void *bias, int32_t act, void *Y, int64_t ldy, void *ws, int64_t ws_bytes,
+                           void *stream);
 
 /*
  * cp_clip_grad_norm -- norm = sqrt(sum of squares over all of n tensors), added up
@@ -258,8 +260,8 @@ int cp_clip_grad_norm(int64_t n, const int32_t *dtypes, const void *const *grads
 /*
  * cp_ops_workspace -- bytes of scratch memory the operator `op` (CP_OP_*)
  * needs at these sizes, whatever its optional arguments; may be 0.  K is
- * ignored by CP_OP_LAYER_NORM_BACKWARD and the codes after it, E by the dense
- * operators and those.  `aligned`:
+ * ignored by CP_OP_LAYER_NORM_BACKWARD and the two codes after it, E by the
+ * dense operators and those.  `aligned`:
  * X, W and dY have 16-byte aligned pointers, row strides, expert strides and
  * row lengths; without that (0) there is room for copies of them that do.
  * Negative status code on bad arguments.  Host only, no device needed.

@@ -26,11 +26,11 @@ for name, args in (
         ("cp_combine_backward", (_i, _l, _i, _l, _l, _p, _l, _p, _l, _p, _p, _p, _p, _l, _p, _p)),
         ("cp_int4_quantize", (_i, _l, _l, _i, _l, _p, _l, _l, _l, _p, _p, _p, _p)),
         ("cp_int4_pack", (_i, _l, _l, _i, _l, _p, _p, _p, _p, _p)),
-        ("cp_linear_int4", (_i, _l, _l, _l, _p, _l, _p, _l, _i, _p, _p, _l, _i, _p, _l, _p)),
-        ("cp_grouped_linear_int4", (_i, _l, _l, _l, _i, _p, _l, _p, _l, _i, _p, _p, _i, _p, _l, _p)),
+        ("cp_linear_int4", (_i, _l, _l, _l, _p, _l, _p, _l, _p, _p, _l, _i, _p, _l, _p, _l, _p)),
+        ("cp_grouped_linear_int4", (_i, _l, _l, _l, _i, _p, _l, _p, _l, _p, _p, _i, _p, _l, _p, _l, _p)),
         ("cp_clip_grad_norm", (_l, _p, _p, _p, _f, _p, _p, _p, _p, _l, _p))):
     getattr(lib, name).argtypes = args
-lib.cp_int4_bytes.argtypes = (_i, _l, _l, _i, _l, _i)
+lib.cp_int4_bytes.argtypes = (_i, _l, _l, _i, _l)
 lib.cp_int4_bytes.restype = _l
 
 
@@ -42,6 +42,7 @@ def refused(rc, code):
 def test_constants():
     src = open(os.path.join(ROOT, "include", "cp_ops.h")).read()
     for c, v in (("CP_OP_ROUTE", ops.OP_ROUTE), ("CP_OP_CLIP_GRAD_NORM", ops.OP_CLIP_GRAD_NORM),
+                 ("CP_OP_LINEAR_INT4", ops.OP_LINEAR_INT4),
                  ("CP_OPS_MAX_ROUTED", ops.MAX_ROUTED), ("CP_OPS_MAX_CHOSEN", ops.MAX_CHOSEN)):
         m = re.search(rf"#define\s+{c}\s+(\d+)", src)
         assert m and int(m.group(1)) == v, c
@@ -51,13 +52,13 @@ def test_sizes():
     for T in (0, 1, 64, 1000, 1 << 20, 1 << 30):
         assert ops.workspace_bytes(ops.OP_ROUTE, BF16, T, 0, 100) <= 256 * (2 * 100 + 1) * 4 + 256
     assert ops.workspace_bytes(ops.OP_CLIP_GRAD_NORM, BF16, 1000, 0, 0) > 0
-    assert lib.cp_int4_bytes(BF16, 128, 16, 1, 128, 0) == 1024 + 32
-    assert lib.cp_int4_bytes(BF16, 129, 17, 3, 64, 1) == 3 * (4 * 1024 + 2 * 3 * 16 * 3)
-    assert lib.cp_int4_bytes(F32, 0, 5, 1, 32, 1) == 0
+    assert lib.cp_int4_bytes(BF16, 128, 16, 1, 128) == 1024 + 64
+    assert lib.cp_int4_bytes(BF16, 129, 17, 3, 64) == 3 * (4 * 1024 + 2 * 3 * 16 * 4)
+    assert lib.cp_int4_bytes(F32, 0, 5, 1, 32) == 0
     for args in ((7, 8, 8, 1, 32), (BF16, -1, 8, 1, 32), (BF16, 8, ops.MAX_WIDTH + 1, 1, 32), (BF16, 8, 8, 0, 32),
                  (BF16, 8, 8, ops.MAX_GROUPS + 1, 32), (BF16, 8, 8, 1, 0), (BF16, 8, 8, 1, 16), (BF16, 8, 8, 1, 96),
                  (BF16, 8, 8, 1, -128), (BF16, 8, 8, 1, 192)):
-        assert lib.cp_int4_bytes(*args, 0) < 0
+        assert lib.cp_int4_bytes(*args) < 0
 
 
 def route(dtype=BF16, T=4, E=8, k=2, logits=P, ld=8, experts=P, gates=P, rows=P, counts=P, offsets=P, loss=P, slopes=P, ws=P,
@@ -117,19 +118,20 @@ def test_exchange_refusals():
 
 
 def test_int4_refusals():
-    def call(dtype=BF16, M=4, K=64, N=8, X=P, ldx=64, w=Q, group=32, bias=None, R=None, ldr=8, act=0, Y=P << 2, ldy=8):
-        return lib.cp_linear_int4(dtype, M, K, N, X, ldx, w, group, 1, bias, R, ldr, act, Y, ldy, None)
+    def call(dtype=BF16, M=4, K=64, N=8, X=P, ldx=64, w=Q, group=32, bias=None, R=None, ldr=8, act=0, Y=P << 2, ldy=8, ws=P, n=1 << 50):
+        return lib.cp_linear_int4(dtype, M, K, N, X, ldx, w, group, bias, R, ldr, act, Y, ldy, ws, n, None)
     for change, code in ((dict(dtype=2), "UNSUPPORTED"), (dict(group=48), "UNSUPPORTED"), (dict(act=4), "UNSUPPORTED"),
                          (dict(M=-1), "SHAPE"), (dict(K=ops.MAX_WIDTH + 1), "SHAPE"), (dict(X=None), "INVALID_ARG"),
                          (dict(ldx=63), "SHAPE"), (dict(w=None), "INVALID_ARG"), (dict(w=Q + 8), "INVALID_ARG"),
                          (dict(bias=P + 1), "INVALID_ARG"), (dict(Y=Q + 64), "INVALID_ARG"), (dict(Y=P), "INVALID_ARG"),
-                         (dict(ldy=7), "SHAPE"), (dict(R=(P << 2) + 8), "INVALID_ARG"),
+                         (dict(ldy=7), "SHAPE"), (dict(K=9000, ldx=9000, ws=None), "INVALID_ARG"),
+                         (dict(K=9000, ldx=9000, ws=P, n=64), "INVALID_ARG"), (dict(R=(P << 2) + 8), "INVALID_ARG"),
                          (dict(M=1 << 30, N=ops.MAX_WIDTH, ldy=ops.MAX_WIDTH, Y=1 << 60), "SHAPE")):
         refused(call(**change), code)
     assert call(M=0, X=None, Y=None, w=None) == nat.CP_OK
 
     def grouped(E=2, off=P, Y=P << 2):
-        return lib.cp_grouped_linear_int4(BF16, 4, 64, 8, E, P, 64, Q, 32, 0, off, None, 0, Y, 8, None)
+        return lib.cp_grouped_linear_int4(BF16, 4, 64, 8, E, P, 64, Q, 32, off, None, 0, Y, 8, None, 0, None)
     for change, code in ((dict(E=0), "SHAPE"), (dict(E=-1), "SHAPE"), (dict(E=ops.MAX_GROUPS + 1), "SHAPE"),
                          (dict(off=None), "INVALID_ARG"), (dict(off=P + 2), "INVALID_ARG")):
         refused(grouped(**change), code)

@@ -580,16 +580,19 @@ const char *cp_ops_last_error(void) { return g_error; }
 int64_t cp_ops_workspace(int32_t op, int32_t dtype, int64_t M, int64_t K, int64_t N, int32_t E, int32_t aligned) {
     g_error[0] = 0;
     CP_TRY(check_dtype(dtype));
-    CP_TRY(check_sizes(M, op >= CP_OP_LAYER_NORM_BACKWARD ? 0 : K, N));
+    CP_TRY(check_sizes(M, op >= CP_OP_LAYER_NORM_BACKWARD && op != CP_OP_LINEAR_INT4 ? 0 : K, N));
     const bool grouped = op == CP_OP_GROUPED_LINEAR || op == CP_OP_GROUPED_LINEAR_BACKWARD;
     if (grouped && (E < 1 || E > CP_OPS_MAX_GROUPS))
         return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
+    if (op == CP_OP_LINEAR_INT4 && (E < 0 || E > CP_OPS_MAX_GROUPS))
+        return fail(CP_ERR_SHAPE, "%d experts (0 to %d)", E, CP_OPS_MAX_GROUPS);
     switch (op) {
         case CP_OP_LINEAR: return forward_ws(dtype, M, K, N, 0, aligned != 0);
         case CP_OP_GROUPED_LINEAR: return forward_ws(dtype, M, K, N, E, aligned != 0);
         case CP_OP_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, 0, aligned != 0);
         case CP_OP_GROUPED_LINEAR_BACKWARD: return backward_ws(dtype, M, K, N, E, aligned != 0);
         case CP_OP_LAYER_NORM_BACKWARD: return norm_ws(M, N);
+        case CP_OP_LINEAR_INT4: return int4_ws(dtype, E, M, K, N);
         case CP_OP_ROUTE: return route_ws(M, N);
         case CP_OP_CLIP_GRAD_NORM: return clip_ws(M);
     }

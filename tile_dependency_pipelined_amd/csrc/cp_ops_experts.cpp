@@ -61,8 +61,8 @@ int check_int4(int dtype, int64_t K, int64_t N, int64_t E, int64_t group) {
 }
 
 int linear_int4(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X, int64_t ldx, const void *packed,
-                int64_t group, bool zero_points, const int32_t *off, const void *bias, const void *R, int64_t ldr, int act,
-                void *Y, int64_t ldy, void *stream) {
+                int64_t group, const int32_t *off, const void *bias, const void *R, int64_t ldr, int act,
+                void *Y, int64_t ldy, void *ws, int64_t ws_bytes, void *stream) {
     CP_TRY(check_int4(dtype, K, N, E ? E : 1, group));
     CP_TRY(check_sizes(M, K, N));
     CP_TRY(check_act(act));
@@ -72,7 +72,7 @@ int linear_int4(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X
     if (R) CP_TRY(check_mat(r, dtype, "R"));
     CP_TRY(check_vector(bias, dtype, "bias"));
     if (E) CP_TRY(check_words(off, E + 1, "offsets"));
-    const Int4Layout l(dtype, K, N, group, zero_points);
+    const Int4Layout l(dtype, K, N, group);
     const int64_t experts = E ? E : 1;
     if (M && N && K) {
         if (!packed) return fail(CP_ERR_INVALID_ARG, "the packed weight is NULL");
@@ -84,12 +84,12 @@ int linear_int4(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X
     CP_TRY(check_apart("Y", out, "bias", Rows(bias, experts * N * elem_size(dtype))));
     CP_TRY(check_apart("Y", out, "offsets", Rows(off, (E + 1) * 4)));
     if (R) CP_TRY(check_apart("Y", out, "R", Rows(r, dtype), true));
+    CP_TRY(check_ws(ws, ws_bytes, int4_ws(dtype, E, M, K, N)));
     if (M == 0 || N == 0) return CP_OK;
     Int4Args a{};
     a.x = (const char *)X;
     a.codes = (const char *)packed;
-    a.scales = a.codes + experts * l.codes;
-    a.zeros = zero_points ? (const uint8_t *)a.scales + experts * l.scales : nullptr;
+    a.meta = a.codes + experts * l.codes;
     a.bias = (const char *)bias;
     a.res = (const char *)R;
     a.y = (char *)Y;
@@ -97,8 +97,7 @@ int linear_int4(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X
     a.ldr = r.ld;
     a.ldy = y.ld;
     a.sc = l.codes;
-    a.ss = l.scales;
-    a.sz = l.zeros;
+    a.sm = l.meta;
     a.off = off;
     a.experts = E;
     a.M = (int)M;
@@ -109,9 +108,34 @@ int linear_int4(int dtype, int64_t M, int64_t K, int64_t N, int E, const void *X
     a.kblocks = (int)l.kblocks;
     a.ngroups = (int)l.ngroups;
     a.group = (int)group;
-    const Int4Tiles t = int4_tiles(E, M, l.ntiles);
-    CP_TRY(check_grid((int64_t)t.ntm * t.ntn, 512));
-    return launched(launch_int4(dtype, a, (hipStream_t)stream), "4-bit linear layer");
+    const Int4Tiles t = int4_tiles(dtype, E, M, l.ntiles, l.kblocks, group);
+    CP_TRY(check_grid((int64_t)t.ntm * t.ntn * t.chunks, 1024));
+    a.ntm = t.ntm;
+    a.ntn = t.ntn;
+    a.chunks = t.chunks;
+    a.kper = t.kper;
+    a.ws = (float *)ws;
+    a.ldws = up(N, 8);
+    // (without a contraction the kernels would have no tile to read: the join's sum over no part is zero)
+    if (K > 0) CP_TRY(launched(launch_int4(dtype, a, t, (hipStream_t)stream), "4-bit linear layer"));
+    if (K > 0 && t.chunks == 1) return CP_OK;
+    GemmArgs g{};
+    g.C = a.y;
+    g.bias = a.bias;
+    g.res = a.res;
+    g.ws = a.ws;
+    g.ldc = a.ldy;
+    g.ldr = a.ldr;
+    g.off = off;
+    g.groups = E;
+    g.mode = E ? kGroupRows : kDense;
+    g.M = a.M;
+    g.N = a.N;
+    g.act = act;
+    g.nsplit = K > 0 ? t.chunks : 0;
+    g.ldws = (int32_t)a.ldws;
+    g.vec = aligned16(y, dtype) && (!R || aligned16(r, dtype)) && aligned16(bias);
+    return launched(launch_join(dtype, g, (hipStream_t)stream), "join");
 }
 
 // ----------------------------------------------------------------- clipping
@@ -404,10 +428,10 @@ int cp_int4_quantize(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t gro
     return launched(launch_int4_quantize(dtype, a, (hipStream_t)stream), "4-bit quantisation");
 }
 
-int64_t cp_int4_bytes(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, int32_t zero_points) {
+int64_t cp_int4_bytes(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group) {
     g_error[0] = 0;
     CP_TRY(check_int4(dtype, K, N, E, group));
-    return Int4Layout(dtype, K, N, group, zero_points != 0).bytes(E);
+    return Int4Layout(dtype, K, N, group).bytes(E);
 }
 
 int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, const uint8_t *codes,
@@ -418,7 +442,7 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
     if (!codes || !scales || !packed) return fail(CP_ERR_INVALID_ARG, "codes, scales or packed is NULL");
     CP_TRY(check_vector(scales, dtype, "scales"));
     if (!aligned16(packed)) return fail(CP_ERR_INVALID_ARG, "packed is not 16-byte aligned");
-    const Int4Layout l(dtype, K, N, group, zeros != nullptr);
+    const Int4Layout l(dtype, K, N, group);
     const Rows out(packed, l.bytes(E));
     CP_TRY(check_apart("packed", out, "codes", Rows(codes, E * K * N)));
     CP_TRY(check_apart("packed", out, "scales", Rows(scales, E * l.ngroups * N * elem_size(dtype))));
@@ -428,31 +452,30 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
     a.zeros = zeros;
     a.scales = (const char *)scales;
     a.codes = (char *)packed;
-    a.pscales = a.codes + E * l.codes;
-    a.pzeros = (uint8_t *)a.pscales + E * l.scales;
+    a.meta = a.codes + E * l.codes;
     a.K = K;
     a.N = N;
     a.E = E;
     a.ntiles = (int)l.ntiles;
     a.kblocks = (int)l.kblocks;
     a.ngroups = (int)l.ngroups;
-    a.scale_bytes = elem_size(dtype);
-    return launched(launch_int4_pack(a, (hipStream_t)stream), "4-bit packing");
+    return launched(launch_int4_pack(dtype, a, (hipStream_t)stream), "4-bit packing");
 }
 
 int cp_linear_int4(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *X, int64_t ldx, const void *packed,
-                   int64_t group, int32_t zero_points, const void *bias, const void *R, int64_t ldr, int32_t act,
-                   void *Y, int64_t ldy, void *stream) {
+                   int64_t group, const void *bias, const void *R, int64_t ldr, int32_t act,
+                   void *Y, int64_t ldy, void *ws, int64_t ws_bytes, void *stream) {
     g_error[0] = 0;
-    return linear_int4(dtype, M, K, N, 0, X, ldx, packed, group, zero_points != 0, nullptr, bias, R, ldr, act, Y, ldy, stream);
+    return linear_int4(dtype, M, K, N, 0, X, ldx, packed, group, nullptr, bias, R, ldr, act, Y, ldy, ws, ws_bytes, stream);
 }
 
 int cp_grouped_linear_int4(int32_t dtype, int64_t T, int64_t K, int64_t N, int32_t E, const void *X, int64_t ldx,
-                           const void *packed, int64_t group, int32_t zero_points, const int32_t *offsets,
-                           const void *bias, int32_t act, void *Y, int64_t ldy, void *stream) {
+                           const void *packed, int64_t group, const int32_t *offsets,
+                           const void *bias, int32_t act, void *Y, int64_t ldy, void *ws, int64_t ws_bytes,
+                           void *stream) {
     g_error[0] = 0;
     if (E < 1) return fail(CP_ERR_SHAPE, "%d experts (1 to %d)", E, CP_OPS_MAX_GROUPS);
-    return linear_int4(dtype, T, K, N, E, X, ldx, packed, group, zero_points != 0, offsets, bias, nullptr, 0, act, Y, ldy,
+    return linear_int4(dtype, T, K, N, E, X, ldx, packed, group, offsets, bias, nullptr, 0, act, Y, ldy, ws, ws_bytes,
                        stream);
 }
 

@@ -71,60 +71,85 @@ hipError_t launch_combine_backward(int dtype, const ExchangeArgs &a, hipStream_t
 // Codes as the matrix instructions take them: tiles of 16 columns x 128 of K,
 // 1 KB each, a column's tiles one after another; lane l of a wave holds column
 // l % 16 and four words, word s the k = 32 s + 8 (l / 16) .. + 7, whose codes i
-// are at bits 4 (i / 2) + 16 (i % 2).  Behind them the scales [column tile]
-// [group][16], behind those the zero points, bytes, the same way.
+// are at bits 4 (i / 2) + 16 (i % 2).  Behind them [column tile][group][16] pairs
+// of the scale and 16 + zero point, both of the layer's type.
 constexpr int kInt4Columns = 16, kInt4Depth = 128, kInt4TileBytes = 1024;
 
 struct Int4Layout {
     int64_t ntiles, kblocks, ngroups;
-    int64_t codes, scales, zeros;  // bytes per expert
-    Int4Layout(int dtype, int64_t K, int64_t N, int64_t group, bool zero_points)
+    int64_t codes, meta;  // bytes per expert
+    Int4Layout(int dtype, int64_t K, int64_t N, int64_t group)
         : ntiles((N + kInt4Columns - 1) / kInt4Columns),
           kblocks((K + kInt4Depth - 1) / kInt4Depth),
           ngroups((K + group - 1) / group),
           codes(ntiles * kblocks * kInt4TileBytes),
-          scales(ntiles * ngroups * kInt4Columns * (dtype == CP_BF16 ? 2 : 4)),
-          zeros(zero_points ? ntiles * ngroups * kInt4Columns : 0) {}
-    int64_t bytes(int64_t E) const { return E * (codes + scales + zeros); }
+          meta(ntiles * ngroups * kInt4Columns * (dtype == CP_BF16 ? 4 : 8)) {}
+    int64_t bytes(int64_t E) const { return E * (codes + meta); }
 };
 
 struct Int4Args {
-    const char *x, *codes, *scales, *bias, *res;
-    const uint8_t *zeros;  // null: 8
+    const char *x, *codes, *meta, *bias, *res;
     char *y;
     int64_t ldx, ldr, ldy;
-    int64_t sc, ss, sz;    // bytes from one expert to the next
+    int64_t sc, sm;        // bytes from one expert to the next
     const int32_t *off;    // device: groups + 1 row offsets, or null
     int32_t experts;       // 0: dense
     int32_t M, K, N, act;
     int32_t ntiles, kblocks, ngroups, group;
     int32_t ntm, ntn;      // row tiles (at most) and column sets of the launch
+    int32_t chunks, kper;  // parts of the contraction, each to its own partial sums, and tiles of one
+    float *ws;             // chunks > 1: [chunks][M][ldws]
+    int64_t ldws;
 };
-// Tiles of a launch: mt x 16 rows, nt x 16 columns.
+// Tiles of a launch: `waves` waves to a block that streams (16 rows, any number of
+// column tiles), or 0: 64 rows and 4 nt column tiles.
 struct Int4Tiles {
-    int32_t mt, nt, ntm, ntn;
+    int32_t waves, nt, ntm, ntn, chunks, kper;
 };
-inline Int4Tiles int4_tiles(int experts, int64_t M, int64_t ntiles) {
-    Int4Tiles t;
+inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, int64_t kblocks, int64_t group) {
+    Int4Tiles t{};
     const int64_t rows = experts ? (M + experts - 1) / experts : M;  // to an expert, on average
-    t.mt = rows <= 16 ? 1 : 4;
-    t.nt = t.mt > 1 ? 4 : (ntiles > 512 ? 2 : 1);
-    const int64_t bm = 16 * t.mt, used = M < experts + 1 ? M : experts + 1;
+    const int64_t bm = rows <= 16 ? 16 : 64, used = M < experts + 1 ? M : experts + 1;
     t.ntm = (int32_t)(experts ? (M + used * (bm - 1)) / bm : (M + bm - 1) / bm);
-    t.ntn = (int32_t)((ntiles + t.nt - 1) / t.nt);
+    t.chunks = 1;
+    if (bm == 16) {
+        // registers for x, 128 or (8 waves) 256 to a lane: beside few scales for more of it
+        const bool bf16 = dtype == CP_BF16;
+        t.waves = kblocks <= 4 ? 4 : (bf16 && group > 32 ? 16 : 8);
+        const int64_t most = !bf16 ? 16 : (group > 64 ? 64 : 32);
+        if (kblocks > most) t.chunks = (int32_t)((kblocks + most - 1) / most);
+        // blocks that fill the device, shared out over the row tiles that are likely there
+        const int64_t tiles = (experts ? (M < experts ? M : experts) : t.ntm) * t.chunks;
+        int64_t blocks = kComputeUnits * (16 / t.waves) / (tiles ? tiles : 1);
+        if (blocks < 1) blocks = 1;
+        t.ntn = (int32_t)(blocks < ntiles ? blocks : ntiles);
+    } else {
+        t.nt = (int64_t)t.ntm * ntiles >= 16 * kComputeUnits ? 4 : ((int64_t)t.ntm * ntiles >= 8 * kComputeUnits ? 2 : 1);
+        const int32_t most = group == 32 ? 1 : (group == 64 ? 2 : 4);  // (registers: small groups keep more scales)
+        if (t.nt > most) t.nt = most;
+        t.ntn = (int32_t)((ntiles + 4 * t.nt - 1) / (4 * t.nt));
+    }
+    t.kper = (int32_t)((kblocks + t.chunks - 1) / t.chunks);
     return t;
 }
-hipError_t launch_int4(int dtype, const Int4Args &a, hipStream_t s);
+inline int64_t int4_ws(int dtype, int experts, int64_t M, int64_t K, int64_t N) {
+    int64_t chunks = 1;  // (whatever the group)
+    for (const int group : {32, 64, 128}) {
+        const int64_t n = int4_tiles(dtype, experts, M, (N + 15) / 16, (K + 127) / 128, group).chunks;
+        if (n > chunks) chunks = n;
+    }
+    return chunks > 1 ? (chunks * M * ((N + 7) / 8 * 8) * 4 + 255) / 256 * 256 : 0;
+}
+hipError_t launch_int4(int dtype, const Int4Args &a, const Int4Tiles &t, hipStream_t s);
 
 struct Int4PackArgs {
     const uint8_t *q, *zeros;
     const char *scales;
-    char *codes, *pscales;
-    uint8_t *pzeros;
+    char *codes, *meta;
     int64_t K, N, E;
-    int32_t ntiles, kblocks, ngroups, scale_bytes;
+    int32_t ntiles, kblocks, ngroups;
 };
-hipError_t launch_int4_pack(const Int4PackArgs &a, hipStream_t s);
+hipError_t launch_int4_pack(int dtype, const Int4PackArgs &a, hipStream_t s);
 
 struct Int4QuantArgs {
     const char *w;

@@ -15,17 +15,22 @@ namespace cpo {
 
 namespace {
 
-__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w) {
-    union {
-        uint32_t u[4];
-        bf16x8_t v;
-    } r;
-    r.u[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    r.u[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    r.u[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    r.u[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
-    return r.v;
-}
+// The constants in registers: an instruction with both takes them from nowhere else.
+struct Spread {
+    uint32_t mask = 0x00780078u, base = 0x41804180u;
+    __device__ __forceinline__ Spread() { asm("" : "+v"(mask), "+v"(base)); }
+    __device__ __forceinline__ bf16x8_t operator()(uint32_t w) const {
+        union {
+            uint32_t u[4];
+            bf16x8_t v;
+        } r;
+        r.u[0] = ((w << 3) & mask) | base;
+        r.u[1] = ((w >> 1) & mask) | base;
+        r.u[2] = ((w >> 5) & mask) | base;
+        r.u[3] = ((w >> 9) & mask) | base;
+        return r.v;
+    }
+};
 __device__ __forceinline__ bf16x8_t ones_bf16() {
     union {
         uint32_t u[4];
@@ -69,135 +74,363 @@ __device__ __forceinline__ void parts(const Row8<float> &r, bf16x8_t (&p)[3]) {
     for (int j = 0; j < 3; ++j) p[j] = a[j].v;
 }
 
-// MT x 16 rows and NT x 16 columns to a block; its W waves take every W-th tile of
-// the contraction and are added up in LDS.  SG: matrix instructions to a group.
-template <class T, int MT, int NT, int W, int SG>
-__global__ __launch_bounds__(W * 64) void int4_kernel(Int4Args g) {
-    constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG, U = 2;
-    __shared__ float red[W][MT * NT * 4][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n16 = lane & 15, quad = lane >> 4;
-    const int b = xcd_remap(blockIdx.x, gridDim.x), rt = b % g.ntm, ct = b / g.ntm;
-    int row0 = rt * 16 * MT, row_end = g.M, e = 0;
+// A group's scale and zero point for one column, as packed.
+template <class T>
+struct Meta;
+template <>
+struct Meta<__bf16> {
+    uint32_t v;  // 16 + z over the scale, both bf16
+    __device__ __forceinline__ float scale() const { return __builtin_bit_cast(float, v << 16); }
+    __device__ __forceinline__ float zero() const { return __builtin_bit_cast(float, v & 0xFFFF0000u); }
+};
+template <>
+struct Meta<float> {
+    float s, z;
+    __device__ __forceinline__ float scale() const { return s; }
+    __device__ __forceinline__ float zero() const { return z; }
+};
+
+// SG matrix instructions, 32 k each, to a group, as far as it lies in a tile.
+template <int SG>
+__device__ __forceinline__ int first_group(const Int4Args &g, int kb) {
+    return SG < 4 ? kb * (4 / SG) : (g.group == kInt4Depth ? kb : kb / (g.group / kInt4Depth));
+}
+template <class T, int SG>
+struct Tile {  // of codes, and its groups' scales
+    static constexpr int NG = 4 / SG;
+    uint4 w;
+    Meta<T> m[NG];
+    // gr: the tile's first group
+    __device__ __forceinline__ void load(const Int4Args &g, const char *codes, const char *meta, int tile, int kb, int gr) {
+        const int lane = threadIdx.x & 63;
+        w = *reinterpret_cast<const uint4 *>(codes + ((int64_t)tile * g.kblocks + kb) * kInt4TileBytes + lane * 16);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const int at = gr + i < g.ngroups ? gr + i : g.ngroups - 1;  // (past K: x is zero)
+            m[i] = reinterpret_cast<const Meta<T> *>(meta)[((int64_t)tile * g.ngroups + at) * kInt4Columns + (lane & 15)];
+        }
+    }
+    __device__ __forceinline__ uint32_t step(int s) const { return s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w; }
+};
+
+// The rows of a block: a tile of `bm` rows, of one expert if there are experts.
+struct BlockRows {
+    int row0, end, expert;
+    bool none;  // rows without an expert
+};
+__device__ __forceinline__ bool block_rows(const Int4Args &g, int bm, int rt, BlockRows &r) {
+    r = {rt * bm, g.M, 0, false};
     if (g.experts) {
         GroupScan s;
-        if (rt >= count_tiles(g.off, g.experts, g.M, 16 * MT, s)) return;
-        const RowTile t = find_tile(g.off, g.experts, g.M, 16 * MT, rt, s);
-        e = t.expert;
-        row0 = t.row0 + (rt - t.before) * 16 * MT;
-        row_end = t.end;
+        if (rt >= count_tiles(g.off, g.experts, g.M, bm, s)) return false;
+        const RowTile t = find_tile(g.off, g.experts, g.M, bm, rt, s);
+        r = {t.row0 + (rt - t.before) * bm, t.end, t.expert < g.experts ? t.expert : 0, t.expert >= g.experts};
     }
-    const bool none = g.experts && e >= g.experts;  // rows without an expert: zeros
-    const int64_t es = none ? 0 : e;
-    const char *codes = g.codes + es * g.sc;
-    const T *scales = reinterpret_cast<const T *>(g.scales + es * g.ss);
-    const uint8_t *zeros = g.zeros ? g.zeros + es * g.sz : nullptr;
+    return true;
+}
 
+template <class T>
+__device__ __forceinline__ void finish_int4(const Int4Args &g, const BlockRows &b, int row, int col, float v) {
+    if (row >= b.end || col >= g.N) return;
+    if (g.bias) v += to_f32(reinterpret_cast<const T *>(g.bias)[(int64_t)b.expert * g.N + col]);
+    v = b.none ? 0.0f : act_apply(v, g.act);
+    if (g.res) v += to_f32(reinterpret_cast<const T *>(g.res)[(int64_t)row * g.ldr + col]);
+    reinterpret_cast<T *>(g.y)[(int64_t)row * g.ldy + col] = from_f32<T>(v);
+}
+
+// Where a block writes: the result, or its part of the contraction's partial sums.
+template <class T>
+__device__ __forceinline__ void put_int4(const Int4Args &g, const BlockRows &b, int chunk, int row, int col, float v) {
+    if (g.chunks == 1) return finish_int4<T>(g, b, row, col, v);
+    if (row < b.end && col < g.N) g.ws[((int64_t)chunk * g.M + row) * g.ldws + col] = v;
+}
+
+// Up to 16 rows (of an expert): a chunk of the contraction to a block, every W-th tile
+// of it to each of its W waves, column tile after column tile.  A wave's part of x
+// stays in its registers for all of them, so that the loop reads codes and scales
+// alone, D column tiles ahead.  The loop has no branch around a load: the compiler
+// could not tell how many are in flight behind it and would wait for all.  For the
+// same reason the sums of a column tile go to LDS and are finished, with what bias and
+// residual have to be read for it, some tiles at a time.
+constexpr int kInt4Flush = 8;
+template <class T, int W, int XK, int D, int SG>
+__global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
+    constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG;
+    __shared__ f32x4_t red[2][W][64];
+    __shared__ float done[kInt4Flush][256];
+    __shared__ f32x4_t sums[W][XK * NG][4];  // of x over the groups
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int b = xcd_remap(blockIdx.x, gridDim.x), part = b / g.ntn, cb = b % g.ntn, rt = part / g.chunks, chunk = part % g.chunks;
+    BlockRows br;
+    if (!block_rows(g, 16, rt, br)) return;
+    const int t0 = (int)((int64_t)cb * g.ntiles / g.ntn), t1 = (int)((int64_t)(cb + 1) * g.ntiles / g.ntn), n = t1 - t0;
+    if (br.none) {
+        for (int i = tid; i < 16 * 16 * n; i += W * 64)
+            put_int4<T>(g, br, chunk, br.row0 + i / (16 * n), t0 * 16 + i % (16 * n), 0.0f);
+        return;
+    }
+    const char *codes = g.codes + (int64_t)br.expert * g.sc, *meta = g.meta + (int64_t)br.expert * g.sm;
+    const Spread spread;
+
+    // tiles of the contraction, past its end the last again, with x of zero
+    const int kb_end = (chunk + 1) * g.kper < g.kblocks ? (chunk + 1) * g.kper : g.kblocks;
+    int kb[XK], gr[XK];
+    Tile<T, SG> w[D][XK];
+#pragma unroll
+    for (int i = 0; i < XK; ++i) {
+        const int at = chunk * g.kper + i * W + wave;
+        kb[i] = at < kb_end ? at : kb_end - 1;
+        gr[i] = first_group<SG>(g, kb[i]);
+    }
+    auto load = [&](int d, int t) {
+#pragma unroll
+        for (int i = 0; i < XK; ++i) w[d][i].load(g, codes, meta, t0 + t, kb[i], gr[i]);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < n) load(d, d);
+    Row8<T> xr[XK][4];
+    {
+        const int row = br.row0 + (lane & 15) < br.end ? br.row0 + (lane & 15) : br.row0;  // (others' results are not used)
+#pragma unroll
+        for (int i = 0; i < XK; ++i) {
+            const bool in = chunk * g.kper + i * W + wave < kb_end;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = kb[i] * kInt4Depth + s * 32 + (lane >> 4) * 8;
+                if (in && k < g.K) xr[i][s].load(g.x + ((int64_t)row * g.ldx + k) * (int64_t)sizeof(T), g.K - k);
+                else xr[i][s].zero();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = j * SG; s < j * SG + SG; ++s) {
+                    bf16x8_t x[XP];
+                    parts(xr[i][s], x);
+#pragma unroll
+                    for (int q = 0; q < XP; ++q) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
+                }
+                if ((lane & 15) == 0) sums[wave][i * NG + j][lane >> 4] = xs;
+            }
+        }
+        __syncthreads();
+    }
+    auto column = [&](int d, int t) {
+        f32x4_t acc{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < XK; ++i)
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const f32x4_t xs = sums[wave][i * NG + j][lane >> 4];
+                f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = j * SG; s < j * SG + SG; ++s) {
+                    const bf16x8_t c = spread(w[d][i].step(s));
+                    bf16x8_t x[XP];
+                    parts(xr[i][s], x);
+#pragma unroll
+                    for (int q = 0; q < XP; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], c, p, 0, 0, 0);
+                }
+                const float sc = w[d][i].m[j].scale(), zp = -w[d][i].m[j].zero();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] = fmaf(sc, fmaf(zp, xs[r], p[r]), acc[r]);
+                __builtin_amdgcn_sched_barrier(0);  // (one group's registers at a time)
+            }
+        // (one barrier to a tile: whoever writes a buffer again has passed the next one,
+        // behind the sums that read it)
+        red[t & 1][wave][lane] = acc;
+    };
+    auto sum = [&](int t) {
+        __syncthreads();
+        if (tid < 256) {  // element tid % 4 of lane tid / 4
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) v += reinterpret_cast<const float *>(&red[t & 1][i][0])[tid];
+            done[t % kInt4Flush][tid] = v;
+        }
+        if ((t + 1) % kInt4Flush && t + 1 < n) return;
+        __syncthreads();
+        const int f0 = t / kInt4Flush * kInt4Flush, cols = (t + 1 - f0) * 16;
+        for (int i = tid; i < 16 * cols; i += W * 64) {
+            const int r = i / cols, c = i % cols;
+            put_int4<T>(g, br, chunk, br.row0 + r, (t0 + f0) * 16 + c, done[c >> 4][((r >> 2) * 16 + (c & 15)) * 4 + (r & 3)]);
+        }
+        __syncthreads();
+    };
+    int t = 0;
+    for (; t + 2 * D <= n; t += D)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            column(d, t + d);
+            load(d, t + D + d);
+            sum(t + d);
+        }
+    for (; t < n; t += D)  // the last, up to 2 D - 1 of them
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (t + d >= n) break;
+            column(d, t + d);
+            if (t + D + d < n) load(d, t + D + d);
+            sum(t + d);
+        }
+}
+
+// More rows: 64 to a block, staged through LDS in the order the matrix instructions
+// take them, while the codes go to the registers of the wave that needs them: wave
+// wn of four has NT column tiles.  WK such quartets take a part of the contraction
+// each.  A wave stages a row tile and with it forms the sums of x over the groups.
+// (The loop has no branch around a load, as above: what lies past K comes last.)
+template <class T, int NT, int WK, int SG>
+__global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
+    constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG, MT = 4;
+    constexpr int kBuf = XP * 4 * MT * 1024, kJoin = WK > 1 ? (WK - 1) * MT * NT * 4096 : 0;
+    __shared__ __attribute__((aligned(16))) char stage[WK * 2 * kBuf > kJoin ? WK * 2 * kBuf : kJoin];
+    __shared__ f32x4_t sums[WK][2][NG][MT][4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 3, wk = wave >> 2, n16 = lane & 15, quad = lane >> 4;
+    const int b = xcd_remap(blockIdx.x, gridDim.x), part = b / g.ntm, rt = b % g.ntm, ct = part / g.chunks, chunk = part % g.chunks;
+    BlockRows br;
+    if (!block_rows(g, 16 * MT, rt, br)) return;
+    const char *codes = g.codes + (int64_t)br.expert * g.sc, *meta = g.meta + (int64_t)br.expert * g.sm;
+    const Spread spread;
+    const int tile0 = (ct * 4 + wn) * NT;
+    const int kb_end = br.none ? 0 : ((chunk + 1) * g.kper < g.kblocks ? (chunk + 1) * g.kper : g.kblocks);
+    const int whole = g.K / kInt4Depth < kb_end ? g.K / kInt4Depth : kb_end;  // tiles without an end of K in them
+    const int first = chunk * g.kper, per = whole > first ? (whole - first + WK - 1) / WK : 0, kb0 = first + wk * per;
+    const int row = br.row0 + wn * 16 + n16;
+    const char *xp = g.x + ((int64_t)(row < br.end ? row : br.row0) * g.ldx + quad * 8) * (int64_t)sizeof(T);
+
+    Row8<T> xr[4];
+    Tile<T, SG> cur[NT], nxt[NT];
+    auto load_codes = [&](Tile<T, SG> (&c)[NT], int kb) {
+        const int gr = first_group<SG>(g, kb);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            c[n].load(g, codes, meta, tile0 + n < g.ntiles ? tile0 + n : g.ntiles - 1, kb, gr);
+    };
+    auto load = [&](Tile<T, SG> (&c)[NT], int it) {
+        const int kb = kb0 + it < whole ? kb0 + it : whole - 1;
+        load_codes(c, kb);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < Row8<T>::kUnits; ++i)
+                __builtin_memcpy(&xr[s].u[i], xp + ((int64_t)kb * kInt4Depth + s * 32) * (int64_t)sizeof(T) + i * 16, 16);
+    };
+    auto put = [&](int buf, bool zero) {
+        if (zero) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) xr[s].zero();
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = j * SG; s < j * SG + SG; ++s) {
+                bf16x8_t x[XP];
+                parts(xr[s], x);
+#pragma unroll
+                for (int q = 0; q < XP; ++q) {
+                    xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
+                    *reinterpret_cast<bf16x8_t *>(stage + (wk * 2 + buf) * kBuf + ((q * 4 + s) * MT + wn) * 1024 + lane * 16) = x[q];
+                }
+            }
+            if (n16 == 0) sums[wk][buf][j][wn][quad] = xs;
+        }
+    };
     f32x4_t acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-    if (!none)
-        for (int kb0 = wave; kb0 < g.kblocks; kb0 += U * W) {
-            uint4 wv[U][NT];
-            T sv[U][NT][NG];
-            uint8_t zv[U][NT][NG];
+    auto multiply = [&](int buf) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int kb = kb0 + u * W < g.kblocks ? kb0 + u * W : kb0;
+        for (int j = 0; j < NG; ++j) {
+            f32x4_t p[MT][NT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) p[m][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = j * SG; s < j * SG + SG; ++s) {
+                bf16x8_t w[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) w[n] = spread(cur[n].step(s));
+#pragma unroll
+                for (int q = 0; q < XP; ++q)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const bf16x8_t x = *reinterpret_cast<const bf16x8_t *>(stage + (wk * 2 + buf) * kBuf +
+                                                                               ((q * 4 + s) * MT + m) * 1024 + lane * 16);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) p[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[n], p[m][n], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const f32x4_t xs = sums[wk][buf][j][m][quad];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int tile = ct * NT + n < g.ntiles ? ct * NT + n : g.ntiles - 1;
-                    wv[u][n] = *reinterpret_cast<const uint4 *>(codes + ((int64_t)tile * g.kblocks + kb) * kInt4TileBytes +
-                                                                lane * 16);
+                    const float sc = cur[n].m[j].scale(), zp = -cur[n].m[j].zero();
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        int gr = SG == 4 ? kb * kInt4Depth / g.group : kb * NG + i;
-                        gr = gr < g.ngroups ? gr : g.ngroups - 1;
-                        const int64_t at = ((int64_t)tile * g.ngroups + gr) * kInt4Columns + n16;
-                        sv[u][n][i] = scales[at];
-                        zv[u][n][i] = zeros ? zeros[at] : (uint8_t)8;
-                    }
+                    for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc, fmaf(zp, xs[r], p[m][n][r]), acc[m][n][r]);
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int kb = kb0 + u * W;
-                if (kb >= g.kblocks) break;  // uniform
-                Row8<T> xr[4][MT];
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const int row = row0 + m * 16 + n16, k = kb * kInt4Depth + s * 32 + quad * 8;
-                        if (row < row_end && k < g.K) xr[s][m].load(g.x + ((int64_t)row * g.ldx + k) * (int64_t)sizeof(T), g.K - k);
-                        else xr[s][m].zero();
-                    }
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    f32x4_t p[MT][NT], xs[MT];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        xs[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) p[m][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                    }
-#pragma unroll
-                    for (int s = i * SG; s < i * SG + SG; ++s) {
-                        bf16x8_t w[NT];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            w[n] = codes_bf16(s == 0 ? wv[u][n].x : s == 1 ? wv[u][n].y : s == 2 ? wv[u][n].z : wv[u][n].w);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            bf16x8_t x[XP];
-                            parts(xr[s][m], x);
-#pragma unroll
-                            for (int j = 0; j < XP; ++j) {
-                                xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], ones_bf16(), xs[m], 0, 0, 0);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    p[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], w[n], p[m][n], 0, 0, 0);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float sc = to_f32(sv[u][n][i]), zp = -(float)(16 + (int)zv[u][n][i]);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                acc[m][n][r] = fmaf(sc, fmaf(zp, xs[m][r], p[m][n][r]), acc[m][n][r]);
-                    }
-                }
-            }
+            __builtin_amdgcn_sched_barrier(0);  // (one group's registers at a time)
         }
+    };
+    if (per) {
+        load(cur, 0);
+        put(0, kb0 >= whole);
+        __syncthreads();
+        for (int it = 0; it + 1 < per; ++it) {
+            load(nxt, it + 1);
+            multiply(it & 1);
+            put(~it & 1, kb0 + it + 1 >= whole);
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cur[n] = nxt[n];
+        }
+        multiply((per - 1) & 1);
+    }
+    if (whole < kb_end) {  // K ends within a tile: the first quartet's
+        load_codes(cur, whole);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int k = whole * kInt4Depth + s * 32 + quad * 8;
+            if (k < g.K) xr[s].load(xp + (int64_t)(k - quad * 8) * (int64_t)sizeof(T), g.K - k);
+            else xr[s].zero();
+        }
+        put(per & 1, wk > 0);
+        __syncthreads();
+        multiply(per & 1);
+    }
+    if constexpr (WK > 1) {
+        __syncthreads();
+        f32x4_t *join = reinterpret_cast<f32x4_t *>(stage);
+        if (wk > 0)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) join[(((wk - 1) * 4 + wn) * MT * NT + m * NT + n) * 64 + lane] = acc[m][n];
+        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int w = 1; w < WK; ++w)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[m][n] += join[(((w - 1) * 4 + wn) * MT * NT + m * NT + n) * 64 + lane];
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) red[wave][(m * NT + n) * 4 + r][lane] = acc[m][n][r];
-    __syncthreads();
-    for (int o = tid; o < MT * NT * 256; o += W * 64) {
-        const int c = o % (NT * 16), row = o / (NT * 16), m = row >> 4, q = (row >> 2) & 3, r = row & 3, n = c >> 4;
-        const int gr = row0 + row, col = ct * NT * 16 + c;
-        if (gr >= row_end || col >= g.N) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += red[w][(m * NT + n) * 4 + r][q * 16 + (c & 15)];
-        if (none) {
-            v = 0.0f;
-        } else {
-            if (g.bias) v += to_f32(reinterpret_cast<const T *>(g.bias)[es * g.N + col]);
-            v = act_apply(v, g.act);
-        }
-        if (g.res) v += to_f32(reinterpret_cast<const T *>(g.res)[(int64_t)gr * g.ldr + col]);
-        reinterpret_cast<T *>(g.y)[(int64_t)gr * g.ldy + col] = from_f32<T>(v);
-    }
+            for (int r = 0; r < 4; ++r)
+                put_int4<T>(g, br, chunk, br.row0 + m * 16 + quad * 4 + r, (tile0 + n) * 16 + n16, acc[m][n][r]);
 }
 
 // ------------------------------------------------- packing and quantisation
@@ -222,6 +455,7 @@ __global__ __launch_bounds__(256) void int4_pack_codes_kernel(Int4PackArgs a) {
     }
 }
 
+template <class T>
 __global__ __launch_bounds__(256) void int4_pack_scales_kernel(Int4PackArgs a) {
     const int64_t per = (int64_t)a.ntiles * a.ngroups * kInt4Columns, all = per * a.E;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
@@ -229,9 +463,10 @@ __global__ __launch_bounds__(256) void int4_pack_scales_kernel(Int4PackArgs a) {
         const int64_t g = w / kInt4Columns % a.ngroups, n = tile * kInt4Columns + w % kInt4Columns;
         const int64_t from = (e * a.ngroups + g) * a.N + n;
         const bool in = n < a.N;
-        if (a.scale_bytes == 2) reinterpret_cast<uint16_t *>(a.pscales)[i] = in ? reinterpret_cast<const uint16_t *>(a.scales)[from] : 0;
-        else reinterpret_cast<uint32_t *>(a.pscales)[i] = in ? reinterpret_cast<const uint32_t *>(a.scales)[from] : 0;
-        if (a.zeros) a.pzeros[i] = in ? a.zeros[from] & 15 : 0;
+        const T s = in ? reinterpret_cast<const T *>(a.scales)[from] : from_f32<T>(0.0f);
+        const T z = from_f32<T>(16.0f + (a.zeros && in ? a.zeros[from] & 15 : 8));
+        reinterpret_cast<T *>(a.meta)[2 * i] = s;
+        reinterpret_cast<T *>(a.meta)[2 * i + 1] = z;
     }
 }
 
@@ -263,39 +498,72 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(Int4QuantArgs a) {
     }
 }
 
-template <class T, int MT, int NT, int W>
-hipError_t by_group(const Int4Args &a, unsigned blocks, hipStream_t s) {
-    if (a.group == 32) hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_kernel<T, MT, NT, W, 1>), dim3(blocks), dim3(W * 64), 0, s, a);
-    else if (a.group == 64) hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_kernel<T, MT, NT, W, 2>), dim3(blocks), dim3(W * 64), 0, s, a);
-    else hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_kernel<T, MT, NT, W, 4>), dim3(blocks), dim3(W * 64), 0, s, a);
+template <class F>
+hipError_t by_group(int group, F &&f) {
+    using std::integral_constant;
+    if (group == 32) return f(integral_constant<int, 1>());
+    if (group == 64) return f(integral_constant<int, 2>());
+    return f(integral_constant<int, 4>());
+}
+
+// W waves, XK tiles of the contraction to each, D column tiles ahead (int4_tiles).
+template <class T, int SG, int W, int XK, int D>
+hipError_t stream_rows(const Int4Args &a, unsigned blocks, hipStream_t s) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_stream_kernel<T, W, XK, D, SG>), dim3(blocks), dim3(W * 64), 0, s, a);
     return hipGetLastError();
+}
+template <class T, int NT, int WK>
+hipError_t many_rows(const Int4Args &a, unsigned blocks, hipStream_t s) {
+    return by_group(a.group, [&](auto sg) {
+        if constexpr (NT > sg()) return hipErrorInvalidValue;  // (int4_tiles)
+        else {
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_rows_kernel<T, NT, WK, sg()>), dim3(blocks), dim3(WK * 256), 0, s, a);
+            return hipGetLastError();
+        }
+    });
 }
 
 template <class T>
-hipError_t int4(Int4Args a, hipStream_t s) {
-    const Int4Tiles t = int4_tiles(a.experts, a.M, a.ntiles);
-    a.ntm = t.ntm;
-    a.ntn = t.ntn;
-    const unsigned blocks = (unsigned)((int64_t)t.ntm * t.ntn);
-    if (t.mt == 1 && t.nt == 1) return by_group<T, 1, 1, 8>(a, blocks, s);
-    if (t.mt == 1) return by_group<T, 1, 2, 8>(a, blocks, s);
-    return by_group<T, 4, 4, 4>(a, blocks, s);
+hipError_t int4(const Int4Args &a, const Int4Tiles &t, hipStream_t s) {
+    constexpr bool kWide = sizeof(T) == 4;
+    constexpr int WK = kWide ? 1 : 2;
+    const unsigned n = (unsigned)(t.ntm * t.ntn * t.chunks);
+    if (!t.waves) {
+        if (t.nt == 1) return many_rows<T, 1, WK>(a, n, s);
+        return t.nt == 2 ? many_rows<T, 2, WK>(a, n, s) : many_rows<T, 4, WK>(a, n, s);
+    }
+    return by_group(a.group, [&](auto sg) {
+        constexpr int SG = sg();
+        if (t.waves == 4) return stream_rows<T, SG, 4, 1, 4>(a, n, s);
+        if constexpr (kWide) {
+            return t.kper <= 8 ? stream_rows<T, SG, 8, 1, 4>(a, n, s) : stream_rows<T, SG, 8, 2, 2>(a, n, s);
+        } else if constexpr (SG == 1) {
+            if (t.kper <= 8) return stream_rows<T, SG, 8, 1, 4>(a, n, s);
+            return t.kper <= 16 ? stream_rows<T, SG, 8, 2, 2>(a, n, s) : stream_rows<T, SG, 8, 4, 1>(a, n, s);
+        } else {
+            if (t.kper <= 16) return stream_rows<T, SG, 16, 1, 4>(a, n, s);
+            if constexpr (SG == 4)
+                if (t.kper > 32) return stream_rows<T, SG, 16, 4, 1>(a, n, s);
+            return stream_rows<T, SG, 16, 2, 2>(a, n, s);
+        }
+    });
 }
 
 }  // namespace
 
-hipError_t launch_int4(int dtype, const Int4Args &a, hipStream_t s) {
-    return dtype == CP_BF16 ? int4<__bf16>(a, s) : int4<float>(a, s);
+hipError_t launch_int4(int dtype, const Int4Args &a, const Int4Tiles &t, hipStream_t s) {
+    return dtype == CP_BF16 ? int4<__bf16>(a, t, s) : int4<float>(a, t, s);
 }
 
-hipError_t launch_int4_pack(const Int4PackArgs &a, hipStream_t s) {
+hipError_t launch_int4_pack(int dtype, const Int4PackArgs &a, hipStream_t s) {
     auto blocks = [](int64_t n) { return dim3((unsigned)((n + 255) / 256 < 16384 ? (n + 255) / 256 : 16384)); };
     const int64_t words = (int64_t)a.ntiles * a.kblocks * (kInt4TileBytes / 4) * a.E;
     const int64_t scales = (int64_t)a.ntiles * a.ngroups * kInt4Columns * a.E;
-    if (words) hipLaunchKernelGGL(int4_pack_codes_kernel, blocks(words), dim3(256), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !scales) return e;
-    hipLaunchKernelGGL(int4_pack_scales_kernel, blocks(scales), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(int4_pack_codes_kernel, blocks(words), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (dtype == CP_BF16) hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_pack_scales_kernel<__bf16>), blocks(scales), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_pack_scales_kernel<float>), blocks(scales), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -540,7 +540,7 @@ PyObject *pack_int4(PyObject *const *a) {
     const auto per = with_rows(q, (K + g - 1) / g);
     vector(a[1], scales, per, "scales", scales.scalar_type());
     const void *zeros = a[2] == Py_None ? nullptr : vector(a[2], scales, per, "zeros", at::kByte);
-    const int64_t n = cp_int4_bytes(code(scales), K, N, (int32_t)E, g, zeros != nullptr);
+    const int64_t n = cp_int4_bytes(code(scales), K, N, (int32_t)E, g);
     check(n, "cp_int4_bytes");
     const c10::DeviceGuard guard(scales.device());
     const Tensor packed = at::empty({n}, scales.options().dtype(at::kByte));
@@ -551,49 +551,49 @@ PyObject *pack_int4(PyObject *const *a) {
 }
 
 // A packed weight's data: as many bytes as its sizes say.
-const Tensor &packed_weight(PyObject *o, const Tensor &x, int64_t K, int64_t N, int64_t E, int64_t group, bool zeros) {
-    const int64_t n = cp_int4_bytes(code(x), K, N, (int32_t)E, group, zeros);
+const Tensor &packed_weight(PyObject *o, const Tensor &x, int64_t K, int64_t N, int64_t E, int64_t group) {
+    const int64_t n = cp_int4_bytes(code(x), K, N, (int32_t)E, group);
     check(n, "cp_int4_bytes");
     const Tensor &t = like(o, x, {n}, "the packed weight", at::kByte);
     if (!t.is_contiguous()) refuse(PyExc_ValueError, "the packed weight must be contiguous");
     return t;
 }
 
-// linear_int4(x, packed, N, group, zeros, bias, residual, act, out)
+// linear_int4(x, packed, N, group, bias, residual, act, out)
 PyObject *linear_int4(PyObject *const *a) {
     const Tensor &x = first(a[0], "x");
     const int64_t M = x.size(0), K = x.size(1), ldx = rows(x, "x"), N = integer(a[2], "N"), g = group_of(a[3]);
-    const bool zeros = truth(a[4]);
-    const Tensor &w = packed_weight(a[1], x, K, N, 1, g, zeros);
-    const void *bias = optional_vector(a[5], x, {N}, "bias");
-    const Tensor *r = a[6] == Py_None ? nullptr : &like(a[6], x, {M, N}, "residual");
+    const Tensor &w = packed_weight(a[1], x, K, N, 1, g);
+    const void *bias = optional_vector(a[4], x, {N}, "bias");
+    const Tensor *r = a[5] == Py_None ? nullptr : &like(a[5], x, {M, N}, "residual");
     const int64_t ldr = r ? rows(*r, "residual") : 0;
-    const int act = activation(a[7]);
+    const int act = activation(a[6]);
     const c10::DeviceGuard guard(x.device());
-    const Tensor y = output(a[8], x, {M, N});
+    const Tensor y = output(a[7], x, {M, N});
     const int64_t ldy = rows(y, "out");
-    check(cp_linear_int4(code(x), M, K, N, x.data_ptr(), ldx, w.data_ptr(), g, zeros, bias, r ? r->data_ptr() : nullptr, ldr,
-                         act, y.data_ptr(), ldy, stream(x)),
+    const Scratch ws(x, CP_OP_LINEAR_INT4, M, K, N, 0, true);
+    check(cp_linear_int4(code(x), M, K, N, x.data_ptr(), ldx, w.data_ptr(), g, bias, r ? r->data_ptr() : nullptr, ldr,
+                         act, y.data_ptr(), ldy, data(ws.t), ws.n, stream(x)),
           "cp_linear_int4");
     written(y);
     return wrap(y);
 }
 
-// grouped_linear_int4(x, packed, E, N, group, zeros, offsets, bias, act, out)
+// grouped_linear_int4(x, packed, E, N, group, offsets, bias, act, out)
 PyObject *grouped_linear_int4(PyObject *const *a) {
     const Tensor &x = first(a[0], "x");
     const int64_t T = x.size(0), K = x.size(1), ldx = rows(x, "x"), E = integer(a[2], "E"), N = integer(a[3], "N");
     const int64_t g = group_of(a[4]);
-    const bool zeros = truth(a[5]);
-    const Tensor &w = packed_weight(a[1], x, K, N, E, g, zeros);
-    const void *off = vector(a[6], x, {E + 1}, "offsets", at::kInt);
-    const void *bias = optional_vector(a[7], x, {E, N}, "bias");
-    const int act = activation(a[8]);
+    const Tensor &w = packed_weight(a[1], x, K, N, E, g);
+    const void *off = vector(a[5], x, {E + 1}, "offsets", at::kInt);
+    const void *bias = optional_vector(a[6], x, {E, N}, "bias");
+    const int act = activation(a[7]);
     const c10::DeviceGuard guard(x.device());
-    const Tensor y = output(a[9], x, {T, N});
+    const Tensor y = output(a[8], x, {T, N});
     const int64_t ldy = rows(y, "out");
-    check(cp_grouped_linear_int4(code(x), T, K, N, (int32_t)E, x.data_ptr(), ldx, w.data_ptr(), g, zeros, (const int32_t *)off,
-                                 bias, act, y.data_ptr(), ldy, stream(x)),
+    const Scratch ws(x, CP_OP_LINEAR_INT4, T, K, N, E, true);
+    check(cp_grouped_linear_int4(code(x), T, K, N, (int32_t)E, x.data_ptr(), ldx, w.data_ptr(), g, (const int32_t *)off,
+                                 bias, act, y.data_ptr(), ldy, data(ws.t), ws.n, stream(x)),
           "cp_grouped_linear_int4");
     written(y);
     return wrap(y);
@@ -728,8 +728,8 @@ PyMethodDef g_methods[] = {CP_METHOD(linear, 7),
                            CP_METHOD(combine_backward, 7),
                            CP_METHOD(quantize_int4, 3),
                            CP_METHOD(pack_int4, 4),
-                           CP_METHOD(linear_int4, 9),
-                           CP_METHOD(grouped_linear_int4, 10),
+                           CP_METHOD(linear_int4, 8),
+                           CP_METHOD(grouped_linear_int4, 9),
                            CP_METHOD(clip_grad_norm, 4),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

@@ -43,7 +43,7 @@ except ImportError as e:
 ACT_NONE, ACT_GELU_TANH, ACT_RELU, ACT_SILU = 0, 1, 2, 3
 ACTS = {"none": ACT_NONE, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU, "silu": ACT_SILU}
 OP_LINEAR, OP_LINEAR_BACKWARD, OP_GROUPED_LINEAR, OP_GROUPED_LINEAR_BACKWARD, OP_LAYER_NORM_BACKWARD = range(5)
-OP_ROUTE, OP_CLIP_GRAD_NORM = 5, 6
+OP_ROUTE, OP_CLIP_GRAD_NORM, OP_LINEAR_INT4 = 5, 6, 7
 MAX_WIDTH = 4194304
 MAX_GROUPS = 4096
 MAX_ROUTED = 1024
@@ -163,11 +163,10 @@ def combine_backward(dout, y, rows, offsets, gates=None, need_y=True, need_gates
 
 class Int4Weight(NamedTuple):
     """A weight [K][N] (or [E][K][N]) of 4-bit codes, as linear_int4 reads it."""
-    data: torch.Tensor     # uint8: codes, scales and zero points, laid out by pack_int4
+    data: torch.Tensor    # uint8: codes, scales and zero points, laid out by pack_int4
     shape: tuple
     group_size: int
-    has_zeros: bool
-    dtype: torch.dtype     # of the scales, and of the rows it is multiplied with
+    dtype: torch.dtype    # of the scales, and of the rows it is multiplied with
 
     def to(self, device):
         """The same on another device."""
@@ -187,7 +186,7 @@ def pack_int4(codes, scales, zeros: Optional[torch.Tensor] = None, group_size=12
     shaped like the scales; None: 8) for linear_int4, once.  group_size is 32, 64 or
     a multiple of 128."""
     data = _native.pack_int4(codes, scales, zeros, group_size)
-    return Int4Weight(data, tuple(codes.shape), group_size, zeros is not None, scales.dtype)
+    return Int4Weight(data, tuple(codes.shape), group_size, scales.dtype)
 
 
 def _check_int4(x, w, dims):
@@ -203,13 +202,13 @@ def linear_int4(x, w, bias=None, residual=None, act=ACT_NONE, out=None):
     """linear with a 4-bit weight (an Int4Weight [K][N]), for decoding and short
     prompts; x of the weight's type, finite.  `out` may be the residual itself."""
     _check_int4(x, w, 2)
-    return _native.linear_int4(x, w.data, w.shape[1], w.group_size, w.has_zeros, bias, residual, act, out)
+    return _native.linear_int4(x, w.data, w.shape[1], w.group_size, bias, residual, act, out)
 
 
 def grouped_linear_int4(x, w, offsets, bias=None, act=ACT_NONE, out=None):
     """grouped_linear with 4-bit weights (an Int4Weight [E][K][N])."""
     _check_int4(x, w, 3)
-    return _native.grouped_linear_int4(x, w.data, w.shape[0], w.shape[2], w.group_size, w.has_zeros, offsets, bias, act, out)
+    return _native.grouped_linear_int4(x, w.data, w.shape[0], w.shape[2], w.group_size, offsets, bias, act, out)
 
 
 def grad_norm(gradients):
