@@ -4,6 +4,7 @@
 // 16-byte units at any alignment, token by token, so that a token's row is read
 // once for all of its experts and no inverse of `rows` is needed.
 #include "cp_ops_experts.h"
+#include "cp_ops_units.h"
 
 namespace cpo {
 
@@ -27,35 +28,6 @@ inline Pieces pieces(int64_t T, int D, int unit, int per_lane) {
     p.items = (T + tokens - 1) / tokens * p.segs;
     if (p.items < 1) p.items = 1;  // (no tokens: rows of zeros may still be due)
     return p;
-}
-
-template <class T>
-__device__ __forceinline__ void store_partial(char *p, uint4 u, int n) {
-    if (n >= kUnit<T>) {
-        __builtin_memcpy(p, &u, 16);
-    } else {
-        T e[kUnit<T>];
-        __builtin_memcpy(e, &u, 16);
-#pragma unroll
-        for (int i = 0; i < kUnit<T> - 1; ++i)
-            if (i < n) reinterpret_cast<T *>(p)[i] = e[i];
-    }
-}
-template <class T>
-__device__ __forceinline__ void unpack_unit(uint4 u, float (&v)[kUnit<T>]) {
-    T e[kUnit<T>];
-    __builtin_memcpy(e, &u, 16);
-#pragma unroll
-    for (int i = 0; i < kUnit<T>; ++i) v[i] = to_f32(e[i]);
-}
-template <class T>
-__device__ __forceinline__ uint4 pack_unit(const float (&v)[kUnit<T>]) {
-    T e[kUnit<T>];
-#pragma unroll
-    for (int i = 0; i < kUnit<T>; ++i) e[i] = from_f32<T>(v[i]);
-    uint4 u;
-    __builtin_memcpy(&u, e, 16);
-    return u;
 }
 
 // Rows of y that belong to no slot: from *end on.

@@ -71,7 +71,7 @@ hipError_t launch_combine_backward(int dtype, const ExchangeArgs &a, hipStream_t
 // Codes as the matrix instructions take them: tiles of 16 columns x 128 of K,
 // 1 KB each, a column's tiles one after another; lane l of a wave holds column
 // l % 16 and four words, word s the k = 32 s + 8 (l / 16) .. + 7, whose codes i
-// are at bits 4 (i / 2) + 16 (i % 2).  Behind them [column tile][group][16] pairs
+// are at bits 4 (i / 2) + 16 (i % 2) + 3, modulo 32.  Behind them [column tile][group][16] pairs
 // of the scale and 16 + zero point, both of the layer's type.
 constexpr int kInt4Columns = 16, kInt4Depth = 128, kInt4TileBytes = 1024;
 
@@ -102,17 +102,18 @@ struct Int4Args {
     int64_t ldws;
 };
 // Tiles of a launch: `waves` waves to a block that streams (16 rows, any number of
-// column tiles), or 0: 64 rows and 4 nt column tiles.
+// column tiles), or 0: mt row tiles and 4 nt column tiles.
 struct Int4Tiles {
-    int32_t waves, nt, ntm, ntn, chunks, kper;
+    int32_t waves, mt, nt, ntm, ntn, chunks, kper;
 };
 inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, int64_t kblocks, int64_t group) {
     Int4Tiles t{};
     const int64_t rows = experts ? (M + experts - 1) / experts : M;  // to an expert, on average
-    const int64_t bm = rows <= 16 ? 16 : 64, used = M < experts + 1 ? M : experts + 1;
-    t.ntm = (int32_t)(experts ? (M + used * (bm - 1)) / bm : (M + bm - 1) / bm);
+    const int64_t used = M < experts + 1 ? M : experts + 1;
+    auto row_tiles = [&](int64_t bm) { return (int32_t)(experts ? (M + used * (bm - 1)) / bm : (M + bm - 1) / bm); };
     t.chunks = 1;
-    if (bm == 16) {
+    if (rows <= 16) {
+        t.ntm = row_tiles(16);
         // registers for x, 128 or (8 waves) 256 to a lane: beside few scales for more of it
         const bool bf16 = dtype == CP_BF16;
         t.waves = kblocks <= 4 ? 4 : (bf16 && group > 32 ? 16 : 8);
@@ -124,10 +125,37 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
         if (blocks < 1) blocks = 1;
         t.ntn = (int32_t)(blocks < ntiles ? blocks : ntiles);
     } else {
-        t.nt = (int64_t)t.ntm * ntiles >= 16 * kComputeUnits ? 4 : ((int64_t)t.ntm * ntiles >= 8 * kComputeUnits ? 2 : 1);
-        const int32_t most = group == 32 ? 1 : (group == 64 ? 2 : 4);  // (registers: small groups keep more scales)
-        if (t.nt > most) t.nt = most;
-        t.ntn = (int32_t)((ntiles + 4 * t.nt - 1) / (4 * t.nt));
+        // Tile and parts of the contraction by the rounds the device takes: microseconds
+        // for 256 k of a block with a CU to itself, and of two that share one (of the
+        // largest only one fits).  Measured with groups of 64 and 128, whole calls
+        // with 2x1 | 2x2 | 5x2 tiles: 64 x 8192 x 8192 29 | 37 | 67, 300 x 8192 x
+        // 8192 - | 93 | 86, 2048 x 8192 x 8192 - | 400 | 508.
+        constexpr struct {
+            int mt, nt;
+            double one, two;
+        } kTiles[] = {{2, 1, 0.58, 1.0}, {2, 2, 0.9, 1.56}, {5, 2, 2.3, 0.0}};
+        double least = 1e300;
+        for (const auto &k : kTiles) {
+            if (k.nt > 1 && group == 32) continue;        // (registers: small groups keep more scales,
+            if (k.mt > 2 && dtype != CP_BF16) continue;   // and fp32 rows are three operands)
+            const int64_t tm = row_tiles(16 * k.mt), tn = (ntiles + 4 * k.nt - 1) / (4 * k.nt);
+            const int64_t likely = experts ? M / (16 * k.mt) + experts / 2 + 1 : tm;  // an expert's last is half empty
+            for (int chunks = 1; chunks <= 8 && (chunks == 1 || kblocks >= 8 * chunks); chunks *= 2) {
+                const int64_t blocks = likely * tn * chunks, per = k.two > 0.0 ? 2 * kComputeUnits : kComputeUnits;
+                const int64_t rest = blocks % per;
+                double us = (double)(blocks / per) * (k.two > 0.0 ? k.two : k.one);
+                us += rest == 0 ? 0.0 : (rest <= kComputeUnits ? k.one : k.two);
+                us *= (double)((kblocks + 2 * chunks - 1) / (2 * chunks));
+                if (chunks > 1) us += 5.0 + 4.0 * chunks * (double)M * (double)ntiles * 16.0 * 4.0 / 8e6;  // partials, a launch
+                if (us >= least) continue;
+                least = us;
+                t.mt = k.mt;
+                t.nt = k.nt;
+                t.ntm = tm;
+                t.ntn = (int32_t)tn;
+                t.chunks = chunks;
+            }
+        }
     }
     t.kper = (int32_t)((kblocks + t.chunks - 1) / t.chunks);
     return t;

@@ -10,6 +10,7 @@
 // them exactly.  The codes lie in memory as the instructions take them (Int4Layout),
 // so a wave reads its operand with whole 16-byte loads and no LDS.
 #include "cp_ops_experts.h"
+#include "cp_ops_units.h"
 
 namespace cpo {
 
@@ -24,10 +25,10 @@ struct Spread {
             uint32_t u[4];
             bf16x8_t v;
         } r;
-        r.u[0] = ((w << 3) & mask) | base;
-        r.u[1] = ((w >> 1) & mask) | base;
-        r.u[2] = ((w >> 5) & mask) | base;
-        r.u[3] = ((w >> 9) & mask) | base;
+        r.u[0] = (w & mask) | base;
+        r.u[1] = ((w >> 4) & mask) | base;
+        r.u[2] = ((w >> 8) & mask) | base;
+        r.u[3] = (__builtin_amdgcn_alignbit(w, w, 12) & mask) | base;
         return r.v;
     }
 };
@@ -82,12 +83,14 @@ struct Meta<__bf16> {
     uint32_t v;  // 16 + z over the scale, both bf16
     __device__ __forceinline__ float scale() const { return __builtin_bit_cast(float, v << 16); }
     __device__ __forceinline__ float zero() const { return __builtin_bit_cast(float, v & 0xFFFF0000u); }
+    __device__ __forceinline__ void hold() { asm volatile("" : "+v"(v)); }
 };
 template <>
 struct Meta<float> {
     float s, z;
     __device__ __forceinline__ float scale() const { return s; }
     __device__ __forceinline__ float zero() const { return z; }
+    __device__ __forceinline__ void hold() { asm volatile("" : "+v"(s), "+v"(z)); }
 };
 
 // SG matrix instructions, 32 k each, to a group, as far as it lies in a tile.
@@ -109,6 +112,13 @@ struct Tile {  // of codes, and its groups' scales
             const int at = gr + i < g.ngroups ? gr + i : g.ngroups - 1;  // (past K: x is zero)
             m[i] = reinterpret_cast<const Meta<T> *>(meta)[((int64_t)tile * g.ngroups + at) * kInt4Columns + (lane & 15)];
         }
+    }
+    // Keeps what is computed from the tile behind this point: unpacked early it takes
+    // several times the registers.
+    __device__ __forceinline__ void hold() {
+        asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+#pragma unroll
+        for (int i = 0; i < NG; ++i) m[i].hold();
     }
     __device__ __forceinline__ uint32_t step(int s) const { return s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w; }
 };
@@ -143,6 +153,37 @@ template <class T>
 __device__ __forceinline__ void put_int4(const Int4Args &g, const BlockRows &b, int chunk, int row, int col, float v) {
     if (g.chunks == 1) return finish_int4<T>(g, b, row, col, v);
     if (row < b.end && col < g.N) g.ws[((int64_t)chunk * g.M + row) * g.ldws + col] = v;
+}
+
+template <class T>
+__device__ __forceinline__ void put_int4_unit(const Int4Args &g, const BlockRows &b, int chunk, int row, int col, const float *v) {
+    constexpr int CE = kUnit<T>;
+    if (row >= b.end || col >= g.N) return;
+    if (g.chunks > 1) {  // (rows of whole units: ldws)
+        float *p = g.ws + ((int64_t)chunk * g.M + row) * g.ldws + col;
+#pragma unroll
+        for (int i = 0; i < CE; ++i) p[i] = v[i];
+        return;
+    }
+    float f[CE];
+#pragma unroll
+    for (int i = 0; i < CE; ++i) f[i] = v[i];
+    const int left = g.N - col;
+    if (g.bias) {
+        float t[CE];
+        unpack_unit<T>(load_partial<T>(g.bias + ((int64_t)b.expert * g.N + col) * (int64_t)sizeof(T), left), t);
+#pragma unroll
+        for (int i = 0; i < CE; ++i) f[i] += t[i];
+    }
+#pragma unroll
+    for (int i = 0; i < CE; ++i) f[i] = b.none ? 0.0f : act_apply(f[i], g.act);
+    if (g.res) {
+        float t[CE];
+        unpack_unit<T>(load_partial<T>(g.res + ((int64_t)row * g.ldr + col) * (int64_t)sizeof(T), left), t);
+#pragma unroll
+        for (int i = 0; i < CE; ++i) f[i] += t[i];
+    }
+    store_partial<T>(g.y + ((int64_t)row * g.ldy + col) * (int64_t)sizeof(T), pack_unit<T>(f), left);
 }
 
 // Up to 16 rows (of an expert): a chunk of the contraction to a block, every W-th tile
@@ -277,17 +318,34 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
         }
 }
 
-// More rows: 64 to a block, staged through LDS in the order the matrix instructions
-// take them, while the codes go to the registers of the wave that needs them: wave
-// wn of four has NT column tiles.  WK such quartets take a part of the contraction
-// each.  A wave stages a row tile and with it forms the sums of x over the groups.
-// (The loop has no branch around a load, as above: what lies past K comes last.)
-template <class T, int NT, int WK, int SG>
+// The sum of each 2 or 4 neighbouring lanes' values, in all of them.
+template <int N>
+__device__ __forceinline__ float sum_neighbours(float v) {
+    auto swapped = [](float u, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, u), ctrl(), 0xf, 0xf, true));
+    };
+    if constexpr (N >= 2) v += swapped(v, std::integral_constant<int, 0xB1>());  // quad_perm 1 0 3 2
+    if constexpr (N >= 4) v += swapped(v, std::integral_constant<int, 0x4E>());  // quad_perm 2 3 0 1
+    return v;
+}
+
+// More rows: MT x 16 to a block, staged through LDS in the order the matrix
+// instructions take them, while the codes go to the registers of the wave that needs
+// them: wave wn of four has NT column tiles.  WK such quartets take a part of the
+// contraction each.  A wave stages 32 or 64 k of 16 rows at a time and adds them up for
+// each row; where the pieces do not go round, some are staged twice, alike.  x and
+// codes are requested two tiles of the contraction ahead, x first: loads come back in
+// order, and x is waited for first, to be staged one tile ahead.  (No branch around a load, as above: what lies past
+// K comes last.)
+template <class T, int MT, int NT, int WK, int SG>
 __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
-    constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG, MT = 4;
-    constexpr int kBuf = XP * 4 * MT * 1024, kJoin = WK > 1 ? (WK - 1) * MT * NT * 4096 : 0;
-    __shared__ __attribute__((aligned(16))) char stage[WK * 2 * kBuf > kJoin ? WK * 2 * kBuf : kJoin];
-    __shared__ f32x4_t sums[WK][2][NG][MT][4];
+    constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG;
+    constexpr int UF = SG < 2 ? SG : 2, UH = 4 / UF, PU = (MT * UH + 3) / 4;  // a unit's pieces of 32 k, units to a row tile, to a wave
+    constexpr int CE = kUnit<T>, LD = NT * 16 + 4;  // columns and stride of a wave's results in LDS
+    constexpr int kBuf = XP * 4 * MT * 1024, kJoin = (WK - 1) * MT * NT * 4096, kOut = 4 * MT * 16 * LD * 4;
+    constexpr int kMost = kJoin > kOut ? kJoin : kOut;
+    __shared__ __attribute__((aligned(16))) char stage[WK * 2 * kBuf > kMost ? WK * 2 * kBuf : kMost];
+    __shared__ f32x4_t sums[WK][2][UH][MT][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave & 3, wk = wave >> 2, n16 = lane & 15, quad = lane >> 4;
     const int b = xcd_remap(blockIdx.x, gridDim.x), part = b / g.ntm, rt = b % g.ntm, ct = part / g.chunks, chunk = part % g.chunks;
@@ -298,46 +356,53 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
     const int tile0 = (ct * 4 + wn) * NT;
     const int kb_end = br.none ? 0 : ((chunk + 1) * g.kper < g.kblocks ? (chunk + 1) * g.kper : g.kblocks);
     const int whole = g.K / kInt4Depth < kb_end ? g.K / kInt4Depth : kb_end;  // tiles without an end of K in them
-    const int first = chunk * g.kper, per = whole > first ? (whole - first + WK - 1) / WK : 0, kb0 = first + wk * per;
-    const int row = br.row0 + wn * 16 + n16;
-    const char *xp = g.x + ((int64_t)(row < br.end ? row : br.row0) * g.ldx + quad * 8) * (int64_t)sizeof(T);
+    const int first = chunk * g.kper, per = whole > first ? (whole - first) / WK : 0, kb0 = first + wk * per;
+    const char *xp[PU];
+    int um[PU], uh[PU];
+#pragma unroll
+    for (int i = 0; i < PU; ++i) {
+        const int u = wn + 4 * i < MT * UH ? wn + 4 * i : MT * UH - 1;
+        um[i] = u / UH;
+        uh[i] = u % UH;
+        const int row = br.row0 + um[i] * 16 + n16;  // (rows past the end: their results are not used)
+        xp[i] = g.x + ((int64_t)(row < br.end ? row : br.row0) * g.ldx + uh[i] * UF * 32 + quad * 8) * (int64_t)sizeof(T);
+    }
 
-    Row8<T> xr[4];
-    Tile<T, SG> cur[NT], nxt[NT];
-    auto load_codes = [&](Tile<T, SG> (&c)[NT], int kb) {
+    Row8<T> xr[PU][UF];
+    Tile<T, SG> c[3][NT];  // in turn: copying one to the next would wait for it
+    auto load_codes = [&](Tile<T, SG> (&to)[NT], int kb) {
         const int gr = first_group<SG>(g, kb);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            c[n].load(g, codes, meta, tile0 + n < g.ntiles ? tile0 + n : g.ntiles - 1, kb, gr);
+            to[n].load(g, codes, meta, tile0 + n < g.ntiles ? tile0 + n : g.ntiles - 1, kb, gr);
     };
-    auto load = [&](Tile<T, SG> (&c)[NT], int it) {
-        const int kb = kb0 + it < whole ? kb0 + it : whole - 1;
-        load_codes(c, kb);
+    auto at = [&](int it) { return kb0 + (it < per ? it : per - 1); };
+    auto load_x = [&](int it) {
+        const int64_t k = (int64_t)at(it) * kInt4Depth * (int64_t)sizeof(T);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int u = 0; u < PU; ++u)
 #pragma unroll
-            for (int i = 0; i < Row8<T>::kUnits; ++i)
-                __builtin_memcpy(&xr[s].u[i], xp + ((int64_t)kb * kInt4Depth + s * 32) * (int64_t)sizeof(T) + i * 16, 16);
+            for (int f = 0; f < UF; ++f)
+#pragma unroll
+                for (int i = 0; i < Row8<T>::kUnits; ++i)
+                    __builtin_memcpy(&xr[u][f].u[i], xp[u] + k + f * 32 * sizeof(T) + i * 16, 16);
     };
-    auto put = [&](int buf, bool zero) {
-        if (zero) {
+    auto put = [&](int buf) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) xr[s].zero();
-        }
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
+        for (int u = 0; u < PU; ++u) {
             f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = j * SG; s < j * SG + SG; ++s) {
+            for (int f = 0; f < UF; ++f) {
                 bf16x8_t x[XP];
-                parts(xr[s], x);
+                parts(xr[u][f], x);
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
                     xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
-                    *reinterpret_cast<bf16x8_t *>(stage + (wk * 2 + buf) * kBuf + ((q * 4 + s) * MT + wn) * 1024 + lane * 16) = x[q];
+                    *reinterpret_cast<bf16x8_t *>(stage + (wk * 2 + buf) * kBuf + ((q * 4 + uh[u] * UF + f) * MT + um[u]) * 1024 +
+                                                  lane * 16) = x[q];
                 }
             }
-            if (n16 == 0) sums[wk][buf][j][wn][quad] = xs;
+            if (n16 == 0) sums[wk][buf][uh[u]][um[u]][quad] = xs;
         }
     };
     f32x4_t acc[MT][NT];
@@ -345,70 +410,107 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    auto multiply = [&](int buf) {
+    auto multiply = [&](Tile<T, SG> (&c0)[NT], int buf) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c0[n].hold();
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            f32x4_t p[MT][NT];
+            bf16x8_t w[SG][NT];
+#pragma unroll
+            for (int s = 0; s < SG; ++s)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) w[s][n] = spread(c0[n].step(j * SG + s));
+            // a row tile's operands are read while the one before is multiplied and the one
+            // before that scaled
+            bf16x8_t x[2][SG][XP];
+            f32x4_t xs[2], ys[2];
+            auto fetch = [&](int m) {
+                xs[m & 1] = sums[wk][buf][SG > UF ? n16 % (SG / UF) : j][m][quad];
+#pragma unroll
+                for (int s = 0; s < SG; ++s)
+#pragma unroll
+                    for (int q = 0; q < XP; ++q)
+                        x[m & 1][s][q] = *reinterpret_cast<const bf16x8_t *>(
+                            stage + (wk * 2 + buf) * kBuf + ((q * 4 + j * SG + s) * MT + m) * 1024 + lane * 16);
+            };
+            f32x4_t p[2][NT];
+            auto scale = [&](int m) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ys[m & 1][r] = sum_neighbours<SG / UF>(ys[m & 1][r]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float sc = c0[n].m[j].scale(), zp = -c0[n].m[j].zero();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc, fmaf(zp, ys[m & 1][r], p[m & 1][n][r]), acc[m][n][r]);
+                }
+            };
+            fetch(0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (m + 1 < MT) fetch(m + 1);
+                ys[m & 1] = xs[m & 1];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) p[m & 1][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < SG; ++s)
+#pragma unroll
+                    for (int q = 0; q < XP; ++q)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            p[m & 1][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m & 1][s][q], w[s][n], p[m & 1][n], 0, 0, 0);
+                if (m > 0) scale(m - 1);
+            }
+            scale(MT - 1);
+            // (here and not where the sums are next used, blocks later, with all that they are made of)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) p[m][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = j * SG; s < j * SG + SG; ++s) {
-                bf16x8_t w[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) w[n] = spread(cur[n].step(s));
-#pragma unroll
-                for (int q = 0; q < XP; ++q)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const bf16x8_t x = *reinterpret_cast<const bf16x8_t *>(stage + (wk * 2 + buf) * kBuf +
-                                                                               ((q * 4 + s) * MT + m) * 1024 + lane * 16);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) p[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[n], p[m][n], 0, 0, 0);
-                    }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const f32x4_t xs = sums[wk][buf][j][m][quad];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float sc = cur[n].m[j].scale(), zp = -cur[n].m[j].zero();
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc, fmaf(zp, xs[r], p[m][n][r]), acc[m][n][r]);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);  // (one group's registers at a time)
+                for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(acc[m][n]));
         }
     };
+    auto step = [&](auto i, int it) {
+        put(~it & 1);
+        load_x(it + 2);
+        load_codes(c[(i() + 2) % 3], at(it + 2));
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(c[i()], it & 1);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);  // (the next step's codes stay packed until then)
+    };
+    using std::integral_constant;
     if (per) {
-        load(cur, 0);
-        put(0, kb0 >= whole);
+        load_x(0);
+        load_codes(c[0], at(0));
+        put(0);
+        load_x(1);
+        load_codes(c[1], at(1));
         __syncthreads();
-        for (int it = 0; it + 1 < per; ++it) {
-            load(nxt, it + 1);
-            multiply(it & 1);
-            put(~it & 1, kb0 + it + 1 >= whole);
-            __syncthreads();
-#pragma unroll
-            for (int n = 0; n < NT; ++n) cur[n] = nxt[n];
+        int it = 0;
+        for (; it + 3 <= per; it += 3) {
+            step(integral_constant<int, 0>(), it);
+            step(integral_constant<int, 1>(), it + 1);
+            step(integral_constant<int, 2>(), it + 2);
         }
-        multiply((per - 1) & 1);
+        if (it < per) step(integral_constant<int, 0>(), it);
+        if (it + 1 < per) step(integral_constant<int, 1>(), it + 1);
     }
-    if (whole < kb_end) {  // K ends within a tile: the first quartet's
-        load_codes(cur, whole);
+    if (first + per * WK < kb_end) {  // what the quartets have not shared out evenly, and a tile that K ends in: one each
+        const int kb = first + per * WK + wk;
+        load_codes(c[0], kb < kb_end ? kb : kb_end - 1);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = whole * kInt4Depth + s * 32 + quad * 8;
-            if (k < g.K) xr[s].load(xp + (int64_t)(k - quad * 8) * (int64_t)sizeof(T), g.K - k);
-            else xr[s].zero();
-        }
-        put(per & 1, wk > 0);
+        for (int u = 0; u < PU; ++u)
+#pragma unroll
+            for (int f = 0; f < UF; ++f) {
+                const int k = kb * kInt4Depth + (uh[u] * UF + f) * 32 + quad * 8;
+                if (kb < kb_end && k < g.K) xr[u][f].load(xp[u] + ((int64_t)kb * kInt4Depth + f * 32) * (int64_t)sizeof(T), g.K - k);
+                else xr[u][f].zero();
+            }
+        put(per & 1);
         __syncthreads();
-        multiply(per & 1);
+        multiply(c[0], per & 1);
     }
+    __syncthreads();
     if constexpr (WK > 1) {
-        __syncthreads();
         f32x4_t *join = reinterpret_cast<f32x4_t *>(stage);
         if (wk > 0)
 #pragma unroll
@@ -416,21 +518,29 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) join[(((wk - 1) * 4 + wn) * MT * NT + m * NT + n) * 64 + lane] = acc[m][n];
         __syncthreads();
+        if (wk == 0)
+#pragma unroll
+            for (int w = 1; w < WK; ++w)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[m][n] += join[(((w - 1) * 4 + wn) * MT * NT + m * NT + n) * 64 + lane];
+        __syncthreads();
         if (wk > 0) return;
-#pragma unroll
-        for (int w = 1; w < WK; ++w)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n] += join[(((w - 1) * 4 + wn) * MT * NT + m * NT + n) * 64 + lane];
     }
+    // out by way of LDS, each wave its own part of it, in whole units of a row
+    float *tile = reinterpret_cast<float *>(stage) + wn * MT * 16 * LD;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                put_int4<T>(g, br, chunk, br.row0 + m * 16 + quad * 4 + r, (tile0 + n) * 16 + n16, acc[m][n][r]);
+            for (int r = 0; r < 4; ++r) tile[(m * 16 + quad * 4 + r) * LD + n * 16 + n16] = acc[m][n][r];
+    __builtin_amdgcn_wave_barrier();
+    for (int i = lane; i < MT * 16 * NT * 16 / CE; i += 64) {
+        const int r = i / (NT * 16 / CE), c0 = i % (NT * 16 / CE) * CE;
+        put_int4_unit<T>(g, br, chunk, br.row0 + r, tile0 * 16 + c0, tile + r * LD + c0);
+    }
 }
 
 // ------------------------------------------------- packing and quantisation
@@ -449,6 +559,7 @@ __global__ __launch_bounds__(256) void int4_pack_codes_kernel(Int4PackArgs a) {
             for (int j = 0; j < 8; ++j)
                 if (k0 + j < a.K)
                     v |= (uint32_t)(a.q[(e * a.K + k0 + j) * a.N + n] & 15) << (4 * (j / 2) + 16 * (j % 2));
+        v = v << 3 | v >> 29;
         const int64_t tile = n / kInt4Columns, kb = k0 / kInt4Depth;
         const int lane = (int)(k8 % 4) * 16 + (int)(n % kInt4Columns), s = (int)(k0 % kInt4Depth) / 32;
         reinterpret_cast<uint32_t *>(a.codes)[e * words + (tile * a.kblocks + kb) * (kInt4TileBytes / 4) + lane * 4 + s] = v;
@@ -512,26 +623,26 @@ hipError_t stream_rows(const Int4Args &a, unsigned blocks, hipStream_t s) {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_stream_kernel<T, W, XK, D, SG>), dim3(blocks), dim3(W * 64), 0, s, a);
     return hipGetLastError();
 }
-template <class T, int NT, int WK>
+template <class T, int SG, int MT, int NT>
 hipError_t many_rows(const Int4Args &a, unsigned blocks, hipStream_t s) {
-    return by_group(a.group, [&](auto sg) {
-        if constexpr (NT > sg()) return hipErrorInvalidValue;  // (int4_tiles)
-        else {
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_rows_kernel<T, NT, WK, sg()>), dim3(blocks), dim3(WK * 256), 0, s, a);
-            return hipGetLastError();
-        }
-    });
+    constexpr int WK = sizeof(T) == 2 ? 2 : 1;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(int4_rows_kernel<T, MT, NT, WK, SG>), dim3(blocks), dim3(WK * 256), 0, s, a);
+    return hipGetLastError();
 }
-
 template <class T>
 hipError_t int4(const Int4Args &a, const Int4Tiles &t, hipStream_t s) {
     constexpr bool kWide = sizeof(T) == 4;
-    constexpr int WK = kWide ? 1 : 2;
     const unsigned n = (unsigned)(t.ntm * t.ntn * t.chunks);
-    if (!t.waves) {
-        if (t.nt == 1) return many_rows<T, 1, WK>(a, n, s);
-        return t.nt == 2 ? many_rows<T, 2, WK>(a, n, s) : many_rows<T, 4, WK>(a, n, s);
-    }
+    if (!t.waves)
+        return by_group(a.group, [&](auto sg) {
+            constexpr int SG = sg();
+            if constexpr (SG > 1) {
+                if (t.mt == 2 && t.nt == 2) return many_rows<T, SG, 2, 2>(a, n, s);
+                if constexpr (!kWide)
+                    if (t.mt == 5) return many_rows<T, SG, 5, 2>(a, n, s);
+            }
+            return many_rows<T, SG, 2, 1>(a, n, s);
+        });
     return by_group(a.group, [&](auto sg) {
         constexpr int SG = sg();
         if (t.waves == 4) return stream_rows<T, SG, 4, 1, 4>(a, n, s);
