@@ -72,28 +72,33 @@ __device__ __forceinline__ void add_squares(const char *p, int64_t n, double (&a
     }
 }
 
-// y = x f over n elements; x and y may be the same memory.
+// y = x f over n elements; x and y may be the same memory.  U steps of eight elements
+// to a thread are requested together.
 template <class T, class O, int NT>
 __device__ __forceinline__ void scale_to(const char *x, char *y, int64_t n, float f) {
-    constexpr int CE = 8;  // elements to a step
-    constexpr int UI = CE / kUnit<T>, UO = CE / kUnit<O>;
-    for (int64_t i = (int64_t)threadIdx.x * CE; i < n; i += (int64_t)NT * CE) {
-        const int left = n - i < CE ? (int)(n - i) : CE;
-        T e[CE];
+    constexpr int CE = 8, U = 4;
+    T e[U][CE];
+    auto load = [&](int u, int64_t i) { __builtin_memcpy(e[u], x + i * (int64_t)sizeof(T), sizeof e[u]); };
+    auto store = [&](int u, int64_t i) {
         O o[CE];
-        if (left == CE) {
-            uint4 v[UI], w[UO];
 #pragma unroll
-            for (int u = 0; u < UI; ++u) __builtin_memcpy(&v[u], x + i * (int64_t)sizeof(T) + u * 16, 16);
-            __builtin_memcpy(e, v, sizeof e);
+        for (int j = 0; j < CE; ++j) o[j] = from_f32<O>(to_f32(e[u][j]) * f);
+        __builtin_memcpy(y + i * (int64_t)sizeof(O), o, sizeof o);
+    };
+    int64_t i = (int64_t)threadIdx.x * CE;
+    for (; i + (int64_t)(U - 1) * NT * CE + CE <= n; i += (int64_t)U * NT * CE) {
 #pragma unroll
-            for (int j = 0; j < CE; ++j) o[j] = from_f32<O>(to_f32(e[j]) * f);
-            __builtin_memcpy(w, o, sizeof o);
+        for (int u = 0; u < U; ++u) load(u, i + (int64_t)u * NT * CE);
 #pragma unroll
-            for (int u = 0; u < UO; ++u) __builtin_memcpy(y + i * (int64_t)sizeof(O) + u * 16, &w[u], 16);
+        for (int u = 0; u < U; ++u) store(u, i + (int64_t)u * NT * CE);
+    }
+    for (; i < n; i += (int64_t)NT * CE) {
+        if (i + CE <= n) {
+            load(0, i);
+            store(0, i);
         } else {
-            for (int j = 0; j < left; ++j)
-                reinterpret_cast<O *>(y)[i + j] = from_f32<O>(to_f32(reinterpret_cast<const T *>(x)[i + j]) * f);
+            for (; i < n; ++i)
+                reinterpret_cast<O *>(y)[i] = from_f32<O>(to_f32(reinterpret_cast<const T *>(x)[i]) * f);
         }
     }
 }
@@ -101,7 +106,7 @@ __device__ __forceinline__ void scale_to(const char *x, char *y, int64_t n, floa
 template <int NT>
 __device__ __forceinline__ void square_chunk(const ClipArgs &a, int64_t c, double (&acc)[4]) {
     const int i = find_tensor(a, c);
-    const int64_t from = (c - a.t[i].before) * kClipChunk, n = a.t[i].n - from < kClipChunk ? a.t[i].n - from : kClipChunk;
+    const int64_t from = (c - a.t[i].before) * a.chunk, n = a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk;
     if (bit(a.bf16_in, i)) add_squares<__bf16, NT>(a.t[i].x + from * 2, n, acc);
     else add_squares<float, NT>(a.t[i].x + from * 4, n, acc);
 }
@@ -110,7 +115,7 @@ template <int NT>
 __device__ __forceinline__ void scale_chunk(const ClipArgs &a, int64_t c, float f) {
     const int i = find_tensor(a, c);
     if (f == 1.0f && a.t[i].y == a.t[i].x) return;  // in place, nothing to do
-    const int64_t from = (c - a.t[i].before) * kClipChunk, n = a.t[i].n - from < kClipChunk ? a.t[i].n - from : kClipChunk;
+    const int64_t from = (c - a.t[i].before) * a.chunk, n = a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk;
     const bool bi = bit(a.bf16_in, i), bo = bit(a.bf16_out, i);
     const char *x = a.t[i].x + from * (bi ? 2 : 4);
     char *y = a.t[i].y + from * (bo ? 2 : 4);

@@ -193,17 +193,19 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
     CP_TRY(check_ws(ws, ws_bytes, clip_ws(n)));
     if (outs) CP_TRY(check_clip_memory(n, dtypes, grads, numels, out_dtypes, outs));
 
+    const int chunk = clip_chunk(total);
     // The launches' arguments, kClipTensors tensors that are not empty at a time,
     // from tensor *i on.
     auto fill = [&](int64_t *i) {
         ClipArgs a{};
         a.max_norm = max_norm;
+        a.chunk = chunk;
         for (; *i < n && a.n < kClipTensors; ++*i) {
             if (!numels[*i]) continue;
             a.t[a.n] = {(const char *)grads[*i], outs ? (char *)outs[*i] : nullptr, numels[*i], a.chunks};
             if (dtypes[*i] == CP_BF16) a.bf16_in[a.n >> 5] |= 1u << (a.n & 31);
             if (outs && out_dtypes[*i] == CP_BF16) a.bf16_out[a.n >> 5] |= 1u << (a.n & 31);
-            a.chunks += ceil_div(numels[*i], kClipChunk);
+            a.chunks += ceil_div(numels[*i], chunk);
             ++a.n;
         }
         a.blocks = (int)std::min<int64_t>(a.chunks, kClipBlocks);
@@ -231,7 +233,7 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
         a.all = partial;
         a.nall = nall;
         a.norm = first ? norm : nullptr;
-        if (!outs) a.blocks = 1;
+        a.blocks = outs ? (int)std::min<int64_t>(a.chunks, 2 * kClipBlocks) : 1;
         CP_TRY(launched(launch_clip(a, s), "gradient clipping"));
     }
     return CP_OK;
@@ -274,8 +276,9 @@ int cp_route(int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t normalize, 
     a.blocks = route_blocks(T);
     a.chunks = route_chunks(T);
     a.hist = (int32_t *)ws;
-    a.psum = (float *)(a.hist + (int64_t)a.blocks * E);
-    a.live = (int32_t *)(a.psum + (int64_t)a.blocks * E);
+    a.stride = (int)up(E, 4);
+    a.psum = (float *)(a.hist + (int64_t)a.blocks * a.stride);
+    a.live = (int32_t *)(a.psum + (int64_t)a.blocks * a.stride);
     return launched(launch_route(dtype, a, (hipStream_t)stream), "router");
 }
 

@@ -9,7 +9,7 @@ namespace cpo {
 // ------------------------------------------------------------------- router
 
 constexpr int kRouteTokens = 64;      // tokens of a chunk: one bit each of an expert's word
-constexpr int kRouteOneBlock = 256;   // tokens that one block takes on its own
+constexpr int kRouteOneBlock = 128;   // tokens that one block takes on its own
 constexpr int kRouteBlocks = 256;     // blocks of a launch at most
 
 struct RouteArgs {
@@ -18,10 +18,11 @@ struct RouteArgs {
     int64_t ld;
     int32_t *experts, *rows, *counts, *offsets;
     float *gates, *loss, *slopes;
-    int32_t *hist, *live;  // scratch: slots of each expert [blocks][E] and tokens with an expert [blocks]
-    float *psum;           // scratch: sums of probabilities [blocks][E]
+    int32_t *hist, *live;  // scratch: slots of each expert [blocks][stride] and tokens with an expert [blocks]
+    float *psum;           // scratch: sums of probabilities [blocks][stride]
     int32_t T, E, k, normalize;
     int32_t blocks, chunks;  // chunks of kRouteTokens per block
+    int32_t stride;          // E in whole 16 bytes
 };
 inline int route_chunks(int64_t T) {
     const int64_t chunks = (T + kRouteTokens - 1) / kRouteTokens;
@@ -34,7 +35,7 @@ inline int route_blocks(int64_t T) {
 }
 inline int64_t route_ws(int64_t T, int64_t E) {
     const int64_t blocks = route_blocks(T);
-    return blocks > 1 ? (blocks * (2 * E + 1) * 4 + 255) / 256 * 256 : 0;
+    return blocks > 1 ? (blocks * (2 * ((E + 3) / 4 * 4) + 1) * 4 + 255) / 256 * 256 : 0;
 }
 hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
 
@@ -122,6 +123,7 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
         // blocks that fill the device, shared out over the row tiles that are likely there
         const int64_t tiles = (experts ? (M < experts ? M : experts) : t.ntm) * t.chunks;
         int64_t blocks = kComputeUnits * (16 / t.waves) / (tiles ? tiles : 1);
+        if (blocks >= 8) blocks = blocks / 8 * 8;  // (as many to each XCD)
         if (blocks < 1) blocks = 1;
         t.ntn = (int32_t)(blocks < ntiles ? blocks : ntiles);
     } else {
@@ -192,7 +194,7 @@ hipError_t launch_int4_quantize(int dtype, const Int4QuantArgs &a, hipStream_t s
 // ------------------------------------------------------ gradient norm, clipping
 
 constexpr int kClipTensors = 96;    // of a launch: its arguments hold their addresses
-constexpr int kClipBlocks = 1024;   // blocks, and partial sums, of a launch
+constexpr int kClipBlocks = 1024;   // partial sums of a launch, at most
 constexpr int64_t kClipOneBlock = 1 << 16;  // elements that one block takes on its own
 
 struct ClipArgs {
@@ -204,6 +206,7 @@ struct ClipArgs {
     } t[kClipTensors];
     uint32_t bf16_in[(kClipTensors + 31) / 32], bf16_out[(kClipTensors + 31) / 32];
     int32_t n, blocks;
+    int32_t chunk;         // elements of a chunk
     int64_t chunks;
     double *partial;       // this launch's
     const double *all;     // of all launches
@@ -211,7 +214,12 @@ struct ClipArgs {
     float max_norm;
     float *norm;
 };
-constexpr int kClipChunk = 16384;   // elements a block takes at a time
+// Elements that a block takes at a time: few where there are few in all, for the
+// blocks to fill the device.
+inline int32_t clip_chunk(int64_t total) {
+    const int64_t n = total / (2 * kClipBlocks) / 2048 * 2048;
+    return (int32_t)(n < 2048 ? 2048 : (n > 16384 ? 16384 : n));
+}
 inline int64_t clip_ws(int64_t tensors) {  // partial sums of every launch
     return (tensors + kClipTensors - 1) / kClipTensors * kClipBlocks * (int64_t)sizeof(double);
 }

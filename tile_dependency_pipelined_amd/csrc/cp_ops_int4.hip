@@ -201,7 +201,10 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
     __shared__ float done[kInt4Flush][256];
     __shared__ f32x4_t sums[W][XK * NG][4];  // of x over the groups
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int b = xcd_remap(blockIdx.x, gridDim.x), part = b / g.ntn, cb = b % g.ntn, rt = part / g.chunks, chunk = part % g.chunks;
+    // An XCD has a range of the columns, for all row tiles: of those the last may not be
+    // there, and would leave it idle were they all its own.
+    const int per = g.ntn % 8 ? g.ntn : g.ntn / 8, b = g.ntn % 8 ? blockIdx.x : blockIdx.x / 8;
+    const int cb = (g.ntn % 8 ? 0 : (blockIdx.x & 7) * per) + b % per, part = b / per, rt = part / g.chunks, chunk = part % g.chunks;
     BlockRows br;
     if (!block_rows(g, 16, rt, br)) return;
     const int t0 = (int)((int64_t)cb * g.ntiles / g.ntn), t1 = (int)((int64_t)(cb + 1) * g.ntiles / g.ntn), n = t1 - t0;

@@ -72,6 +72,11 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return x != x ? 0xFFFFFFFFu : (x == -__builtin_inff() ? 0u : u);
 }
 
+// The logit of a key above 0 (NaN of any kind for the largest).
+__device__ __forceinline__ float key_value(uint32_t u) {
+    return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
 // V consecutive logits of a row from column c on; -inf past the last expert.
 template <class T, int V>
 __device__ __forceinline__ void load_logits(const char *row, int c, int E, float (&x)[V]) {
@@ -89,8 +94,11 @@ __device__ __forceinline__ void load_logits(const char *row, int c, int E, float
 
 // Probabilities; all zero where every logit is -inf, all NaN with a NaN or inf
 // among them.
+struct Scale {  // p = e^(x - most) inv
+    float most, inv;
+};
 template <int LPR, int V>
-__device__ __forceinline__ void softmax(const float (&x)[V], float (&p)[V]) {
+__device__ __forceinline__ Scale softmax(const float (&x)[V], float (&p)[V]) {
     float m = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
@@ -107,6 +115,7 @@ __device__ __forceinline__ void softmax(const float (&x)[V], float (&p)[V]) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] *= inv;
+    return {m, inv};
 }
 
 // -------------------------------------------------- counts, offsets and loss
@@ -167,7 +176,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     float *part = reinterpret_cast<float *>(mask + a.E);                  // [kSumSlices][E]
     float *slot_p = part + kSumSlices * a.E;                              // [64][k]
     int32_t *slot_e = reinterpret_cast<int32_t *>(slot_p + kRouteTokens * a.k);
-    float *chosen = reinterpret_cast<float *>(slot_e + kRouteTokens * a.k);  // [64]: sum over a token's slots
+    float *chosen = reinterpret_cast<float *>(slot_e + kRouteTokens * a.k);  // [64]: sum over a token's slots, or 1
     int32_t *used = reinterpret_cast<int32_t *>(chosen + kRouteTokens);   // [E]
     int32_t *off = used + a.E;                                            // [E + 1]
     __shared__ int32_t live;
@@ -198,43 +207,38 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
 #pragma unroll
                 for (int v = 0; v < V; ++v) x[v] = -__builtin_inff();
             }
-            softmax<LPR, V>(x, p);
+            const Scale sc = softmax<LPR, V>(x, p);
             uint32_t key[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 acc[v] += p[v];
                 key[v] = order_key(x[v]);
             }
-            float mine = 0.0f;
+            float sum = 0.0f;
             for (int j = 0; j < a.k; ++j) {
                 uint32_t best = key[0];
 #pragma unroll
                 for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];
                 const uint32_t top = group_max<LPR>(best);
+                const float pe = top ? exp_below_one(key_value(top) - sc.most) * sc.inv : 0.0f;  // (NaN: inv is)
+                sum += pe;
                 // of equal logits the lowest index: the first lane that has one, its first
                 const uint64_t owners = __ballot(best == top);
                 if (best == top && !(owners & below)) {
                     int e = -1;
-                    float pe = 0.0f;
                     if (top) {
 #pragma unroll
-                        for (int v = V - 1; v >= 0; --v)
-                            if (key[v] == top) {
-                                e = v;
-                                pe = p[v];
-                            }
+                        for (int v = V - 1; v >= 0; --v) e = key[v] == top ? v : e;
 #pragma unroll
                         for (int v = 0; v < V; ++v) key[v] = v == e ? 0u : key[v];
                         e += col;
                         atomicOr((unsigned long long *)&mask[e], 1ull << row);
-                        mine += pe;
                     }
                     slot_e[row * a.k + j] = e;
                     slot_p[row * a.k + j] = pe;
                 }
             }
-            const float sum = group_sum<LPR>(mine);
-            if (sub == 0) chosen[row] = sum;
+            if (sub == 0) chosen[row] = a.normalize ? sum : 1.0f;
         }
         __syncthreads();
         const int rows = a.T - tc < kRouteTokens ? (int)(a.T - tc) : kRouteTokens;
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
             const int row = i / a.k, e = slot_e[i];
             const int64_t o = tc * a.k + i;
             a.experts[o] = e;
-            a.gates[o] = e < 0 ? 0.0f : (a.normalize ? slot_p[i] / chosen[row] : slot_p[i]);
+            a.gates[o] = e < 0 ? 0.0f : slot_p[i] / chosen[row];
             a.rows[o] = e < 0 ? -1 : used[e] + __popcll(mask[e] & ((1ull << row) - 1));
         }
         if (wave == 0) {
@@ -277,11 +281,16 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
         for (int i = 1; i < kSumSlices; ++i) s += part[i * a.E + e];
         part[e] = s;
         if (a.blocks > 1) {
-            a.psum[(int64_t)blockIdx.x * a.E + e] = s;
-            a.hist[(int64_t)blockIdx.x * a.E + e] = used[e];
+            a.psum[(int64_t)blockIdx.x * a.stride + e] = s;
+            a.hist[(int64_t)blockIdx.x * a.stride + e] = used[e];
         }
     }
     if (a.blocks > 1) {
+        const int e = a.E + tid;  // the rest of the row's last 16 bytes
+        if (e < a.stride) {
+            a.psum[(int64_t)blockIdx.x * a.stride + e] = 0.0f;
+            a.hist[(int64_t)blockIdx.x * a.stride + e] = 0;
+        }
         if (tid == 0) a.live[blockIdx.x] = live;
         return;
     }
@@ -301,76 +310,101 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
 }
 
 // Places among all of an expert's slots: those of the blocks before, from their
-// counts, and of the experts before.  Every block adds up the counts of all (at
-// most 256 x E, from the L2), which costs less than a launch that does it once;
-// the last block writes the totals.
-constexpr int kJoinThreads = 1024;
+// counts, and of the experts before.  Every block adds up the counts of all, at most
+// 256 x E from the L2, four experts to a thread and all its loads in flight at once:
+// that costs less than a launch that does it once.  The last block writes the totals.
+constexpr int kJoinThreads = 1024, kJoinParts = 64;
+struct JoinShape {
+    int quads, parts;  // 16 bytes of a row; ranges of the rows
+    __host__ __device__ explicit JoinShape(int stride)
+        : quads(stride / 4), parts(kJoinThreads / (stride / 4) < kJoinParts ? kJoinThreads / (stride / 4) : kJoinParts) {}
+};
+inline size_t join_lds(int E, int stride) { return ((size_t)2 * JoinShape(stride).parts * stride + 3 * (size_t)E + 1) * 4; }
+
+// This thread's part of the rows' column sums: of all rows, and of those of the
+// blocks before b.
+template <class V>
+__device__ __forceinline__ void column_sums(const RouteArgs &a, const JoinShape &j, const V *rows, int b, V (&s)[4], V (&t)[4]) {
+    const int q = threadIdx.x % j.quads, part = threadIdx.x / j.quads;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[c] = t[c] = V(0);
+    if (part >= j.parts) return;
+#pragma unroll 8
+    for (int i = part; i < a.blocks; i += j.parts) {
+        V v[4];
+        __builtin_memcpy(v, __builtin_assume_aligned(rows + (int64_t)i * a.stride + q * 4, 16), 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s[c] += v[c];
+            t[c] += i < b ? v[c] : V(0);
+        }
+    }
+}
+template <class V>
+__device__ __forceinline__ void put_sums(const RouteArgs &a, const JoinShape &j, V *to, const V (&s)[4]) {
+    const int q = threadIdx.x % j.quads, part = threadIdx.x / j.quads;
+    if (part < j.parts) __builtin_memcpy(__builtin_assume_aligned(to + part * a.stride + q * 4, 16), s, 16);
+}
+// Column e of what put_sums left, the parts in order.
+template <class V>
+__device__ __forceinline__ V total_of(const RouteArgs &a, const JoinShape &j, const V *from, int e) {
+    V s = V(0);
+#pragma unroll 8
+    for (int i = 0; i < j.parts; ++i) s += from[i * a.stride + e];
+    return s;
+}
+
 __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(RouteArgs a) {
     extern __shared__ uint64_t lds[];
-    int32_t *total = reinterpret_cast<int32_t *>(lds);  // [E]
-    int32_t *base = total + a.E;                        // [E]
-    int32_t *off = base + a.E;                          // [E + 1]
-    int32_t *sum = off + a.E + 1;                       // [1024] and [1024]
+    const JoinShape j(a.stride);
+    int32_t *all = reinterpret_cast<int32_t *>(lds), *before = all + j.parts * a.stride;  // [parts][stride]
+    int32_t *total = before + j.parts * a.stride, *base = total + a.E, *off = base + a.E;  // [E], [E], [E + 1]
     const int tid = threadIdx.x, b = blockIdx.x;
     const bool totals = b == a.blocks;
-    const int per = a.E < kJoinThreads ? a.E : kJoinThreads, parts = kJoinThreads / per;
-    const int e0 = tid % per, part = tid / per;
-    for (int e = e0; e < a.E; e += per) {  // (E <= 1024: once)
-        int all = 0, before = 0;
-        if (part < parts)
-#pragma unroll 8
-            for (int i = part; i < a.blocks; i += parts) {
-                const int h = a.hist[(int64_t)i * a.E + e];
-                all += h;
-                before += i < b ? h : 0;
-            }
-        sum[tid] = all;
-        sum[kJoinThreads + tid] = before;
+    // the block's first slots, requested ahead; the last block's other inputs likewise
+    const int64_t from = (int64_t)b * a.chunks * kRouteTokens * a.k, every = (int64_t)a.T * a.k;
+    const int64_t to = from + (int64_t)a.chunks * kRouteTokens * a.k < every ? from + (int64_t)a.chunks * kRouteTokens * a.k : every;
+    int e0 = -1, r0 = 0;
+    if (from + tid < to) {
+        e0 = a.experts[from + tid];
+        r0 = a.rows[from + tid];
     }
-    __syncthreads();
-    for (int e = tid; e < a.E; e += kJoinThreads) {
-        int all = 0, before = 0;
-        for (int i = 0; i < parts; ++i) {
-            all += sum[i * per + e];
-            before += sum[kJoinThreads + i * per + e];
-        }
-        total[e] = all;
-        base[e] = before;
-    }
-    __syncthreads();
-    if (tid < 64) scan_counts(total, off, a.E);
+    float ps[4], none[4];
+    int live = 0;
     if (totals) {
-        __syncthreads();
-        float *p = reinterpret_cast<float *>(sum);
-        float s = 0.0f;
-        if (part < parts)
-#pragma unroll 8
-            for (int i = part; i < a.blocks; i += parts) s += a.psum[(int64_t)i * a.E + e0];
-        p[tid] = s;
-        __syncthreads();
-        float *q = reinterpret_cast<float *>(base);
-        for (int e = tid; e < a.E; e += kJoinThreads) {
-            float v = 0.0f;
-            for (int i = 0; i < parts; ++i) v += p[i * per + e];
-            q[e] = v;
-        }
-        __syncthreads();
-        if (tid >= 64) return;
-        int live = 0;
-        for (int i = tid; i < a.blocks; i += 64) live += a.live[i];
-#pragma unroll
-        for (int d = 32; d; d >>= 1) live += __shfl_xor(live, d);
-        write_totals(a, total, off, q, live);
-        return;
+        column_sums<float>(a, j, a.psum, 0, ps, none);
+        if (tid < 64)
+            for (int i = tid; i < a.blocks; i += 64) live += a.live[i];
     }
+    int32_t s[4], t[4];
+    column_sums<int32_t>(a, j, a.hist, b, s, t);
+    put_sums(a, j, all, s);
+    if (totals) put_sums(a, j, reinterpret_cast<float *>(before), ps);  // (it has no use for the others)
+    else put_sums(a, j, before, t);
     __syncthreads();
-    for (int e = tid; e < a.E; e += kJoinThreads) base[e] += off[e];
+    // one thread to a column, the counts' and the others' columns by different waves
+    for (int e = tid; e < a.E; e += kJoinThreads / 2)
+        if (tid < kJoinThreads / 2) total[e] = total_of(a, j, all, e);
+    for (int e = tid - kJoinThreads / 2; e < a.E; e += kJoinThreads / 2)
+        if (tid >= kJoinThreads / 2) {
+            if (totals) reinterpret_cast<float *>(base)[e] = total_of(a, j, reinterpret_cast<const float *>(before), e);
+            else base[e] = total_of(a, j, before, e);
+        }
     __syncthreads();
-    const int64_t from = (int64_t)b * a.chunks * kRouteTokens * a.k, all = (int64_t)a.T * a.k;
-    const int64_t to = from + (int64_t)a.chunks * kRouteTokens * a.k < all ? from + (int64_t)a.chunks * kRouteTokens * a.k : all;
-    for (int64_t o = from + tid; o < to; o += kJoinThreads) {
+    if (tid < 64) {
+        scan_counts(total, off, a.E);
+        if (totals) {
+#pragma unroll
+            for (int d = 32; d; d >>= 1) live += __shfl_xor(live, d);
+            write_totals(a, total, off, reinterpret_cast<const float *>(base), live);
+        }
+    }
+    if (totals) return;
+    __syncthreads();
+    if (e0 >= 0) a.rows[from + tid] = r0 + base[e0] + off[e0];
+    for (int64_t o = from + tid + kJoinThreads; o < to; o += kJoinThreads) {
         const int e = a.experts[o];
-        if (e >= 0) a.rows[o] += base[e];
+        if (e >= 0) a.rows[o] += base[e] + off[e];
     }
 }
 
@@ -471,7 +505,7 @@ hipError_t route(const RouteArgs &a, hipStream_t s) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || a.blocks == 1) return e;
         hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)a.blocks + 1), dim3(kJoinThreads),
-                           (size_t)(3 * a.E + 1 + 2 * kJoinThreads) * 4, s, a);
+                           join_lds(a.E, a.stride), s, a);
         return hipGetLastError();
     });
 }

@@ -370,6 +370,26 @@ double number(PyObject *o) {
     return v;
 }
 
+// Several outputs in one allocation, each from a multiple of 256 bytes on: a call to
+// the allocator costs as much as a quarter of a launch.
+struct Pool {
+    Tensor t;
+    int64_t used = 0, size = 0;
+    static int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
+    Pool(const Tensor &x, std::initializer_list<int64_t> bytes) {
+        for (int64_t n : bytes) size += up(n);
+        t = at::empty({size}, x.options().dtype(at::kByte));
+    }
+    Tensor take(at::IntArrayRef shape, at::ScalarType type) {
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), c10::scalarTypeToTypeMeta(type));
+        const int64_t es = (int64_t)c10::elementSize(type);
+        impl->set_storage_offset((t.storage_offset() + used) / es);
+        impl->set_sizes_contiguous(shape);
+        used += up(impl->numel() * es);
+        return Tensor(std::move(impl));
+    }
+};
+
 // An int32 matrix [T][k] of a token's slots.
 const Tensor &slots(PyObject *o, const Tensor &x, const char *name) {
     const Tensor &t = tensor(o, name);
@@ -395,15 +415,16 @@ PyObject *route(PyObject *const *a) {
         refuse(PyExc_ValueError, "%lld of %lld experts to a token (1 to %d of at most %d)", (long long)k, (long long)E,
                CP_OPS_MAX_CHOSEN, CP_OPS_MAX_ROUTED);
     const c10::DeviceGuard guard(x.device());
-    const auto i32 = x.options().dtype(at::kInt), f32 = x.options().dtype(at::kFloat);
-    const Tensor experts = at::empty({T, k}, i32), gates = at::empty({T, k}, f32), places = at::empty({T, k}, i32);
-    const Tensor counts = at::empty({E}, i32), offsets = at::empty({E + 1}, i32), loss = at::empty({}, f32);
-    const Tensor slopes = at::empty({E}, f32);
-    const Scratch ws(x, CP_OP_ROUTE, T, 0, E, 0, true);
+    const int64_t ws = cp_ops_workspace(CP_OP_ROUTE, code(x), T, 0, E, 0, 1);
+    check(ws, "cp_ops_workspace");
+    Pool pool(x, {T * k * 4, T * k * 4, T * k * 4, E * 4, (E + 1) * 4, 4, E * 4, ws});
+    const Tensor experts = pool.take({T, k}, at::kInt), gates = pool.take({T, k}, at::kFloat);
+    const Tensor places = pool.take({T, k}, at::kInt), counts = pool.take({E}, at::kInt);
+    const Tensor offsets = pool.take({E + 1}, at::kInt), loss = pool.take({}, at::kFloat), slopes = pool.take({E}, at::kFloat);
     check(cp_route(code(x), T, (int32_t)E, (int32_t)k, normalize, x.data_ptr(), ld, (const uint8_t *)valid,
                    (int32_t *)experts.data_ptr(), (float *)gates.data_ptr(), (int32_t *)places.data_ptr(),
                    (int32_t *)counts.data_ptr(), (int32_t *)offsets.data_ptr(), (float *)loss.data_ptr(),
-                   (float *)slopes.data_ptr(), data(ws.t), ws.n, stream(x)),
+                   (float *)slopes.data_ptr(), ws ? (char *)pool.t.data_ptr() + pool.used : nullptr, ws, stream(x)),
           "cp_route");
     return wrap_tuple(experts, gates, places, counts, offsets, loss, slopes);
 }
