@@ -64,15 +64,16 @@ __device__ __forceinline__ float exp_below_one(float d) {
     return fmaf(y * 0.693147180559945309f, r, y);
 }
 
-// A value's place in the order of choice: larger comes first, NaN before all,
-// -inf and what is no expert: 0, never chosen.
-__device__ __forceinline__ uint32_t order_key(float x) {
+// A value's place in the order of choice: larger comes first, NaN of either sign
+// before all.  -inf, and what is no expert, has kNoKey: it is never chosen.
+constexpr uint32_t kNoKey = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t order_key(float x) {  // (not for NaN)
     x += 0.0f;  // -0 to 0: they tie
-    const uint32_t b = __builtin_bit_cast(uint32_t, x), u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return x != x ? 0xFFFFFFFFu : (x == -__builtin_inff() ? 0u : u);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-// The logit of a key above 0 (NaN of any kind for the largest).
+// The logit of a key (NaN for the largest).
 __device__ __forceinline__ float key_value(uint32_t u) {
     return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
@@ -92,6 +93,10 @@ __device__ __forceinline__ void load_logits(const char *row, int c, int E, float
     }
 }
 
+// e^d for the sums: d log2(e) is rounded once more than above, which is |d| ulp of
+// terms that count less the larger |d| is.
+__device__ __forceinline__ float exp_term(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896340736f); }
+
 // Probabilities; all zero where every logit is -inf, all NaN with a NaN or inf
 // among them.
 struct Scale {  // p = e^(x - most) inv
@@ -107,8 +112,7 @@ __device__ __forceinline__ Scale softmax(const float (&x)[V], float (&p)[V]) {
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        p[v] = exp_below_one(x[v] - m);
-        p[v] = x[v] == -__builtin_inff() ? 0.0f * p[v] : p[v];
+        p[v] = exp_term(x[v] - m);
         sum += p[v];
     }
     sum = group_sum<LPR>(sum);
@@ -157,7 +161,8 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, const int32_t *
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kSumSlices = 4;  // waves that add their sums to LDS at a time
+// Waves that add their sums to LDS at a time: all, unless the experts are many.
+__host__ __device__ constexpr int sum_slices(int E) { return E <= 256 ? 16 : 4; }
 
 template <int LPR>
 constexpr int kRouteThreads = 64 * LPR < 1024 ? 64 * LPR : 1024;
@@ -165,7 +170,7 @@ constexpr int kRouteThreads = 64 * LPR < 1024 ? 64 * LPR : 1024;
 // LDS: a word per expert, its slots so far, offsets, sums of probabilities; then
 // a chunk's slots.
 inline size_t route_lds(int E, int k) {
-    return (size_t)E * 8 + (size_t)(2 * E + 1) * 4 + (size_t)kSumSlices * E * 4 + (size_t)kRouteTokens * (8 * k + 4) + 16;
+    return (size_t)E * 8 + (size_t)(2 * E + 1) * 4 + (size_t)sum_slices(E) * E * 4 + (size_t)kRouteTokens * (8 * k + 8) + 16;
 }
 
 template <class T, int LPR, int V>
@@ -173,11 +178,12 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     constexpr int NT = kRouteThreads<LPR>, RPW = 64 / LPR, PASSES = kRouteTokens * LPR / NT, W = NT / 64;
     extern __shared__ uint64_t lds[];
     uint64_t *mask = lds;
-    float *part = reinterpret_cast<float *>(mask + a.E);                  // [kSumSlices][E]
-    float *slot_p = part + kSumSlices * a.E;                              // [64][k]
+    const int slices = sum_slices(a.E);
+    float *part = reinterpret_cast<float *>(mask + a.E);                     // [slices][E]
+    float *slot_p = part + slices * a.E;                                     // [64][k]: the logit's key, then p
     int32_t *slot_e = reinterpret_cast<int32_t *>(slot_p + kRouteTokens * a.k);
-    float *chosen = reinterpret_cast<float *>(slot_e + kRouteTokens * a.k);  // [64]: sum over a token's slots, or 1
-    int32_t *used = reinterpret_cast<int32_t *>(chosen + kRouteTokens);   // [E]
+    Scale *scale = reinterpret_cast<Scale *>(slot_e + kRouteTokens * a.k);   // [64]
+    int32_t *used = reinterpret_cast<int32_t *>(scale + kRouteTokens);       // [E]
     int32_t *off = used + a.E;                                            // [E + 1]
     __shared__ int32_t live;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane % LPR, col = sub * V;
@@ -214,39 +220,54 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
                 acc[v] += p[v];
                 key[v] = order_key(x[v]);
             }
-            float sum = 0.0f;
+            if (__any(sc.inv != sc.inv))  // NaN (or inf) among them
+#pragma unroll
+                for (int v = 0; v < V; ++v) key[v] = x[v] != x[v] ? 0xFFFFFFFFu : key[v];
+            if (sub == 0) scale[row] = sc;
             for (int j = 0; j < a.k; ++j) {
                 uint32_t best = key[0];
 #pragma unroll
                 for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];
                 const uint32_t top = group_max<LPR>(best);
-                const float pe = top ? exp_below_one(key_value(top) - sc.most) * sc.inv : 0.0f;  // (NaN: inv is)
-                sum += pe;
                 // of equal logits the lowest index: the first lane that has one, its first
                 const uint64_t owners = __ballot(best == top);
                 if (best == top && !(owners & below)) {
                     int e = -1;
-                    if (top) {
+                    if (top > kNoKey) {
+                        bool seen = false;
 #pragma unroll
-                        for (int v = V - 1; v >= 0; --v) e = key[v] == top ? v : e;
-#pragma unroll
-                        for (int v = 0; v < V; ++v) key[v] = v == e ? 0u : key[v];
+                        for (int v = 0; v < V; ++v) {
+                            const bool hit = key[v] == top && !seen;
+                            seen |= hit;
+                            e = hit ? v : e;
+                            key[v] = hit ? 0u : key[v];
+                        }
                         e += col;
                         atomicOr((unsigned long long *)&mask[e], 1ull << row);
                     }
                     slot_e[row * a.k + j] = e;
-                    slot_p[row * a.k + j] = pe;
+                    slot_p[row * a.k + j] = __builtin_bit_cast(float, top);
                 }
             }
-            if (sub == 0) chosen[row] = a.normalize ? sum : 1.0f;
         }
         __syncthreads();
         const int rows = a.T - tc < kRouteTokens ? (int)(a.T - tc) : kRouteTokens;
         for (int i = tid; i < rows * a.k; i += NT) {
+            const Scale sc = scale[i / a.k];
+            const float x = key_value(__builtin_bit_cast(uint32_t, slot_p[i]));
+            slot_p[i] = slot_e[i] < 0 ? 0.0f : exp_below_one(x - sc.most) * sc.inv;  // (with NaN, inv is)
+        }
+        __syncthreads();
+        for (int i = tid; i < rows * a.k; i += NT) {
             const int row = i / a.k, e = slot_e[i];
             const int64_t o = tc * a.k + i;
+            float sum = 1.0f;
+            if (a.normalize) {
+                sum = 0.0f;
+                for (int j = 0; j < a.k; ++j) sum += slot_p[row * a.k + j];
+            }
             a.experts[o] = e;
-            a.gates[o] = e < 0 ? 0.0f : slot_p[i] / chosen[row];
+            a.gates[o] = e < 0 ? 0.0f : slot_p[i] / sum;
             a.rows[o] = e < 0 ? -1 : used[e] + __popcll(mask[e] & ((1ull << row) - 1));
         }
         if (wave == 0) {
@@ -265,8 +286,8 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int d = LPR; d < 64; d *= 2) acc[v] += __shfl_xor(acc[v], d);
-    for (int w0 = 0; w0 < W; w0 += kSumSlices) {
-        if (wave >= w0 && wave < w0 + kSumSlices && lane < LPR)
+    for (int w0 = 0; w0 < W; w0 += slices) {
+        if (wave >= w0 && wave < w0 + slices && lane < LPR)
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (col + v < a.E) {
@@ -277,8 +298,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     }
     for (int e = tid; e < a.E; e += NT) {
         float s = part[e];
-#pragma unroll
-        for (int i = 1; i < kSumSlices; ++i) s += part[i * a.E + e];
+        for (int i = 1; i < (W < slices ? W : slices); ++i) s += part[i * a.E + e];
         part[e] = s;
         if (a.blocks > 1) {
             a.psum[(int64_t)blockIdx.x * a.stride + e] = s;
@@ -416,14 +436,19 @@ __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(RouteArgs a) {
 //   gates p_e / P, P the sum over the chosen:  dx = p (c - sum p c) + g (d - sum g d)
 // The probabilities are computed again from the logits, in registers: cheaper
 // than to store and read them.
+// The gates' gradients go to the lanes of their experts by way of LDS: compared with
+// every logit's index in registers instead, they took most of the time.
 template <class T, int LPR, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a) {
     constexpr int RPW = 64 / LPR;
+    constexpr uint32_t kNone = 0xFFFFFFFFu;  // no slot's: a NaN that no gradient is made of
+    __shared__ __attribute__((aligned(16))) uint32_t spread[4][RPW][LPR * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPR, col = sub * V;
     const float dloss = a.dloss ? *a.dloss : 0.0f;
     float c[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = a.dloss && col + v < a.E ? dloss * a.slopes[col + v] : 0.0f;
+    uint32_t *row_d = spread[wave][lane / LPR];
     const int64_t step = (int64_t)gridDim.x * 4 * RPW;
     for (int64_t t = ((int64_t)blockIdx.x * 4 + wave) * RPW + lane / LPR; t - lane / LPR < a.T; t += step) {
         const bool in = t < a.T;
@@ -436,19 +461,28 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] = -__builtin_inff();
         }
+        uint32_t u[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) d[v] = s[v] = 0.0f;
-        if (has && a.dgates)
-            for (int j = 0; j < a.k; ++j) {
-                const int e = ex[j] - col;
-                const float g = a.dgates[t * a.k + j];
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (e == v) {
-                        d[v] += g;
-                        s[v] = 1.0f;
-                    }
+        for (int v = 0; v < V; ++v) u[v] = kNone;
+        if (a.dgates) {  // (a wave's own part of LDS: its accesses are in order)
+            __builtin_memcpy(__builtin_assume_aligned(row_d + col, 16), u, sizeof u);
+            __builtin_amdgcn_wave_barrier();
+            for (int j = sub; j < a.k; j += LPR) {
+                const int e = ex[j];
+                if (has && e >= 0 && e < a.E) {
+                    const float g = a.dgates[t * a.k + j];
+                    row_d[e] = g != g ? 0x7FC00000u : __builtin_bit_cast(uint32_t, g);
+                }
             }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_memcpy(u, __builtin_assume_aligned(row_d + col, 16), sizeof u);
+            __builtin_amdgcn_wave_barrier();
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            s[v] = u[v] == kNone ? 0.0f : 1.0f;
+            d[v] = u[v] == kNone ? 0.0f : __builtin_bit_cast(float, u[v]);
+        }
         softmax<LPR, V>(x, p);
         float pc = 0.0f, pd = 0.0f, ps = 0.0f;
 #pragma unroll
