@@ -13,15 +13,16 @@ namespace {
 
 constexpr int kClipThreads = 256;
 
-// The tensor that holds chunk c (uniform): the last that begins at or before it.
-__device__ __forceinline__ int find_tensor(const ClipArgs &a, int64_t c) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.t[mid].before <= c) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+// The tensor that holds chunk c (uniform): the last that begins at or before it.  The
+// arguments lie in the host's memory, so all are looked at at once: a search, step
+// after step, waits for it each time.
+template <class Args>
+__device__ __forceinline__ int find_tensor(const Args &a, int64_t c) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int base = 0; base < a.n; base += 64)
+        n += __popcll(__ballot(base + lane < a.n && a.t[base + lane < a.n ? base + lane : 0].before <= c));
+    return n - 1;
 }
 __device__ __forceinline__ bool bit(const uint32_t *w, int i) { return w[i >> 5] >> (i & 31) & 1; }
 
@@ -103,26 +104,37 @@ __device__ __forceinline__ void scale_to(const char *x, char *y, int64_t n, floa
     }
 }
 
-template <int NT>
-__device__ __forceinline__ void square_chunk(const ClipArgs &a, int64_t c, double (&acc)[4]) {
+// Where a block's chunk lies.
+struct Piece {
+    const char *x;
+    char *y;
+    int64_t n;
+    bool bf16_in, bf16_out;
+};
+template <class Args>
+__device__ __forceinline__ Piece piece_of(const Args &a, int64_t c) {
     const int i = find_tensor(a, c);
-    const int64_t from = (c - a.t[i].before) * a.chunk, n = a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk;
-    if (bit(a.bf16_in, i)) add_squares<__bf16, NT>(a.t[i].x + from * 2, n, acc);
-    else add_squares<float, NT>(a.t[i].x + from * 4, n, acc);
+    const int64_t from = (c - a.t[i].before) * a.chunk;
+    const bool bi = bit(a.bf16_in, i), bo = bit(a.bf16_out, i);
+    return {a.t[i].x + from * (bi ? 2 : 4), a.t[i].y + from * (bo ? 2 : 4), a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk, bi,
+            bo};
 }
 
-template <int NT>
-__device__ __forceinline__ void scale_chunk(const ClipArgs &a, int64_t c, float f) {
-    const int i = find_tensor(a, c);
-    if (f == 1.0f && a.t[i].y == a.t[i].x) return;  // in place, nothing to do
-    const int64_t from = (c - a.t[i].before) * a.chunk, n = a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk;
-    const bool bi = bit(a.bf16_in, i), bo = bit(a.bf16_out, i);
-    const char *x = a.t[i].x + from * (bi ? 2 : 4);
-    char *y = a.t[i].y + from * (bo ? 2 : 4);
-    if (bi && bo) scale_to<__bf16, __bf16, NT>(x, y, n, f);
-    else if (bi) scale_to<__bf16, float, NT>(x, y, n, f);
-    else if (bo) scale_to<float, __bf16, NT>(x, y, n, f);
-    else scale_to<float, float, NT>(x, y, n, f);
+template <int NT, class Args>
+__device__ __forceinline__ void square_chunk(const Args &a, int64_t c, double (&acc)[4]) {
+    const Piece p = piece_of(a, c);
+    if (p.bf16_in) add_squares<__bf16, NT>(p.x, p.n, acc);
+    else add_squares<float, NT>(p.x, p.n, acc);
+}
+
+template <int NT, class Args>
+__device__ __forceinline__ void scale_chunk(const Args &a, int64_t c, float f) {
+    const Piece p = piece_of(a, c);
+    if (f == 1.0f && p.y == p.x) return;  // in place, nothing to do
+    if (p.bf16_in && p.bf16_out) scale_to<__bf16, __bf16, NT>(p.x, p.y, p.n, f);
+    else if (p.bf16_in) scale_to<__bf16, float, NT>(p.x, p.y, p.n, f);
+    else if (p.bf16_out) scale_to<float, __bf16, NT>(p.x, p.y, p.n, f);
+    else scale_to<float, float, NT>(p.x, p.y, p.n, f);
 }
 
 __device__ __forceinline__ float clip_factor(float norm, float most) {
@@ -130,7 +142,8 @@ __device__ __forceinline__ float clip_factor(float norm, float most) {
     return f > 1.0f || most == __builtin_inff() ? 1.0f : f;  // (a norm of NaN gives NaN)
 }
 
-__global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs a) {
+template <int N>
+__global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs<N> a) {
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) square_chunk<kClipThreads>(a, c, acc);
     const double s = block_sum<kClipThreads>((acc[0] + acc[1]) + (acc[2] + acc[3]));
@@ -139,19 +152,75 @@ __global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs a)
 
 // The partial sums, at most a few KB, are added up by every block, which spares a
 // launch in between; the chunks go last to first, as the last read are the ones
-// that the caches still hold.
-__global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs a) {
+// that the caches still hold.  A block of one small chunk requests its elements before
+// the partial sums, whose wait is as long.
+template <int N>
+__global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
+    const int64_t c0 = a.chunks - 1 - blockIdx.x;
+    const bool single = a.t[0].y && a.chunk == kClipThreads * 8 && c0 < gridDim.x;  // (uniform)
+    const int64_t at = (int64_t)threadIdx.x * 8;
+    Piece p{};
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    bool whole = false;
+    if (single) {
+        p = piece_of(a, c0);
+        whole = at + 8 <= p.n;
+        if (whole) {  // (bf16: the same 16 bytes twice)
+            const char *x = p.x + at * (p.bf16_in ? 2 : 4);
+            __builtin_memcpy(&v0, x, 16);
+            __builtin_memcpy(&v1, x + (p.bf16_in ? 0 : 16), 16);
+        }
+    }
     double s = 0.0;
-    for (int i = threadIdx.x; i < a.nall; i += kClipThreads) s += a.all[i];
+    for (int i = threadIdx.x; i < a.nall; i += 8 * kClipThreads) {
+        double t[8];  // requested together
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = a.all[i + u * kClipThreads < a.nall ? i + u * kClipThreads : i];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += i + u * kClipThreads < a.nall ? t[u] : 0.0;
+    }
     const float norm = (float)sqrt(block_sum<kClipThreads>(s));
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
     const float f = clip_factor(norm, a.max_norm);
-    if (a.t[0].y)  // (all have an output, or none)
-        for (int64_t c = a.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) scale_chunk<kClipThreads>(a, c, f);
+    if (!a.t[0].y) return;  // (all have an output, or none)
+    if (!single) {
+        for (int64_t c = c0; c >= 0; c -= gridDim.x) scale_chunk<kClipThreads>(a, c, f);
+        return;
+    }
+    if (f == 1.0f && p.x == p.y) return;
+    float e[8];
+    if (whole) {
+        if (p.bf16_in) {
+            __bf16 h[8];
+            __builtin_memcpy(h, &v0, 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = to_f32(h[j]) * f;
+        } else {
+            __builtin_memcpy(e, &v0, 16);
+            __builtin_memcpy(e + 4, &v1, 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] *= f;
+        }
+        if (p.bf16_out) {
+            __bf16 h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = from_f32<__bf16>(e[j]);
+            __builtin_memcpy(p.y + at * 2, h, 16);
+        } else {
+            __builtin_memcpy(p.y + at * 4, e, 32);
+        }
+        return;
+    }
+    for (int64_t i = at; i < p.n; ++i) {
+        const float x = p.bf16_in ? to_f32(reinterpret_cast<const __bf16 *>(p.x)[i]) : reinterpret_cast<const float *>(p.x)[i];
+        if (p.bf16_out) reinterpret_cast<__bf16 *>(p.y)[i] = from_f32<__bf16>(x * f);
+        else reinterpret_cast<float *>(p.y)[i] = x * f;
+    }
 }
 
 constexpr int kClipOneThreads = 1024;
-__global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs a) {
+template <int N>
+__global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs<N> a) {
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int64_t c = 0; c < a.chunks; ++c) square_chunk<kClipOneThreads>(a, c, acc);
     const float norm = (float)sqrt(block_sum<kClipOneThreads>((acc[0] + acc[1]) + (acc[2] + acc[3])));
@@ -163,17 +232,26 @@ __global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs a) {
 
 }  // namespace
 
-hipError_t launch_norm_partials(const ClipArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(norm_partials_kernel, dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
+template <int N>
+hipError_t launch_norm_partials(const ClipArgs<N> &a, hipStream_t s) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_partials_kernel<N>), dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
     return hipGetLastError();
 }
-hipError_t launch_clip(const ClipArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(clip_kernel, dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
+template <int N>
+hipError_t launch_clip(const ClipArgs<N> &a, hipStream_t s) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(clip_kernel<N>), dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
     return hipGetLastError();
 }
-hipError_t launch_clip_one(const ClipArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(clip_one_kernel, dim3(1), dim3(kClipOneThreads), 0, s, a);
+template <int N>
+hipError_t launch_clip_one(const ClipArgs<N> &a, hipStream_t s) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(clip_one_kernel<N>), dim3(1), dim3(kClipOneThreads), 0, s, a);
     return hipGetLastError();
 }
+#define CP_CLIP(n)                                                            \
+    template hipError_t launch_norm_partials<n>(const ClipArgs<n> &, hipStream_t); \
+    template hipError_t launch_clip<n>(const ClipArgs<n> &, hipStream_t);     \
+    template hipError_t launch_clip_one<n>(const ClipArgs<n> &, hipStream_t);
+CP_CLIP(kClipFew)
+CP_CLIP(kClipTensors)
 
 }  // namespace cpo

@@ -170,6 +170,54 @@ int check_clip_memory(int64_t n, const int32_t *dtypes, const void *const *grads
     return CP_OK;
 }
 
+// The launches for `total` elements in `used` tensors that are not empty, up to N to
+// a launch.
+template <int N>
+int launch_clips(int64_t n, int64_t total, int64_t used, const int32_t *dtypes, const void *const *grads, const int64_t *numels,
+                 float max_norm, const int32_t *out_dtypes, void *const *outs, float *norm, double *partial, hipStream_t s) {
+    const int chunk = clip_chunk(total);
+    auto fill = [&](int64_t *i) {  // from tensor *i on
+        ClipArgs<N> a{};
+        a.max_norm = max_norm;
+        a.chunk = chunk;
+        for (; *i < n && a.n < N; ++*i) {
+            if (!numels[*i]) continue;
+            a.t[a.n] = {(const char *)grads[*i], outs ? (char *)outs[*i] : nullptr, numels[*i], a.chunks};
+            if (dtypes[*i] == CP_BF16) a.bf16_in[a.n >> 5] |= 1u << (a.n & 31);
+            if (outs && out_dtypes[*i] == CP_BF16) a.bf16_out[a.n >> 5] |= 1u << (a.n & 31);
+            a.chunks += ceil_div(numels[*i], chunk);
+            ++a.n;
+        }
+        a.blocks = (int)std::min<int64_t>(a.chunks, kClipBlocks);
+        return a;
+    };
+    int64_t i = 0;
+    if (total <= kClipOneBlock && used <= N) {
+        ClipArgs<N> a = fill(&i);
+        a.norm = norm;
+        return launched(launch_clip_one(a, s), "gradient norm");
+    }
+    int nall = 0;
+    while (i < n) {
+        ClipArgs<N> a = fill(&i);
+        if (!a.n) break;
+        a.partial = partial + nall;
+        nall += a.blocks;
+        CP_TRY(launched(launch_norm_partials(a, s), "gradient norm"));
+    }
+    bool first = true;
+    for (i = 0; i < n && (outs || first); first = false) {
+        ClipArgs<N> a = fill(&i);
+        if (!a.n) break;
+        a.all = partial;
+        a.nall = nall;
+        a.norm = first ? norm : nullptr;
+        a.blocks = outs ? (int)std::min<int64_t>(a.chunks, 2 * kClipBlocks) : 1;
+        CP_TRY(launched(launch_clip(a, s), "gradient clipping"));
+    }
+    return CP_OK;
+}
+
 int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64_t *numels, float max_norm,
          const int32_t *out_dtypes, void *const *outs, float *norm, void *ws, int64_t ws_bytes, hipStream_t s) {
     if (n < 0 || n > kMaxRows) return fail(CP_ERR_SHAPE, "%lld tensors", (long long)n);
@@ -192,51 +240,8 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
     }
     CP_TRY(check_ws(ws, ws_bytes, clip_ws(n)));
     if (outs) CP_TRY(check_clip_memory(n, dtypes, grads, numels, out_dtypes, outs));
-
-    const int chunk = clip_chunk(total);
-    // The launches' arguments, kClipTensors tensors that are not empty at a time,
-    // from tensor *i on.
-    auto fill = [&](int64_t *i) {
-        ClipArgs a{};
-        a.max_norm = max_norm;
-        a.chunk = chunk;
-        for (; *i < n && a.n < kClipTensors; ++*i) {
-            if (!numels[*i]) continue;
-            a.t[a.n] = {(const char *)grads[*i], outs ? (char *)outs[*i] : nullptr, numels[*i], a.chunks};
-            if (dtypes[*i] == CP_BF16) a.bf16_in[a.n >> 5] |= 1u << (a.n & 31);
-            if (outs && out_dtypes[*i] == CP_BF16) a.bf16_out[a.n >> 5] |= 1u << (a.n & 31);
-            a.chunks += ceil_div(numels[*i], chunk);
-            ++a.n;
-        }
-        a.blocks = (int)std::min<int64_t>(a.chunks, kClipBlocks);
-        return a;
-    };
-    int64_t i = 0;
-    if (total <= kClipOneBlock && used <= kClipTensors) {
-        ClipArgs a = fill(&i);
-        a.norm = norm;
-        return launched(launch_clip_one(a, s), "gradient norm");
-    }
-    double *partial = (double *)ws;
-    int nall = 0;
-    while (i < n) {
-        ClipArgs a = fill(&i);
-        if (!a.n) break;
-        a.partial = partial + nall;
-        nall += a.blocks;
-        CP_TRY(launched(launch_norm_partials(a, s), "gradient norm"));
-    }
-    bool first = true;
-    for (i = 0; i < n && (outs || first); first = false) {
-        ClipArgs a = fill(&i);
-        if (!a.n) break;
-        a.all = partial;
-        a.nall = nall;
-        a.norm = first ? norm : nullptr;
-        a.blocks = outs ? (int)std::min<int64_t>(a.chunks, 2 * kClipBlocks) : 1;
-        CP_TRY(launched(launch_clip(a, s), "gradient clipping"));
-    }
-    return CP_OK;
+    return (used <= kClipFew ? launch_clips<kClipFew> : launch_clips<kClipTensors>)(n, total, used, dtypes, grads, numels, max_norm,
+                                                                                    out_dtypes, outs, norm, (double *)ws, s);
 }
 
 }  // namespace

@@ -193,18 +193,21 @@ hipError_t launch_int4_quantize(int dtype, const Int4QuantArgs &a, hipStream_t s
 
 // ------------------------------------------------------ gradient norm, clipping
 
-constexpr int kClipTensors = 96;    // of a launch: its arguments hold their addresses
+constexpr int kClipTensors = 96;    // of a launch, at most: its arguments hold their addresses
+constexpr int kClipFew = 8;         // of a launch with shorter arguments
 constexpr int kClipBlocks = 1024;   // partial sums of a launch, at most
 constexpr int64_t kClipOneBlock = 1 << 16;  // elements that one block takes on its own
 
+struct ClipTensor {
+    const char *x;
+    char *y;               // output, or null
+    int64_t n;
+    int64_t before;        // chunks of the tensors before it in this launch
+};
+template <int N>
 struct ClipArgs {
-    struct One {
-        const char *x;
-        char *y;           // output, or null
-        int64_t n;
-        int64_t before;    // chunks of the tensors before it in this launch
-    } t[kClipTensors];
-    uint32_t bf16_in[(kClipTensors + 31) / 32], bf16_out[(kClipTensors + 31) / 32];
+    ClipTensor t[N];
+    uint32_t bf16_in[(N + 31) / 32], bf16_out[(N + 31) / 32];
     int32_t n, blocks;
     int32_t chunk;         // elements of a chunk
     int64_t chunks;
@@ -223,8 +226,12 @@ inline int32_t clip_chunk(int64_t total) {
 inline int64_t clip_ws(int64_t tensors) {  // partial sums of every launch
     return (tensors + kClipTensors - 1) / kClipTensors * kClipBlocks * (int64_t)sizeof(double);
 }
-hipError_t launch_norm_partials(const ClipArgs &a, hipStream_t s);
-hipError_t launch_clip(const ClipArgs &a, hipStream_t s);
-hipError_t launch_clip_one(const ClipArgs &a, hipStream_t s);
+// (N: kClipTensors or kClipFew)
+template <int N>
+hipError_t launch_norm_partials(const ClipArgs<N> &a, hipStream_t s);
+template <int N>
+hipError_t launch_clip(const ClipArgs<N> &a, hipStream_t s);
+template <int N>
+hipError_t launch_clip_one(const ClipArgs<N> &a, hipStream_t s);
 
 }  // namespace cpo
