@@ -7,7 +7,9 @@ decode step.
 
 The dense block is y = x + W2 gelu(W1 norm(x) + b1) + b2, the expert block the same
 with each token's weights chosen by a fixed router.  Both blocks learn to
-reproduce a target: the printed loss has to fall.
+reproduce a target: the printed loss has to fall.  The routed block learns its router
+with the rest, two experts to a token, under a balance loss and with its gradients
+clipped; its decode step runs with 4-bit weights.
 """
 import argparse
 import os
@@ -103,6 +105,69 @@ class Experts(Dense):
         return {"g": dg, "b": db, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2}, dx + dy
 
 
+class Routed(Dense):
+    """Experts chosen by a router that is learned: norm -> logits -> the k best of each
+    token, their rows through the experts, the results weighted and summed."""
+    balance = 0.01  # weight of the balance loss
+    max_norm = 20.0
+
+    def __init__(self, width, hidden, experts, dtype, k=2, seed=0):
+        super().__init__(width, hidden, dtype, seed)
+        g = torch.Generator(device="cuda").manual_seed(seed + 2)
+
+        def normal(*shape, std):
+            return torch.randn(*shape, generator=g, device="cuda") * std
+        self.k, E = k, experts
+        self.params.update(wr=normal(width, E, std=width ** -0.5), w1=normal(E, width, hidden, std=width ** -0.5),
+                           b1=torch.zeros(E, hidden, device="cuda"), w2=normal(E, hidden, width, std=hidden ** -0.5),
+                           b2=torch.zeros(E, width, device="cuda"))
+
+    def forward(self, x, keep=True):
+        p = self.weights()
+        n, mean, rstd = ops.layer_norm(x, p["g"], p["b"])
+        logits = ops.linear(n, p["wr"])
+        r = ops.route(logits, self.k, normalize=True)
+        rows = ops.dispatch(n, r.rows, r.offsets)
+        h = ops.grouped_linear(rows, p["w1"], r.offsets, p["b1"], act=ops.ACT_GELU_TANH, need_pre=keep)
+        h, z = h if keep else (h, None)
+        out = ops.grouped_linear(h, p["w2"], r.offsets, p["b2"])
+        y = ops.combine(out, r.rows, r.gates, residual=x)
+        self.saved = (p, x, n, mean, rstd, logits, r, rows, h, z, out)
+        return y
+
+    def backward(self, dy):
+        p, x, n, mean, rstd, logits, r, rows, h, z, out = self.saved
+        dout, dgates = ops.combine_backward(dy, out, r.rows, r.offsets, r.gates)
+        dh, dw2, db2 = ops.grouped_linear_backward(dout, h, p["w2"], r.offsets)
+        drows, dw1, db1 = ops.grouped_linear_backward(dh, rows, p["w1"], r.offsets, pre=z, act=ops.ACT_GELU_TANH)
+        weight = torch.full((), self.balance, device=x.device)
+        dlogits = ops.route_backward(dgates, weight, logits, r.experts, r.slopes, normalize=True)
+        dn, dwr, _ = ops.linear_backward(dlogits, n, p["wr"], need_bias=False)
+        dn = ops.combine(drows, r.rows, residual=dn)
+        dx, dg, db = ops.layer_norm_backward(dn, x, mean, rstd, p["g"])
+        return {"g": dg, "b": db, "wr": dwr, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2}, dx + dy
+
+    def step(self, grads, lr):
+        clipped = {k: torch.empty_like(v, dtype=torch.float32) for k, v in grads.items()}
+        self.norm = ops.clip_grad_norm(list(grads.values()), self.max_norm, out=list(clipped.values()))
+        for k, v in self.params.items():
+            v -= lr * clipped[k]
+
+    def pack(self, group_size=64):
+        """4-bit weights of the experts, for decode."""
+        p = self.weights()
+        self.packed = {k: ops.pack_int4(*ops.quantize_int4(p[k], group_size), group_size=group_size) for k in ("w1", "w2")}
+
+    def decode(self, x):
+        p = self.weights()
+        n, _, _ = ops.layer_norm(x, p["g"], p["b"])
+        r = ops.route(ops.linear(n, p["wr"]), self.k, normalize=True)
+        rows = ops.dispatch(n, r.rows, r.offsets)
+        h = ops.grouped_linear_int4(rows, self.packed["w1"], r.offsets, p["b1"], act=ops.ACT_GELU_TANH)
+        out = ops.grouped_linear_int4(h, self.packed["w2"], r.offsets, p["b2"])
+        return ops.combine(out, r.rows, r.gates, residual=x)
+
+
 def train(block, x, target, steps, lr):
     """Mean squared error before each step."""
     losses = []
@@ -139,6 +204,15 @@ def main(argv=None):
         print(f"{name}: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps; "
               f"one token alone is {off:.4f} from the same token in the batch", flush=True)
         result[name] = (losses, off)
+    block = Routed(a.width, a.hidden, a.experts, dtype, k=min(2, a.experts))
+    losses = train(block, x, target, a.steps, a.lr)
+    r = block.saved[6]
+    block.pack()
+    full, packed = block.forward(x[:1], keep=False), block.decode(x[:1])
+    off = ((packed.float() - full.float()).norm() / (full.float() - x[:1].float()).norm()).item()
+    print(f"routed: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps; balance loss {r.loss.item():.3f} (1: even), "
+          f"rows per expert {r.counts.min().item()} to {r.counts.max().item()}, last gradient norm {block.norm.item():.3f}; "
+          f"one token with 4-bit weights is {off:.3f} of the block's output from that with all", flush=True)
     return result
 
 

@@ -166,8 +166,8 @@ int cp_route(int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t normalize, 
 /*
  * cp_route_backward -- dlogits[T][E] of cp_route for dgates[T][k] and dloss
  * (fp32, device memory; each may be NULL: zero), from the same logits and the
- * experts and slopes it gave.  Counts are constants.  Zero for tokens without
- * an expert.  dlogits may be logits (same pointer and ld).
+ * experts and slopes it gave (a token's experts are different).  Counts are
+ * constants.  Zero for tokens without an expert.  dlogits may be logits (same pointer and ld).
  */
 int cp_route_backward(int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t normalize, const float *dgates,
                       const float *dloss, const void *logits, int64_t ld, const int32_t *experts, const float *slopes,

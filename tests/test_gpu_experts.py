@@ -378,6 +378,8 @@ INT4 = [  # M, K, N, group
     (1, 128, 16, 128), (1, 1, 1, 32), (1, 4096, 512, 128), (1, 1000, 200, 64), (2, 65, 33, 32), (3, 300, 17, 256), (5, 64, 72, 64),
     (16, 2048, 144, 128), (17, 264, 136, 32), (13, 4300, 9000, 128), (31, 128, 1, 128), (33, 40, 24, 64), (64, 512, 264, 32),
     (65, 1001, 65, 64), (130, 384, 200, 384), (300, 200, 130, 128), (3, 0, 5, 32), (0, 8, 8, 32), (4, 8, 0, 32),
+    (1, 4200, 40, 32), (5, 9001, 40, 128), (16, 8200, 33, 64), (40, 2048, 64, 128), (33, 2100, 100, 32), (100, 9000, 72, 64),
+    (320, 1300, 2064, 128),
 ]
 
 
@@ -415,6 +417,7 @@ def test_linear_int4(ops, size, name):
 
 GROUPED = [  # K, N, group, rows of each expert, rows behind
     (128, 64, 128, [1], 0), (200, 136, 64, [3, 0, 5, 1], 0), (512, 96, 32, [0, 0, 17, 2, 0], 3), (72, 40, 128, [100, 0, 90, 70], 0),
+    (9000, 40, 128, [3, 0, 2], 4), (4600, 24, 32, [1, 20], 2), (2048, 64, 64, [40, 25], 9),
     (384, 130, 128, [2] * 70, 1), (64, 24, 32, [0, 0], 2), (1024, 9000, 128, [1, 4, 0, 2], 0), (136, 72, 64, [300], 20),
 ]
 
@@ -489,6 +492,65 @@ def test_int4_against_bf16_layer(ops):
     y = ops.linear_int4(x.float().cuda(), ops.pack_int4(q, s, z, group_size=64))
     want = ops.linear(x.float().cuda(), back.float().cuda()).double().cpu()
     close(y, want, int4_tol(x, back, sk, None, want, want, "none", 64, "f32") + 700 * E32 * (x.abs() @ back.abs()), "y")
+
+
+def test_beyond_32_bits(ops):
+    """Rows, codes, logits and gradients behind 2^31 elements (4-bit codes: bytes): the same as in small tensors."""
+    say("beyond 32 bits")
+    d = torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(6)
+    # experts' codes: the last of 70, 67 MB each
+    K, N, E = 8192, 16384, 70
+    q = torch.zeros(E, K, N, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(E, K // 128, N, dtype=d, device="cuda")
+    q[-1] = torch.randint(0, 16, (K, N), generator=g, device="cuda", dtype=torch.uint8)
+    s[-1] = 0.01
+    x = torch.randn(5, K, generator=g, device="cuda").to(d)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = 5
+    one = ops.grouped_linear_int4(x, ops.pack_int4(q[-1:].clone(), s[-1:].clone()), torch.tensor([0, 5], dtype=torch.int32, device="cuda"))
+    w = ops.pack_int4(q, s)
+    assert w.data.numel() > 1 << 32
+    del q, s
+    assert torch.equal(ops.grouped_linear_int4(x, w, off), one) and one.float().abs().sum() > 0
+    del w
+    # rows of a large expert buffer
+    T, k, D = 140000, 2, 8192
+    rows = torch.randperm(T * k, generator=g, device="cuda").int().view(T, k)
+    x = torch.randn(T, D, generator=g, device="cuda", dtype=d)
+    gates = torch.rand(T, k, generator=g, device="cuda")
+    end = torch.tensor([T * k], dtype=torch.int32, device="cuda")
+    y = ops.dispatch(x, rows, end)
+    assert y.numel() > 1 << 31
+    last = rows.max(1).values.argsort(descending=True)[:50]
+    assert torch.equal(y[rows[last].long()], x[last][:, None].expand(-1, k, -1))
+    small = torch.arange(100, dtype=torch.int32, device="cuda").view(50, 2)
+    part = y[rows[last].long()].reshape(100, D)
+    assert torch.equal(ops.combine(y, rows, gates)[last], ops.combine(part, small, gates[last].contiguous()))
+    dy, dg = ops.combine_backward(x, y, rows, end, gates)
+    sy, sg = ops.combine_backward(x[last].contiguous(), part, small, torch.tensor([100], dtype=torch.int32, device="cuda"),
+                                  gates[last].contiguous())
+    assert torch.equal(dy[rows[last].long()].reshape(100, D), sy)
+    # (a token's dot product is split over waves where tokens are few: another order of the same sum)
+    assert bool(((dg[last] - sg).abs() <= 2 * (D + 8) * E32 * (x[last].float().abs()[:, None] * part.float().abs().view(50, 2, D)).sum(2)).all())
+    del x, y, dy
+    # logits
+    T, E = 1 << 22, 520
+    x = torch.zeros(T, E, dtype=d, device="cuda")
+    x[-64:] = torch.randn(64, E, generator=g, device="cuda")
+    r, tail = ops.route(x, 3), ops.route(x[-64:], 3)
+    assert torch.equal(r.experts[-64:], tail.experts) and torch.equal(r.gates[-64:], tail.gates)
+    assert r.experts[:-64].amax().item() == 2 and r.offsets[-1].item() == 3 * T
+    assert torch.equal(r.rows[:-64, 1], torch.arange(T - 64, device="cuda", dtype=torch.int32) + r.offsets[1])
+    dg = torch.randn(T, 3, generator=g, device="cuda")
+    assert torch.equal(ops.route_backward(dg, None, x, r.experts, r.slopes)[-64:],
+                       ops.route_backward(dg[-64:].contiguous(), None, x[-64:], tail.experts, tail.slopes))
+    del x
+    # gradients
+    x = torch.zeros((1 << 31) + 1000, dtype=d, device="cuda")
+    x[-1], x[5] = 3.0, 4.0
+    assert ops.clip_grad_norm([x], 1.0).item() == 5.0
+    assert abs(x[-1].item() - 0.6) < 0.6 * 2 ** -8 + 1e-6 and abs(x[5].item() - 0.8) < 0.8 * 2 ** -8 + 1e-6
 
 
 # ----------------------------------------------------------------- clipping
@@ -656,6 +718,26 @@ def test_out_is_marked_as_written(ops):
                 f(leaf)
 
 
+def test_routing_tensors_are_ordinary(ops):
+    """They come from one allocation: each is written, copied and differentiated like any other."""
+    say("routing tensors")
+    x = torch.randn(300, 40, device="cuda")
+    r, want = ops.route(x, 4), ops.route(x, 4)
+    r.counts.add_(1)
+    r.experts.fill_(-7)
+    r.loss.zero_()
+    for name in ("gates", "rows", "offsets", "slopes"):
+        assert torch.equal(getattr(r, name), getattr(want, name)), name
+    for v in want:
+        assert v.is_contiguous() and v._version == 0 and torch.equal(v.clone().cpu(), v.cpu()) and not v._is_view()
+    gates = want.gates.requires_grad_()
+    (gates * 3).sum().backward()
+    assert (gates.grad == 3).all()
+    assert not ops.route_backward(None, None, x, want.experts, want.slopes).any()
+    with torch.inference_mode():
+        assert torch.equal(ops.route(x, 4).rows, want.rows)
+
+
 def test_refusals(ops):
     say("refusals")
     d = torch.bfloat16
@@ -712,6 +794,9 @@ def test_refusals(ops):
         (ValueError, lambda: ops.pack_int4(q, s, s, group_size=32)),
         (ValueError, lambda: ops.pack_int4(q.t(), s, group_size=32)),
         (TypeError, lambda: ops.linear_int4(x64, q)),
+        (TypeError, lambda: ops.linear_int4(None, w)),
+        (TypeError, lambda: ops.linear_int4(x64.cpu(), w)),
+        (ValueError, lambda: ops.linear_int4(x64[0], w)),
         (ValueError, lambda: ops.linear_int4(x64.float(), w)),
         (ValueError, lambda: ops.linear_int4(new(4, 65), w)),
         (ValueError, lambda: ops.linear_int4(x64, w3)),

@@ -137,9 +137,9 @@ __device__ __forceinline__ void scale_chunk(const Args &a, int64_t c, float f) {
     else scale_to<float, float, NT>(p.x, p.y, p.n, f);
 }
 
-__device__ __forceinline__ float clip_factor(float norm, float most) {
-    const float f = most / (norm + 1e-6f);
-    return f > 1.0f || most == __builtin_inff() ? 1.0f : f;  // (a norm of NaN gives NaN)
+__device__ __forceinline__ float clip_factor(double norm, float most) {
+    const double f = (double)most / (norm + 1e-6);
+    return f > 1.0 || most == __builtin_inff() ? 1.0f : (float)f;  // (a norm of NaN gives NaN)
 }
 
 template <int N>
@@ -179,8 +179,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += i + u * kClipThreads < a.nall ? t[u] : 0.0;
     }
-    const float norm = (float)sqrt(block_sum<kClipThreads>(s));
-    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+    const double norm = sqrt(block_sum<kClipThreads>(s));
+    if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
     const float f = clip_factor(norm, a.max_norm);
     if (!a.t[0].y) return;  // (all have an output, or none)
     if (!single) {
@@ -223,8 +223,8 @@ template <int N>
 __global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs<N> a) {
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int64_t c = 0; c < a.chunks; ++c) square_chunk<kClipOneThreads>(a, c, acc);
-    const float norm = (float)sqrt(block_sum<kClipOneThreads>((acc[0] + acc[1]) + (acc[2] + acc[3])));
-    if (threadIdx.x == 0) *a.norm = norm;
+    const double norm = sqrt(block_sum<kClipOneThreads>((acc[0] + acc[1]) + (acc[2] + acc[3])));
+    if (threadIdx.x == 0) *a.norm = (float)norm;
     const float f = clip_factor(norm, a.max_norm);
     if (a.t[0].y)
         for (int64_t c = 0; c < a.chunks; ++c) scale_chunk<kClipOneThreads>(a, c, f);

@@ -138,8 +138,9 @@ def route(logits, k, normalize=False, valid=None):
 
 def route_backward(dgates, dloss, logits, experts, slopes, normalize=False):
     """Gradient of the logits for dgates (float32 [T][k]) and dloss (float32 [],
-    on the device; each may be None), from what route was given and gave.  The
-    counts are constants; slots and tokens without an expert get zeros."""
+    on the device; each may be None), from what route was given and gave (a token's
+    experts are different).  The counts are constants; tokens without an expert get
+    zeros."""
     return _native.route_backward(dgates, dloss, logits, experts, slopes, normalize)
 
 
@@ -194,7 +195,9 @@ def _check_int4(x, w, dims):
         raise TypeError("w must be an Int4Weight (pack_int4)")
     if len(w.shape) != dims:
         raise ValueError(f"w must have {dims} dimensions, got {w.shape}")
-    if x.dtype != w.dtype or x.shape[-1] != w.shape[-2]:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a device tensor")
+    if x.dtype != w.dtype or x.dim() != 2 or x.shape[1] != w.shape[-2]:
         raise ValueError(f"x must be {w.dtype} with rows of {w.shape[-2]}, got {x.dtype} {tuple(x.shape)}")
 
 
