@@ -115,10 +115,9 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
     t.chunks = 1;
     if (rows <= 16) {
         t.ntm = row_tiles(16);
-        // registers for x, 128 or (8 waves) 256 to a lane: beside few scales for more of it
         const bool bf16 = dtype == CP_BF16;
-        t.waves = kblocks <= 4 ? 4 : (bf16 && group > 32 ? 16 : 8);
-        const int64_t most = !bf16 ? 16 : (group > 64 ? 64 : 32);
+        t.waves = kblocks <= 4 ? 4 : (bf16 ? 16 : 8);
+        const int64_t most = bf16 ? 64 : 16;  // tiles of x that a block's registers hold (fp32: three operands each)
         if (kblocks > most) t.chunks = (int32_t)((kblocks + most - 1) / most);
         // blocks that fill the device, shared out over the row tiles that are likely there
         const int64_t tiles = (experts ? (M < experts ? M : experts) : t.ntm) * t.chunks;
@@ -135,7 +134,7 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
         constexpr struct {
             int mt, nt;
             double one, two;
-        } kTiles[] = {{2, 1, 0.58, 1.0}, {2, 2, 0.9, 1.56}, {5, 2, 2.3, 0.0}};
+        } kTiles[] = {{2, 1, 0.72, 1.0}, {2, 2, 0.9, 1.56}, {5, 2, 2.3, 0.0}};
         double least = 1e300;
         for (const auto &k : kTiles) {
             if (k.nt > 1 && group == 32) continue;        // (registers: small groups keep more scales,
@@ -147,8 +146,8 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
                 const int64_t rest = blocks % per;
                 double us = (double)(blocks / per) * (k.two > 0.0 ? k.two : k.one);
                 us += rest == 0 ? 0.0 : (rest <= kComputeUnits ? k.one : k.two);
-                us *= (double)((kblocks + 2 * chunks - 1) / (2 * chunks));
-                if (chunks > 1) us += 5.0 + 4.0 * chunks * (double)M * (double)ntiles * 16.0 * 4.0 / 8e6;  // partials, a launch
+                us *= (double)((kblocks + 2 * chunks - 1) / (2 * chunks)) * (dtype == CP_BF16 ? 1.0 : 2.5);
+                if (chunks > 1) us += 3.0 + 3.0 * chunks * (double)M * (double)ntiles * 16.0 * 4.0 / 8e6;  // partials, a launch
                 if (us >= least) continue;
                 least = us;
                 t.mt = k.mt;

@@ -226,9 +226,10 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
         kb[i] = at < kb_end ? at : kb_end - 1;
         gr[i] = first_group<SG>(g, kb[i]);
     }
+    auto load_one = [&](int d, int i, int t) { w[d][i].load(g, codes, meta, t0 + t, kb[i], gr[i]); };
     auto load = [&](int d, int t) {
 #pragma unroll
-        for (int i = 0; i < XK; ++i) w[d][i].load(g, codes, meta, t0 + t, kb[i], gr[i]);
+        for (int i = 0; i < XK; ++i) load_one(d, i, t);
     };
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -281,6 +282,10 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[r] = fmaf(sc, fmaf(zp, xs[r], p[r]), acc[r]);
                 __builtin_amdgcn_sched_barrier(0);  // (one group's registers at a time)
+                if (D == 1 && j == NG - 1) {  // the next tile's part as soon as its registers are free
+                    asm volatile("" : "+v"(acc));
+                    load_one(0, i, t + 1 < n ? t + 1 : t);
+                }
             }
         // (one barrier to a tile: whoever writes a buffer again has passed the next one,
         // behind the sums that read it)
@@ -304,6 +309,13 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
         __syncthreads();
     };
     int t = 0;
+    if constexpr (D == 1) {
+        for (; t < n; ++t) {
+            column(0, t);
+            sum(t);
+        }
+        return;
+    }
     for (; t + 2 * D <= n; t += D)
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -651,14 +663,9 @@ hipError_t int4(const Int4Args &a, const Int4Tiles &t, hipStream_t s) {
         if (t.waves == 4) return stream_rows<T, SG, 4, 1, 4>(a, n, s);
         if constexpr (kWide) {
             return t.kper <= 8 ? stream_rows<T, SG, 8, 1, 4>(a, n, s) : stream_rows<T, SG, 8, 2, 2>(a, n, s);
-        } else if constexpr (SG == 1) {
-            if (t.kper <= 8) return stream_rows<T, SG, 8, 1, 4>(a, n, s);
-            return t.kper <= 16 ? stream_rows<T, SG, 8, 2, 2>(a, n, s) : stream_rows<T, SG, 8, 4, 1>(a, n, s);
         } else {
             if (t.kper <= 16) return stream_rows<T, SG, 16, 1, 4>(a, n, s);
-            if constexpr (SG == 4)
-                if (t.kper > 32) return stream_rows<T, SG, 16, 4, 1>(a, n, s);
-            return stream_rows<T, SG, 16, 2, 2>(a, n, s);
+            return t.kper <= 32 ? stream_rows<T, SG, 16, 2, (SG > 1 ? 2 : 1)>(a, n, s) : stream_rows<T, SG, 16, 4, 1>(a, n, s);
         }
     });
 }
