@@ -73,18 +73,26 @@ __device__ __forceinline__ void add_squares(const char *p, int64_t n, double (&a
     }
 }
 
-// y = x f over n elements; x and y may be the same memory.  U steps of eight elements
-// to a thread are requested together.
+// y = x f over n elements; x and y may be the same memory.  A lane takes 16 bytes of
+// the wider type at a time, so that a wave stores whole lines, U such steps requested
+// together.  Stores to 16-byte boundaries go past the caches, which keep more of the
+// gradients for this second reading so: 134 M elements bf16 to bf16 148 -> 122 us.
 template <class T, class O, int NT>
 __device__ __forceinline__ void scale_to(const char *x, char *y, int64_t n, float f) {
-    constexpr int CE = 8, U = 4;
+    constexpr int CE = sizeof(T) == 4 || sizeof(O) == 4 ? 4 : 8, U = 32 / CE;
+    typedef uint32_t word_t __attribute__((ext_vector_type(CE * sizeof(O) / 4)));
+    const bool past = reinterpret_cast<uintptr_t>(y) % 16 == 0;
     T e[U][CE];
     auto load = [&](int u, int64_t i) { __builtin_memcpy(e[u], x + i * (int64_t)sizeof(T), sizeof e[u]); };
     auto store = [&](int u, int64_t i) {
         O o[CE];
 #pragma unroll
         for (int j = 0; j < CE; ++j) o[j] = from_f32<O>(to_f32(e[u][j]) * f);
-        __builtin_memcpy(y + i * (int64_t)sizeof(O), o, sizeof o);
+        word_t w;
+        __builtin_memcpy(&w, o, sizeof o);
+        char *to = y + i * (int64_t)sizeof(O);
+        if (past) __builtin_nontemporal_store(w, reinterpret_cast<word_t *>(to));
+        else __builtin_memcpy(to, &w, sizeof w);
     };
     int64_t i = (int64_t)threadIdx.x * CE;
     for (; i + (int64_t)(U - 1) * NT * CE + CE <= n; i += (int64_t)U * NT * CE) {
