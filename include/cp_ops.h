@@ -134,9 +134,11 @@ int cp_layer_norm_backward(int32_t dtype, int64_t M, int64_t N, const void *dY, 
                            int64_t ldx, const float *mean, const float *rstd, const void *w, void *dX, int64_t lddx,
                            void *dw, void *db, void *ws, int64_t ws_bytes, void *stream);
 
-/* experts that cp_route chooses from, and experts to a token, at most */
+/* experts that cp_route chooses from, experts to a token, and tensors of
+ * cp_clip_grad_norm, at most */
 #define CP_OPS_MAX_ROUTED 1024
 #define CP_OPS_MAX_CHOSEN 32
+#define CP_OPS_MAX_TENSORS 16777216
 
 /*
  * cp_route -- the router of an expert layer: of each token's logits[T][E]
@@ -229,10 +231,13 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
 
 /*
  * cp_linear_int4, cp_grouped_linear_int4 -- cp_linear and cp_grouped_linear with
- * a packed weight.  Products of x with the codes are exact and added up in fp32, a
- * group at a time; the weight itself is never rounded.  x is meant to be finite and
- * below 2^115: a row with infinities gives NaN.  A product of more than 2^22 tiles
- * of 64 x 64 is refused.
+ * a packed weight, for decoding and short prompts: from some hundred rows on the
+ * layer with a bf16 weight is faster (2048 x 8192 x 8192 213 us, here 490).
+ * Products of x with the codes are exact and added up in fp32, a group at a time;
+ * the weight itself is never rounded.  x is meant to be finite and below 2^115: a
+ * row with infinities gives NaN.  More than 2^22 workgroups are refused with
+ * CP_ERR_SHAPE: tiles of 32 x 64 at least (an expert's last one counting in full)
+ * or, with at most 16 rows to an expert, experts times parts of K of 2048 at least.
  */
 int cp_linear_int4(int32_t dtype, int64_t M, int64_t K, int64_t N, const void *X, int64_t ldx, const void *packed,
                    int64_t group, const void *bias, const void *R, int64_t ldr, int32_t act,

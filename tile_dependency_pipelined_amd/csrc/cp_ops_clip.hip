@@ -226,18 +226,6 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
     }
 }
 
-constexpr int kClipOneThreads = 1024;
-template <int N>
-__global__ __launch_bounds__(kClipOneThreads) void clip_one_kernel(ClipArgs<N> a) {
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t c = 0; c < a.chunks; ++c) square_chunk<kClipOneThreads>(a, c, acc);
-    const double norm = sqrt(block_sum<kClipOneThreads>((acc[0] + acc[1]) + (acc[2] + acc[3])));
-    if (threadIdx.x == 0) *a.norm = (float)norm;
-    const float f = clip_factor(norm, a.max_norm);
-    if (a.t[0].y)
-        for (int64_t c = 0; c < a.chunks; ++c) scale_chunk<kClipOneThreads>(a, c, f);
-}
-
 }  // namespace
 
 template <int N>
@@ -250,15 +238,9 @@ hipError_t launch_clip(const ClipArgs<N> &a, hipStream_t s) {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(clip_kernel<N>), dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);
     return hipGetLastError();
 }
-template <int N>
-hipError_t launch_clip_one(const ClipArgs<N> &a, hipStream_t s) {
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(clip_one_kernel<N>), dim3(1), dim3(kClipOneThreads), 0, s, a);
-    return hipGetLastError();
-}
 #define CP_CLIP(n)                                                            \
     template hipError_t launch_norm_partials<n>(const ClipArgs<n> &, hipStream_t); \
-    template hipError_t launch_clip<n>(const ClipArgs<n> &, hipStream_t);     \
-    template hipError_t launch_clip_one<n>(const ClipArgs<n> &, hipStream_t);
+    template hipError_t launch_clip<n>(const ClipArgs<n> &, hipStream_t);
 CP_CLIP(kClipFew)
 CP_CLIP(kClipTensors)
 

@@ -56,6 +56,8 @@ __device__ __forceinline__ void zero_rows(const ExchangeArgs &a, const Pieces &p
     }
 }
 
+// Four units of a lane at a time keep enough in flight; the rows of one token are written
+// from the same registers.  8192 x 2 x 4096 bf16: 42.5 us, 4.7 TB/s.
 constexpr int kDispatchUnits = 4;
 template <class T>
 __global__ __launch_bounds__(256) void dispatch_kernel(ExchangeArgs a, Pieces p) {
@@ -87,7 +89,9 @@ __global__ __launch_bounds__(256) void dispatch_kernel(ExchangeArgs a, Pieces p)
     zero_rows<T, U>(a, p, item, p.items, a.out, a.ldo);
 }
 
-// Slots C at a time, their rows requested together.
+// Slots C at a time, their rows requested together: of two slots one step of two (8192 x 2
+// x 4096 bf16, a quarter of the tokens padding: 45.7 us, 5.1 TB/s), of more, steps of
+// four.
 template <class T, int U, int C>
 __global__ __launch_bounds__(256) void combine_kernel(ExchangeArgs a, Pieces p) {
     constexpr int CE = kUnit<T>;
@@ -160,7 +164,8 @@ __device__ __forceinline__ float sum_lanes(float v, int lanes) {
 
 // A token's whole row to the same lanes, as its gates' gradients are sums over it:
 // C slots at a time, one unit of each requested together.  With `W` > 1 the waves
-// of a block share a token and add up in LDS.
+// of a block share a token and add up in LDS.  One pass gives both gradients: dout is
+// read once for all slots, y and dy go by once.  4099 x 4 x 2048 bf16: 33.6 us, 4.5 TB/s.
 template <class T, int C, int W>
 __global__ __launch_bounds__(256) void combine_backward_kernel(ExchangeArgs a, Pieces p) {
     constexpr int CE = kUnit<T>;
@@ -258,7 +263,13 @@ template <class T>
 hipError_t combine_backward(const ExchangeArgs &a, hipStream_t s) {
     const Pieces p = pieces(a.T, a.D, kUnit<T>, 1);
     const int64_t tokens = 64 >> p.shift, waves = a.T ? (a.T + tokens - 1) / tokens : 1;
-    const bool shared = p.lanes == 64 && p.units > 64 && a.T < 8 * kComputeUnits;
+    // Waves that share a token: where tokens are too few to fill the device with a wave to
+    // each (256 x 4 x 4096 bf16 16.2 us against 7.7, 1024 x 4 x 8192 43 against 26), and where y and
+    // dy are far from fitting the last cache of 256 MB, as fewer rows are then open at a time
+    // (6000 x 4 x 6144 186 us against 138).  In between a wave to a token is faster: no
+    // barriers (4096 x 4 x 4096 61 us against 67, 4096 x 4 x 1024 16 against 25).
+    const int64_t bytes = a.T * a.k * a.D * (int64_t)sizeof(T);
+    const bool shared = p.lanes == 64 && p.units > 64 && (a.T < 8 * kComputeUnits || bytes > (int64_t(160) << 20));
     if (shared)
         hipLaunchKernelGGL(HIP_KERNEL_NAME(combine_backward_kernel<T, 4, 4>), grid_of(waves, 256), dim3(256), 0, s, a, p);
     else

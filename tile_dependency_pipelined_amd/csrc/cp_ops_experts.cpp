@@ -170,10 +170,9 @@ int check_clip_memory(int64_t n, const int32_t *dtypes, const void *const *grads
     return CP_OK;
 }
 
-// The launches for `total` elements in `used` tensors that are not empty, up to N to
-// a launch.
+// The launches for `total` elements, up to N tensors that are not empty to a launch.
 template <int N>
-int launch_clips(int64_t n, int64_t total, int64_t used, const int32_t *dtypes, const void *const *grads, const int64_t *numels,
+int launch_clips(int64_t n, int64_t total, const int32_t *dtypes, const void *const *grads, const int64_t *numels,
                  float max_norm, const int32_t *out_dtypes, void *const *outs, float *norm, double *partial, hipStream_t s) {
     const int chunk = clip_chunk(total);
     auto fill = [&](int64_t *i) {  // from tensor *i on
@@ -192,11 +191,6 @@ int launch_clips(int64_t n, int64_t total, int64_t used, const int32_t *dtypes, 
         return a;
     };
     int64_t i = 0;
-    if (total <= kClipOneBlock && used <= N) {
-        ClipArgs<N> a = fill(&i);
-        a.norm = norm;
-        return launched(launch_clip_one(a, s), "gradient norm");
-    }
     int nall = 0;
     while (i < n) {
         ClipArgs<N> a = fill(&i);
@@ -206,13 +200,13 @@ int launch_clips(int64_t n, int64_t total, int64_t used, const int32_t *dtypes, 
         CP_TRY(launched(launch_norm_partials(a, s), "gradient norm"));
     }
     bool first = true;
-    for (i = 0; i < n && (outs || first); first = false) {
+    for (i = 0; first || (outs && i < n); first = false) {  // (one for the norm, also of nothing)
         ClipArgs<N> a = fill(&i);
-        if (!a.n) break;
+        if (!a.n && !first) break;
         a.all = partial;
         a.nall = nall;
         a.norm = first ? norm : nullptr;
-        a.blocks = outs ? (int)std::min<int64_t>(a.chunks, 2 * kClipBlocks) : 1;
+        a.blocks = outs && a.n ? (int)std::min<int64_t>(a.chunks, 2 * kClipBlocks) : 1;
         CP_TRY(launched(launch_clip(a, s), "gradient clipping"));
     }
     return CP_OK;
@@ -220,7 +214,7 @@ int launch_clips(int64_t n, int64_t total, int64_t used, const int32_t *dtypes, 
 
 int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64_t *numels, float max_norm,
          const int32_t *out_dtypes, void *const *outs, float *norm, void *ws, int64_t ws_bytes, hipStream_t s) {
-    if (n < 0 || n > kMaxRows) return fail(CP_ERR_SHAPE, "%lld tensors", (long long)n);
+    if (n < 0 || n > CP_OPS_MAX_TENSORS) return fail(CP_ERR_SHAPE, "%lld tensors (at most %d)", (long long)n, CP_OPS_MAX_TENSORS);
     if (n && (!dtypes || !grads || !numels || (outs && !out_dtypes)))
         return fail(CP_ERR_INVALID_ARG, "a list of tensors is NULL");
     if (!(max_norm >= 0.0f)) return fail(CP_ERR_INVALID_ARG, "max_norm %g", (double)max_norm);
@@ -240,7 +234,7 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
     }
     CP_TRY(check_ws(ws, ws_bytes, clip_ws(n)));
     if (outs) CP_TRY(check_clip_memory(n, dtypes, grads, numels, out_dtypes, outs));
-    return (used <= kClipFew ? launch_clips<kClipFew> : launch_clips<kClipTensors>)(n, total, used, dtypes, grads, numels, max_norm,
+    return (used <= kClipFew ? launch_clips<kClipFew> : launch_clips<kClipTensors>)(n, total, dtypes, grads, numels, max_norm,
                                                                                     out_dtypes, outs, norm, (double *)ws, s);
 }
 
@@ -278,8 +272,8 @@ int cp_route(int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t normalize, 
     a.E = E;
     a.k = k;
     a.normalize = normalize;
-    a.blocks = route_blocks(T);
-    a.chunks = route_chunks(T);
+    a.blocks = route_blocks(T, E);
+    a.chunks = route_chunks(T, E);
     a.hist = (int32_t *)ws;
     a.stride = (int)up(E, 4);
     a.psum = (float *)(a.hist + (int64_t)a.blocks * a.stride);
