@@ -131,9 +131,9 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
     } else {
         // Tile and parts of the contraction by the rounds the device takes: microseconds
         // for 256 k of a block with a CU to itself, and of two that share one (of the
-        // largest only one fits).  Measured with groups of 64 and 128, whole calls
-        // with 2x1 | 2x2 | 5x2 tiles: 64 x 8192 x 8192 29 | 37 | 67, 300 x 8192 x
-        // 8192 - | 93 | 86, 2048 x 8192 x 8192 - | 400 | 508.
+        // largest only one fits).  Whole calls with groups of 128 and 2x1 | 2x2 | 5x2 tiles:
+        // 17 x 4096 x 4096 9.4 | 9.9 | 13.7, 64 x 8192 x 8192 28 | 24 | 28, 300 x 8192 x 8192
+        // 103 | 78 | 74, 2048 x 8192 x 8192 616 | 434 | 509.
         constexpr struct {
             int mt, nt;
             double one, two;

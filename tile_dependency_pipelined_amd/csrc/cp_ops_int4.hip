@@ -1,6 +1,7 @@
-// cp_ops_int4.hip -- linear layers with 4-bit weights, w_kn = s_gn (q_kn - z_gn),
-// for a few rows at a time (decoding): bound by reading the codes, a quarter of
-// the bf16 weight.
+// cp_ops_int4.hip -- linear layers with 4-bit weights, w_kn = s_gn (q_kn - z_gn).  For
+// a few rows at a time (decoding) bound by reading the codes, a quarter of the bf16
+// weight; for more rows by unpacking and scaling, which the vector unit does beside
+// the matrix cores.
 //
 // The matrix cores multiply x with the codes as bf16, exactly: a code's four bits
 // in bits 3 .. 6 of a bf16 pattern 0x4180 make it 16 + q, two codes with one shift
@@ -193,6 +194,9 @@ __device__ __forceinline__ void put_int4_unit(const Int4Args &g, const BlockRows
 // could not tell how many are in flight behind it and would wait for all.  For the
 // same reason the sums of a column tile go to LDS and are finished, with what bias and
 // residual have to be read for it, some tiles at a time.
+// 1 x 4096 x 4096 bf16 7.2 us (a launch and one trip to memory; 8.9 MB), 13 x 8192 x
+// 28672 30.7 us (125 MB, 4.1 TB/s), 32 rows over 8 experts of 4096 x 4096 16.6 us (62 MB of
+// the seven in use, 3.7 TB/s); half of the wave cycles wait for memory.
 constexpr int kInt4Flush = 8;
 template <class T, int W, int XK, int D, int SG>
 __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
@@ -350,8 +354,11 @@ __device__ __forceinline__ float sum_neighbours(float v) {
 // contraction each.  A wave stages 32 or 64 k of 16 rows at a time and adds them up for
 // each row; where the pieces do not go round, some are staged twice, alike.  x and
 // codes are requested two tiles of the contraction ahead, x first: loads come back in
-// order, and x is waited for first, to be staged one tile ahead.  (No branch around a load, as above: what lies past
-// K comes last.)
+// order, and x is waited for first, to be staged one tile ahead.  (No branch around a
+// load, as above: what lies past K comes last.)
+// 300 x 8192 x 8191, groups of 64, bf16: 82 us, 490 TFLOP/s.  The matrix cores are busy
+// for 21% of it, LDS for 28%; waves wait for 36% of their cycles and issue vector
+// instructions for most of the rest: two per result and group, beside the unpacking.
 template <class T, int MT, int NT, int WK, int SG>
 __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
     constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG;
@@ -560,7 +567,9 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
 
 // ------------------------------------------------- packing and quantisation
 
-// A thread per word of the codes: eight k of a column.
+// A thread per word of the codes: eight k of a column.  Bytes are read along the columns
+// and words written 16 bytes apart, which the L2 gathers: 8192 x 28672 121 us.  Once per
+// weight, not for every call.
 __global__ __launch_bounds__(256) void int4_pack_codes_kernel(Int4PackArgs a) {
     const int64_t words = (int64_t)a.ntiles * a.kblocks * (kInt4TileBytes / 4), all = words * a.E;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {

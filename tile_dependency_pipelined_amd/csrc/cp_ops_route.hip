@@ -8,6 +8,11 @@
 // expert at most once, so 64 tokens' choices of one expert are the bits of a
 // word: a slot's place among its expert's is a count of the bits below its own,
 // and does not depend on the order in which they were set.
+//
+// The bytes are few (16384 x 128 fp32, k 8: 10 MB, 2 us).  What bounds the kernels is
+// latency: the chain of k selections, each a maximum over the lanes, and then the
+// launch that joins the blocks.  16 x 8 bf16 in one block 4.2 us; 16384 x 128 in 256
+// blocks 11.1 and the join 8.2; backward 8191 x 60 4.9.
 #include "cp_ops_experts.h"
 
 namespace cpo {
@@ -160,6 +165,10 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, const int32_t *
 }
 
 // ------------------------------------------------------------------ forward
+
+// A block takes 64 tokens at a time.  Selection writes the chosen logit's key to LDS, and
+// each slot's gate is computed from it afterwards, once, by one thread, and not by all
+// the lanes of a token in every step of the selection (16384 x 128 20.7 -> 18.7 us in all).
 
 // Waves that add their sums to LDS at a time: all, unless the experts are many.
 __host__ __device__ constexpr int sum_slices(int E) { return E <= 256 ? 16 : 4; }
@@ -437,7 +446,8 @@ __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(RouteArgs a) {
 // The probabilities are computed again from the logits, in registers: cheaper
 // than to store and read them.
 // The gates' gradients go to the lanes of their experts by way of LDS: compared with
-// every logit's index in registers instead, they took most of the time.
+// every logit's index in registers instead, they took most of the time (32768 x 512 bf16,
+// k 8: 42 us, so 31).
 template <class T, int LPR, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a) {
     constexpr int RPW = 64 / LPR;
