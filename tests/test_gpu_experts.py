@@ -130,7 +130,7 @@ def routing(x, k, normalize, valid=None):
 ROUTES = [  # T, E, k: no token to several blocks of them, each width of the lanes, whole and ragged
     (0, 8, 2), (1, 1, 1), (1, 8, 2), (16, 8, 2), (5, 3, 3), (63, 16, 4), (65, 17, 4), (200, 60, 6), (256, 64, 8), (257, 65, 8),
     (320, 128, 8), (300, 129, 5), (1000, 256, 8), (700, 300, 32), (130, 512, 3), (129, 513, 7), (300, 1024, 32), (5000, 12, 2),
-    (16500, 33, 4), (40000, 5, 1),
+    (16500, 33, 4), (40000, 5, 1), (100, 20, 3), (128, 32, 4), (128, 33, 4),
 ]
 
 
@@ -245,7 +245,7 @@ def test_route_gradient_against_differences(ops):
 
 MOVES = [  # T, E, k, D
     (0, 4, 2, 16), (1, 1, 1, 1), (1, 8, 2, 4096), (7, 5, 3, 33), (64, 8, 2, 8), (65, 8, 8, 17), (300, 16, 1, 200), (129, 60, 6, 520),
-    (33, 64, 32, 96), (500, 8, 2, 1000), (40, 4, 4, 8200), (2100, 6, 3, 136), (9, 5, 2, 0),
+    (33, 64, 32, 96), (500, 8, 2, 1000), (40, 4, 4, 8200), (2100, 6, 3, 136), (9, 5, 2, 0), (2049, 5, 2, 1040),
 ]
 
 

@@ -340,8 +340,8 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
 
 // Places among all of an expert's slots: those of the blocks before, from their
 // counts, and of the experts before.  Every block adds up the counts of all, at most
-// 256 x E from the L2, four experts to a thread and all its loads in flight at once:
-// that costs less than a launch that does it once.  The last block writes the totals.
+// 256 x E from the caches, four experts to a thread and all its loads in flight at once,
+// which spares another launch.  The last block writes the totals.
 constexpr int kJoinThreads = 1024, kJoinParts = 64;
 struct JoinShape {
     int quads, parts;  // 16 bytes of a row; ranges of the rows

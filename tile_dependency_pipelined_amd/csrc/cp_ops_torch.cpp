@@ -395,6 +395,7 @@ const Tensor &slots(PyObject *o, const Tensor &x, const char *name) {
     const Tensor &t = tensor(o, name);
     if (t.scalar_type() != at::kInt || t.dim() != 2 || !t.is_contiguous() || t.device() != x.device())
         refuse(PyExc_ValueError, "%s must be a contiguous int32 matrix on %s", name, x.device().str().c_str());
+    if (t.size(1) > INT32_MAX) refuse(PyExc_ValueError, "%s has %lld slots to a token", name, (long long)t.size(1));
     return t;
 }
 // The last of offsets [E + 1].
@@ -433,6 +434,7 @@ PyObject *route(PyObject *const *a) {
 PyObject *route_backward(PyObject *const *a) {
     const Tensor &x = first(a[2], "logits");
     const int64_t T = x.size(0), E = x.size(1), ld = rows(x, "logits");
+    if (E > CP_OPS_MAX_ROUTED) refuse(PyExc_ValueError, "%lld experts (at most %d)", (long long)E, CP_OPS_MAX_ROUTED);
     const Tensor &experts = slots(a[3], x, "experts");
     const int64_t k = experts.size(1);
     like(a[3], x, {T, k}, "experts", at::kInt);
