@@ -232,7 +232,7 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
 /*
  * cp_linear_int4, cp_grouped_linear_int4 -- cp_linear and cp_grouped_linear with
  * a packed weight, for decoding and short prompts: from some hundred rows on the
- * layer with a bf16 weight is faster (2048 x 8192 x 8192 213 us, here 490).
+ * layer with a bf16 weight is faster (2048 x 8192 x 8192 208 us, here 454).
  * Products of x with the codes are exact and added up in fp32, a group at a time;
  * the weight itself is never rounded.  x is meant to be finite and below 2^115: a
  * row with infinities gives NaN.  More than 2^22 workgroups are refused with
@@ -251,7 +251,8 @@ int cp_grouped_linear_int4(int32_t dtype, int64_t T, int64_t K, int64_t N, int32
  * cp_clip_grad_norm -- norm = sqrt(sum of squares over all of n tensors), added up
  * in fp64, and outs[i] = grads[i] min(1, max_norm / (norm + 1e-6)).
  *   dtypes[n], grads[n], numels[n], out_dtypes[n], outs[n]: HOST arrays, read
- *   during the call; tensor i has numels[i] elements side by side
+ *   during the call; tensor i has numels[i] elements side by side, all together
+ *   2^44 at most
  * outs[i] may be grads[i] (of the same type); apart from that no output shares
  * memory with an input or another output, which is checked.  outs NULL: the norm
  * alone (out_dtypes is not read).  norm: fp32, device memory.  max_norm >= 0; with

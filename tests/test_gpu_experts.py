@@ -571,7 +571,7 @@ def gradients(g, shapes, kinds):
     return out
 
 
-CLIPS = [[1], [0, 5, 0], [7, 6, 12, 1000], [65536], [65537], [100000, 3, 0, 12345, 777777, 60000], [17] * 96, [17, 30, 6] * 70,
+CLIPS = [[1], [0, 5, 0], [7, 6, 12, 1000], [65536], [65537], [100000, 3, 0, 12345, 777777, 60000], [17] * 96, [17, 30, 6] * 70, [5, 0, 4097, 2048, 2049] * 33,
          [1 << 20, 1 << 22, 99999, 1], [0, 0]]
 
 

@@ -1,6 +1,6 @@
 // cp_ops_clip.hip -- the norm over all the gradients of a model and their scaling:
 // N = sqrt(sum x^2), x min(1, c / (N + 1e-6)).  Two passes over the tensors, a launch
-// each for every 96 of them: the tensors are cut into chunks, numbered through, and
+// each for every 160 of them: the tensors are cut into chunks, numbered through, and
 // their addresses ride in the launch's arguments.  Squares are added in 64 bits,
 // which hold any fp32 value's square, and in an order that only the sizes set, so a
 // norm does not depend on timing and no finite gradient overflows it.  Both
@@ -19,11 +19,11 @@ constexpr int kClipThreads = 256;
 // arguments lie in the host's memory, so all are looked at at once: a search, step
 // after step, waits for it each time.
 template <class Args>
-__device__ __forceinline__ int find_tensor(const Args &a, int64_t c) {
+__device__ __forceinline__ int find_tensor(const Args &a, int c) {
     const int lane = threadIdx.x & 63;
     int n = 0;
     for (int base = 0; base < a.n; base += 64)
-        n += __popcll(__ballot(base + lane < a.n && a.t[base + lane < a.n ? base + lane : 0].before <= c));
+        n += __popcll(__ballot(base + lane < a.n && a.before[base + lane < a.n ? base + lane : 0] <= c));
     return n - 1;
 }
 __device__ __forceinline__ bool bit(const uint32_t *w, int i) { return w[i >> 5] >> (i & 31) & 1; }
@@ -122,23 +122,22 @@ struct Piece {
     bool bf16_in, bf16_out;
 };
 template <class Args>
-__device__ __forceinline__ Piece piece_of(const Args &a, int64_t c) {
-    const int i = find_tensor(a, c);
-    const int64_t from = (c - a.t[i].before) * a.chunk;
+__device__ __forceinline__ Piece piece_of(const Args &a, int c) {
+    const int i = find_tensor(a, c), end = i + 1 < a.n ? a.before[i + 1] : a.chunks;
+    const int64_t from = (int64_t)(c - a.before[i]) * a.chunk;
     const bool bi = bit(a.bf16_in, i), bo = bit(a.bf16_out, i);
-    return {a.t[i].x + from * (bi ? 2 : 4), a.t[i].y + from * (bo ? 2 : 4), a.t[i].n - from < a.chunk ? a.t[i].n - from : a.chunk, bi,
-            bo};
+    return {a.x[i] + from * (bi ? 2 : 4), a.y[i] + from * (bo ? 2 : 4), c + 1 < end ? a.chunk : a.last[i], bi, bo};
 }
 
 template <int NT, class Args>
-__device__ __forceinline__ void square_chunk(const Args &a, int64_t c, double (&acc)[4]) {
+__device__ __forceinline__ void square_chunk(const Args &a, int c, double (&acc)[4]) {
     const Piece p = piece_of(a, c);
     if (p.bf16_in) add_squares<__bf16, NT>(p.x, p.n, acc);
     else add_squares<float, NT>(p.x, p.n, acc);
 }
 
 template <int NT, class Args>
-__device__ __forceinline__ void scale_chunk(const Args &a, int64_t c, float f) {
+__device__ __forceinline__ void scale_chunk(const Args &a, int c, float f) {
     const Piece p = piece_of(a, c);
     if (f == 1.0f && p.y == p.x) return;  // in place, nothing to do
     if (p.bf16_in && p.bf16_out) scale_to<__bf16, __bf16, NT>(p.x, p.y, p.n, f);
@@ -155,7 +154,7 @@ __device__ __forceinline__ float clip_factor(double norm, float most) {
 template <int N>
 __global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs<N> a) {
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) square_chunk<kClipThreads>(a, c, acc);
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) square_chunk<kClipThreads>(a, c, acc);
     const double s = block_sum<kClipThreads>((acc[0] + acc[1]) + (acc[2] + acc[3]));
     if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
 }
@@ -166,8 +165,8 @@ __global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs<N>
 // the partial sums, whose wait is as long.
 template <int N>
 __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
-    const int64_t c0 = a.chunks - 1 - blockIdx.x;
-    const bool single = a.t[0].y && a.chunk == kClipThreads * 8 && c0 < gridDim.x;  // (uniform)
+    const int c0 = a.chunks - 1 - (int)blockIdx.x;
+    const bool single = a.y[0] && a.chunk == kClipThreads * 8 && c0 < (int)gridDim.x;  // (uniform)
     const int64_t at = (int64_t)threadIdx.x * 8;
     Piece p{};
     uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
@@ -192,9 +191,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
     const double norm = sqrt(block_sum<kClipThreads>(s));
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
     const float f = clip_factor(norm, a.max_norm);
-    if (!a.t[0].y) return;  // (all have an output, or none)
+    if (!a.y[0]) return;  // (all have an output, or none)
     if (!single) {
-        for (int64_t c = c0; c >= 0; c -= gridDim.x) scale_chunk<kClipThreads>(a, c, f);
+        for (int c = c0; c >= 0; c -= (int)gridDim.x) scale_chunk<kClipThreads>(a, c, f);
         return;
     }
     if (f == 1.0f && p.x == p.y) return;

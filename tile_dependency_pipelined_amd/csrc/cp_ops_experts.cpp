@@ -181,10 +181,14 @@ int launch_clips(int64_t n, int64_t total, const int32_t *dtypes, const void *co
         a.chunk = chunk;
         for (; *i < n && a.n < N; ++*i) {
             if (!numels[*i]) continue;
-            a.t[a.n] = {(const char *)grads[*i], outs ? (char *)outs[*i] : nullptr, numels[*i], a.chunks};
+            const int64_t own = ceil_div(numels[*i], chunk);
+            a.x[a.n] = (const char *)grads[*i];
+            a.y[a.n] = outs ? (char *)outs[*i] : nullptr;
+            a.before[a.n] = a.chunks;
+            a.last[a.n] = (int32_t)(numels[*i] - (own - 1) * chunk);
             if (dtypes[*i] == CP_BF16) a.bf16_in[a.n >> 5] |= 1u << (a.n & 31);
             if (outs && out_dtypes[*i] == CP_BF16) a.bf16_out[a.n >> 5] |= 1u << (a.n & 31);
-            a.chunks += ceil_div(numels[*i], chunk);
+            a.chunks += (int32_t)own;
             ++a.n;
         }
         a.blocks = (int)std::min<int64_t>(a.chunks, kClipBlocks);
@@ -223,8 +227,9 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
     for (int64_t i = 0; i < n; ++i) {
         CP_TRY(check_dtype(dtypes[i]));
         if (outs) CP_TRY(check_dtype(out_dtypes[i]));
-        if (numels[i] < 0 || numels[i] > (int64_t(1) << 48))
-            return fail(CP_ERR_SHAPE, "tensor %lld: %lld elements", (long long)i, (long long)numels[i]);
+        // (chunks of 16384 are counted in 32 bits)
+        if (numels[i] < 0 || numels[i] > (int64_t(1) << 44) - total)
+            return fail(CP_ERR_SHAPE, "tensor %lld: %lld elements (at most 2^44 in all)", (long long)i, (long long)numels[i]);
         if (!numels[i]) continue;
         if (!grads[i] || (outs && !outs[i])) return fail(CP_ERR_INVALID_ARG, "tensor %lld is NULL", (long long)i);
         CP_TRY(check_vector(grads[i], dtypes[i], "a gradient"));

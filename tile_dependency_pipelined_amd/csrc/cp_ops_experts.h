@@ -195,23 +195,20 @@ hipError_t launch_int4_quantize(int dtype, const Int4QuantArgs &a, hipStream_t s
 
 // ------------------------------------------------------ gradient norm, clipping
 
-constexpr int kClipTensors = 96;    // of a launch, at most: its arguments, up to 4 KB, hold their addresses
+constexpr int kClipTensors = 160;   // of a launch, at most: its arguments, up to 4 KB, hold their addresses
 constexpr int kClipFew = 8;         // of a launch with shorter arguments, which are quicker to hand over
 constexpr int kClipBlocks = 1024;   // partial sums of a launch, at most
 
-struct ClipTensor {
-    const char *x;
-    char *y;               // output, or null
-    int64_t n;
-    int64_t before;        // chunks of the tensors before it in this launch
-};
 template <int N>
 struct ClipArgs {
-    ClipTensor t[N];
+    const char *x[N];
+    char *y[N];            // outputs, or null
+    int32_t before[N];     // chunks of the tensors before it in this launch
+    int32_t last[N];       // elements of its last chunk
     uint32_t bf16_in[(N + 31) / 32], bf16_out[(N + 31) / 32];
     int32_t n, blocks;
     int32_t chunk;         // elements of a chunk
-    int64_t chunks;
+    int32_t chunks;
     double *partial;       // this launch's
     const double *all;     // of all launches
     int32_t nall;
