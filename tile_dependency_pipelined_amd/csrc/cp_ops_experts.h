@@ -215,6 +215,7 @@ struct ClipArgs {
     float max_norm;
     float *norm;
 };
+static_assert(sizeof(ClipArgs<kClipTensors>) <= 4096, "arguments of a launch");
 // Elements that a block takes at a time: few where there are few in all, for the
 // blocks to fill the device.
 inline int32_t clip_chunk(int64_t total) {
