@@ -129,12 +129,13 @@ __device__ __forceinline__ Scale softmax(const float (&x)[V], float (&p)[V]) {
 
 // -------------------------------------------------- counts, offsets and loss
 
-// Exclusive scan of cnt[E] into off[E + 1] (LDS), by the first wave.
-__device__ __forceinline__ void scan_counts(const int32_t *cnt, int32_t *off, int E) {
+// Exclusive scan of the E counts cnt(e) into off[E + 1] (LDS), by the first wave.
+template <class Counts>
+__device__ __forceinline__ void scan_counts(Counts &&cnt, int32_t *off, int E) {
     const int lane = threadIdx.x;
     int carry = 0;
     for (int base = 0; base < E; base += 64) {
-        const int e = base + lane, c = e < E ? cnt[e] : 0;
+        const int e = base + lane, c = e < E ? cnt(e) : 0;
         const int incl = wave_scan(c, [](int a, int b) { return a + b; }) + carry;
         if (e < E) off[e] = incl - c;
         carry = __builtin_amdgcn_readlane(incl, 63);
@@ -170,16 +171,19 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, const int32_t *
 // each slot's gate is computed from it afterwards, once, by one thread, and not by all
 // the lanes of a token in every step of the selection (16384 x 128 20.7 -> 18.7 us in all).
 
-// Waves that add their sums to LDS at a time: all, unless the experts are many.
-__host__ __device__ constexpr int sum_slices(int E) { return E <= 256 ? 16 : 4; }
+// Waves that add their sums to LDS at a time: all, unless the experts are many (and a
+// token's lanes a wave, by_experts).
+template <int LPR>
+constexpr int kSumSlices = LPR < 64 ? 16 : 4;
 
 template <int LPR>
 constexpr int kRouteThreads = 64 * LPR < 1024 ? 64 * LPR : 1024;
 
 // LDS: a word per expert, its slots so far, offsets, sums of probabilities; then
 // a chunk's slots.
-inline size_t route_lds(int E, int k) {
-    return (size_t)E * 8 + (size_t)(2 * E + 1) * 4 + (size_t)sum_slices(E) * E * 4 + (size_t)kRouteTokens * (8 * k + 8) + 16;
+template <int LPR>
+size_t route_lds(int E, int k) {
+    return (size_t)E * 8 + (size_t)(2 * E + 1) * 4 + (size_t)kSumSlices<LPR> * E * 4 + (size_t)kRouteTokens * (8 * k + 8) + 16;
 }
 
 template <class T, int LPR, int V>
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     constexpr int NT = kRouteThreads<LPR>, RPW = 64 / LPR, PASSES = kRouteTokens * LPR / NT, W = NT / 64;
     extern __shared__ uint64_t lds[];
     uint64_t *mask = lds;
-    const int slices = sum_slices(a.E);
+    constexpr int slices = kSumSlices<LPR>;
     float *part = reinterpret_cast<float *>(mask + a.E);                     // [slices][E]
     float *slot_p = part + slices * a.E;                                     // [64][k]: the logit's key, then p
     int32_t *slot_e = reinterpret_cast<int32_t *>(slot_p + kRouteTokens * a.k);
@@ -203,6 +207,8 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
         used[e] = 0;
     }
     if (tid == 0) live = 0;
+    // One chunk is all there is: its offsets are known before its places are written.
+    const bool single = a.blocks == 1 && a.T > 0 && a.T <= kRouteTokens;
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
@@ -215,6 +221,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
         for (int pass = 0; pass < PASSES; ++pass) {
             const int row = (pass * W + wave) * RPW + lane / LPR;
             const int64_t t = tc + row;
+            if (t - lane / LPR >= a.T) break;  // none of the wave's: nothing reads what it would leave
             float x[V], p[V];
             if (t < a.T && (!a.valid || a.valid[t])) {
                 load_logits<T, V>(a.logits + t * a.ld * (int64_t)sizeof(T), col, a.E, x);
@@ -261,6 +268,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
         }
         __syncthreads();
         const int rows = a.T - tc < kRouteTokens ? (int)(a.T - tc) : kRouteTokens;
+        if (single && wave == 0) scan_counts([&](int e) { return __popcll(mask[e]); }, off, a.E);
         for (int i = tid; i < rows * a.k; i += NT) {
             const Scale sc = scale[i / a.k];
             const float x = key_value(__builtin_bit_cast(uint32_t, slot_p[i]));
@@ -277,7 +285,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
             }
             a.experts[o] = e;
             a.gates[o] = e < 0 ? 0.0f : slot_p[i] / sum;
-            a.rows[o] = e < 0 ? -1 : used[e] + __popcll(mask[e] & ((1ull << row) - 1));
+            a.rows[o] = e < 0 ? -1 : (single ? off[e] : used[e]) + __popcll(mask[e] & ((1ull << row) - 1));
         }
         if (wave == 0) {
             const uint64_t has = __ballot(lane < rows && slot_e[lane * a.k] >= 0);
@@ -307,6 +315,7 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
     }
     for (int e = tid; e < a.E; e += NT) {
         float s = part[e];
+#pragma unroll
         for (int i = 1; i < (W < slices ? W : slices); ++i) s += part[i * a.E + e];
         part[e] = s;
         if (a.blocks > 1) {
@@ -324,9 +333,12 @@ __global__ __launch_bounds__(kRouteThreads<LPR>) void route_kernel(RouteArgs a) 
         return;
     }
     __syncthreads();
-    if (wave == 0) scan_counts(used, off, a.E);
-    __syncthreads();
+    if (!single) {
+        if (wave == 0) scan_counts([&](int e) { return used[e]; }, off, a.E);
+        __syncthreads();
+    }
     if (wave == 0) write_totals(a, used, off, part, live);
+    if (single) return;
     // each thread on the slots it wrote above
     for (int64_t tc = 0; tc < a.T; tc += kRouteTokens) {
         const int rows = a.T - tc < kRouteTokens ? (int)(a.T - tc) : kRouteTokens;
@@ -421,7 +433,7 @@ __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(RouteArgs a) {
         }
     __syncthreads();
     if (tid < 64) {
-        scan_counts(total, off, a.E);
+        scan_counts([&](int e) { return total[e]; }, off, a.E);
         if (totals) {
 #pragma unroll
             for (int d = 32; d; d >>= 1) live += __shfl_xor(live, d);
@@ -545,7 +557,7 @@ template <class T>
 hipError_t route(const RouteArgs &a, hipStream_t s) {
     return by_experts(a.E, [&](auto lpr, auto v) {
         hipLaunchKernelGGL(HIP_KERNEL_NAME(route_kernel<T, lpr(), v()>), dim3((unsigned)a.blocks), dim3(kRouteThreads<lpr()>),
-                           route_lds(a.E, a.k), s, a);
+                           route_lds<lpr()>(a.E, a.k), s, a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || a.blocks == 1) return e;
         hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)a.blocks + 1), dim3(kJoinThreads),
