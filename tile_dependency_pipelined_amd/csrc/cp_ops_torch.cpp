@@ -17,6 +17,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -634,20 +635,27 @@ const Tensor &dense(PyObject *o, const char *name) {
     return t;
 }
 
+// The tensors of any iterable, which is gone through once; they live as long as this.
 struct Sequence {
     PyObject *s;
-    explicit Sequence(PyObject *o) : s(PySequence_Fast(o, "gradients and out must be sequences of tensors")) {
+    explicit Sequence(PyObject *o) {
+        PyObject *items = PySequence_Fast(o, "gradients and out must be sequences of tensors");
+        if (!items) throw Raised{};
+        s = PySequence_Tuple(items);  // (a list is the caller's and can change)
+        Py_DECREF(items);
         if (!s) throw Raised{};
     }
     ~Sequence() { Py_DECREF(s); }
     Sequence(const Sequence &) = delete;
-    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(s); }
-    PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
+    Py_ssize_t size() const { return PyTuple_GET_SIZE(s); }
+    PyObject *operator[](Py_ssize_t i) const { return PyTuple_GET_ITEM(s, i); }
 };
 
 // clip_grad_norm(gradients, max_norm, out, scale) -> norm; out: None for in place
 PyObject *clip_grad_norm(PyObject *const *a) {
     const Sequence grads(a[0]);
+    std::optional<Sequence> outs;
+    if (a[2] != Py_None) outs.emplace(a[2]);
     const double max_norm = number(a[1]);
     const bool scale = truth(a[3]);
     const Py_ssize_t n = grads.size();
@@ -671,17 +679,16 @@ PyObject *clip_grad_norm(PyObject *const *a) {
             refuse(PyExc_RuntimeError, "a tensor to write requires a gradient, which is not recorded here; pass .detach() or "
                                        "call under torch.no_grad()");
     };
-    if (a[2] == Py_None) {
+    if (!outs) {
         for (Py_ssize_t i = 0; i < n; ++i) {
             const Tensor &x = dense(grads[i], "gradients");
             if (scale) writable(x);
             enter(i, x, x);
         }
     } else {
-        const Sequence outs(a[2]);
-        if (outs.size() != n) refuse(PyExc_ValueError, "%zd gradients and %zd outputs", n, outs.size());
+        if (outs->size() != n) refuse(PyExc_ValueError, "%zd gradients and %zd outputs", n, outs->size());
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const Tensor &x = dense(grads[i], "gradients"), &y = dense(outs[i], "out");
+            const Tensor &x = dense(grads[i], "gradients"), &y = dense((*outs)[i], "out");
             bool same = x.sizes() == y.sizes();
             for (int64_t d = 0; same && d < x.dim(); ++d)
                 same = x.numel() == 0 || x.size(d) == 1 || x.stride(d) == y.stride(d);
@@ -699,14 +706,8 @@ PyObject *clip_grad_norm(PyObject *const *a) {
     check(cp_clip_grad_norm(n, types.data(), from.data(), numels.data(), (float)max_norm, out_types.data(),
                             scale ? to.data() : nullptr, (float *)norm.data_ptr(), data(ws.t), ws.n, stream(x0)),
           "cp_clip_grad_norm");
-    if (scale) {
-        if (a[2] == Py_None) {
-            for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(grads[i]));
-        } else {
-            const Sequence outs(a[2]);
-            for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(outs[i]));
-        }
-    }
+    if (scale)
+        for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(outs ? (*outs)[i] : grads[i]));
     return wrap(norm);
 }
 

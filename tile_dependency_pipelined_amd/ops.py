@@ -222,6 +222,7 @@ def grad_norm(gradients):
 def clip_grad_norm(gradients, max_norm, out=None):
     """Scales the tensors (float32 and bfloat16, any mix, dense) by min(1, max_norm /
     (norm + 1e-6)) and returns the norm they had.  In place, or into `out`: a
-    tensor of the same shape and strides for each, of either type.  Nothing is read back to the
-    host: a norm that is not finite shows in the norm and in the results."""
+    tensor of the same shape and strides for each, of either type.  Both may be any
+    iterable, and are gone through once.  Nothing is read back to the host: a norm that
+    is not finite shows in the norm and in the results."""
     return _native.clip_grad_norm(gradients, max_norm, out, True)
