@@ -159,10 +159,31 @@ __global__ __launch_bounds__(kClipThreads) void norm_partials_kernel(ClipArgs<N>
     if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
 }
 
-// The partial sums, at most a few KB, are added up by every block, which spares a
-// launch in between; the chunks go last to first, as the last read are the ones
-// that the caches still hold.  A block of one small chunk requests its elements before
-// the partial sums, whose wait is as long.
+// The sum of the partial sums: up to 8 of a thread requested together, in an order that
+// their number alone sets.
+__device__ __forceinline__ double sum_partials(const double *all, int n) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += 8 * kClipThreads) {
+        double t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = all[i + u * kClipThreads < n ? i + u * kClipThreads : i];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += i + u * kClipThreads < n ? t[u] : 0.0;
+    }
+    return block_sum<kClipThreads>(s);
+}
+
+// One block: many launches' partial sums to their sum, in the place of the first.  (The
+// sum's barriers lie between the last read and the write.)
+__global__ __launch_bounds__(kClipThreads) void norm_total_kernel(double *all, int n) {
+    const double s = sum_partials(all, n);
+    if (threadIdx.x == 0) all[0] = s;
+}
+
+// Up to kClipPartials partial sums, 16 KB, are added up by every block, which spares a
+// launch in between (norm_total_kernel); the chunks go last to first, as the last read
+// are the ones that the caches still hold.  A block of one small chunk requests its
+// elements before the partial sums, whose wait is as long.
 template <int N>
 __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
     const int c0 = a.chunks - 1 - (int)blockIdx.x;
@@ -180,15 +201,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
             __builtin_memcpy(&v1, x + (p.bf16_in ? 0 : 16), 16);
         }
     }
-    double s = 0.0;
-    for (int i = threadIdx.x; i < a.nall; i += 8 * kClipThreads) {
-        double t[8];  // requested together
-#pragma unroll
-        for (int u = 0; u < 8; ++u) t[u] = a.all[i + u * kClipThreads < a.nall ? i + u * kClipThreads : i];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) s += i + u * kClipThreads < a.nall ? t[u] : 0.0;
-    }
-    const double norm = sqrt(block_sum<kClipThreads>(s));
+    const double norm = sqrt(sum_partials(a.all, a.nall));
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
     const float f = clip_factor(norm, a.max_norm);
     if (!a.y[0]) return;  // (all have an output, or none)
@@ -229,6 +242,10 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipArgs<N> a) {
 
 }  // namespace
 
+hipError_t launch_norm_total(double *all, int n, hipStream_t s) {
+    hipLaunchKernelGGL(norm_total_kernel, dim3(1), dim3(kClipThreads), 0, s, all, n);
+    return hipGetLastError();
+}
 template <int N>
 hipError_t launch_norm_partials(const ClipArgs<N> &a, hipStream_t s) {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(norm_partials_kernel<N>), dim3((unsigned)a.blocks), dim3(kClipThreads), 0, s, a);

@@ -203,6 +203,10 @@ int launch_clips(int64_t n, int64_t total, const int32_t *dtypes, const void *co
         nall += a.blocks;
         CP_TRY(launched(launch_norm_partials(a, s), "gradient norm"));
     }
+    if (nall > kClipPartials) {
+        CP_TRY(launched(launch_norm_total(partial, nall, s), "gradient norm"));
+        nall = 1;
+    }
     bool first = true;
     for (i = 0; first || (outs && i < n); first = false) {  // (one for the norm, also of nothing)
         ClipArgs<N> a = fill(&i);
