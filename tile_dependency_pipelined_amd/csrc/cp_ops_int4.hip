@@ -558,7 +558,7 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 4; ++r) tile[(m * 16 + quad * 4 + r) * LD + n * 16 + n16] = acc[m][n][r];
-    __builtin_amdgcn_wave_barrier();
+    settle_lds();
     for (int i = lane; i < MT * 16 * NT * 16 / CE; i += 64) {
         const int r = i / (NT * 16 / CE), c0 = i % (NT * 16 / CE) * CE;
         put_int4_unit<T>(g, br, chunk, br.row0 + r, tile0 * 16 + c0, tile + r * LD + c0);

@@ -14,6 +14,7 @@
 // launch that joins the blocks.  16 x 8 bf16 in one block 4.2 us; 16384 x 128 in 256
 // blocks 11.1 and the join 8.2; backward 8191 x 60 4.9.
 #include "cp_ops_experts.h"
+#include "cp_ops_units.h"
 
 namespace cpo {
 
@@ -486,9 +487,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a) {
         uint32_t u[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) u[v] = kNone;
-        if (a.dgates) {  // (a wave's own part of LDS: its accesses are in order)
+        if (a.dgates) {  // (a wave's own part of LDS)
             __builtin_memcpy(__builtin_assume_aligned(row_d + col, 16), u, sizeof u);
-            __builtin_amdgcn_wave_barrier();
+            settle_lds();
             for (int j = sub; j < a.k; j += LPR) {
                 const int e = ex[j];
                 if (has && e >= 0 && e < a.E) {
@@ -496,9 +497,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a) {
                     row_d[e] = g != g ? 0x7FC00000u : __builtin_bit_cast(uint32_t, g);
                 }
             }
-            __builtin_amdgcn_wave_barrier();
+            settle_lds();
             __builtin_memcpy(u, __builtin_assume_aligned(row_d + col, 16), sizeof u);
-            __builtin_amdgcn_wave_barrier();
+            settle_lds();
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {

@@ -1,9 +1,18 @@
-// cp_ops_units.h -- 16-byte units of elements: stored in part, unpacked, packed.
-// Internal to the library.
+// cp_ops_units.h -- 16-byte units of elements: stored in part, unpacked, packed; and the
+// order of a wave's accesses to LDS.  Internal to the library.
 #pragma once
 #include "cp_ops_device.h"
 
 namespace cpo {
+
+// Between a wave's accesses to LDS by which its lanes pass values to each other.  They
+// execute in order; the compiler, to which a lane's own stores are all there is, must
+// keep it.  No instruction comes of it.
+__device__ __forceinline__ void settle_lds() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // The first `n` elements of a unit (all, if it has no more) to memory of any alignment.
 template <class T>
