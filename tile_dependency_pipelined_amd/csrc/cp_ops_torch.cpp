@@ -371,22 +371,32 @@ double number(PyObject *o) {
     return v;
 }
 
-// Several outputs in one allocation, each from a multiple of 256 bytes on: a call to
-// the allocator costs as much as a quarter of a launch.
+// Outputs of one element type in one allocation on the current device, each from a
+// multiple of 256 bytes on: at::empty costs as much as a quarter of a launch each time,
+// its allocator alone less.  (Not outputs of two types: torch.save refuses memory that
+// tensors view as both.)
 struct Pool {
-    Tensor t;
-    int64_t used = 0, size = 0;
-    static int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
-    Pool(const Tensor &x, std::initializer_list<int64_t> bytes) {
-        for (int64_t n : bytes) size += up(n);
-        t = at::empty({size}, x.options().dtype(at::kByte));
+    c10::Storage storage;
+    caffe2::TypeMeta type;
+    int64_t used = 0;
+    static int64_t up(int64_t n) { return (n + 63) / 64 * 64; }  // elements of 4 bytes
+    static size_t bytes(std::initializer_list<int64_t> elements) {
+        int64_t n = 0;
+        for (int64_t e : elements) n += up(e);
+        return (size_t)n * 4;
     }
-    Tensor take(at::IntArrayRef shape, at::ScalarType type) {
-        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), c10::scalarTypeToTypeMeta(type));
-        const int64_t es = (int64_t)c10::elementSize(type);
-        impl->set_storage_offset((t.storage_offset() + used) / es);
+    // at::empty's allocator, the same for every device and as long as the process lives
+    static c10::Allocator *allocator(const Tensor &x) {
+        static c10::Allocator *const a = at::empty({0}, x.options()).storage().allocator();
+        return a;
+    }
+    Pool(const Tensor &x, at::ScalarType t, std::initializer_list<int64_t> elements)
+        : storage(c10::Storage::use_byte_size_t(), bytes(elements), allocator(x), true), type(c10::scalarTypeToTypeMeta(t)) {}
+    Tensor take(at::IntArrayRef shape) {
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
+        impl->set_storage_offset(used);
         impl->set_sizes_contiguous(shape);
-        used += up(impl->numel() * es);
+        used += up(impl->numel());
         return Tensor(std::move(impl));
     }
 };
@@ -419,14 +429,15 @@ PyObject *route(PyObject *const *a) {
     const c10::DeviceGuard guard(x.device());
     const int64_t ws = cp_ops_workspace(CP_OP_ROUTE, code(x), T, 0, E, 0, 1);
     check(ws, "cp_ops_workspace");
-    Pool pool(x, {T * k * 4, T * k * 4, T * k * 4, E * 4, (E + 1) * 4, 4, E * 4, ws});
-    const Tensor experts = pool.take({T, k}, at::kInt), gates = pool.take({T, k}, at::kFloat);
-    const Tensor places = pool.take({T, k}, at::kInt), counts = pool.take({E}, at::kInt);
-    const Tensor offsets = pool.take({E + 1}, at::kInt), loss = pool.take({}, at::kFloat), slopes = pool.take({E}, at::kFloat);
+    Pool ints(x, at::kInt, {T * k, T * k, E, E + 1}), floats(x, at::kFloat, {T * k, E}), one(x, at::kFloat, {1});
+    const Tensor experts = ints.take({T, k}), places = ints.take({T, k}), counts = ints.take({E}), offsets = ints.take({E + 1});
+    const Tensor gates = floats.take({T, k}), slopes = floats.take({E});
+    const Tensor loss = one.take({});  // by itself: the one that a program keeps for its log
+    const Tensor scratch = ws ? at::empty({ws}, x.options().dtype(at::kByte)) : Tensor();
     check(cp_route(code(x), T, (int32_t)E, (int32_t)k, normalize, x.data_ptr(), ld, (const uint8_t *)valid,
                    (int32_t *)experts.data_ptr(), (float *)gates.data_ptr(), (int32_t *)places.data_ptr(),
                    (int32_t *)counts.data_ptr(), (int32_t *)offsets.data_ptr(), (float *)loss.data_ptr(),
-                   (float *)slopes.data_ptr(), ws ? (char *)pool.t.data_ptr() + pool.used : nullptr, ws, stream(x)),
+                   (float *)slopes.data_ptr(), data(scratch), ws, stream(x)),
           "cp_route");
     return wrap_tuple(experts, gates, places, counts, offsets, loss, slopes);
 }

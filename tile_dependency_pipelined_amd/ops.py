@@ -116,7 +116,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, need_x=True, need_weight
 
 
 class Routing(NamedTuple):
-    """What route returns, for T tokens, E experts and k slots to a token."""
+    """What route returns, for T tokens, E experts and k slots to a token.  The int32
+    tensors share an allocation, gates and slopes another; the loss has its own."""
     experts: torch.Tensor  # int32 [T][k], largest logit first; -1: no expert
     gates: torch.Tensor    # float32 [T][k]; 0 without an expert
     rows: torch.Tensor     # int32 [T][k]: the slot's row in expert order; -1 without an expert
