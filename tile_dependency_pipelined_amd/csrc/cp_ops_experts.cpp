@@ -330,6 +330,7 @@ int cp_dispatch(int32_t dtype, int64_t T, int32_t k, int64_t R, int64_t D, const
     CP_TRY(check_words(end, R, "end"));
     CP_TRY(check_apart("out", Rows(mo, dtype), "x", Rows(mx, dtype)));
     CP_TRY(check_apart("out", Rows(mo, dtype), "rows", Rows(rows, T * k * 4)));
+    CP_TRY(check_apart("out", Rows(mo, dtype), "end", Rows(end, 4)));
     if (D == 0 || R == 0) return CP_OK;
     ExchangeArgs a{};
     a.x = (const char *)x;
@@ -385,15 +386,27 @@ int cp_combine_backward(int32_t dtype, int64_t T, int32_t k, int64_t R, int64_t 
     Mat md{dout, T, D, ldd}, my{y, R, D, ldy}, mo{dy, R, D, lddy};
     CP_TRY(check_mat(md, dtype, "dout"));
     if (dgates) CP_TRY(check_mat(my, dtype, "y"));
+    CP_TRY(check_words(gates, gates ? 1 : 0, "gates"));
+    CP_TRY(check_words(dgates, dgates ? 1 : 0, "dgates"));
+    const Rows in_rows(rows, T * k * 4), in_gates(gates, T * k * 4), in_end(dy ? end : nullptr, 4), slots(dgates, T * k * 4);
     if (dy) {
         CP_TRY(check_mat(mo, dtype, "dy"));
         CP_TRY(check_words(end, R, "end"));
-        CP_TRY(check_apart("dy", Rows(mo, dtype), "dout", Rows(md, dtype)));
-        if (dgates) CP_TRY(check_apart("dy", Rows(mo, dtype), "y", Rows(my, dtype)));
-        CP_TRY(check_apart("dy", Rows(mo, dtype), "rows", Rows(rows, T * k * 4)));
+        const Rows o(mo, dtype);
+        CP_TRY(check_apart("dy", o, "dout", Rows(md, dtype)));
+        if (dgates) CP_TRY(check_apart("dy", o, "y", Rows(my, dtype)));
+        CP_TRY(check_apart("dy", o, "rows", in_rows));
+        CP_TRY(check_apart("dy", o, "gates", in_gates));
+        CP_TRY(check_apart("dy", o, "end", in_end));
+        CP_TRY(check_apart("dgates", slots, "dy", o));
     }
-    CP_TRY(check_words(gates, gates ? 1 : 0, "gates"));
-    CP_TRY(check_words(dgates, dgates ? 1 : 0, "dgates"));
+    if (dgates) {
+        CP_TRY(check_apart("dgates", slots, "dout", Rows(md, dtype)));
+        CP_TRY(check_apart("dgates", slots, "y", Rows(my, dtype)));
+        CP_TRY(check_apart("dgates", slots, "rows", in_rows));
+        CP_TRY(check_apart("dgates", slots, "gates", in_gates));
+        CP_TRY(check_apart("dgates", slots, "end", in_end));
+    }
     if (!dy && !dgates) return CP_OK;
     if (T == 0 && (!dy || R == 0 || D == 0)) return CP_OK;
     ExchangeArgs a{};
