@@ -253,11 +253,11 @@ int cp_grouped_linear_int4(int32_t dtype, int64_t T, int64_t K, int64_t N, int32
  *   dtypes[n], grads[n], numels[n], out_dtypes[n], outs[n]: HOST arrays, read
  *   during the call; tensor i has numels[i] elements side by side, all together
  *   2^44 at most
- * outs[i] may be grads[i] (of the same type); apart from that no output shares
- * memory with an input or another output, which is checked.  outs NULL: the norm
- * alone (out_dtypes is not read).  norm: fp32, device memory.  max_norm >= 0; with
- * an infinite one nothing is scaled; a norm that is not finite makes the factor 0
- * or NaN.  n may be 0: the norm is 0.
+ * outs[i] may be grads[i] (of the same type); apart from that no output, norm among
+ * them, shares memory with an input or another output, which is checked.  outs NULL:
+ * the norm alone (out_dtypes is not read).  norm: fp32, device memory.  max_norm >= 0;
+ * with an infinite one nothing is scaled; a norm that is not finite makes the factor
+ * 0 or NaN.  n may be 0: the norm is 0.
  */
 int cp_clip_grad_norm(int64_t n, const int32_t *dtypes, const void *const *grads, const int64_t *numels,
                       float max_norm, const int32_t *out_dtypes, void *const *outs, float *norm, void *ws,

@@ -1,5 +1,6 @@
-"""Host tests: outputs of the rows' way to the experts and back that share memory with
-anything the kernels still read, or with each other, are refused before a launch."""
+"""Host tests: outputs of the rows' way to the experts and back and of the clipping that
+share memory with anything the kernels still read, or with each other, are refused
+before a launch."""
 import ctypes
 
 import pytest
@@ -9,10 +10,11 @@ nat = pytest.importorskip("tile_dependency_pipelined_amd.native",
                           reason="libcpchain.so not built (python -m tile_dependency_pipelined_amd.build)")
 from tile_dependency_pipelined_amd import ops  # noqa: E402,F401
 
-_p, _i, _l = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_p, _i, _l, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 lib = nat.lib()
 lib.cp_dispatch.argtypes = (_i, _l, _i, _l, _l, _p, _l, _p, _p, _p, _l, _p)
 lib.cp_combine_backward.argtypes = (_i, _l, _i, _l, _l, _p, _l, _p, _l, _p, _p, _p, _p, _l, _p, _p)
+lib.cp_clip_grad_norm.argtypes = (_l, _p, _p, _p, _f, _p, _p, _p, _p, _l, _p)
 A, B, C, D, E, F, G = (n << 20 for n in range(1, 8))     # plausible addresses that no call below may touch
 
 
@@ -49,3 +51,12 @@ def test_empty_outputs_are_not_refused():
     assert lib.cp_dispatch(nat.CP_F32, 4, 2, 8, 0, A, 8, B, A, A, 8, None) == nat.CP_OK
     assert lib.cp_combine_backward(nat.CP_F32, 0, 2, 8, 0, A, 8, A, 8, A, A, A, A, 8, A, None) == nat.CP_OK
     assert lib.cp_combine_backward(nat.CP_F32, 4, 2, 8, 8, A, 8, None, 8, A, None, A, None, 8, None, None) == nat.CP_OK
+
+
+@pytest.mark.parametrize("norm, outs", [(A, (C, D)), (A + 396, (C, D)), (B + 196, (C, D)), (C + 396, (C, D)), (D + 4, (C, D)),
+                                        (B, (A, B)), (A, None), (B + 196, None)], ids=str)
+def test_norm(norm, outs):
+    """A gradient of 100 fp32 elements, one of 100 in bf16."""
+    types = (_i * 2)(nat.CP_F32, nat.CP_BF16)
+    refused(lib.cp_clip_grad_norm(2, types, (_p * 2)(A, B), (_l * 2)(100, 100), 1.0, types, None if outs is None else (_p * 2)(*outs),
+                                  norm, E, 1 << 20, None))

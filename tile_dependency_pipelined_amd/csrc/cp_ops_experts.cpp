@@ -238,6 +238,8 @@ int clip(int64_t n, const int32_t *dtypes, const void *const *grads, const int64
         if (!grads[i] || (outs && !outs[i])) return fail(CP_ERR_INVALID_ARG, "tensor %lld is NULL", (long long)i);
         CP_TRY(check_vector(grads[i], dtypes[i], "a gradient"));
         if (outs) CP_TRY(check_vector(outs[i], out_dtypes[i], "an output"));
+        CP_TRY(check_apart("norm", Rows(norm, 4), "a gradient", Rows(grads[i], numels[i] * elem_size(dtypes[i]))));
+        if (outs) CP_TRY(check_apart("norm", Rows(norm, 4), "an output", Rows(outs[i], numels[i] * elem_size(out_dtypes[i]))));
         total += numels[i];
         ++used;
     }
