@@ -180,6 +180,19 @@ def train(block, x, target, steps, lr):
     return losses
 
 
+def train_routed(block, x, target, steps, lr):
+    """Losses, and how far one token's output with 4-bit weights is from that with all."""
+    losses = train(block, x, target, steps, lr)
+    r = block.saved[6]
+    block.pack()
+    full, packed = block.forward(x[:1], keep=False), block.decode(x[:1])
+    off = ((packed.float() - full.float()).norm() / (full.float() - x[:1].float()).norm()).item()
+    print(f"routed: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {steps} steps; balance loss {r.loss.item():.3f} (1: even), "
+          f"rows per expert {r.counts.min().item()} to {r.counts.max().item()}, last gradient norm {block.norm.item():.3f}; "
+          f"one token with 4-bit weights is {off:.3f} of the block's output from that with all", flush=True)
+    return losses, off
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--tokens", type=int, default=2048)
@@ -204,15 +217,7 @@ def main(argv=None):
         print(f"{name}: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps; "
               f"one token alone is {off:.4f} from the same token in the batch", flush=True)
         result[name] = (losses, off)
-    block = Routed(a.width, a.hidden, a.experts, dtype, k=min(2, a.experts))
-    losses = train(block, x, target, a.steps, a.lr)
-    r = block.saved[6]
-    block.pack()
-    full, packed = block.forward(x[:1], keep=False), block.decode(x[:1])
-    off = ((packed.float() - full.float()).norm() / (full.float() - x[:1].float()).norm()).item()
-    print(f"routed: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps; balance loss {r.loss.item():.3f} (1: even), "
-          f"rows per expert {r.counts.min().item()} to {r.counts.max().item()}, last gradient norm {block.norm.item():.3f}; "
-          f"one token with 4-bit weights is {off:.3f} of the block's output from that with all", flush=True)
+    train_routed(Routed(a.width, a.hidden, a.experts, dtype, k=min(2, a.experts)), x, target, a.steps, a.lr)
     return result
 
 
