@@ -337,14 +337,12 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
         }
 }
 
-// The sum of each 2 or 4 neighbouring lanes' values, in all of them.
+// The sum of each 2 neighbouring lanes' values, in both (N = 1: the value).
 template <int N>
 __device__ __forceinline__ float sum_neighbours(float v) {
-    auto swapped = [](float u, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, u), ctrl(), 0xf, 0xf, true));
-    };
-    if constexpr (N >= 2) v += swapped(v, std::integral_constant<int, 0xB1>());  // quad_perm 1 0 3 2
-    if constexpr (N >= 4) v += swapped(v, std::integral_constant<int, 0x4E>());  // quad_perm 2 3 0 1
+    static_assert(N == 1 || N == 2, "pieces of a group");
+    if constexpr (N == 2)  // quad_perm 1 0 3 2
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, true));
     return v;
 }
 
