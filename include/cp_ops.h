@@ -234,7 +234,9 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
  * a packed weight, for decoding and short prompts: from some hundred rows on the
  * layer with a bf16 weight is faster (2048 x 8192 x 8192 208 us, here 454).
  * Products of x with the codes are exact and added up in fp32, a group at a time;
- * the weight itself is never rounded.  x is meant to be finite and below 2^115: a
+ * the weight itself is never rounded.  With fp32 rows a result is as good as that of
+ * the weight in fp32; with bf16 rows it is off by a few 2^-24 of 31 scales sum |x|
+ * beside its rounding to bf16, also where all codes are their zero points.  x is meant to be finite and below 2^115: a
  * row with infinities gives NaN.  More than 2^22 workgroups are refused with
  * CP_ERR_SHAPE: tiles of 32 x 64 at least (an expert's last one counting in full)
  * or, with at most 16 rows to an expert, experts times parts of K of 2048 at least.

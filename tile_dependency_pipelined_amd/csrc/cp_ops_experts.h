@@ -119,7 +119,9 @@ inline Int4Tiles int4_tiles(int dtype, int experts, int64_t M, int64_t ntiles, i
     if (rows <= 16) {
         t.ntm = row_tiles(16);
         const bool bf16 = dtype == CP_BF16;
-        t.waves = kblocks <= 4 ? 4 : (bf16 ? 16 : 8);
+        // (fp32 with more than 8 tiles of K: 16 waves of one tile each rather than 8 of two, whose
+        // registers leave room for two waves to a SIMD: 13 x 8192 x 8192 25 us against 18)
+        t.waves = kblocks <= 4 ? 4 : (bf16 || kblocks > 8 ? 16 : 8);
         const int64_t most = bf16 ? 64 : 16;  // tiles of x that a block's registers hold (fp32: three operands each)
         if (kblocks > most) t.chunks = (int32_t)((kblocks + most - 1) / most);
         // blocks that fill the device, shared out over the row tiles that are likely there

@@ -7,9 +7,14 @@
 // in bits 3 .. 6 of a bf16 pattern 0x4180 make it 16 + q, two codes with one shift
 // and one and-or.  A product with ones gives sum x, and per group
 //     s_n (sum x (16 + q) - (16 + z_n) sum x)
-// joins the fp32 accumulator.  fp32 rows run as three bf16 parts that add up to
-// them exactly.  The codes lie in memory as the instructions take them (Int4Layout),
-// so a wave reads its operand with whole 16-byte loads and no LDS.
+// joins the fp32 accumulator: of two sums up to four times as large as their difference
+// can be, whose roundings, some 2^-24 of them, only a bf16 result near zero shows.
+// fp32 rows run as three bf16 parts that add up to them exactly, and q - z is the other
+// operand, as exact as 16 + q and more work to unpack: a result is as good as that of the
+// weight in fp32 (K 4096, x of one sign: off by 1.3e-7 of its norm, by way of the
+// two sums 1.8e-6), and weights of zero add nothing.  The codes lie in memory as the
+// instructions take them (Int4Layout), so a wave reads its operand with whole 16-byte
+// loads and no LDS.
 #include "cp_ops_experts.h"
 #include "cp_ops_units.h"
 
@@ -33,6 +38,30 @@ struct Spread {
         return r.v;
     }
 };
+// q - z, for the fp32 rows.  Four codes at a time in bytes: 0x80 + q - z borrows nothing from
+// its neighbours, and without the 0x80 is signed.  20 instructions to eight codes, by way of
+// fp32 differences of 16 + q 27; 16 + q itself is 7, which many experts of few rows feel
+// (64 rows over 32 experts of 1024 x 4096 18.9 us, so 23.9).
+__device__ __forceinline__ uint32_t centre_of(float zero) {  // zero: 16 + z
+    return 0x80808080u - (uint32_t)((int)zero - 16) * 0x01010101u;
+}
+__device__ __forceinline__ bf16x8_t centred(uint32_t w, uint32_t centre) {
+    auto bytes = [&](uint32_t q) { return ((q & 0x0F0F0F0Fu) + centre) ^ 0x80808080u; };
+    auto pair = [](uint32_t d, int i) {  // bytes i and i + 2: whole numbers of up to 5 bits, the upper halves of their fp32
+        const float lo = (float)(int)(int8_t)(d >> (8 * i)), hi = (float)(int)(int8_t)(d >> (8 * i + 16));
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+    };
+    const uint32_t a = bytes(w >> 3), b = bytes(__builtin_amdgcn_alignbit(w, w, 7));
+    union {
+        uint32_t u[4];
+        bf16x8_t v;
+    } r;
+    r.u[0] = pair(a, 0);
+    r.u[1] = pair(b, 0);
+    r.u[2] = pair(a, 1);
+    r.u[3] = pair(b, 1);
+    return r.v;
+}
 __device__ __forceinline__ bf16x8_t ones_bf16() {
     union {
         uint32_t u[4];
@@ -203,7 +232,7 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
     constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG;
     __shared__ f32x4_t red[2][W][64];
     __shared__ float done[kInt4Flush][256];
-    __shared__ f32x4_t sums[W][XK * NG][4];  // of x over the groups
+    __shared__ f32x4_t sums[XP == 1 ? W : 1][XK * NG][4];  // of x over the groups
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // An XCD has a range of the columns, for all row tiles: of those the last may not be
     // there, and would leave it idle were they all its own.
@@ -251,20 +280,20 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
                 else xr[i][s].zero();
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if constexpr (XP == 1)
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int j = 0; j < NG; ++j) {
+                    f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int s = j * SG; s < j * SG + SG; ++s) {
-                    bf16x8_t x[XP];
-                    parts(xr[i][s], x);
-#pragma unroll
-                    for (int q = 0; q < XP; ++q) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
+                    for (int s = j * SG; s < j * SG + SG; ++s) {
+                        bf16x8_t x[XP];
+                        parts(xr[i][s], x);
+                        xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], ones_bf16(), xs, 0, 0, 0);
+                    }
+                    if ((lane & 15) == 0) sums[wave][i * NG + j][lane >> 4] = xs;
                 }
-                if ((lane & 15) == 0) sums[wave][i * NG + j][lane >> 4] = xs;
-            }
         }
-        __syncthreads();
+        if constexpr (XP == 1) __syncthreads();
     }
     auto column = [&](int d, int t) {
         f32x4_t acc{0.0f, 0.0f, 0.0f, 0.0f};
@@ -272,19 +301,21 @@ __global__ __launch_bounds__(W * 64) void int4_stream_kernel(Int4Args g) {
         for (int i = 0; i < XK; ++i)
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                const f32x4_t xs = sums[wave][i * NG + j][lane >> 4];
+                const float sc = w[d][i].m[j].scale(), zero = w[d][i].m[j].zero();
+                const uint32_t centre = XP > 1 ? centre_of(zero) : 0;
+                f32x4_t xs{0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (XP == 1) xs = sums[wave][i * NG + j][lane >> 4];
                 f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = j * SG; s < j * SG + SG; ++s) {
-                    const bf16x8_t c = spread(w[d][i].step(s));
+                    const bf16x8_t c = XP == 1 ? spread(w[d][i].step(s)) : centred(w[d][i].step(s), centre);
                     bf16x8_t x[XP];
                     parts(xr[i][s], x);
 #pragma unroll
                     for (int q = 0; q < XP; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], c, p, 0, 0, 0);
                 }
-                const float sc = w[d][i].m[j].scale(), zp = -w[d][i].m[j].zero();
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] = fmaf(sc, fmaf(zp, xs[r], p[r]), acc[r]);
+                for (int r = 0; r < 4; ++r) acc[r] = fmaf(sc, XP == 1 ? fmaf(-zero, xs[r], p[r]) : p[r], acc[r]);
                 __builtin_amdgcn_sched_barrier(0);  // (one group's registers at a time)
                 if (D == 1 && j == NG - 1) {  // the next tile's part as soon as its registers are free
                     asm volatile("" : "+v"(acc));
@@ -365,7 +396,7 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
     constexpr int kBuf = XP * 4 * MT * 1024, kJoin = (WK - 1) * MT * NT * 4096, kOut = 4 * MT * 16 * LD * 4;
     constexpr int kMost = kJoin > kOut ? kJoin : kOut;
     __shared__ __attribute__((aligned(16))) char stage[WK * 2 * kBuf > kMost ? WK * 2 * kBuf : kMost];
-    __shared__ f32x4_t sums[WK][2][UH][MT][4];
+    __shared__ f32x4_t sums[XP == 1 ? WK : 1][2][UH][MT][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave & 3, wk = wave >> 2, n16 = lane & 15, quad = lane >> 4;
     const int b = xcd_remap(blockIdx.x, gridDim.x), part = b / g.ntm, rt = b % g.ntm, ct = part / g.chunks, chunk = part % g.chunks;
@@ -417,12 +448,13 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
                 parts(xr[u][f], x);
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
+                    if constexpr (XP == 1) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], ones_bf16(), xs, 0, 0, 0);
                     *reinterpret_cast<bf16x8_t *>(stage + (wk * 2 + buf) * kBuf + ((q * 4 + uh[u] * UF + f) * MT + um[u]) * 1024 +
                                                   lane * 16) = x[q];
                 }
             }
-            if (n16 == 0) sums[wk][buf][uh[u]][um[u]][quad] = xs;
+            if constexpr (XP == 1)
+                if (n16 == 0) sums[wk][buf][uh[u]][um[u]][quad] = xs;
         }
     };
     f32x4_t acc[MT][NT];
@@ -436,16 +468,20 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             bf16x8_t w[SG][NT];
+            uint32_t centre[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) centre[n] = XP > 1 ? centre_of(c0[n].m[j].zero()) : 0;
 #pragma unroll
             for (int s = 0; s < SG; ++s)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) w[s][n] = spread(c0[n].step(j * SG + s));
+                for (int n = 0; n < NT; ++n)
+                    w[s][n] = XP == 1 ? spread(c0[n].step(j * SG + s)) : centred(c0[n].step(j * SG + s), centre[n]);
             // a row tile's operands are read while the one before is multiplied and the one
             // before that scaled
             bf16x8_t x[2][SG][XP];
             f32x4_t xs[2], ys[2];
             auto fetch = [&](int m) {
-                xs[m & 1] = sums[wk][buf][SG > UF ? n16 % (SG / UF) : j][m][quad];
+                if constexpr (XP == 1) xs[m & 1] = sums[wk][buf][SG > UF ? n16 % (SG / UF) : j][m][quad];
 #pragma unroll
                 for (int s = 0; s < SG; ++s)
 #pragma unroll
@@ -455,20 +491,24 @@ __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
             };
             f32x4_t p[2][NT];
             auto scale = [&](int m) {
+                if constexpr (XP == 1)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) ys[m & 1][r] = sum_neighbours<SG / UF>(ys[m & 1][r]);
+                    for (int r = 0; r < 4; ++r) ys[m & 1][r] = sum_neighbours<SG / UF>(ys[m & 1][r]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float sc = c0[n].m[j].scale(), zp = -c0[n].m[j].zero();
+                    const float sc = c0[n].m[j].scale(), zero = c0[n].m[j].zero();
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc, fmaf(zp, ys[m & 1][r], p[m & 1][n][r]), acc[m][n][r]);
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = XP == 1 ? fmaf(-zero, ys[m & 1][r], p[m & 1][n][r]) : p[m & 1][n][r];
+                        acc[m][n][r] = fmaf(sc, v, acc[m][n][r]);
+                    }
                 }
             };
             fetch(0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 if (m + 1 < MT) fetch(m + 1);
-                ys[m & 1] = xs[m & 1];
+                if constexpr (XP == 1) ys[m & 1] = xs[m & 1];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) p[m & 1][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -706,9 +746,11 @@ hipError_t int4(const Int4Args &a, const Int4Tiles &t, hipStream_t s) {
         });
     return by_group(a.group, [&](auto sg) {
         constexpr int SG = sg();
-        if (t.waves == 4) return stream_rows<T, SG, 4, 1, 4>(a, n, s);
+        // (fp32: as far ahead as leaves the registers for four waves to a SIMD.  13 x 512 x 28672
+        // 4 ahead 8.8 us, 2 7.8; 13 x 1024 x 28672 4 ahead 10.4, 3 10.3, 2 10.9, with groups of 64 14.5, 10.8, 11.4)
+        if (t.waves == 4) return stream_rows<T, SG, 4, 1, kWide ? 2 : 4>(a, n, s);
         if constexpr (kWide) {
-            return t.kper <= 8 ? stream_rows<T, SG, 8, 1, 4>(a, n, s) : stream_rows<T, SG, 8, 2, 2>(a, n, s);
+            return t.waves == 8 ? stream_rows<T, SG, 8, 1, 3>(a, n, s) : stream_rows<T, SG, 16, 1, 2>(a, n, s);
         } else {
             if (t.kper <= 16) return stream_rows<T, SG, 16, 1, 4>(a, n, s);
             return t.kper <= 32 ? stream_rows<T, SG, 16, 2, (SG > 1 ? 2 : 1)>(a, n, s) : stream_rows<T, SG, 16, 4, 1>(a, n, s);
