@@ -202,7 +202,9 @@ int cp_combine(int32_t dtype, int64_t T, int32_t k, int64_t R, int64_t D, const 
  *   dy[rows[t][j]] = gates[t][j] dout[t], zero from *end on
  *   dgates[t][j]   = sum_d dout[t][d] y[rows[t][j]][d], fp32, 0 without a slot
  * dy[R][D] and dgates[T][k] may each be NULL; y may be NULL without dgates,
- * end without dy.  (The gradient of res is dout itself.)
+ * end without dy.  (The gradient of res is dout itself.)  The order in which a
+ * token's dgates are added up goes by T, k and D, so with other tokens in the call
+ * they may differ in the last bits.
  */
 int cp_combine_backward(int32_t dtype, int64_t T, int32_t k, int64_t R, int64_t D, const void *dout, int64_t ldd,
                         const void *y, int64_t ldy, const int32_t *rows, const int32_t *end, const float *gates,
@@ -231,12 +233,15 @@ int cp_int4_pack(int32_t dtype, int64_t K, int64_t N, int32_t E, int64_t group, 
 
 /*
  * cp_linear_int4, cp_grouped_linear_int4 -- cp_linear and cp_grouped_linear with
- * a packed weight, for decoding and short prompts: from some hundred rows on the
- * layer with a bf16 weight is faster (2048 x 8192 x 8192 208 us, here 454).
+ * a packed weight, for decoding and short prompts: the layer with a bf16 weight is
+ * faster from about 400 rows on, from about 100 where that weight stays in the last
+ * cache (8192 x 8192: 256 rows 56 us, with bf16 63 and in the cache 45; 2048 rows
+ * 433 to 454 and 195 to 208).
  * Products of x with the codes are exact and added up in fp32, a group at a time;
  * the weight itself is never rounded.  With fp32 rows a result is as good as that of
  * the weight in fp32; with bf16 rows it is off by a few 2^-24 of 31 scales sum |x|
- * beside its rounding to bf16, also where all codes are their zero points.  x is meant to be finite and below 2^115: a
+ * beside its rounding to bf16, also where all codes are their zero points.  x is
+ * meant to be finite and below 2^115: a
  * row with infinities gives NaN.  More than 2^22 workgroups are refused with
  * CP_ERR_SHAPE: tiles of 32 x 64 at least (an expert's last one counting in full)
  * or, with at most 16 rows to an expert, experts times parts of K of 2048 at least.

@@ -385,9 +385,10 @@ __device__ __forceinline__ float sum_neighbours(float v) {
 // codes are requested two tiles of the contraction ahead, x first: loads come back in
 // order, and x is waited for first, to be staged one tile ahead.  (No branch around a
 // load, as above: what lies past K comes last.)
-// 300 x 8192 x 8191, groups of 64, bf16: 82 us, 490 TFLOP/s.  The matrix cores are busy
-// for 21% of it, LDS for 28%; waves wait for 36% of their cycles and issue vector
-// instructions for most of the rest: two per result and group, beside the unpacking.
+// 300 x 8192 x 8191, groups of 64, bf16: 82 us, 490 TFLOP/s.  A wave has 46 matrix and
+// 248 vector instructions to 128 k, 20 and 26 us of a SIMD's time for its two waves; the
+// matrix cores are busy for 21% of the time, LDS for 28%.  The rest is waiting: one block
+// fits a CU, and its waves meet at a barrier every 128 k.
 template <class T, int MT, int NT, int WK, int SG>
 __global__ __launch_bounds__(WK * 256) void int4_rows_kernel(Int4Args g) {
     constexpr int XP = sizeof(T) == 2 ? 1 : 3, NG = 4 / SG;

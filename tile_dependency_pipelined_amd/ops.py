@@ -159,7 +159,8 @@ def combine(y, rows, gates=None, residual=None, out=None):
 
 def combine_backward(dout, y, rows, offsets, gates=None, need_y=True, need_gates=True):
     """Gradients (dy, dgates) of combine for dout [T][D]; None for those not asked
-    for.  Rows of dy from offsets[E] on are zero.  The residual's is dout."""
+    for.  Rows of dy from offsets[E] on are zero.  The residual's is dout.  With other
+    numbers of tokens dgates may be added up in another order."""
     return _native.combine_backward(dout, y, rows, offsets, gates, need_y, need_gates)
 
 
